@@ -16,8 +16,10 @@
  * ssd_verify_ring (verify rounds on a device-resident ring of recent states, with
  * rollback), the per-device pieces of the sequence-parallel scan (ssd_seq_*) and, as a comparison kernel on the same data, ssd_selective_scan_fwd
  * (the selective scan with one channel per head and a diagonal A that SSD replaces).
+ * Beside them: the gated delta rule (ssd_gated_delta_*), a recurrence of the same layout
+ * with another update, and the norms around a block (ssd_norm_*).
  *
- * Both compute, per batch row b and head h (group g = h / (H/G)):
+ * ssd_chunk_scan_fwd and ssd_verify_step compute, per batch row b and head h (group g = h / (H/G)):
  *
  *   h_t = exp(dt_t * A_h) * h_{t-1} + dt_t * x_t (outer) B_t      state [P x N]
  *   y_t = C_t . h_t + D_h * x_t                                    (sum over N)
@@ -431,6 +433,100 @@ ssd_status_t ssd_chunk_scan_bwd(const void *x, const float *dt, const float *A, 
                                 float *dA, void *dB, void *dC, float *dD, float *d_init, int b,
                                 int L, int H, int P, int N, int G, ssd_dtype_t io,
                                 void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/*
+ * The gated delta rule: the recurrence of this file with an update that first takes out
+ * what the state already holds for a key.  Per batch row b and head h (group
+ * g = h / (H/G) of keys and queries), with S the state [P x N]:
+ *
+ *   S'  = exp(a_t) S_{t-1}
+ *   u_t = beta_t (v_t - S' k_t)
+ *   S_t = S' + u_t (outer) k_t
+ *   y_t = scale * S_t q_t                                       (sum over N)
+ *
+ * v stands where x does above, k and q where B and C do, and a_t is the step's log decay
+ * (what dt_t A_h is above), given per token and head.
+ *   q, k       [b, L, G, N]  io      v, y  [b, L, H, P]  io
+ *   a, beta    [b, L, H]     fp32    states [b, H, P, N]  fp32
+ * a <= 0 and beta |k|^2 <= 2 is the domain (outside it the recurrence itself grows).
+ * a = -infinity forgets the state; a token with a = 0 and beta = 0 leaves it as it is,
+ * so sequences of unequal length are padded with such tokens.
+ *
+ * ssd_gated_delta_step: K tokens on an existing state (K = 1: decoding; K > 1: draft
+ *   tokens being verified).  accept_len [b] int32, or NULL for K everywhere: state_out is
+ *   the state after accept_len[b] tokens (0 copies state_in bit for bit), y is written
+ *   for all K.  Values outside [0, K] are clamped and set *err_flag (NULL allowed) to 1.
+ *   state_out may equal state_in exactly.  K in [1, 16], N in {16, 32, 64, 128, 256},
+ *   any P >= 1.  q, k and states 16-byte aligned.
+ *
+ * ssd_gated_delta_fwd: a whole sequence from init_state (NULL = zeros); final_state
+ *   (NULL = skip) is the state after the last token.  N in {16, 32, 64, 128, 256}, any
+ *   P >= 1.  workspace: ssd_gated_delta_fwd_workspace_bytes bytes ((size_t)-1: dimensions
+ *   this build does not run), 16-byte aligned, scratch without preparation; calls that
+ *   overlap in time need one each.  L = 0 copies init_state (or zeros) to final_state.
+ *   q, k, v, y, states 16-byte aligned, a and beta 4-byte.
+ *
+ * Outputs must not overlap inputs, each other or the workspace.  States and all sums are
+ * kept in fp32; y is rounded once.  Errors as for the other entry points.
+ */
+ssd_status_t ssd_gated_delta_step(const float *state_in, const void *q, const void *k,
+                                  const void *v, const float *a, const float *beta,
+                                  const int32_t *accept_len, void *y, float *state_out,
+                                  int32_t *err_flag, int b, int K, int H, int P, int N, int G,
+                                  float scale, ssd_dtype_t io, void *hip_stream);
+size_t ssd_gated_delta_fwd_workspace_bytes(int b, int L, int H, int P, int N, int G,
+                                           ssd_dtype_t io);
+ssd_status_t ssd_gated_delta_fwd(const void *q, const void *k, const void *v, const float *a,
+                                 const float *beta, const float *init_state, void *y,
+                                 float *final_state, int b, int L, int H, int P, int N, int G,
+                                 float scale, ssd_dtype_t io, void *workspace,
+                                 size_t workspace_bytes, void *hip_stream);
+
+/*
+ * The norms around a mixer block, each fused with what stands next to it; act(z) =
+ * z / (1 + e^-z), w fp32.
+ *
+ * ssd_norm_gate_fwd: the norm after the mixer with its gate, one norm per group of
+ *   `group` channels (group divides D; group = D is one norm per row, group = P one per
+ *   head), r = 1 / sqrt(mean(u^2) + eps) over the group:
+ *     gate_first == 0:  u = x,          y = u r w act(z)
+ *     gate_first != 0:  u = x act(z),   y = u r w
+ *   x, z, y [rows, D] io; z NULL means no gate; w [D].
+ * ssd_norm_gate_bwd: dx, dz (like x; dz NULL exactly when z is) and dw [D] fp32 from dy.
+ *
+ * ssd_norm_add_fwd: the residual sum with a per-channel scale and the norm of the next
+ *   block:  sum = residual + scale x (rounded to the residual's type),
+ *   y = sum r w, r = 1 / sqrt(mean(sum^2) + eps) over the row.
+ *   x, y [rows, D] io; residual, sum [rows, D] of type res_io (fp32, or io); scale [D]
+ *   fp32, NULL means 1; w [D].  sum may equal residual exactly.
+ * ssd_norm_add_bwd: from dy and d_sum (the gradient that reaches sum from elsewhere, like
+ *   sum; NULL = zero): dx, d_residual (like x, like sum), d_scale [D] fp32 (NULL exactly
+ *   when scale is) and dw [D] fp32.  sum is the forward call's output; x is read for
+ *   d_scale alone and may be NULL without scale.
+ *
+ * The backward calls take scratch of ssd_norm_bwd_workspace_bytes bytes (group = D for
+ * norm_add; params = the number of [D] gradients: 1, or 2 for norm_add with a scale;
+ * (size_t)-1: invalid dimensions).  Parameter gradients are summed in a fixed order.
+ * Any D >= 1, rows >= 0 (rows = 0 zeroes the parameter gradients).  All pointers 16-byte
+ * aligned.  Sums in fp32, every output rounded once.  Outputs must not overlap inputs
+ * (but for sum), each other or the workspace.  Errors as for the other entry points.
+ */
+ssd_status_t ssd_norm_gate_fwd(const void *x, const void *z, const float *w, void *y, int rows,
+                               int D, int group, float eps, int gate_first, ssd_dtype_t io,
+                               void *hip_stream);
+size_t ssd_norm_bwd_workspace_bytes(int rows, int D, int group, int params, ssd_dtype_t io);
+ssd_status_t ssd_norm_gate_bwd(const void *x, const void *z, const float *w, const void *dy,
+                               void *dx, void *dz, float *dw, int rows, int D, int group,
+                               float eps, int gate_first, ssd_dtype_t io, void *workspace,
+                               size_t workspace_bytes, void *hip_stream);
+ssd_status_t ssd_norm_add_fwd(const void *x, const void *residual, const float *scale,
+                              const float *w, void *sum, void *y, int rows, int D, float eps,
+                              ssd_dtype_t io, ssd_dtype_t res_io, void *hip_stream);
+ssd_status_t ssd_norm_add_bwd(const void *x, const void *sum, const float *scale, const float *w,
+                              const void *dy, const void *d_sum, void *dx, void *d_residual,
+                              float *d_scale, float *dw, int rows, int D, float eps,
+                              ssd_dtype_t io, ssd_dtype_t res_io, void *workspace,
+                              size_t workspace_bytes, void *hip_stream);
 
 /* Static, human-readable name of a status code. */
 const char *ssd_status_string(ssd_status_t status);

@@ -35,6 +35,9 @@ EXPORTED = ("ssd_chunk_scan_workspace_bytes", "ssd_chunk_scan_workspace_init",
             "ssd_verify_ring_init", "ssd_verify_ring", "ssd_verify_ring_rollback",
             "ssd_seq_slice_state_workspace_bytes", "ssd_seq_slice_state",
             "ssd_seq_total_decay", "ssd_seq_combine", "ssd_seq_apply_state",
+            "ssd_gated_delta_step", "ssd_gated_delta_fwd_workspace_bytes",
+            "ssd_gated_delta_fwd", "ssd_norm_gate_fwd", "ssd_norm_bwd_workspace_bytes",
+            "ssd_norm_gate_bwd", "ssd_norm_add_fwd", "ssd_norm_add_bwd",
             "ssd_status_string", "ssd_version")
 
 _lib = None
@@ -90,6 +93,23 @@ def lib() -> ctypes.CDLL:
         L.ssd_seq_combine.restype = i32
         L.ssd_seq_apply_state.argtypes = [vp] * 6 + [i32] * 6 + [i32, vp]
         L.ssd_seq_apply_state.restype = i32
+        f32 = ctypes.c_float
+        L.ssd_gated_delta_step.argtypes = [vp] * 10 + [i32] * 6 + [f32, i32, vp]
+        L.ssd_gated_delta_step.restype = i32
+        L.ssd_gated_delta_fwd_workspace_bytes.argtypes = [i32] * 7
+        L.ssd_gated_delta_fwd_workspace_bytes.restype = sz
+        L.ssd_gated_delta_fwd.argtypes = [vp] * 8 + [i32] * 6 + [f32, i32, vp, sz, vp]
+        L.ssd_gated_delta_fwd.restype = i32
+        L.ssd_norm_gate_fwd.argtypes = [vp] * 4 + [i32] * 3 + [f32, i32, i32, vp]
+        L.ssd_norm_gate_fwd.restype = i32
+        L.ssd_norm_bwd_workspace_bytes.argtypes = [i32] * 5
+        L.ssd_norm_bwd_workspace_bytes.restype = sz
+        L.ssd_norm_gate_bwd.argtypes = [vp] * 7 + [i32] * 3 + [f32, i32, i32, vp, sz, vp]
+        L.ssd_norm_gate_bwd.restype = i32
+        L.ssd_norm_add_fwd.argtypes = [vp] * 6 + [i32] * 2 + [f32, i32, i32, vp]
+        L.ssd_norm_add_fwd.restype = i32
+        L.ssd_norm_add_bwd.argtypes = [vp] * 10 + [i32] * 2 + [f32, i32, i32, vp, sz, vp]
+        L.ssd_norm_add_bwd.restype = i32
         L.ssd_status_string.argtypes = [i32]
         L.ssd_status_string.restype = ctypes.c_char_p
         L.ssd_version.argtypes = []
@@ -370,6 +390,168 @@ def ssd_seq_apply_state(y, final_state, dt, A, C, h_in, stream=None) -> None:
         raise SSDError(st, "ssd_seq_apply_state")
 
 
+# ------------------------------------------------ gated delta rule, norms of a block
+# These check shapes and devices too, and launch on the tensors' device whatever the
+# current one is.
+def _tensor(t, name, shape, dtype, device) -> Optional[int]:
+    """The device pointer of ``t`` after checking what the C call cannot see; None stays None."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _enqueue(name, device, stream, *args) -> None:
+    """Call the C entry point ``name`` with ``args`` and a stream of ``device`` (default:
+    its current one)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors are on {device}")
+    if device.index == torch.cuda.current_device():
+        st = getattr(lib(), name)(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = getattr(lib(), name)(*args, stream.cuda_stream)
+    if st != 0:
+        raise SSDError(st, name)
+
+
+class _NoSwitch:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+def _allocating_on(stream):
+    """What a wrapper allocates for work on ``stream`` is allocated on that stream."""
+    return _NoSwitch() if stream is None else torch.cuda.stream(stream)
+
+
+def _scratch(nbytes, device) -> Optional[torch.Tensor]:
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _workspace_arg(workspace, device):
+    if workspace is None:
+        return None, 0
+    return (_tensor(workspace, "workspace", workspace.shape, torch.uint8, device), workspace.numel())
+
+
+def _delta_dims(k, v):
+    if k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and k are [b, L, G, N], v is [b, L, H, P]")
+    return (*v.shape, k.shape[3], k.shape[2])
+
+
+def ssd_gated_delta_step(state_in, q, k, v, a, beta, accept_len, y, state_out, scale, err_flag=None,
+                         stream=None) -> None:
+    """Enqueue K tokens of the gated delta rule on a kept state (see include/ssd_mi355x.h)."""
+    b, K, H, P, N, G = _delta_dims(k, v)
+    dev, io, f32 = v.device, v.dtype, torch.float32
+    qk, vy, gt, st = (b, K, G, N), (b, K, H, P), (b, K, H), (b, H, P, N)
+    _enqueue("ssd_gated_delta_step", dev, stream,
+             _tensor(state_in, "state_in", st, f32, dev), _tensor(q, "q", qk, io, dev),
+             _tensor(k, "k", qk, io, dev), _tensor(v, "v", vy, io, dev),
+             _tensor(a, "a", gt, f32, dev), _tensor(beta, "beta", gt, f32, dev),
+             _tensor(accept_len, "accept_len", (b,), torch.int32, dev),
+             _tensor(y, "y", vy, io, dev), _tensor(state_out, "state_out", st, f32, dev),
+             None if err_flag is None else _tensor(err_flag, "err_flag", err_flag.shape, torch.int32, dev),
+             b, K, H, P, N, G, scale, _io_code(v))
+
+
+def ssd_gated_delta_fwd_workspace_bytes(b, L, H, P, N, G, io: int) -> int:
+    n = lib().ssd_gated_delta_fwd_workspace_bytes(b, L, H, P, N, G, io)
+    if n == ctypes.c_size_t(-1).value:
+        raise SSDError(4, "ssd_gated_delta_fwd_workspace_bytes")
+    return n
+
+
+def ssd_gated_delta_fwd(q, k, v, a, beta, init_state, y, final_state, scale, workspace,
+                        stream=None) -> None:
+    """Enqueue the gated delta rule over whole sequences: q, k [b,L,G,N], v, y [b,L,H,P]
+    (one type, float32 or bfloat16), a, beta [b,L,H], states [b,H,P,N] float32."""
+    b, L, H, P, N, G = _delta_dims(k, v)
+    dev, io, f32 = v.device, v.dtype, torch.float32
+    qk, vy, gt, st = (b, L, G, N), (b, L, H, P), (b, L, H), (b, H, P, N)
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _enqueue("ssd_gated_delta_fwd", dev, stream, _tensor(q, "q", qk, io, dev),
+             _tensor(k, "k", qk, io, dev), _tensor(v, "v", vy, io, dev),
+             _tensor(a, "a", gt, f32, dev), _tensor(beta, "beta", gt, f32, dev),
+             _tensor(init_state, "init_state", st, f32, dev), _tensor(y, "y", vy, io, dev),
+             _tensor(final_state, "final_state", st, f32, dev), b, L, H, P, N, G, scale,
+             _io_code(v), ws, ws_bytes)
+
+
+def ssd_norm_gate_fwd(x, z, w, y, group, eps, gate_first, stream=None) -> None:
+    """Enqueue the gated norm of x [..., D] (z like x or None, w [D] float32) into y."""
+    D, dev = x.shape[-1], x.device
+    rows = x.numel() // D if D else 0
+    _enqueue("ssd_norm_gate_fwd", dev, stream, _tensor(x, "x", x.shape, x.dtype, dev),
+             _tensor(z, "z", x.shape, x.dtype, dev), _tensor(w, "w", (D,), torch.float32, dev),
+             _tensor(y, "y", x.shape, x.dtype, dev), rows, D, group, eps, 1 if gate_first else 0,
+             _io_code(x))
+
+
+def ssd_norm_bwd_workspace_bytes(rows, D, group, params, io: int) -> int:
+    n = lib().ssd_norm_bwd_workspace_bytes(rows, D, group, params, io)
+    if n == ctypes.c_size_t(-1).value:
+        raise SSDError(2, "ssd_norm_bwd_workspace_bytes")
+    return n
+
+
+def ssd_norm_gate_bwd(x, z, w, dy, dx, dz, dw, group, eps, gate_first, workspace, stream=None) -> None:
+    """Enqueue the gradients of the gated norm: dx, dz like x (dz None when z is), dw [D]."""
+    D, dev, f32 = x.shape[-1], x.device, torch.float32
+    rows = x.numel() // D if D else 0
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _enqueue("ssd_norm_gate_bwd", dev, stream, _tensor(x, "x", x.shape, x.dtype, dev),
+             _tensor(z, "z", x.shape, x.dtype, dev), _tensor(w, "w", (D,), f32, dev),
+             _tensor(dy, "dy", x.shape, x.dtype, dev), _tensor(dx, "dx", x.shape, x.dtype, dev),
+             _tensor(dz, "dz", x.shape, x.dtype, dev), _tensor(dw, "dw", (D,), f32, dev), rows, D,
+             group, eps, 1 if gate_first else 0, _io_code(x), ws, ws_bytes)
+
+
+def ssd_norm_add_fwd(x, residual, scale, w, sum, y, eps, stream=None) -> None:
+    """Enqueue sum = residual + scale x and y = its norm times w; x, y [..., D], residual
+    and sum of x's shape (float32 or x's type), scale [D] float32 or None, w [D] float32."""
+    D, dev, f32 = x.shape[-1], x.device, torch.float32
+    rows = x.numel() // D if D else 0
+    _enqueue("ssd_norm_add_fwd", dev, stream, _tensor(x, "x", x.shape, x.dtype, dev),
+             _tensor(residual, "residual", x.shape, residual.dtype, dev),
+             _tensor(scale, "scale", (D,), f32, dev), _tensor(w, "w", (D,), f32, dev),
+             _tensor(sum, "sum", x.shape, residual.dtype, dev),
+             _tensor(y, "y", x.shape, x.dtype, dev), rows, D, eps, _io_code(x), _io_code(residual))
+
+
+def ssd_norm_add_bwd(x, sum, scale, w, dy, d_sum, dx, d_residual, d_scale, dw, eps, workspace,
+                     stream=None) -> None:
+    """Enqueue the gradients of ssd_norm_add_fwd from dy and d_sum (None = zero); x may be
+    None without scale."""
+    D, dev, f32, res = dy.shape[-1], dy.device, torch.float32, sum.dtype
+    shape, io = dy.shape, dy.dtype
+    rows = dy.numel() // D if D else 0
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _enqueue("ssd_norm_add_bwd", dev, stream, _tensor(x, "x", shape, io, dev),
+             _tensor(sum, "sum", shape, res, dev), _tensor(scale, "scale", (D,), f32, dev),
+             _tensor(w, "w", (D,), f32, dev), _tensor(dy, "dy", shape, io, dev),
+             _tensor(d_sum, "d_sum", shape, res, dev), _tensor(dx, "dx", shape, io, dev),
+             _tensor(d_residual, "d_residual", shape, res, dev),
+             _tensor(d_scale, "d_scale", (D,), f32, dev), _tensor(dw, "dw", (D,), f32, dev), rows, D,
+             eps, _io_code(dy), _io_code(sum), ws, ws_bytes)
+
+
 # ------------------------------------------------------------ allocating wrappers
 def chunk_scan_workspace(x, B, Q, stream=None) -> torch.Tensor:
     """Allocate and prepare a workspace for chunk scans of x's and B's shapes."""
@@ -446,6 +628,69 @@ def selective_scan_fwd(x, dt, A, B, C, D, init_state=None, stream=None):
     final_state = torch.empty((b, Dch, N), dtype=torch.float32, device=x.device)
     ssd_selective_scan_fwd(x, dt, A, B, C, D, init_state, y, final_state, stream)
     return y, final_state
+
+
+def gated_delta_step(state, q, k, v, a, beta, scale, accept_len=None, stream=None):
+    """Allocate the outputs; returns (y, state_out): y for all K tokens, the state after
+    accept_len [b] of them (None: after all)."""
+    with _allocating_on(stream):
+        y, state_out = torch.empty_like(v), torch.empty_like(state)
+    ssd_gated_delta_step(state, q, k, v, a, beta, accept_len, y, state_out, scale, stream=stream)
+    return y, state_out
+
+
+def gated_delta_fwd(q, k, v, a, beta, scale, init_state=None, workspace=None, stream=None):
+    """Allocate y, final_state (and the workspace if not given); returns (y, final_state)."""
+    b, L, H, P, N, G = _delta_dims(k, v)
+    with _allocating_on(stream):
+        y = torch.empty_like(v)
+        final_state = torch.empty((b, H, P, N), dtype=torch.float32, device=v.device)
+        if workspace is None:
+            workspace = _scratch(ssd_gated_delta_fwd_workspace_bytes(b, L, H, P, N, G, _io_code(v)), v.device)
+    ssd_gated_delta_fwd(q, k, v, a, beta, init_state, y, final_state, scale, workspace, stream)
+    return y, final_state
+
+
+def norm_gate_fwd(x, z, w, group, eps, gate_first=False, stream=None):
+    """Allocate and return y, the gated norm of x."""
+    with _allocating_on(stream):
+        y = torch.empty_like(x)
+    ssd_norm_gate_fwd(x, z, w, y, group, eps, gate_first, stream)
+    return y
+
+
+def norm_gate_bwd(x, z, w, dy, group, eps, gate_first=False, workspace=None, stream=None):
+    """Allocate the gradients (and the workspace if not given); returns (dx, dz, dw), dz
+    None without z."""
+    D = x.shape[-1]
+    with _allocating_on(stream):
+        dx, dz, dw = torch.empty_like(x), None if z is None else torch.empty_like(z), torch.empty_like(w)
+        if workspace is None:
+            workspace = _scratch(ssd_norm_bwd_workspace_bytes(x.numel() // D, D, group, 1, _io_code(x)), x.device)
+    ssd_norm_gate_bwd(x, z, w, dy, dx, dz, dw, group, eps, gate_first, workspace, stream)
+    return dx, dz, dw
+
+
+def norm_add_fwd(x, residual, w, eps, scale=None, stream=None):
+    """Allocate and return (y, sum): sum = residual + scale x, y its norm times w."""
+    with _allocating_on(stream):
+        y, total = torch.empty_like(x), torch.empty_like(residual)
+    ssd_norm_add_fwd(x, residual, scale, w, total, y, eps, stream)
+    return y, total
+
+
+def norm_add_bwd(x, sum, w, dy, d_sum, eps, scale=None, workspace=None, stream=None):
+    """Allocate the gradients (and the workspace if not given); returns (dx, d_residual,
+    dw, d_scale), d_scale None without scale.  d_sum None = zero."""
+    D = dy.shape[-1]
+    with _allocating_on(stream):
+        dx, d_res, dw = torch.empty_like(dy), torch.empty_like(sum), torch.empty_like(w)
+        d_scale = None if scale is None else torch.empty_like(scale)
+        if workspace is None:
+            n = ssd_norm_bwd_workspace_bytes(dy.numel() // D, D, D, 1 if scale is None else 2, _io_code(dy))
+            workspace = _scratch(n, dy.device)
+    ssd_norm_add_bwd(x, sum, scale, w, dy, d_sum, dx, d_res, d_scale, dw, eps, workspace, stream)
+    return dx, d_res, dw, d_scale
 
 
 def to_device(arr, device="cuda"):

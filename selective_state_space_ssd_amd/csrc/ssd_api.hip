@@ -6,6 +6,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "ssd_checks.h"
 #include "ssd_kernels.h"
 #include "ssd_mi355x.h"
 
@@ -47,16 +48,8 @@ ssd_status_t noalloc_workspace(hipStream_t stream, void **out) {
     return SSD_OK;
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Range {
-    uintptr_t lo = 0, hi = 0;   // [lo, hi); empty when lo == hi
-    Range() = default;
-    Range(const void *p, size_t bytes)
-        : lo(reinterpret_cast<uintptr_t>(p)), hi(reinterpret_cast<uintptr_t>(p) + (p ? bytes : 0)) {}
-    bool overlaps(const Range &o) const { return lo < o.hi && o.lo < hi; }
-    bool same(const Range &o) const { return lo == o.lo && hi == o.hi; }
-};
+using ssd::aligned;
+using ssd::Range;
 
 }  // namespace
 
