@@ -24,4 +24,25 @@ struct DeltaStepArgs {
 bool delta_step_supported_n(int N);
 hipError_t launch_delta_step(const DeltaStepArgs &a, hipStream_t stream);
 
+// In chunks of 64 tokens on the matrix cores (ssd_delta_chunk.hip): P a multiple of 16, N
+// in {32, 64, 128} and, for bf16, 256.
+struct DeltaChunkArgs {
+    const void *q, *k, *v;
+    const float *a, *beta;
+    const float *init_state;    // null: zeros
+    void *y;
+    float *final_state;         // null: not wanted
+    int b, L, H, P, N, G;
+    float scale;
+    bool bf16;
+    void *workspace;
+};
+
+struct DeltaChunkPlan {
+    bool supported = false;
+    size_t total = 0;           // workspace bytes: one image per (batch, head, chunk)
+};
+DeltaChunkPlan plan_delta_chunk(int b, int L, int H, int P, int N, bool bf16);
+hipError_t launch_delta_chunk(const DeltaChunkArgs &a, hipStream_t stream);
+
 }  // namespace ssd

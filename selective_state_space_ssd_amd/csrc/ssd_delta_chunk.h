@@ -1,0 +1,186 @@
+// ssd_delta_chunk.h -- device building blocks of the chunked gated delta rule.
+//
+// The rule over a chunk of C = 64 tokens, with g_i the running sum of a inside the chunk
+// and S the state that enters it (per head; rows p of S never meet):
+//   D_ij = e^{g_i - g_j},  Lo = the strictly lower part of (k_i . k_j) D_ij
+//   M = -(I + Lo diag(beta))^-1 Lo                       (strictly lower)
+//   R = V - e^g (K S^T),   E = R + M (beta R),   U = beta E
+//   Y = scale (e^g Q S^T + [(q_i . k_j) D_ij, j <= i] U)
+//   S <- e^{g_C} S + U^T (e^{g_C - g} K)
+// E holds the bracket v - S' k of every token, U what each token adds.  M and the scores
+// do not depend on the state: one kernel forms them for all chunks at once.  What is left
+// is a chain over the chunks, which each wave runs for 16 rows p of its own.
+//
+// Matrix tiles (16 x 16, wave64; lane l: c = l & 15, q = l >> 4).  The columns of a chain
+// wave's tiles are its 16 rows p.  An accumulator element r of lane (q, c) is row 4 q + r;
+// an operand holds 8 consecutive values of the summed index, 8 q .. 8 q + 7, per block of
+// 32.  So that an accumulator can be the next product's operand without leaving its lanes,
+// the rows of the two tiles (e = 0, 1) of a block of 32 are numbered
+//   row m of tile e  <->  index 8 (m >> 2) + 4 e + (m & 3),
+// whence lane q's accumulators of the two tiles are exactly indices 8 q .. 8 q + 7.  The
+// other operand's rows are read from LDS in that order, which costs nothing.
+#pragma once
+
+#include "ssd_device.h"
+
+namespace ssd {
+
+constexpr int kC = 64;      // tokens per chunk
+
+// A gate sum of -infinity would make differences of sums NaN; from -1e5 on a decay is 0
+// in any case, and the sums (in 64 bits) keep the digits of the small ones beside it.
+__device__ __forceinline__ double gate(float a) { return a < -1e5f ? -1e5 : double(a); }
+
+// LDS tiles: rows of RB bytes in chunks of 16; chunk `ch` of row r lies at ch ^ place(r).
+// The 16 lanes of a row read (rows 8 (c >> 2) + (c & 3) + const, one chunk) and the 16 of
+// a transposing read (rows (c >> 2) + const, chunks (c & 3) + const) then fall on 16
+// different 16-byte columns of the 256-byte bank row.
+template <int RB>
+__device__ __forceinline__ int place(int r) {
+    if constexpr (RB >= 256) return (r & 3) * 4 + ((r >> 3) & 3);
+    else if constexpr (RB == 128) return ((r >> 1) & 1) * 4 + ((r >> 3) & 3);
+    else return (r >> 3) & 3;
+}
+
+// The tile row of lane c: index 32 s + 8 (c >> 2) + 4 e + (c & 3).
+__device__ __forceinline__ int tile_row(int s, int e, int c) { return 32 * s + 8 * (c >> 2) + 4 * e + (c & 3); }
+
+// An operand: 8 consecutive values of the summed index per lane.  Matrix products run on
+// bf16; a 32-bit value goes in as NP planes, each the rounding of what the ones before it
+// left (8 bits a plane).  Products of planes i + j >= max planes are below the last
+// plane's rounding and left out.  fp32 I/O uses the fp32 matrix instruction instead.
+template <typename IO, int NP>
+struct Op {
+    bf16x8 p[NP];
+};
+template <int NP>
+struct Op<float, NP> {
+    f32x4 v[2];
+};
+
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mma(const Op<bf16_bits, NA> &a, const Op<bf16_bits, NB> &b, f32x4 acc) {
+    constexpr int NM = NA > NB ? NA : NB;
+#pragma unroll
+    for (int i = NA - 1; i >= 0; --i)       // small terms first
+#pragma unroll
+        for (int j = NB - 1; j >= 0; --j)
+            if (i + j < NM) acc = mfma_bf16(a.p[i], b.p[j], acc);
+    return acc;
+}
+
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mma(const Op<float, NA> &a, const Op<float, NB> &b, f32x4 acc) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc = mfma_f32(a.v[e][r], b.v[e][r], acc);
+    return acc;
+}
+
+// The operand of 8 fp32 values (indices 8 q .. 8 q + 7: two accumulators).
+template <typename IO, int NP>
+__device__ __forceinline__ Op<IO, NP> to_op(f32x4 lo, f32x4 hi) {
+    Op<IO, NP> o;
+    if constexpr (std::is_same_v<IO, float>) {
+        o.v[0] = lo;
+        o.v[1] = hi;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const uint4 w = make_uint4(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]),
+                                       pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]));
+            o.p[i] = as_bf16x8(w);
+            if (i + 1 < NP) {
+                lo -= f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+                hi -= f32x4{bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
+            }
+        }
+    }
+    return o;
+}
+
+// The first NF planes alone.
+template <int NF, typename IO, int NP>
+__device__ __forceinline__ Op<IO, NF> first_planes(const Op<IO, NP> &o) {
+    Op<IO, NF> f;
+    if constexpr (std::is_same_v<IO, float>) {
+        f.v[0] = o.v[0];
+        f.v[1] = o.v[1];
+    } else {
+#pragma unroll
+        for (int i = 0; i < NF; ++i) f.p[i] = o.p[i];
+    }
+    return f;
+}
+
+// Row `row` of a tile, values 8 (4 ks + q) .. + 7, from NP planes `stride` bytes apart.
+template <typename IO, int NP, int RB>
+__device__ __forceinline__ Op<IO, NP> read_row(const char *tile, int stride, int row, int ks, int q) {
+    Op<IO, NP> o;
+    const int x = place<RB>(row);
+    const char *r = tile + row * RB;
+    if constexpr (std::is_same_v<IO, float>) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) o.v[e] = *reinterpret_cast<const f32x4 *>(r + (((8 * ks + 2 * q + e) ^ x) * 16));
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) o.p[i] = as_bf16x8(*reinterpret_cast<const uint4 *>(r + i * stride + (((4 * ks + q) ^ x) * 16)));
+    }
+    return o;
+}
+
+// Column n0 + tile_row(0, e, c) of a tile (n0 a multiple of 32), rows k0 + 8 q .. + 7:
+// for bf16 two transposing reads of a 4 x 16 block each, in which lane c of a group of 16
+// addresses row c >> 2, columns 4 (c & 3) .. + 3, and receives column c of the 4 rows.
+template <typename IO, int NP, int RB>
+__device__ __forceinline__ Op<IO, NP> read_col(const char *tile, int stride, int k0, int n0, int e, int c, int q) {
+    Op<IO, NP> o;
+    if constexpr (std::is_same_v<IO, float>) {
+        const int n = n0 + tile_row(0, e, c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int row = k0 + 8 * q + j;
+            o.v[j >> 2][j & 3] = *reinterpret_cast<const float *>(tile + row * RB + (((n >> 2) ^ place<RB>(row)) * 16) + (n & 3) * 4);
+        }
+    } else {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            s16x4 h[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = k0 + 8 * q + 4 * j + (c >> 2);
+                const char *at = tile + i * stride + row * RB + (((n0 / 8 + (c & 3)) ^ place<RB>(row)) * 16) + 8 * e;
+                h[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4 *)(at));
+            }
+            o.p[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    }
+    return o;
+}
+
+// Copy 16 bytes per lane from global memory into LDS without passing through registers:
+// lane l's go to dst + 16 l (dst the same for the whole wave).
+__device__ __forceinline__ void copy16(const void *src, char *dst) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t *)(src),
+                                     (__attribute__((address_space(3))) uint32_t *)(dst), 16, 0, 0);
+}
+
+// Every copy16 of this wave has arrived (vmcnt 0; the other counters left alone).
+__device__ __forceinline__ void copies_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+
+// What the chain kernels share: sizes of one chunk's images in the workspace.
+//   M   NM planes of [64][64], scores NQ planes of [64][64] (fp32 I/O: one fp32 image
+//   each), then [3][64] fp32: e^g, e^{g_C - g}, beta.
+template <typename IO, int NM, int NQ>
+struct ChunkImage {
+    static constexpr int kPlanesM = std::is_same_v<IO, float> ? 1 : NM, kPlanesQ = std::is_same_v<IO, float> ? 1 : NQ;
+    static constexpr int kPlane = kC * kC * int(sizeof(IO));
+    static constexpr int kRow = kC * int(sizeof(IO));       // bytes per row
+    static constexpr int kM = 0, kQ = kPlanesM * kPlane, kGates = kQ + kPlanesQ * kPlane;
+    static constexpr int kBytes = kGates + 1024;            // [3][64] fp32, rounded up to 1 KiB
+};
+
+}  // namespace ssd

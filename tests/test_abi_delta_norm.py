@@ -123,6 +123,14 @@ def test_norm_workspace(lib, call):
     assert need > 0 and call(lib, ws_bytes=need - 1) == WS
 
 
+def test_delta_workspace(lib):
+    assert FWD(lib, ws=None) == WS
+    need = bd.ssd_gated_delta_fwd_workspace_bytes(2, 100, 4, 64, 64, 2, 1)
+    assert need > 0 and FWD(lib, ws_bytes=need - 1) == WS
+    for name in ("q", "v", "y", "final"):
+        assert FWD(lib, ws=FWD.address(name)) == ALIAS
+
+
 def test_workspace_sizes():
     with pytest.raises(bd.SSDError):
         bd.ssd_gated_delta_fwd_workspace_bytes(1, 10, 4, 64, 40, 2, 1)

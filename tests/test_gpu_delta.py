@@ -17,13 +17,13 @@ pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 
 
-def check_fwd(c, scale, L, N, dtype):
+def check_fwd(c, scale, L, N, dtype, amplified=1.0):
     y, S = bd.gated_delta_fwd(*inputs_of(c), scale, init_state=c["init_state"])
     ey, es = delta.delta_f64(*inputs_of({n: t if t is None else t.cpu() for n, t in c.items()}), scale,
                              None if c["init_state"] is None else c["init_state"].cpu())
     assert y.dtype == dtype and S.dtype == F32
-    assert rel(y, ey) <= tol_out(dtype, L, N, 4)
-    assert rel(S, es[-1]) <= tol32(L, N)
+    assert rel(y, ey) <= tol_out(dtype, L, N, 4) + (amplified - 1) * tol32(L, N)
+    assert rel(S, es[-1]) <= amplified * tol32(L, N)
     return y, S
 
 
@@ -88,8 +88,14 @@ def test_equal_keys(dtype):
     c["beta"].fill_(1.0)
     _, S = check_fwd(c, 1.0, 140, 64, dtype)
     assert rel(S[0, :, :, 3], c["v"][0, -1].float()) <= tol32(140, 64)
-    c["beta"].fill_(2.0)      # the far end: every update reflects
-    check_fwd(c, 1.0, 140, 64, dtype)
+    # the far end, every update reflects.  In a chunk of 64, E_i = R_i + sum_j M_ij beta_j R_j
+    # with R the brackets at the chunk's start.  For one unit key k_i . k_j = 1 and Lo is all
+    # ones below the diagonal, so (I + 2 Lo) M = -Lo has M_ij = (-1)^(i - j): every weight
+    # M_ij beta_j is 2 or -2.  The brackets' independent errors of one rounding each come out
+    # 2 sqrt(63) < 16 times as large, while E, the bracket itself, does not grow: the token
+    # by token form reflects, |E_i| <= |v_i| + |w|
+    c["beta"].fill_(2.0)
+    check_fwd(c, 1.0, 140, 64, dtype, amplified=16.0)
 
 
 def test_padded_tokens_change_nothing():
