@@ -42,7 +42,8 @@ struct DeltaChunkPlan {
     bool supported = false;
     size_t total = 0;           // workspace bytes: one image per (batch, head, chunk)
 };
-DeltaChunkPlan plan_delta_chunk(int b, int L, int H, int P, int N, bool bf16);
+bool delta_chunk_supported(int b, int L, int H, int P, int N, int G, bool bf16);
+DeltaChunkPlan plan_delta_chunk(int b, int L, int H, int P, int N, int G, bool bf16);
 hipError_t launch_delta_chunk(const DeltaChunkArgs &a, hipStream_t stream);
 
 }  // namespace ssd

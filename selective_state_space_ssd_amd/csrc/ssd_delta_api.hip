@@ -24,9 +24,9 @@ ssd_status_t check_dims(int b, int L, int H, int P, int N, int G, ssd_dtype_t io
 constexpr int kShort = 16;
 
 // The chunked path of a sequence, unless it is short or no chunk kernel runs its shape.
-ssd::DeltaChunkPlan sequence_plan(int b, int L, int H, int P, int N, ssd_dtype_t io) {
+ssd::DeltaChunkPlan sequence_plan(int b, int L, int H, int P, int N, int G, ssd_dtype_t io) {
     if (b == 0 || L <= kShort) return {};
-    return ssd::plan_delta_chunk(b, L, H, P, N, io == SSD_DTYPE_BF16);
+    return ssd::plan_delta_chunk(b, L, H, P, N, G, io == SSD_DTYPE_BF16);
 }
 
 ssd_status_t done(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
@@ -68,7 +68,7 @@ ssd_status_t ssd_gated_delta_step(const float *state_in, const void *q, const vo
 size_t ssd_gated_delta_fwd_workspace_bytes(int b, int L, int H, int P, int N, int G,
                                            ssd_dtype_t io) {
     if (check_dims(b, L, H, P, N, G, io) != SSD_OK) return size_t(-1);
-    return sequence_plan(b, L, H, P, N, io).total;
+    return sequence_plan(b, L, H, P, N, G, io).total;
 }
 
 ssd_status_t ssd_gated_delta_fwd(const void *q, const void *k, const void *v, const float *a,
@@ -92,7 +92,7 @@ ssd_status_t ssd_gated_delta_fwd(const void *q, const void *k, const void *v, co
     const size_t esz = bf16 ? 2 : 4;
     const size_t qk = size_t(b) * L * G * N * esz, vy = size_t(b) * L * H * P * esz, gt = size_t(b) * L * H * 4;
     const Range ins[] = {Range(q, qk), Range(k, qk), Range(v, vy), Range(a, gt), Range(beta, gt), rinit};
-    const ssd::DeltaChunkPlan plan = sequence_plan(b, L, H, P, N, io);
+    const ssd::DeltaChunkPlan plan = sequence_plan(b, L, H, P, N, G, io);
     if (plan.total > 0 && (!workspace || workspace_bytes < plan.total)) return SSD_ERR_WORKSPACE;
     const Range outs[] = {Range(y, vy), rfin, Range(workspace, plan.total)};
     if (any_alias(ins, outs)) return SSD_ERR_ALIAS;

@@ -1,0 +1,283 @@
+// ssd_delta_chain.h -- the chain over the chunks of the gated delta rule, forward (see
+// ssd_delta_chunk.h for the formulas and the tile layout).
+#pragma once
+
+#include "ssd_delta_chunk.h"
+
+namespace ssd {
+
+// What the forward chain leaves for the backward pass, per (batch, head):
+//   E       [nc][P / 16][4][64] f32x4: a wave's accumulators of the brackets, as held
+//   S       [nc][P][N] io: the state that enters each chunk
+//   anchor  [P / 16][segments][N / 16][64] f32x4: the state after each segment of chunks
+//   ydy     [nc][P / 16][64] fp32: y . dy of each token over the wave's 16 rows
+constexpr int kSegment = 4;     // chunks per segment
+
+struct DeltaSaved {
+    float *E;
+    void *S;
+    float *anchor;
+    float *ydy;
+};
+
+// Planes of the values that stay 32-bit on their way through the bf16 matrix products:
+// the state, what is added to it, M and the vectors M meets (3: 24 bits).  y is rounded to
+// bf16 at the end, but its terms may be much larger than it is (keys that repeat: each U
+// takes back most of the one before), so its operands keep 16 bits; for the backward
+// pass, whose gate gradients are differences of y . dy, all 24.
+template <bool SAVE>
+struct DeltaPlanes {
+    static constexpr int kS = 3, kM = 3, kQ = SAVE ? 3 : 2;
+};
+
+template <typename IO, int N, bool SAVE>
+struct ChainTile {
+    using Pl = DeltaPlanes<SAVE>;
+    using Img = ChunkImage<IO, Pl::kM, Pl::kQ>;
+    static constexpr int RB = N * int(sizeof(IO));          // bytes per row of k or q
+    static constexpr int kRows = kC * RB;                   // bytes of a k or q tile
+    static constexpr int kBytes = 2 * kRows + Img::kBytes;  // k, q, then the image
+    static constexpr int kBufs = 2 * kBytes <= 160 * 1024 ? 2 : 1;
+    static constexpr int kLds = kBufs * kBytes;
+};
+
+// Start the copies of one chunk's k, q and image into an LDS buffer.
+template <typename T, typename IO, int N, int W>
+__device__ __forceinline__ void fetch_chunk(const IO *k0, const IO *q0, const char *img, uint32_t buf, uint32_t gn,
+                                            int last) {
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int kThreads = 64 * W;
+#pragma unroll
+    for (int i = 0; i < T::kRows / 16 / kThreads; ++i) {
+        const int at = i * kThreads + tid, r = at / (T::RB / 16), col = (at % (T::RB / 16)) ^ place<T::RB>(r);
+        const uint32_t off = uint32_t(min(r, last)) * gn + uint32_t(col) * 16;     // rows past the end: the last one
+        const uint32_t dst = buf + uint32_t(i * kThreads + 64 * w) * 16;
+        copy16(k0, off, dst);
+        copy16(q0, off, dst + T::kRows);
+    }
+#pragma unroll
+    for (int i = 0; i < (T::Img::kBytes / 1024 + W - 1) / W; ++i)
+        if (i * W + w < T::Img::kBytes / 1024)
+            copy16(img, uint32_t(i * W + w) * 1024 + lane * 16, buf + 2 * T::kRows + uint32_t(i * W + w) * 1024);
+}
+
+// One element / 4 consecutive ones of a range-checked view; past its end: 0.
+template <typename IO>
+__device__ __forceinline__ IO load_checked(__amdgpu_buffer_rsrc_t v, uint32_t off) {
+    if constexpr (std::is_same_v<IO, float>) return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(v, int(off), 0, 0));
+    else return __builtin_amdgcn_raw_buffer_load_b16(v, int(off), 0, 0);
+}
+template <typename IO>
+using Raw4 = std::conditional_t<std::is_same_v<IO, float>, f32x4, u32x2>;
+template <typename IO>
+__device__ __forceinline__ Raw4<IO> load4_checked(__amdgpu_buffer_rsrc_t v, uint32_t off) {
+    if constexpr (std::is_same_v<IO, float>) return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(v, int(off), 0, 0));
+    else return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(v, int(off), 0, 0));
+}
+template <typename IO>
+__device__ __forceinline__ f32x4 widen(Raw4<IO> v) {
+    if constexpr (std::is_same_v<IO, float>) return v;
+    else return f32x4{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
+}
+template <typename IO>
+__device__ __forceinline__ Raw4<IO> narrow(f32x4 v) {
+    if constexpr (std::is_same_v<IO, float>) return v;
+    else return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
+// block = (batch, head, W * 16 rows of the state), one wave per 16 rows.  k, q and the
+// chunk's image go through LDS, shared by the waves; the next chunk's are copied into the
+// other buffer meanwhile (one buffer where two do not fit).
+// SAVE: instead of y and the final state, what the backward pass needs (dyg is read).
+template <typename IO, int N, int W, bool SAVE>
+__global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ qg, const IO *__restrict__ kg,
+                                                        const IO *__restrict__ vg, const char *__restrict__ images,
+                                                        const float *__restrict__ init, IO *__restrict__ yg,
+                                                        float *__restrict__ fin, const IO *__restrict__ dyg,
+                                                        DeltaSaved saved, int L, int H, int P, int G, int nc, int pblocks,
+                                                        float scale) {
+    using T = ChainTile<IO, N, SAVE>;
+    using Img = typename T::Img;
+    using Pl = DeltaPlanes<SAVE>;
+    extern __shared__ __align__(16) char lds[];
+    constexpr int KS = N / 32, kSz = int(sizeof(IO));
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
+    const int pb = blockIdx.x % pblocks, bh = blockIdx.x / pblocks;
+    const int h = bh % H, bi = bh / H, g = h / (H / G);
+    const int p0 = (pb * W + w) * 16, p = p0 + c, ptiles = P / 16;
+    const bool live = p0 < P;       // the same for a whole wave
+    const size_t hp = size_t(H) * P, gn = size_t(G) * N;
+    const char *img = images + size_t(bh) * nc * Img::kBytes;
+    const IO *k0 = kg + size_t(bi) * L * gn + size_t(g) * N, *q0 = qg + size_t(bi) * L * gn + size_t(g) * N;
+    const IO *v0 = vg + size_t(bi) * L * hp + size_t(h) * P;
+    const uint32_t lds0 = lds_address(lds), tok = uint32_t(hp) * kSz;
+
+    IO rv[16];
+    auto fetch = [&](int ch, uint32_t buf) {
+        const int t0 = ch * kC, rows = min(kC, L - t0);
+        fetch_chunk<T, IO, N, W>(k0 + size_t(t0) * gn, q0 + size_t(t0) * gn, img + size_t(ch) * Img::kBytes, buf,
+                                 uint32_t(gn) * kSz, rows - 1);
+        if (live) {
+            const __amdgpu_buffer_rsrc_t view = buffer_rsrc(v0 + size_t(t0) * hp, uint32_t(rows - 1) * tok + uint32_t(P) * kSz);
+            const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) rv[4 * t + r] = load_checked<IO>(view, off + uint32_t(32 * (t >> 1) + 4 * (t & 1) + r) * tok);
+        }
+    };
+
+    f32x4 S[N / 16];
+#pragma unroll
+    for (int t = 0; t < N / 16; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (init && live)
+#pragma unroll
+        for (int t = 0; t < N / 16; ++t)
+            S[t] = *reinterpret_cast<const f32x4 *>(init + (size_t(bh) * P + p) * N + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
+    f32x4 V[4];
+    auto take_v = [&]() {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) V[t][r] = to_f32<IO>(rv[4 * t + r]);
+    };
+    fetch(0, lds0);
+    copies_done();
+    take_v();
+    __syncthreads();
+
+    for (int ch = 0; ch < nc; ++ch) {
+        const int t0 = ch * kC, rows = min(kC, L - t0);
+        const char *buf = lds + (T::kBufs == 2 ? (ch & 1) * T::kBytes : 0);
+        if (T::kBufs == 2 && ch + 1 < nc) fetch(ch + 1, lds0 + ((ch + 1) & 1) * T::kBytes);
+        Raw4<IO> yo[4];
+        f32x4 E[4];
+        if (live) {
+            const char *tk = buf, *tq = buf + T::kRows, *tm = buf + 2 * T::kRows + Img::kM, *ts = buf + 2 * T::kRows + Img::kQ;
+            const float *gates = reinterpret_cast<const float *>(buf + 2 * T::kRows + Img::kGates);
+            if constexpr (SAVE) {
+                const __amdgpu_buffer_rsrc_t view = buffer_rsrc(dyg + (size_t(bi) * L + t0) * hp + size_t(h) * P, uint32_t(rows - 1) * tok + uint32_t(P) * kSz);
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    yo[t] = load4_checked<IO>(view, uint32_t(tile_row(t >> 1, t & 1, c)) * tok + uint32_t(p0 + 4 * q) * kSz);
+            }
+            Op<IO, Pl::kS> so[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) so[s] = to_op<IO, Pl::kS>(S[2 * s], S[2 * s + 1]);
+            if constexpr (SAVE) {
+                IO *dst = static_cast<IO *>(saved.S) + ((size_t(bh) * nc + ch) * P + p) * N + 8 * q;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    if constexpr (kSz == 4) {
+                        *reinterpret_cast<f32x4 *>(dst + 32 * s) = S[2 * s];
+                        *reinterpret_cast<f32x4 *>(dst + 32 * s + 4) = S[2 * s + 1];
+                    } else {
+                        *reinterpret_cast<bf16x8 *>(dst + 32 * s) = so[s].p[0];
+                    }
+                }
+            }
+            // R = V - e^g K S^T, and beta R
+            Op<IO, Pl::kM> br[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                f32x4 b[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) z = mma(read_row<IO, 1, T::RB>(tk, 0, tile_row(s, e, c), ks, q), so[ks], z);
+                    const f32x4 fs = *reinterpret_cast<const f32x4 *>(gates + 32 * s + 8 * q + 4 * e);
+                    const f32x4 bt = *reinterpret_cast<const f32x4 *>(gates + 2 * kC + 32 * s + 8 * q + 4 * e);
+                    E[2 * s + e] = V[2 * s + e] - fs * z;
+                    b[e] = bt * E[2 * s + e];
+                }
+                br[s] = to_op<IO, Pl::kM>(b[0], b[1]);
+            }
+            // E = R + M (beta R), U = beta E
+            Op<IO, Pl::kQ> uy[2];
+            Op<IO, Pl::kS> ud[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                f32x4 u[2], d[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f32x4 z = E[2 * s + e];
+#pragma unroll
+                    for (int ks = 0; ks <= s; ++ks) z = mma(tri_row<IO, Pl::kM>(tm, s, e, ks, c, q), br[ks], z);
+                    E[2 * s + e] = z;
+                    const f32x4 te = *reinterpret_cast<const f32x4 *>(gates + kC + 32 * s + 8 * q + 4 * e);
+                    const f32x4 bt = *reinterpret_cast<const f32x4 *>(gates + 2 * kC + 32 * s + 8 * q + 4 * e);
+                    u[e] = bt * z;
+                    d[e] = te * u[e];
+                }
+                uy[s] = to_op<IO, Pl::kQ>(u[0], u[1]);
+                ud[s] = to_op<IO, Pl::kS>(d[0], d[1]);
+            }
+            // Y, its rows p in registers: 4 consecutive ones of one token per lane
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int row = tile_row(t >> 1, t & 1, c);
+                f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) y = mma(first_planes<Pl::kQ>(so[ks]), read_row<IO, 1, T::RB>(tq, 0, row, ks, q), y);
+                y *= scale * gates[row];
+#pragma unroll
+                for (int ks = 0; ks <= (t >> 1); ++ks) y = mma(uy[ks], tri_row<IO, Pl::kQ>(ts, t >> 1, t & 1, ks, c, q), y);
+                if constexpr (SAVE) {
+                    const f32x4 d = widen<IO>(yo[t]);
+                    const float dot = group4_sum(y[0] * d[0] + y[1] * d[1] + y[2] * d[2] + y[3] * d[3]);
+                    if (q == 0) saved.ydy[((size_t(bh) * nc + ch) * ptiles + p0 / 16) * kC + row] = dot;
+                } else {
+                    yo[t] = narrow<IO>(y);
+                }
+            }
+            // S <- e^{g_C} S + K^T (e^{g_C - g} U)
+            const float alpha = gates[kC - 1];
+#pragma unroll
+            for (int t = 0; t < N / 16; ++t) {
+                f32x4 z = S[t] * alpha;
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) z = mma(read_col<IO, 1, T::RB>(tk, 0, 32 * ks, 32 * (t >> 1), t & 1, c, q), ud[ks], z);
+                S[t] = z;
+            }
+        }
+        if (ch + 1 < nc) {
+            if constexpr (T::kBufs == 1) {
+                __syncthreads();
+                fetch(ch + 1, lds0);
+            }
+            copies_done();
+            take_v();
+            __syncthreads();
+        }
+        // stores last: nothing waits for them before the next chunk's copies
+        if (live) {
+            if constexpr (SAVE) {
+                f32x4 *dst = reinterpret_cast<f32x4 *>(saved.E) + ((size_t(bh) * nc + ch) * ptiles + p0 / 16) * 256 + lane;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) dst[64 * t] = E[t];
+                if (ch % kSegment == kSegment - 1 || ch == nc - 1) {
+                    const int segs = (nc + kSegment - 1) / kSegment;
+                    f32x4 *at = reinterpret_cast<f32x4 *>(saved.anchor) +
+                                ((size_t(bh) * ptiles + p0 / 16) * segs + ch / kSegment) * (N / 16) * 64 + lane;
+#pragma unroll
+                    for (int t = 0; t < N / 16; ++t) at[64 * t] = S[t];
+                }
+            } else {
+                const __amdgpu_buffer_rsrc_t view = buffer_rsrc(yg + (size_t(bi) * L + t0) * hp + size_t(h) * P, uint32_t(rows - 1) * tok + uint32_t(P) * kSz);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int off = int(uint32_t(tile_row(t >> 1, t & 1, c)) * tok + uint32_t(p0 + 4 * q) * kSz);
+                    if constexpr (kSz == 4) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, yo[t]), view, off, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b64(yo[t], view, off, 0, 0);
+                }
+            }
+        }
+    }
+    if (!SAVE && fin && live)
+#pragma unroll
+        for (int t = 0; t < N / 16; ++t)
+            *reinterpret_cast<f32x4 *>(fin + (size_t(bh) * P + p) * N + 32 * (t >> 1) + 8 * q + 4 * (t & 1)) = S[t];
+}
+
+}  // namespace ssd

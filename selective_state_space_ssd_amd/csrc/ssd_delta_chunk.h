@@ -161,26 +161,52 @@ __device__ __forceinline__ Op<IO, NP> read_col(const char *tile, int stride, int
     return o;
 }
 
-// Copy 16 bytes per lane from global memory into LDS without passing through registers:
-// lane l's go to dst + 16 l (dst the same for the whole wave).
-__device__ __forceinline__ void copy16(const void *src, char *dst) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t *)(src),
-                                     (__attribute__((address_space(3))) uint32_t *)(dst), 16, 0, 0);
+// Copy 16 bytes per lane from global memory (base + off, base the same for the whole wave)
+// into LDS without passing through registers: lane l's go to LDS byte dst + 16 l.  Written
+// in assembly because the compiler waits for every such copy at the next LDS read,
+// whichever buffer that reads; here the copy into the other buffer stays in flight until
+// copies_done().  It has no output register; the wait states cover an M0 or an address
+// pair written just before.
+__device__ __forceinline__ void copy16(const void *base, uint32_t off, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :: "s"(dst), "v"(off), "s"(base) : "memory");
 }
 
-// Every copy16 of this wave has arrived (vmcnt 0; the other counters left alone).
+// Every copy16 (and load and store) of this wave has arrived: vmcnt 0, the other counters
+// left alone.  A block barrier after it makes the copies of all waves readable.
 __device__ __forceinline__ void copies_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }
 
-// What the chain kernels share: sizes of one chunk's images in the workspace.
-//   M   NM planes of [64][64], scores NQ planes of [64][64] (fp32 I/O: one fp32 image
-//   each), then [3][64] fp32: e^g, e^{g_C - g}, beta.
+__device__ __forceinline__ uint32_t lds_address(const char *p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char *)p));
+}
+
+// One chunk's image in the workspace and in LDS:
+//   M in NM planes and the scores in NQ (fp32 I/O: one fp32 plane each), both lower
+//   triangular: a plane holds rows 0 .. 31 of columns 0 .. 31, then rows 32 .. 63 whole;
+//   then [3][64] fp32: e^g, e^{g_C - g}, beta.
 template <typename IO, int NM, int NQ>
 struct ChunkImage {
-    static constexpr int kPlanesM = std::is_same_v<IO, float> ? 1 : NM, kPlanesQ = std::is_same_v<IO, float> ? 1 : NQ;
-    static constexpr int kPlane = kC * kC * int(sizeof(IO));
-    static constexpr int kRow = kC * int(sizeof(IO));       // bytes per row
+    static constexpr int kSz = int(sizeof(IO));
+    static constexpr int kPlanesM = kSz == 4 ? 1 : NM, kPlanesQ = kSz == 4 ? 1 : NQ;
+    static constexpr int kTop = 32 * 32 * kSz, kPlane = kTop + 32 * 64 * kSz;
     static constexpr int kM = 0, kQ = kPlanesM * kPlane, kGates = kQ + kPlanesQ * kPlane;
-    static constexpr int kBytes = kGates + 1024;            // [3][64] fp32, rounded up to 1 KiB
+    static constexpr int kBytes = kGates + 1024;            // the gates rounded up to 1 KiB
 };
+
+// Operands from a lower triangular matrix of an image, blocks of 32: rows tile_row(s, e, c),
+// columns 32 ks + 8 q .. (ks <= s);
+template <typename IO, int NP>
+__device__ __forceinline__ Op<IO, NP> tri_row(const char *m, int s, int e, int ks, int c, int q) {
+    using Img = ChunkImage<IO, 1, 1>;
+    if (s == 0) return read_row<IO, NP, 32 * Img::kSz>(m, Img::kPlane, tile_row(0, e, c), 0, q);
+    return read_row<IO, NP, 64 * Img::kSz>(m + Img::kTop, Img::kPlane, tile_row(0, e, c), ks, q);
+}
+// columns tile_row(s, e, c), rows 32 ks + 8 q .. (ks >= s).
+template <typename IO, int NP>
+__device__ __forceinline__ Op<IO, NP> tri_col(const char *m, int ks, int s, int e, int c, int q) {
+    using Img = ChunkImage<IO, 1, 1>;
+    if (ks == 0) return read_col<IO, NP, 32 * Img::kSz>(m, Img::kPlane, 0, 0, e, c, q);
+    return read_col<IO, NP, 64 * Img::kSz>(m + Img::kTop, Img::kPlane, 0, 32 * s, e, c, q);
+}
 
 }  // namespace ssd

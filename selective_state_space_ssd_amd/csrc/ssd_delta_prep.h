@@ -27,21 +27,25 @@ __device__ __forceinline__ Op<IO, 1> load_row8(const IO *p) {
     return o;
 }
 
-// Copy an fp32 [64][64] matrix from LDS into its image: NP planes, 16-byte chunks placed
-// as the chain's LDS tiles hold them.
+// Copy an fp32 lower triangular [64][64] matrix from LDS into its image: NP planes,
+// 16-byte chunks placed as the chain's LDS tiles hold them.
 template <typename IO, int NP>
 __device__ __forceinline__ void write_image(const float *m, char *dst) {
-    constexpr int RB = kC * int(sizeof(IO)), per_row = RB / 16, E = 16 / int(sizeof(IO));
-    for (int i = threadIdx.x; i < kC * per_row; i += 256) {
-        const int r = i / per_row, col = ((i % per_row) ^ place<RB>(r)) * E;
-        const float *s = m + r * kLd + col;
+    using Img = ChunkImage<IO, 1, 1>;
+    constexpr int kRowTop = 32 * Img::kSz, kRow = 64 * Img::kSz, E = 16 / Img::kSz;
+    for (int i = threadIdx.x; i < Img::kPlane / 16; i += 256) {
+        const bool top = i < Img::kTop / 16;
+        const int at = top ? i : i - Img::kTop / 16, per_row = (top ? kRowTop : kRow) / 16;
+        const int r = at / per_row, pos = at % per_row;
+        const int col = (pos ^ (top ? place<kRowTop>(r) : place<kRow>(r))) * E;
+        const float *s = m + (top ? r : 32 + r) * kLd + col;
         if constexpr (std::is_same_v<IO, float>) {
             *reinterpret_cast<float4 *>(dst + i * 16) = make_float4(s[0], s[1], s[2], s[3]);
         } else {
             const Op<IO, NP> o = to_op<IO, NP>(f32x4{s[0], s[1], s[2], s[3]}, f32x4{s[4], s[5], s[6], s[7]});
 #pragma unroll
             for (int p = 0; p < NP; ++p)
-                *reinterpret_cast<uint4 *>(dst + p * kC * RB + i * 16) = __builtin_bit_cast(uint4, o.p[p]);
+                *reinterpret_cast<uint4 *>(dst + p * Img::kPlane + i * 16) = __builtin_bit_cast(uint4, o.p[p]);
         }
     }
 }
@@ -126,7 +130,6 @@ __global__ __launch_bounds__(256) void k_delta_prep(const IO *__restrict__ qg, c
         }
 #pragma unroll
         for (int i = 1; i < 16; ++i) mm[(16 * q + i) * kLd + 16 * q + c] = m[i];
-    } else {        // the other waves write the scores out meanwhile (wave 0's share after)
     }
     __syncthreads();
     if (w < 2) {    // blocks (1, 0) and (3, 2)
