@@ -176,69 +176,108 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                     }
                 }
             }
-            // R = V - e^g K S^T, and beta R
+            f32x4 fs[4], te[4], bt[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const float *at = gates + 32 * (t >> 1) + 8 * q + 4 * (t & 1);
+                fs[t] = *reinterpret_cast<const f32x4 *>(at);
+                te[t] = *reinterpret_cast<const f32x4 *>(at + kC);
+                bt[t] = *reinterpret_cast<const f32x4 *>(at + 2 * kC);
+            }
+            // R = V - e^g K S^T, and the state's part of Y (its rows p in registers)
+            f32x4 Y[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) E[t] = Y[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                Op<IO, 1> a[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tk, 0, tile_row(t >> 1, t & 1, c), ks, q);
+                mma(E, a, so[ks]);
+            }
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                Op<IO, 1> a[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tq, 0, tile_row(t >> 1, t & 1, c), ks, q);
+                mma(Y, first_planes<Pl::kQ>(so[ks]), a);
+            }
             Op<IO, Pl::kM> br[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                f32x4 b[2];
+            for (int t = 0; t < 4; ++t) E[t] = V[t] - fs[t] * E[t];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    f32x4 z = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) z = mma(read_row<IO, 1, T::RB>(tk, 0, tile_row(s, e, c), ks, q), so[ks], z);
-                    const f32x4 fs = *reinterpret_cast<const f32x4 *>(gates + 32 * s + 8 * q + 4 * e);
-                    const f32x4 bt = *reinterpret_cast<const f32x4 *>(gates + 2 * kC + 32 * s + 8 * q + 4 * e);
-                    E[2 * s + e] = V[2 * s + e] - fs * z;
-                    b[e] = bt * E[2 * s + e];
-                }
-                br[s] = to_op<IO, Pl::kM>(b[0], b[1]);
-            }
+            for (int s = 0; s < 2; ++s) br[s] = to_op<IO, Pl::kM>(bt[2 * s] * E[2 * s], bt[2 * s + 1] * E[2 * s + 1]);
             // E = R + M (beta R), U = beta E
+            {
+                Op<IO, Pl::kM> a[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) a[t] = tri_row<IO, Pl::kM>(tm, t >> 1, t & 1, 0, c, q);
+                mma(E, a, br[0]);
+            }
+            {
+                f32x4 lower[2] = {E[2], E[3]};
+                Op<IO, Pl::kM> a[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) a[e] = tri_row<IO, Pl::kM>(tm, 1, e, 1, c, q);
+                mma(lower, a, br[1]);
+                E[2] = lower[0];
+                E[3] = lower[1];
+            }
             Op<IO, Pl::kQ> uy[2];
             Op<IO, Pl::kS> ud[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                f32x4 u[2], d[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    f32x4 z = E[2 * s + e];
-#pragma unroll
-                    for (int ks = 0; ks <= s; ++ks) z = mma(tri_row<IO, Pl::kM>(tm, s, e, ks, c, q), br[ks], z);
-                    E[2 * s + e] = z;
-                    const f32x4 te = *reinterpret_cast<const f32x4 *>(gates + kC + 32 * s + 8 * q + 4 * e);
-                    const f32x4 bt = *reinterpret_cast<const f32x4 *>(gates + 2 * kC + 32 * s + 8 * q + 4 * e);
-                    u[e] = bt * z;
-                    d[e] = te * u[e];
-                }
-                uy[s] = to_op<IO, Pl::kQ>(u[0], u[1]);
-                ud[s] = to_op<IO, Pl::kS>(d[0], d[1]);
-            }
-            // Y, its rows p in registers: 4 consecutive ones of one token per lane
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int row = tile_row(t >> 1, t & 1, c);
-                f32x4 y = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) y = mma(first_planes<Pl::kQ>(so[ks]), read_row<IO, 1, T::RB>(tq, 0, row, ks, q), y);
-                y *= scale * gates[row];
-#pragma unroll
-                for (int ks = 0; ks <= (t >> 1); ++ks) y = mma(uy[ks], tri_row<IO, Pl::kQ>(ts, t >> 1, t & 1, ks, c, q), y);
-                if constexpr (SAVE) {
-                    const f32x4 d = widen<IO>(yo[t]);
-                    const float dot = group4_sum(y[0] * d[0] + y[1] * d[1] + y[2] * d[2] + y[3] * d[3]);
-                    if (q == 0) saved.ydy[((size_t(bh) * nc + ch) * ptiles + p0 / 16) * kC + row] = dot;
-                } else {
-                    yo[t] = narrow<IO>(y);
-                }
+                const f32x4 u0 = bt[2 * s] * E[2 * s], u1 = bt[2 * s + 1] * E[2 * s + 1];
+                ud[s] = to_op<IO, Pl::kS>(te[2 * s] * u0, te[2 * s + 1] * u1);
+                uy[s] = to_op<IO, Pl::kQ>(u0, u1);
             }
             // S <- e^{g_C} S + K^T (e^{g_C - g} U)
             const float alpha = gates[kC - 1];
 #pragma unroll
-            for (int t = 0; t < N / 16; ++t) {
-                f32x4 z = S[t] * alpha;
+            for (int t = 0; t < N / 16; ++t) S[t] *= alpha;
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) z = mma(read_col<IO, 1, T::RB>(tk, 0, 32 * ks, 32 * (t >> 1), t & 1, c, q), ud[ks], z);
-                S[t] = z;
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int t0 = 0; t0 < N / 16; t0 += 4) {     // 4 tiles a turn (N = 32 has 2)
+                    constexpr int NT = N / 16 < 4 ? N / 16 : 4;
+                    f32x4 z[NT];
+                    Op<IO, 1> a[NT];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        z[t] = S[t0 + t];
+                        a[t] = read_col<IO, 1, T::RB>(tk, 0, 32 * ks, 32 * ((t0 + t) >> 1), t & 1, c, q);
+                    }
+                    mma(z, a, ud[ks]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) S[t0 + t] = z[t];
+                }
+            // Y = scale e^g Q S^T + scores U: 4 consecutive rows p of one token per lane
+#pragma unroll
+            for (int t = 0; t < 4; ++t) Y[t] *= scale * gates[tile_row(t >> 1, t & 1, c)];
+            {
+                Op<IO, Pl::kQ> a[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) a[t] = tri_row<IO, Pl::kQ>(ts, t >> 1, t & 1, 0, c, q);
+                mma(Y, uy[0], a);
+            }
+            {
+                f32x4 lower[2] = {Y[2], Y[3]};
+                Op<IO, Pl::kQ> a[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) a[e] = tri_row<IO, Pl::kQ>(ts, 1, e, 1, c, q);
+                mma(lower, uy[1], a);
+                Y[2] = lower[0];
+                Y[3] = lower[1];
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if constexpr (SAVE) {
+                    const f32x4 d = widen<IO>(yo[t]);
+                    const float dot = group4_sum(Y[t][0] * d[0] + Y[t][1] * d[1] + Y[t][2] * d[2] + Y[t][3] * d[3]);
+                    if (q == 0) saved.ydy[((size_t(bh) * nc + ch) * ptiles + p0 / 16) * kC + tile_row(t >> 1, t & 1, c)] = dot;
+                } else {
+                    yo[t] = narrow<IO>(Y[t]);
+                }
             }
         }
         if (ch + 1 < nc) {

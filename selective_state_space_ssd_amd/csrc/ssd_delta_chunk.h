@@ -58,24 +58,48 @@ struct Op<float, NP> {
     f32x4 v[2];
 };
 
-template <int NA, int NB>
-__device__ __forceinline__ f32x4 mma(const Op<bf16_bits, NA> &a, const Op<bf16_bits, NB> &b, f32x4 acc) {
+// acc[t] += A[t] B for the NT tiles of a step (or A B[t]: products commute lane by lane).
+// Tiles innermost: a product waits for the one before it in the same accumulator, so the
+// tiles take turns.  Small terms first.
+template <int NT, int NA, int NB>
+__device__ __forceinline__ void mma(f32x4 (&acc)[NT], const Op<bf16_bits, NA> (&a)[NT], const Op<bf16_bits, NB> &b) {
     constexpr int NM = NA > NB ? NA : NB;
 #pragma unroll
-    for (int i = NA - 1; i >= 0; --i)       // small terms first
+    for (int i = NA - 1; i >= 0; --i)
 #pragma unroll
         for (int j = NB - 1; j >= 0; --j)
-            if (i + j < NM) acc = mfma_bf16(a.p[i], b.p[j], acc);
-    return acc;
+            if (i + j < NM)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[t] = mfma_bf16(a[t].p[i], b.p[j], acc[t]);
 }
-
-template <int NA, int NB>
-__device__ __forceinline__ f32x4 mma(const Op<float, NA> &a, const Op<float, NB> &b, f32x4 acc) {
+template <int NT, int NA, int NB>
+__device__ __forceinline__ void mma(f32x4 (&acc)[NT], const Op<float, NA> (&a)[NT], const Op<float, NB> &b) {
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc = mfma_f32(a.v[e][r], b.v[e][r], acc);
-    return acc;
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = mfma_f32(a[t].v[e][r], b.v[e][r], acc[t]);
+}
+template <int NT, int NA, int NB>
+__device__ __forceinline__ void mma(f32x4 (&acc)[NT], const Op<bf16_bits, NA> &a, const Op<bf16_bits, NB> (&b)[NT]) {
+    constexpr int NM = NA > NB ? NA : NB;
+#pragma unroll
+    for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+        for (int j = NB - 1; j >= 0; --j)
+            if (i + j < NM)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[t] = mfma_bf16(a.p[i], b[t].p[j], acc[t]);
+}
+template <int NT, int NA, int NB>
+__device__ __forceinline__ void mma(f32x4 (&acc)[NT], const Op<float, NA> &a, const Op<float, NB> (&b)[NT]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = mfma_f32(a.v[e][r], b[t].v[e][r], acc[t]);
 }
 
 // The operand of 8 fp32 values (indices 8 q .. 8 q + 7: two accumulators).

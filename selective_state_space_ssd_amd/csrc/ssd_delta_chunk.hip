@@ -17,9 +17,7 @@ hipError_t launch_n(const DeltaChunkArgs &a, hipStream_t stream) {
     const int nc = (a.L + kC - 1) / kC;
     char *images = static_cast<char *>(a.workspace);
     const auto *q = static_cast<const IO *>(a.q), *k = static_cast<const IO *>(a.k), *v = static_cast<const IO *>(a.v);
-    hipLaunchKernelGGL((k_delta_prep<IO, N, Pl::kM, Pl::kQ>), dim3(unsigned(a.b * a.H * nc)), dim3(256), 0, stream, q, k, a.a, a.beta,
-                       images, a.L, a.H, a.G, nc, a.scale);
-    hipError_t e = hipGetLastError();
+    hipError_t e = launch_delta_prep<IO, N, Pl::kM, Pl::kQ>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
     if (e != hipSuccess) return e;
     constexpr int W = 4;
     const int pblocks = (a.P + 16 * W - 1) / (16 * W);

@@ -1,13 +1,15 @@
 // ssd_delta_prep.h -- the part of the chunked gated delta rule that does not depend on the
 // state: M and the scores of every chunk (see ssd_delta_chunk.h for the formulas).
 //
-// One block per (batch, head, chunk).  k_i . k_j and q_i . k_j are matrix products (exact
+// One block per chunk and a few heads of a group.  k_i . k_j and q_i . k_j are matrix products (exact
 // operands, fp32 sums).  M solves (I + Lo diag(beta)) M = -Lo: row by row inside the four
 // diagonal blocks of 16 (one lane per column), and from there by
 //   M21 = -(I + M22 b2) Lo21 (I + b1 M11)
 // for the blocks below the diagonal, 16 then 32 wide, on the fp32 matrix instruction.  No
 // power of Lo is formed, so keys that repeat do not make the terms grow.
 #pragma once
+
+#include <algorithm>
 
 #include "ssd_delta_chunk.h"
 
@@ -28,12 +30,13 @@ __device__ __forceinline__ Op<IO, 1> load_row8(const IO *p) {
 }
 
 // Copy an fp32 lower triangular [64][64] matrix from LDS into its image: NP planes,
-// 16-byte chunks placed as the chain's LDS tiles hold them.
+// 16-byte chunks placed as the chain's LDS tiles hold them; by `threads` threads, this one
+// the `first`.
 template <typename IO, int NP>
-__device__ __forceinline__ void write_image(const float *m, char *dst) {
+__device__ __forceinline__ void write_image(const float *m, char *dst, int first, int threads) {
     using Img = ChunkImage<IO, 1, 1>;
     constexpr int kRowTop = 32 * Img::kSz, kRow = 64 * Img::kSz, E = 16 / Img::kSz;
-    for (int i = threadIdx.x; i < Img::kPlane / 16; i += 256) {
+    for (int i = first; i < Img::kPlane / 16; i += threads) {
         const bool top = i < Img::kTop / 16;
         const int at = top ? i : i - Img::kTop / 16, per_row = (top ? kRowTop : kRow) / 16;
         const int r = at / per_row, pos = at % per_row;
@@ -50,23 +53,29 @@ __device__ __forceinline__ void write_image(const float *m, char *dst) {
     }
 }
 
-template <typename IO, int N, int NM, int NQ>
-__global__ __launch_bounds__(256) void k_delta_prep(const IO *__restrict__ qg, const IO *__restrict__ kg,
-                                                    const float *__restrict__ a, const float *__restrict__ beta,
-                                                    char *__restrict__ images, int L, int H, int G, int nc, float scale) {
-    using Img = ChunkImage<IO, NM, NQ>;
-    __shared__ double gd[kC];
-    __shared__ float sb[kC];
-    __shared__ float lo[kC * kLd], mm[kC * kLd], sc[kC * kLd], yt[32 * 33];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, q = lane >> 4;
-    const int ch = blockIdx.x % nc, bh = blockIdx.x / nc;
-    const int h = bh % H, bi = bh / H, g = h / (H / G);
-    const int t0 = ch * kC, valid = min(kC, L - t0);
-    char *img = images + size_t(blockIdx.x) * Img::kBytes;
+// Heads of a group that one block takes, sharing the products of the group's keys.
+constexpr int kPrepHeads = 4;
 
-    for (int i = tid; i < kC * kLd; i += 256) lo[i] = mm[i] = sc[i] = 0.f;
-    if (w == 0) {
-        const size_t at = (size_t(bi) * L + t0 + min(lane, valid - 1)) * H + h;
+template <typename IO, int N, int NM, int NQ>
+__global__ __launch_bounds__(256, 3) void k_delta_prep(const IO *__restrict__ qg, const IO *__restrict__ kg,
+                                                    const float *__restrict__ a, const float *__restrict__ beta,
+                                                    char *__restrict__ images, int L, int H, int G, int nc, int hb,
+                                                    float scale) {
+    using Img = ChunkImage<IO, NM, NQ>;
+    __shared__ double gd[kPrepHeads][kC];
+    __shared__ float sbs[kPrepHeads][kC];
+    __shared__ __align__(16) float mm[kC * kLd], sc[kC * kLd];  // Lo, then M over it; scores
+    float *yt = sc;                                             // later [32][33] of it
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, q = lane >> 4;
+    const int r = H / G, hblocks = (r + hb - 1) / hb;
+    const int ch = blockIdx.x % nc, hblk = blockIdx.x / nc % hblocks, bg = blockIdx.x / nc / hblocks;
+    const int g = bg % G, bi = bg / G;
+    const int h0 = g * r + hblk * hb, nh = min(hb, r - hblk * hb);
+    const int t0 = ch * kC, valid = min(kC, L - t0);
+    auto image = [&](int j) { return images + (size_t(bi * H + h0 + j) * nc + ch) * Img::kBytes; };
+
+    if (w < nh) {       // wave w: the gates of head h0 + w
+        const size_t at = (size_t(bi) * L + t0 + min(lane, valid - 1)) * H + h0 + w;
         double s = lane < valid ? gate(a[at]) : 0.0;
         const float bt = lane < valid ? beta[at] : 0.f;
 #pragma unroll
@@ -75,108 +84,141 @@ __global__ __launch_bounds__(256) void k_delta_prep(const IO *__restrict__ qg, c
             if (lane >= off) s += o;
         }
         const double end = __shfl(s, 63, 64);
-        gd[lane] = s;
-        sb[lane] = bt;
-        float *gates = reinterpret_cast<float *>(img + Img::kGates);
+        gd[w][lane] = s;
+        sbs[w][lane] = bt;
+        float *gates = reinterpret_cast<float *>(image(w) + Img::kGates);
         gates[lane] = expf(float(s));
         gates[kC + lane] = expf(float(end - s));
         gates[2 * kC + lane] = bt;
     }
-    __syncthreads();
-
-    {   // wave w: rows 16 w .. of both products, columns up to the diagonal
+    // wave w: row tile w of k k^T and row tile 3 - w of q k^T, up to the diagonal (5 tiles)
+    f32x4 kk[4], qk[4];
+    const int wq = 3 - w;
+    {
         const size_t ts = size_t(G) * N;
         const size_t base = (size_t(bi) * L + t0) * ts + size_t(g) * N + 8 * q;
-        const size_t arow = base + min(16 * w + c, valid - 1) * ts;
-        f32x4 kk[4], qk[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < N / 32; ++ks) {
-            const Op<IO, 1> ak = load_row8<IO>(kg + arow + 32 * ks), aq = load_row8<IO>(qg + arow + 32 * ks);
+            const Op<IO, 1> ak = load_row8<IO>(kg + base + min(16 * w + c, valid - 1) * ts + 32 * ks);
+            const Op<IO, 1> aq = load_row8<IO>(qg + base + min(16 * wq + c, valid - 1) * ts + 32 * ks);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (j > w) break;
-                const Op<IO, 1> bk = load_row8<IO>(kg + base + min(16 * j + c, valid - 1) * ts + 32 * ks);
-                kk[j] = mma(ak, bk, kk[j]);
-                qk[j] = mma(aq, bk, qk[j]);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j > w) break;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * w + 4 * q + r, jj = 16 * j + c;
-                if (jj > i) continue;
-                const float d = expf(float(gd[i] - gd[jj]));
-                sc[i * kLd + jj] = scale * qk[j][r] * d;
-                if (jj < i) lo[i * kLd + jj] = kk[j][r] * d;
+                if (j > w && j > wq) continue;
+                const Op<IO, 1> bk[1] = {load_row8<IO>(kg + base + min(16 * j + c, valid - 1) * ts + 32 * ks)};
+                f32x4 one[1];
+                if (j <= w) {
+                    one[0] = kk[j];
+                    mma(one, ak, bk);
+                    kk[j] = one[0];
+                }
+                if (j <= wq) {
+                    one[0] = qk[j];
+                    mma(one, aq, bk);
+                    qk[j] = one[0];
+                }
             }
         }
     }
-    __syncthreads();
-
-    if (w == 0) {   // diagonal blocks of 16: lane = (block q, column c)
-        float m[16], bm[16];
-        const float *l0 = lo + 16 * q * kLd + 16 * q;
+    for (int j = 0; j < nh; ++j) {
+        const float *sb = sbs[j];
+        char *img = image(j);
+        __syncthreads();            // the gates; the last head's matrices are written out
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float v = -l0[i * kLd + c];
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int k = 0; k < i; ++k) v -= l0[i * kLd + k] * bm[k];
-            m[i] = v;
-            bm[i] = v * sb[16 * q + i];
-        }
-#pragma unroll
-        for (int i = 1; i < 16; ++i) mm[(16 * q + i) * kLd + 16 * q + c] = m[i];
-    }
-    __syncthreads();
-    if (w < 2) {    // blocks (1, 0) and (3, 2)
-        const int r0 = 32 * w + 16, c0 = 32 * w;
-        f32x4 y;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) y[r] = lo[(r0 + 4 * q + r) * kLd + c0 + c];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int k = c0 + 4 * t + q;
-            y = mfma_f32(lo[(r0 + c) * kLd + k], sb[k] * mm[k * kLd + c0 + c], y);
-        }
-        f32x4 z = y;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int k = r0 + 4 * q + r;
-            z = mfma_f32(mm[(r0 + c) * kLd + k], sb[k] * y[r], z);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) mm[(r0 + 4 * q + r) * kLd + c0 + c] = -z[r];
-    }
-    write_image<IO, Img::kPlanesQ>(sc, img + Img::kQ);
-    __syncthreads();
-    {               // rows 32 .. 63, columns 0 .. 31: tile (ti, tj) of wave w
-        const int r0 = 32 + 16 * (w >> 1), c0 = 16 * (w & 1);
-        f32x4 y;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) y[r] = lo[(r0 + 4 * q + r) * kLd + c0 + c];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const int k = 4 * t + q;
-            y = mfma_f32(lo[(r0 + c) * kLd + k], sb[k] * mm[k * kLd + c0 + c], y);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) yt[(r0 - 32 + 4 * q + r) * 33 + c0 + c] = y[r];
+            for (int i = 0; i < 4; ++i) {
+                // above the diagonal: zeros (the tiles there are zero, their decay unused)
+                const int col = 16 * t + c, rk = 16 * w + 4 * q + i, rq = 16 * wq + 4 * q + i;
+                mm[rk * kLd + col] = col < rk ? kk[t][i] * expf(float(gd[j][rk] - gd[j][col])) : 0.f;
+                sc[rq * kLd + col] = col <= rq ? scale * qk[t][i] * expf(float(gd[j][rq] - gd[j][col])) : 0.f;
+            }
         __syncthreads();
-        f32x4 z = y;
+        if (w > 0) {    // the other waves write the scores out meanwhile
+            write_image<IO, Img::kPlanesQ>(sc, img + Img::kQ, tid - 64, 192);
+        } else {        // diagonal blocks of 16, lane = (block q, column c): each row found
+                        // is taken out of all later ones
+            float *l0 = mm + 16 * q * kLd + 16 * q;
+            float m[16];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const int k = 4 * t + q;
-            z = mfma_f32(mm[(r0 + c) * kLd + 32 + k], sb[32 + k] * yt[k * 33 + c0 + c], z);
+            for (int i = 1; i < 16; ++i) m[i] = -l0[i * kLd + c];
+#pragma unroll
+            for (int k0 = 0; k0 < 16; k0 += 4) {    // 4 columns of Lo in registers at a time
+                float lo[16][4];
+#pragma unroll
+                for (int i = k0 + 1; i < 16; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) lo[i][k] = l0[i * kLd + k0 + k];
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int k = k0 == 0 ? 1 : 0; k < 4; ++k) {
+                    const float bm = m[k0 + k] * sb[16 * q + k0 + k];
+#pragma unroll
+                    for (int i = k0 + k + 1; i < 16; ++i) m[i] -= lo[i][k] * bm;
+                }
+            }
+#pragma unroll
+            for (int i = 1; i < 16; ++i) l0[i * kLd + c] = m[i];
         }
+        __syncthreads();
+        if (w < 2) {    // blocks (1, 0) and (3, 2)
+            const int r0 = 32 * w + 16, c0 = 32 * w;
+            f32x4 y;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) mm[(r0 + 4 * q + r) * kLd + c0 + c] = -z[r];
+            for (int i = 0; i < 4; ++i) y[i] = mm[(r0 + 4 * q + i) * kLd + c0 + c];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int k = c0 + 4 * t + q;
+                y = mfma_f32(mm[(r0 + c) * kLd + k], sb[k] * mm[k * kLd + c0 + c], y);
+            }
+            f32x4 z = y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = r0 + 4 * q + i;
+                z = mfma_f32(mm[(r0 + c) * kLd + k], sb[k] * y[i], z);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mm[(r0 + 4 * q + i) * kLd + c0 + c] = -z[i];
+        }
+        __syncthreads();
+        {               // rows 32 .. 63, columns 0 .. 31: one tile per wave
+            const int r0 = 32 + 16 * (w >> 1), c0 = 16 * (w & 1);
+            f32x4 y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = mm[(r0 + 4 * q + i) * kLd + c0 + c];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const int k = 4 * t + q;
+                y = mfma_f32(mm[(r0 + c) * kLd + k], sb[k] * mm[k * kLd + c0 + c], y);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) yt[(r0 - 32 + 4 * q + i) * 33 + c0 + c] = y[i];
+            __syncthreads();
+            f32x4 z = y;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const int k = 4 * t + q;
+                z = mfma_f32(mm[(r0 + c) * kLd + 32 + k], sb[32 + k] * yt[k * 33 + c0 + c], z);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mm[(r0 + 4 * q + i) * kLd + c0 + c] = -z[i];
+        }
+        __syncthreads();
+        write_image<IO, Img::kPlanesM>(mm, img + Img::kM, tid, 256);
     }
-    __syncthreads();
-    write_image<IO, Img::kPlanesM>(mm, img + Img::kM);
+}
+
+// One launch over all chunks.  A block per chunk, group and kPrepHeads heads where that
+// fills the device, per head where it does not.
+template <typename IO, int N, int NM, int NQ>
+hipError_t launch_delta_prep(const IO *q, const IO *k, const float *a, const float *beta, char *images, int b, int L, int H,
+                             int G, float scale, hipStream_t stream) {
+    const int nc = (L + kC - 1) / kC, r = H / G;
+    const int hb = int64_t(b) * nc * G * ((r + kPrepHeads - 1) / kPrepHeads) >= 512 ? std::min(r, kPrepHeads) : 1;
+    const unsigned blocks = unsigned(int64_t(b) * nc * G * ((r + hb - 1) / hb));
+    hipLaunchKernelGGL((k_delta_prep<IO, N, NM, NQ>), dim3(blocks), dim3(256), 0, stream, q, k, a, beta, images, L, H, G, nc, hb, scale);
+    return hipGetLastError();
 }
 
 }  // namespace ssd
