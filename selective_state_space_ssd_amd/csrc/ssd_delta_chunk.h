@@ -32,14 +32,17 @@ constexpr int kC = 64;      // tokens per chunk
 __device__ __forceinline__ double gate(float a) { return a < -1e5f ? -1e5 : double(a); }
 
 // LDS tiles: rows of RB bytes in chunks of 16; chunk `ch` of row r lies at ch ^ place(r).
-// The 16 lanes of a row read (rows 8 (c >> 2) + (c & 3) + const, one chunk) and the 16 of
-// a transposing read (rows (c >> 2) + const, chunks (c & 3) + const) then fall on 16
-// different 16-byte columns of the 256-byte bank row.
+// A 128-bit read serves 16 lanes a cycle, lanes {0-3, 12-15, 20-27} and {4-11, 16-19,
+// 28-31} and the same 32 further on, from 64 banks; a 64-bit read the 32 lanes of a half.
+// These placements, found by a search over the maps that are linear in the row's bits,
+// give 16 different 16-byte columns to each such group of a row read (rows tile_row(.),
+// or consecutive ones) and at most two lanes a column to a transposing read, which only
+// ever uses one half of each column.
 template <int RB>
 __device__ __forceinline__ int place(int r) {
-    if constexpr (RB >= 256) return (r & 3) * 4 + ((r >> 3) & 3);
-    else if constexpr (RB == 128) return ((r >> 1) & 1) * 4 + ((r >> 3) & 3);
-    else return (r >> 3) & 3;
+    if constexpr (RB >= 256) return (r & 1) ^ ((r & 2) << 1) ^ ((r & 4) >> 1) ^ ((r & 8) | ((r & 8) >> 3)) ^ ((r & 16) >> 3);
+    else if constexpr (RB == 128) return ((r & 2) >> 1) ^ ((r & 4) >> 1) ^ ((r & 8) >> 1) ^ ((r & 16) >> 3);
+    else return (r & 8) >> 2;
 }
 
 // The tile row of lane c: index 32 s + 8 (c >> 2) + 4 e + (c & 3).
