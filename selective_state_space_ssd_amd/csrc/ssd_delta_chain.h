@@ -30,43 +30,48 @@ struct DeltaPlanes {
     static constexpr int kS = 3, kM = 3, kQ = SAVE ? 3 : 2;
 };
 
-template <typename IO, int N, bool SAVE>
+// LDS buffer of one chunk: k, q, the block's 16 W columns of v, the image.
+template <typename IO, int N, int W, bool SAVE>
 struct ChainTile {
     using Pl = DeltaPlanes<SAVE>;
     using Img = ChunkImage<IO, Pl::kM, Pl::kQ>;
-    static constexpr int RB = N * int(sizeof(IO));          // bytes per row of k or q
-    static constexpr int kRows = kC * RB;                   // bytes of a k or q tile
-    static constexpr int kBytes = 2 * kRows + Img::kBytes;  // k, q, then the image
+    static constexpr int kSz = int(sizeof(IO));
+    static constexpr int RB = N * kSz;                      // bytes per row of k or q
+    static constexpr int RV = 16 * W * kSz;                 // bytes per row of v
+    static constexpr int kRows = kC * RB, kVals = kC * RV;  // bytes of the tiles
+    static constexpr int kQt = kRows, kVt = 2 * kRows, kImg = 2 * kRows + kVals;
+    static constexpr int kBytes = kImg + Img::kBytes;
     static constexpr int kBufs = 2 * kBytes <= 160 * 1024 ? 2 : 1;
     static constexpr int kLds = kBufs * kBytes;
 };
 
-// Start the copies of one chunk's k, q and image into an LDS buffer.
-template <typename T, typename IO, int N, int W>
-__device__ __forceinline__ void fetch_chunk(const IO *k0, const IO *q0, const char *img, uint32_t buf, uint32_t gn,
-                                            int last) {
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    constexpr int kThreads = 64 * W;
+// Start the copies of ROWS rows of RB bytes (row r at base + r * stride bytes; rows
+// past `last`: that one; 16-byte chunks of a row past `chunks`: the last one) into a tile.
+// The block's waves take 1 KiB in turn; this call starts part PART of PARTS.
+template <int RB, int ROWS, int W, int PART, int PARTS>
+__device__ __forceinline__ void copy_rows(const void *base, uint32_t stride, int last, int chunks, uint32_t dst) {
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kIt = ROWS * RB / 1024 / W, kPer = (kIt + PARTS - 1) / PARTS;
 #pragma unroll
-    for (int i = 0; i < T::kRows / 16 / kThreads; ++i) {
-        const int at = i * kThreads + tid, r = at / (T::RB / 16), col = (at % (T::RB / 16)) ^ place<T::RB>(r);
-        const uint32_t off = uint32_t(min(r, last)) * gn + uint32_t(col) * 16;     // rows past the end: the last one
-        const uint32_t dst = buf + uint32_t(i * kThreads + 64 * w) * 16;
-        copy16(k0, off, dst);
-        copy16(q0, off, dst + T::kRows);
+    for (int i = PART * kPer; i < (PART + 1) * kPer && i < kIt; ++i) {
+        const int at = (i * W + w) * 64 + lane, r = at / (RB / 16), col = min((at % (RB / 16)) ^ place<RB>(r), chunks - 1);
+        copy16(base, uint32_t(min(r, last)) * stride + uint32_t(col) * 16, dst + uint32_t(i * W + w) * 1024);
     }
-#pragma unroll
-    for (int i = 0; i < (T::Img::kBytes / 1024 + W - 1) / W; ++i)
-        if (i * W + w < T::Img::kBytes / 1024)
-            copy16(img, uint32_t(i * W + w) * 1024 + lane * 16, buf + 2 * T::kRows + uint32_t(i * W + w) * 1024);
 }
 
-// One element / 4 consecutive ones of a range-checked view; past its end: 0.
-template <typename IO>
-__device__ __forceinline__ IO load_checked(__amdgpu_buffer_rsrc_t v, uint32_t off) {
-    if constexpr (std::is_same_v<IO, float>) return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(v, int(off), 0, 0));
-    else return __builtin_amdgcn_raw_buffer_load_b16(v, int(off), 0, 0);
+// The same for an image, linear; a KiB past its end: its last one again.
+template <int BYTES, int W, int PART, int PARTS>
+__device__ __forceinline__ void copy_image(const char *img, uint32_t dst) {
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kIt = (BYTES / 1024 + W - 1) / W, kPer = (kIt + PARTS - 1) / PARTS;
+#pragma unroll
+    for (int i = PART * kPer; i < (PART + 1) * kPer && i < kIt; ++i) {
+        const int at = min(i * W + w, BYTES / 1024 - 1) * 1024;
+        copy16(img + at, uint32_t(lane) * 16, dst + uint32_t(at));
+    }
 }
+
+// 4 consecutive elements of a range-checked view; past its end: 0.
 template <typename IO>
 using Raw4 = std::conditional_t<std::is_same_v<IO, float>, f32x4, u32x2>;
 template <typename IO>
@@ -85,9 +90,9 @@ __device__ __forceinline__ Raw4<IO> narrow(f32x4 v) {
     else return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
-// block = (batch, head, W * 16 rows of the state), one wave per 16 rows.  k, q and the
-// chunk's image go through LDS, shared by the waves; the next chunk's are copied into the
-// other buffer meanwhile (one buffer where two do not fit).
+// block = (batch, head, W * 16 rows of the state), one wave per 16 rows.  k, q, v and the
+// chunk's image go through LDS; the next chunk's are copied into the other buffer
+// meanwhile, a part of them between any two steps (one buffer where two do not fit).
 // SAVE: instead of y and the final state, what the backward pass needs (dyg is read).
 template <typename IO, int N, int W, bool SAVE>
 __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ qg, const IO *__restrict__ kg,
@@ -96,7 +101,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                                                         float *__restrict__ fin, const IO *__restrict__ dyg,
                                                         DeltaSaved saved, int L, int H, int P, int G, int nc, int pblocks,
                                                         float scale) {
-    using T = ChainTile<IO, N, SAVE>;
+    using T = ChainTile<IO, N, W, SAVE>;
     using Img = typename T::Img;
     using Pl = DeltaPlanes<SAVE>;
     extern __shared__ __align__(16) char lds[];
@@ -109,22 +114,24 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
     const size_t hp = size_t(H) * P, gn = size_t(G) * N;
     const char *img = images + size_t(bh) * nc * Img::kBytes;
     const IO *k0 = kg + size_t(bi) * L * gn + size_t(g) * N, *q0 = qg + size_t(bi) * L * gn + size_t(g) * N;
-    const IO *v0 = vg + size_t(bi) * L * hp + size_t(h) * P;
+    const IO *v0 = vg + size_t(bi) * L * hp + size_t(h) * P + size_t(pb) * W * 16;
+    const int vchunks = min(16 * W, P - pb * W * 16) * kSz / 16;
     const uint32_t lds0 = lds_address(lds), tok = uint32_t(hp) * kSz;
 
-    IO rv[16];
-    auto fetch = [&](int ch, uint32_t buf) {
-        const int t0 = ch * kC, rows = min(kC, L - t0);
-        fetch_chunk<T, IO, N, W>(k0 + size_t(t0) * gn, q0 + size_t(t0) * gn, img + size_t(ch) * Img::kBytes, buf,
-                                 uint32_t(gn) * kSz, rows - 1);
-        if (live) {
-            const __amdgpu_buffer_rsrc_t view = buffer_rsrc(v0 + size_t(t0) * hp, uint32_t(rows - 1) * tok + uint32_t(P) * kSz);
-            const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) rv[4 * t + r] = load_checked<IO>(view, off + uint32_t(32 * (t >> 1) + 4 * (t & 1) + r) * tok);
-        }
+    // the copies of chunk ch into the buffer at `buf`, in 4 parts
+    auto fetch = [&](int ch, uint32_t buf, auto part) {
+        constexpr int kPart = decltype(part)::value;
+        const int t0 = ch * kC, last = min(kC, L - t0) - 1;
+        copy_rows<T::RB, kC, W, kPart, 4>(k0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf);
+        copy_rows<T::RB, kC, W, kPart, 4>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf + T::kQt);
+        copy_rows<T::RV, kC, W, kPart, 4>(v0 + size_t(t0) * hp, tok, last, vchunks, buf + T::kVt);
+        copy_image<Img::kBytes, W, kPart, 4>(img + size_t(ch) * Img::kBytes, buf + T::kImg);
+    };
+    auto fetch_all = [&](int ch, uint32_t buf) {
+        fetch(ch, buf, std::integral_constant<int, 0>{});
+        fetch(ch, buf, std::integral_constant<int, 1>{});
+        fetch(ch, buf, std::integral_constant<int, 2>{});
+        fetch(ch, buf, std::integral_constant<int, 3>{});
     };
 
     f32x4 S[N / 16];
@@ -134,27 +141,22 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
 #pragma unroll
         for (int t = 0; t < N / 16; ++t)
             S[t] = *reinterpret_cast<const f32x4 *>(init + (size_t(bh) * P + p) * N + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
-    f32x4 V[4];
-    auto take_v = [&]() {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) V[t][r] = to_f32<IO>(rv[4 * t + r]);
-    };
-    fetch(0, lds0);
+    fetch_all(0, lds0);
     copies_done();
-    take_v();
     __syncthreads();
 
     for (int ch = 0; ch < nc; ++ch) {
         const int t0 = ch * kC, rows = min(kC, L - t0);
         const char *buf = lds + (T::kBufs == 2 ? (ch & 1) * T::kBytes : 0);
-        if (T::kBufs == 2 && ch + 1 < nc) fetch(ch + 1, lds0 + ((ch + 1) & 1) * T::kBytes);
+        auto ahead = [&](auto part) {       // past the last chunk: that one again
+            if constexpr (T::kBufs == 2) fetch(min(ch + 1, nc - 1), lds0 + ((ch + 1) & 1) * T::kBytes, part);
+        };
+        ahead(std::integral_constant<int, 0>{});
         Raw4<IO> yo[4];
         f32x4 E[4];
         if (live) {
-            const char *tk = buf, *tq = buf + T::kRows, *tm = buf + 2 * T::kRows + Img::kM, *ts = buf + 2 * T::kRows + Img::kQ;
-            const float *gates = reinterpret_cast<const float *>(buf + 2 * T::kRows + Img::kGates);
+            const char *tk = buf, *tq = buf + T::kQt, *tm = buf + T::kImg + Img::kM, *ts = buf + T::kImg + Img::kQ;
+            const float *gates = reinterpret_cast<const float *>(buf + T::kImg + Img::kGates);
             if constexpr (SAVE) {
                 const __amdgpu_buffer_rsrc_t view = buffer_rsrc(dyg + (size_t(bi) * L + t0) * hp + size_t(h) * P, uint32_t(rows - 1) * tok + uint32_t(P) * kSz);
 #pragma unroll
@@ -184,6 +186,14 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                 te[t] = *reinterpret_cast<const f32x4 *>(at + kC);
                 bt[t] = *reinterpret_cast<const f32x4 *>(at + 2 * kC);
             }
+            f32x4 V[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + r, at = (16 * w + c) * kSz;
+                    V[t][r] = to_f32<IO>(*reinterpret_cast<const IO *>(buf + T::kVt + row * T::RV + (((at >> 4) ^ place<T::RV>(row)) << 4) + (at & 15)));
+                }
             // R = V - e^g K S^T, and the state's part of Y (its rows p in registers)
             f32x4 Y[4];
 #pragma unroll
@@ -195,6 +205,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                 for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tk, 0, tile_row(t >> 1, t & 1, c), ks, q);
                 mma(E, a, so[ks]);
             }
+            ahead(std::integral_constant<int, 1>{});
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 Op<IO, 1> a[4];
@@ -207,6 +218,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
             for (int t = 0; t < 4; ++t) E[t] = V[t] - fs[t] * E[t];
 #pragma unroll
             for (int s = 0; s < 2; ++s) br[s] = to_op<IO, Pl::kM>(bt[2 * s] * E[2 * s], bt[2 * s + 1] * E[2 * s + 1]);
+            ahead(std::integral_constant<int, 2>{});
             // E = R + M (beta R), U = beta E
             {
                 Op<IO, Pl::kM> a[4];
@@ -231,6 +243,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                 ud[s] = to_op<IO, Pl::kS>(te[2 * s] * u0, te[2 * s + 1] * u1);
                 uy[s] = to_op<IO, Pl::kQ>(u0, u1);
             }
+            ahead(std::integral_constant<int, 3>{});
             // S <- e^{g_C} S + K^T (e^{g_C - g} U)
             const float alpha = gates[kC - 1];
 #pragma unroll
@@ -279,16 +292,17 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                     yo[t] = narrow<IO>(Y[t]);
                 }
             }
+        } else {
+            ahead(std::integral_constant<int, 1>{});
+            ahead(std::integral_constant<int, 2>{});
+            ahead(std::integral_constant<int, 3>{});
         }
-        if (ch + 1 < nc) {
-            if constexpr (T::kBufs == 1) {
-                __syncthreads();
-                fetch(ch + 1, lds0);
-            }
-            copies_done();
-            take_v();
+        if constexpr (T::kBufs == 1) {
             __syncthreads();
+            if (ch + 1 < nc) fetch_all(ch + 1, lds0);
         }
+        copies_done();
+        __syncthreads();
         // stores last: nothing waits for them before the next chunk's copies
         if (live) {
             if constexpr (SAVE) {

@@ -105,6 +105,23 @@ __device__ __forceinline__ void mma(f32x4 (&acc)[NT], const Op<float, NA> &a, co
             for (int t = 0; t < NT; ++t) acc[t] = mfma_f32(a.v[e][r], b[t].v[e][r], acc[t]);
 }
 
+// A constant in a scalar register.  The bf16 pair (0, -1) has the bits of fp32 -1, which
+// the compiler takes for an inline constant that the instruction reads as (-1, 0).
+__device__ __forceinline__ bf16x2 pair_constant(uint32_t bits) {
+    uint32_t v;
+    asm("s_mov_b32 %0, %1" : "=s"(v) : "n"(bits));
+    return __builtin_bit_cast(bf16x2, v);
+}
+
+// v minus the low / high bf16 of a packed pair, exact (the pair holds v's own rounding in
+// that half): one two-term dot product instead of a widening and a subtraction.
+__device__ __forceinline__ float minus_lo(float v, uint32_t pair) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), pair_constant(0x0000bf80u), v, false);
+}
+__device__ __forceinline__ float minus_hi(float v, uint32_t pair) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), pair_constant(0xbf800000u), v, false);
+}
+
 // The operand of 8 fp32 values (indices 8 q .. 8 q + 7: two accumulators).
 template <typename IO, int NP>
 __device__ __forceinline__ Op<IO, NP> to_op(f32x4 lo, f32x4 hi) {
@@ -119,8 +136,8 @@ __device__ __forceinline__ Op<IO, NP> to_op(f32x4 lo, f32x4 hi) {
                                        pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]));
             o.p[i] = as_bf16x8(w);
             if (i + 1 < NP) {
-                lo -= f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-                hi -= f32x4{bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
+                lo = f32x4{minus_lo(lo[0], w.x), minus_hi(lo[1], w.x), minus_lo(lo[2], w.y), minus_hi(lo[3], w.y)};
+                hi = f32x4{minus_lo(hi[0], w.z), minus_hi(hi[1], w.z), minus_lo(hi[2], w.w), minus_hi(hi[3], w.w)};
             }
         }
     }

@@ -12,7 +12,6 @@ namespace {
 
 template <typename IO, int N>
 hipError_t launch_n(const DeltaChunkArgs &a, hipStream_t stream) {
-    using T = ChainTile<IO, N, false>;
     using Pl = DeltaPlanes<false>;
     const int nc = (a.L + kC - 1) / kC;
     char *images = static_cast<char *>(a.workspace);
@@ -20,6 +19,7 @@ hipError_t launch_n(const DeltaChunkArgs &a, hipStream_t stream) {
     hipError_t e = launch_delta_prep<IO, N, Pl::kM, Pl::kQ>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
     if (e != hipSuccess) return e;
     constexpr int W = 4;
+    using T = ChainTile<IO, N, W, false>;
     const int pblocks = (a.P + 16 * W - 1) / (16 * W);
     auto kern = k_delta_chain<IO, N, W, false>;
     e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
