@@ -466,8 +466,21 @@ ssd_status_t ssd_chunk_scan_bwd(const void *x, const float *dt, const float *A, 
  *   overlap in time need one each.  L = 0 copies init_state (or zeros) to final_state.
  *   q, k, v, y, states 16-byte aligned, a and beta 4-byte.
  *
+ * ssd_gated_delta_bwd: from dy (of y) and d_final (of final_state; NULL = zero) the
+ *   gradients of sum(dy y) + sum(d_final final_state) with respect to every input:
+ *     dq, dk [b, L, G, N] io (summed over the heads of a group), dv [b, L, H, P] io,
+ *     da, dbeta [b, L, H] fp32, d_init [b, H, P, N] fp32 (NULL = not wanted).
+ *   Everything of the forward pass is computed again.  Sums run in a fixed order, so the
+ *   results repeat.  P a multiple of 16; N in {32, 64, 128}, and 256 for bf16 I/O.
+ *   workspace: ssd_gated_delta_bwd_workspace_bytes bytes, as above.  L = 0 copies d_final
+ *   (or zeros) to d_init.
+ *
  * Outputs must not overlap inputs, each other or the workspace.  States and all sums are
- * kept in fp32; y is rounded once.  Errors as for the other entry points.
+ * kept in fp32; with bf16 I/O the products run on the bf16 matrix cores, 32-bit operands
+ * split into bf16 planes of 8 bits, so states and the gradients da, dbeta and d_init keep
+ * fp32 accuracy.  Every output is rounded once.  A NaN or an infinity reaches every output
+ * that depends on it; inside its chunk of 64 tokens and its head it may also reach the
+ * outputs of earlier tokens.  Errors as for the other entry points.
  */
 ssd_status_t ssd_gated_delta_step(const float *state_in, const void *q, const void *k,
                                   const void *v, const float *a, const float *beta,
@@ -480,6 +493,14 @@ ssd_status_t ssd_gated_delta_fwd(const void *q, const void *k, const void *v, co
                                  const float *beta, const float *init_state, void *y,
                                  float *final_state, int b, int L, int H, int P, int N, int G,
                                  float scale, ssd_dtype_t io, void *workspace,
+                                 size_t workspace_bytes, void *hip_stream);
+size_t ssd_gated_delta_bwd_workspace_bytes(int b, int L, int H, int P, int N, int G,
+                                           ssd_dtype_t io);
+ssd_status_t ssd_gated_delta_bwd(const void *q, const void *k, const void *v, const float *a,
+                                 const float *beta, const float *init_state, const void *dy,
+                                 const float *d_final, void *dq, void *dk, void *dv, float *da,
+                                 float *dbeta, float *d_init, int b, int L, int H, int P, int N,
+                                 int G, float scale, ssd_dtype_t io, void *workspace,
                                  size_t workspace_bytes, void *hip_stream);
 
 /*

@@ -36,7 +36,8 @@ EXPORTED = ("ssd_chunk_scan_workspace_bytes", "ssd_chunk_scan_workspace_init",
             "ssd_seq_slice_state_workspace_bytes", "ssd_seq_slice_state",
             "ssd_seq_total_decay", "ssd_seq_combine", "ssd_seq_apply_state",
             "ssd_gated_delta_step", "ssd_gated_delta_fwd_workspace_bytes",
-            "ssd_gated_delta_fwd", "ssd_norm_gate_fwd", "ssd_norm_bwd_workspace_bytes",
+            "ssd_gated_delta_fwd", "ssd_gated_delta_bwd_workspace_bytes",
+            "ssd_gated_delta_bwd", "ssd_norm_gate_fwd", "ssd_norm_bwd_workspace_bytes",
             "ssd_norm_gate_bwd", "ssd_norm_add_fwd", "ssd_norm_add_bwd",
             "ssd_status_string", "ssd_version")
 
@@ -100,6 +101,10 @@ def lib() -> ctypes.CDLL:
         L.ssd_gated_delta_fwd_workspace_bytes.restype = sz
         L.ssd_gated_delta_fwd.argtypes = [vp] * 8 + [i32] * 6 + [f32, i32, vp, sz, vp]
         L.ssd_gated_delta_fwd.restype = i32
+        L.ssd_gated_delta_bwd_workspace_bytes.argtypes = [i32] * 7
+        L.ssd_gated_delta_bwd_workspace_bytes.restype = sz
+        L.ssd_gated_delta_bwd.argtypes = [vp] * 14 + [i32] * 6 + [f32, i32, vp, sz, vp]
+        L.ssd_gated_delta_bwd.restype = i32
         L.ssd_norm_gate_fwd.argtypes = [vp] * 4 + [i32] * 3 + [f32, i32, i32, vp]
         L.ssd_norm_gate_fwd.restype = i32
         L.ssd_norm_bwd_workspace_bytes.argtypes = [i32] * 5
@@ -494,6 +499,32 @@ def ssd_gated_delta_fwd(q, k, v, a, beta, init_state, y, final_state, scale, wor
              _io_code(v), ws, ws_bytes)
 
 
+def ssd_gated_delta_bwd_workspace_bytes(b, L, H, P, N, G, io: int) -> int:
+    n = lib().ssd_gated_delta_bwd_workspace_bytes(b, L, H, P, N, G, io)
+    if n == ctypes.c_size_t(-1).value:
+        raise SSDError(4, "ssd_gated_delta_bwd_workspace_bytes")
+    return n
+
+
+def ssd_gated_delta_bwd(q, k, v, a, beta, init_state, dy, d_final, dq, dk, dv, da, dbeta, d_init,
+                        scale, workspace, stream=None) -> None:
+    """Enqueue the gradients of ssd_gated_delta_fwd: inputs as there plus dy (like v) and
+    d_final [b,H,P,N] float32 (may be None); dq, dk, dv like q, k, v; da, dbeta [b,L,H]
+    float32; d_init like d_final (may be None)."""
+    b, L, H, P, N, G = _delta_dims(k, v)
+    dev, io, f32 = v.device, v.dtype, torch.float32
+    qk, vy, gt, st = (b, L, G, N), (b, L, H, P), (b, L, H), (b, H, P, N)
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _enqueue("ssd_gated_delta_bwd", dev, stream, _tensor(q, "q", qk, io, dev),
+             _tensor(k, "k", qk, io, dev), _tensor(v, "v", vy, io, dev),
+             _tensor(a, "a", gt, f32, dev), _tensor(beta, "beta", gt, f32, dev),
+             _tensor(init_state, "init_state", st, f32, dev), _tensor(dy, "dy", vy, io, dev),
+             _tensor(d_final, "d_final", st, f32, dev), _tensor(dq, "dq", qk, io, dev),
+             _tensor(dk, "dk", qk, io, dev), _tensor(dv, "dv", vy, io, dev),
+             _tensor(da, "da", gt, f32, dev), _tensor(dbeta, "dbeta", gt, f32, dev),
+             _tensor(d_init, "d_init", st, f32, dev), b, L, H, P, N, G, scale, _io_code(v), ws, ws_bytes)
+
+
 def ssd_norm_gate_fwd(x, z, w, y, group, eps, gate_first, stream=None) -> None:
     """Enqueue the gated norm of x [..., D] (z like x or None, w [D] float32) into y."""
     D, dev = x.shape[-1], x.device
@@ -649,6 +680,23 @@ def gated_delta_fwd(q, k, v, a, beta, scale, init_state=None, workspace=None, st
             workspace = _scratch(ssd_gated_delta_fwd_workspace_bytes(b, L, H, P, N, G, _io_code(v)), v.device)
     ssd_gated_delta_fwd(q, k, v, a, beta, init_state, y, final_state, scale, workspace, stream)
     return y, final_state
+
+
+def gated_delta_bwd(q, k, v, a, beta, scale, dy, init_state=None, d_final=None, workspace=None,
+                    stream=None):
+    """Allocate the gradients (and the workspace if not given); returns
+    (dq, dk, dv, da, dbeta, d_init)."""
+    b, L, H, P, N, G = _delta_dims(k, v)
+    dev, f32 = v.device, torch.float32
+    with _allocating_on(stream):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        da, dbeta = torch.empty((b, L, H), dtype=f32, device=dev), torch.empty((b, L, H), dtype=f32, device=dev)
+        d_init = torch.empty((b, H, P, N), dtype=f32, device=dev)
+        if workspace is None:
+            workspace = _scratch(ssd_gated_delta_bwd_workspace_bytes(b, L, H, P, N, G, _io_code(v)), dev)
+    ssd_gated_delta_bwd(q, k, v, a, beta, init_state, dy, d_final, dq, dk, dv, da, dbeta, d_init, scale,
+                        workspace, stream)
+    return dq, dk, dv, da, dbeta, d_init
 
 
 def norm_gate_fwd(x, z, w, group, eps, gate_first=False, stream=None):

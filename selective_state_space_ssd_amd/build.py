@@ -29,7 +29,7 @@ SOURCES = ["ssd_api.hip", "ssd_verify.hip", "ssd_chunk_scan.hip", "ssd_chunk_fus
            "ssd_selective_scan.hip", "ssd_chunk_bwd.hip",
            "ssd_chunk_bwd_bf16.hip", "ssd_seqpar.hip", "ssd_slice_state.hip",
            "ssd_delta_api.hip", "ssd_delta_step.hip",
-           "ssd_delta_chunk.hip", "ssd_norm_api.hip", "ssd_norm.hip"]
+           "ssd_delta_chunk.hip", "ssd_delta_bwd.hip", "ssd_norm_api.hip", "ssd_norm.hip"]
 ARCH = "gfx950"
 
 COMMON_FLAGS = [

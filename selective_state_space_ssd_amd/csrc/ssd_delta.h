@@ -46,4 +46,29 @@ bool delta_chunk_supported(int b, int L, int H, int P, int N, int G, bool bf16);
 DeltaChunkPlan plan_delta_chunk(int b, int L, int H, int P, int N, int G, bool bf16);
 hipError_t launch_delta_chunk(const DeltaChunkArgs &a, hipStream_t stream);
 
+// Gradients (ssd_delta_bwd.hip); the shapes of the chunked path.
+struct DeltaBwdArgs {
+    const void *q, *k, *v;
+    const float *a, *beta;
+    const float *init_state;    // null: zeros
+    const void *dy;
+    const float *d_final;       // null: zero
+    void *dq, *dk, *dv;
+    float *da, *dbeta;
+    float *d_init;              // null: not wanted
+    int b, L, H, P, N, G;
+    float scale;
+    bool bf16;
+    void *workspace;
+};
+
+// The workspace begins with the chunk images; byte offsets of what follows.
+struct DeltaBwdPlan {
+    bool supported = false;
+    size_t off_e = 0, off_s = 0, off_ds = 0, off_anchor = 0, off_ydy = 0, off_xe = 0, off_vdv = 0, off_lam = 0;
+    size_t total = 0;
+};
+DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16);
+hipError_t launch_delta_bwd(const DeltaBwdArgs &a, const DeltaBwdPlan &plan, hipStream_t stream);
+
 }  // namespace ssd

@@ -110,4 +110,48 @@ ssd_status_t ssd_gated_delta_fwd(const void *q, const void *k, const void *v, co
     return done(ssd::launch_delta_step(s, stream));
 }
 
+size_t ssd_gated_delta_bwd_workspace_bytes(int b, int L, int H, int P, int N, int G,
+                                           ssd_dtype_t io) {
+    if (check_dims(b, L, H, P, N, G, io) != SSD_OK) return size_t(-1);
+    if (!ssd::delta_chunk_supported(b, L, H, P, N, G, io == SSD_DTYPE_BF16)) return size_t(-1);
+    return ssd::plan_delta_bwd(b, L, H, P, N, G, io == SSD_DTYPE_BF16).total;
+}
+
+ssd_status_t ssd_gated_delta_bwd(const void *q, const void *k, const void *v, const float *a,
+                                 const float *beta, const float *init_state, const void *dy,
+                                 const float *d_final, void *dq, void *dk, void *dv, float *da,
+                                 float *dbeta, float *d_init, int b, int L, int H, int P, int N,
+                                 int G, float scale, ssd_dtype_t io, void *workspace,
+                                 size_t workspace_bytes, void *hip_stream) {
+    if (const ssd_status_t st = check_dims(b, L, H, P, N, G, io); st != SSD_OK) return st;
+    const bool bf16 = io == SSD_DTYPE_BF16;
+    if (!ssd::delta_chunk_supported(b, L, H, P, N, G, bf16)) return SSD_ERR_UNSUPPORTED;
+    const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    const size_t st = size_t(b) * H * P * N * 4;
+    const Range rdf(d_final, st), rdi(d_init, st);
+    if (b == 0) return SSD_OK;
+    if (!aligned(d_final, 16) || !aligned(d_init, 16)) return SSD_ERR_ALIGN;
+    if (rdi.overlaps(rdf)) return SSD_ERR_ALIAS;
+    if (L == 0) return d_init ? done(ssd::launch_copy_state(d_final, d_init, st / 4, stream)) : SSD_OK;
+    if (!q || !k || !v || !a || !beta || !dy || !dq || !dk || !dv || !da || !dbeta) return SSD_ERR_NULL_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(dy, 16) || !aligned(dq, 16) ||
+        !aligned(dk, 16) || !aligned(dv, 16) || !aligned(init_state, 16) || !aligned(a, 4) || !aligned(beta, 4) ||
+        !aligned(da, 4) || !aligned(dbeta, 4) || !aligned(workspace, 16))
+        return SSD_ERR_ALIGN;
+    const ssd::DeltaBwdPlan plan = ssd::plan_delta_bwd(b, L, H, P, N, G, bf16);
+    if (!workspace || workspace_bytes < plan.total) return SSD_ERR_WORKSPACE;
+    const size_t esz = bf16 ? 2 : 4;
+    const size_t qk = size_t(b) * L * G * N * esz, vy = size_t(b) * L * H * P * esz, gt = size_t(b) * L * H * 4;
+    const Range ins[] = {Range(q, qk), Range(k, qk), Range(v, vy), Range(a, gt), Range(beta, gt),
+                         Range(init_state, st), Range(dy, vy), rdf};
+    const Range outs[] = {Range(dq, qk), Range(dk, qk), Range(dv, vy), Range(da, gt), Range(dbeta, gt), rdi,
+                          Range(workspace, plan.total)};
+    if (any_alias(ins, outs)) return SSD_ERR_ALIAS;
+    ssd::DeltaBwdArgs c{};
+    c.q = q; c.k = k; c.v = v; c.a = a; c.beta = beta; c.init_state = init_state; c.dy = dy; c.d_final = d_final;
+    c.dq = dq; c.dk = dk; c.dv = dv; c.da = da; c.dbeta = dbeta; c.d_init = d_init; c.workspace = workspace;
+    c.b = b; c.L = L; c.H = H; c.P = P; c.N = N; c.G = G; c.scale = scale; c.bf16 = bf16;
+    return done(ssd::launch_delta_bwd(c, plan, stream));
+}
+
 }  // extern "C"

@@ -1,0 +1,610 @@
+// ssd_delta_bwd.hip -- gradients of the gated delta rule, in chunks of 64 tokens (formulas,
+// names and tile layout of the forward pass: ssd_delta_chunk.h).
+//
+// Nothing is kept from the forward pass; five kernels:
+//   1 prep       M and the scores of every chunk (ssd_delta_prep.h)
+//   2 chain      forward over the chunks: E, the entering states, y . dy (ssd_delta_chain.h)
+//   3 chain back from d_final, with dS the gradient of the state a chunk leaves:
+//        dU = scores^T dY + e^{g_C - g} (K dS^T),   X = dU + M^T (beta dU)
+//        dv = beta X,   dbeta_i = X_i . E_i
+//        dS <- e^{g_C} dS + (scale e^g dY)^T Q - (e^g dv)^T K
+//   4 grads      per chunk, all heads of a group in one block (dq and dk are their sums):
+//        dq = scale e^g dY S + W K,                      W_ij = scale (dy_i . u_j) D_ij, j <= i
+//        dk = -e^g dv S + e^{g_C - g} U dS + W^T Q + G K,  G = F + F^T, F_ij = -(dv_i . u_j) D_ij, j < i
+//   5 gates      da.  The gates only scale v going in and y coming out of an ungated rule,
+//        so the gradient of the gate sum at token t is y_t . dy_t - v_t . dv_t, and
+//        da_t = sum of it from t to the end of a segment + <dS, S> at the segment's end.
+// 2 and 3 are chains over the chunks whose waves keep 16 rows of the state each, as in the
+// forward pass: 32-bit values throughout, since da and dbeta come out of differences.
+#include <algorithm>
+
+#include "ssd_delta.h"
+#include "ssd_delta_chain.h"
+#include "ssd_delta_prep.h"
+
+namespace ssd {
+namespace {
+
+constexpr int kW = 4;       // waves per chain block
+
+// Sums over a chain wave's 16 rows, per token: fp32 [nc][P / 16][64] each.
+struct BackSums {
+    float *xe, *vdv;
+    float *lam;         // [P / 16][segments]: <dS, S> at the end of each segment
+};
+
+// Kernel 3.
+template <typename IO, int N, int W>
+__global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restrict__ qg, const IO *__restrict__ kg,
+                                                             const IO *__restrict__ vg, const IO *__restrict__ dyg,
+                                                             const char *__restrict__ images, const float *__restrict__ d_final,
+                                                             const f32x4 *__restrict__ E, const f32x4 *__restrict__ anchor,
+                                                             IO *__restrict__ dvg, IO *__restrict__ dSg,
+                                                             float *__restrict__ d_init, BackSums sums, int L, int H, int P,
+                                                             int G, int nc, int pblocks, float scale) {
+    using T = ChainTile<IO, N, W, true>;
+    using Img = typename T::Img;
+    using Pl = DeltaPlanes<true>;
+    extern __shared__ __align__(16) char lds[];
+    constexpr int KS = N / 32, kSz = int(sizeof(IO));
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
+    const int pb = blockIdx.x % pblocks, bh = blockIdx.x / pblocks;
+    const int h = bh % H, bi = bh / H, g = h / (H / G);
+    const int p0 = (pb * W + w) * 16, p = p0 + c, ptiles = P / 16, segs = (nc + kSegment - 1) / kSegment;
+    const bool live = p0 < P;
+    const size_t hp = size_t(H) * P, gn = size_t(G) * N;
+    const char *img = images + size_t(bh) * nc * Img::kBytes;
+    const IO *k0 = kg + size_t(bi) * L * gn + size_t(g) * N, *q0 = qg + size_t(bi) * L * gn + size_t(g) * N;
+    const IO *y0 = dyg + size_t(bi) * L * hp + size_t(h) * P + size_t(pb) * W * 16;
+    const int ychunks = min(16 * W, P - pb * W * 16) * kSz / 16;
+    const uint32_t lds0 = lds_address(lds), tok = uint32_t(hp) * kSz;
+
+    auto fetch = [&](int ch, uint32_t buf, auto part) {
+        constexpr int kPart = decltype(part)::value;
+        const int t0 = ch * kC, last = min(kC, L - t0) - 1;
+        copy_rows<T::RB, kC, W, kPart, 4>(k0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf);
+        copy_rows<T::RB, kC, W, kPart, 4>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf + T::kQt);
+        copy_rows<T::RV, kC, W, kPart, 4>(y0 + size_t(t0) * hp, tok, last, ychunks, buf + T::kVt);
+        copy_image<Img::kBytes, W, kPart, 4>(img + size_t(ch) * Img::kBytes, buf + T::kImg);
+    };
+    auto fetch_all = [&](int ch, uint32_t buf) {
+        fetch(ch, buf, std::integral_constant<int, 0>{});
+        fetch(ch, buf, std::integral_constant<int, 1>{});
+        fetch(ch, buf, std::integral_constant<int, 2>{});
+        fetch(ch, buf, std::integral_constant<int, 3>{});
+    };
+
+    f32x4 S[N / 16];        // dS
+#pragma unroll
+    for (int t = 0; t < N / 16; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (d_final && live)
+#pragma unroll
+        for (int t = 0; t < N / 16; ++t)
+            S[t] = *reinterpret_cast<const f32x4 *>(d_final + (size_t(bh) * P + p) * N + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
+    fetch_all(nc - 1, lds0);
+    copies_done();
+    __syncthreads();
+
+    for (int i = 0; i < nc; ++i) {
+        const int ch = nc - 1 - i, t0 = ch * kC, rows = min(kC, L - t0);
+        const char *buf = lds + (T::kBufs == 2 ? (i & 1) * T::kBytes : 0);
+        auto ahead = [&](auto part) {       // past the first chunk: that one again
+            if constexpr (T::kBufs == 2) fetch(max(ch - 1, 0), lds0 + ((i + 1) & 1) * T::kBytes, part);
+        };
+        f32x4 dv[4];
+        f32x4 xe[4], vd[4];
+        if (live) {
+            const char *tk = buf, *tq = buf + T::kQt, *tm = buf + T::kImg + Img::kM, *ts = buf + T::kImg + Img::kQ;
+            const float *gates = reinterpret_cast<const float *>(buf + T::kImg + Img::kGates);
+            const size_t unit = size_t(bh) * nc + ch;
+            // what the end of the chunk needs, asked for first
+            f32x4 Ev[4];
+            IO rv[16];
+            {
+                const f32x4 *src = E + (unit * ptiles + p0 / 16) * 256 + lane;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) Ev[t] = src[64 * t];
+                const __amdgpu_buffer_rsrc_t view = buffer_rsrc(vg + (size_t(bi) * L + t0) * hp + size_t(h) * P, uint32_t(rows - 1) * tok + uint32_t(P) * kSz);
+                const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int at = int(off + uint32_t(32 * (t >> 1) + 4 * (t & 1) + r) * tok);
+                        if constexpr (kSz == 4) rv[4 * t + r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(view, at, 0, 0));
+                        else rv[4 * t + r] = __builtin_amdgcn_raw_buffer_load_b16(view, at, 0, 0);
+                    }
+            }
+            if (ch % kSegment == kSegment - 1 || ch == nc - 1) {
+                const size_t at = (size_t(bh) * ptiles + p0 / 16) * segs + ch / kSegment;
+                const f32x4 *src = anchor + at * (N / 16) * 64 + lane;
+                float dot = 0.f;
+#pragma unroll
+                for (int t = 0; t < N / 16; ++t) {
+                    const f32x4 a = src[64 * t];
+                    dot += S[t][0] * a[0] + S[t][1] * a[1] + S[t][2] * a[2] + S[t][3] * a[3];
+                }
+                dot = wave_sum(dot);
+                if (lane == 0) sums.lam[at] = dot;
+            }
+            ahead(std::integral_constant<int, 0>{});
+            Op<IO, Pl::kS> so[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) so[s] = to_op<IO, Pl::kS>(S[2 * s], S[2 * s + 1]);
+            {
+                IO *dst = dSg + (unit * P + p) * N + 8 * q;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    if constexpr (kSz == 4) {
+                        *reinterpret_cast<f32x4 *>(dst + 32 * s) = S[2 * s];
+                        *reinterpret_cast<f32x4 *>(dst + 32 * s + 4) = S[2 * s + 1];
+                    } else {
+                        *reinterpret_cast<bf16x8 *>(dst + 32 * s) = so[s].p[0];
+                    }
+                }
+            }
+            f32x4 fs[4], te[4], bt[4], dy[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const float *at = gates + 32 * (t >> 1) + 8 * q + 4 * (t & 1);
+                fs[t] = *reinterpret_cast<const f32x4 *>(at);
+                te[t] = *reinterpret_cast<const f32x4 *>(at + kC);
+                bt[t] = *reinterpret_cast<const f32x4 *>(at + 2 * kC);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {   // rows past the sequence hold its last one: not theirs
+                    const int row = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + r, col = (16 * w + c) * kSz;
+                    const float d = to_f32<IO>(*reinterpret_cast<const IO *>(buf + T::kVt + row * T::RV + (((col >> 4) ^ place<T::RV>(row)) << 4) + (col & 15)));
+                    dy[t][r] = row < rows ? d : 0.f;
+                }
+            }
+            // dU = e^{g_C - g} K dS^T + scores^T dY
+            f32x4 dU[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) dU[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                Op<IO, 1> a[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tk, 0, tile_row(t >> 1, t & 1, c), ks, q);
+                mma(dU, a, so[ks]);
+            }
+            ahead(std::integral_constant<int, 1>{});
+#pragma unroll
+            for (int t = 0; t < 4; ++t) dU[t] *= te[t];
+            {
+                Op<IO, Pl::kQ> a[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) a[t] = tri_col<IO, Pl::kQ>(ts, 1, t >> 1, t & 1, c, q);
+                mma(dU, a, to_op<IO, 1>(dy[2], dy[3]));
+            }
+            {
+                f32x4 upper[2] = {dU[0], dU[1]};
+                Op<IO, Pl::kQ> a[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) a[e] = tri_col<IO, Pl::kQ>(ts, 0, 0, e, c, q);
+                mma(upper, a, to_op<IO, 1>(dy[0], dy[1]));
+                dU[0] = upper[0];
+                dU[1] = upper[1];
+            }
+            // X = dU + M^T (beta dU), in place
+            const Op<IO, Pl::kM> br0 = to_op<IO, Pl::kM>(bt[0] * dU[0], bt[1] * dU[1]);
+            const Op<IO, Pl::kM> br1 = to_op<IO, Pl::kM>(bt[2] * dU[2], bt[3] * dU[3]);
+            ahead(std::integral_constant<int, 2>{});
+            {
+                Op<IO, Pl::kM> a[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) a[t] = tri_col<IO, Pl::kM>(tm, 1, t >> 1, t & 1, c, q);
+                mma(dU, a, br1);
+            }
+            {
+                f32x4 upper[2] = {dU[0], dU[1]};
+                Op<IO, Pl::kM> a[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) a[e] = tri_col<IO, Pl::kM>(tm, 0, 0, e, c, q);
+                mma(upper, a, br0);
+                dU[0] = upper[0];
+                dU[1] = upper[1];
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) dv[t] = bt[t] * dU[t];
+            // dS <- e^{g_C} dS + Q^T (scale e^g dY) - K^T (e^g dv)
+            Op<IO, Pl::kS> oq[2], ok[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                oq[s] = to_op<IO, Pl::kS>(scale * fs[2 * s] * dy[2 * s], scale * fs[2 * s + 1] * dy[2 * s + 1]);
+                ok[s] = to_op<IO, Pl::kS>(-fs[2 * s] * dv[2 * s], -fs[2 * s + 1] * dv[2 * s + 1]);
+            }
+            ahead(std::integral_constant<int, 3>{});
+            const float alpha = gates[kC - 1];
+#pragma unroll
+            for (int t = 0; t < N / 16; ++t) S[t] *= alpha;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int u0 = 0; u0 < N / 16; u0 += 4) {
+                    constexpr int NT = N / 16 < 4 ? N / 16 : 4;
+                    f32x4 z[NT];
+                    Op<IO, 1> a[NT], b[NT];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        z[t] = S[u0 + t];
+                        a[t] = read_col<IO, 1, T::RB>(tq, 0, 32 * ks, 32 * ((u0 + t) >> 1), t & 1, c, q);
+                        b[t] = read_col<IO, 1, T::RB>(tk, 0, 32 * ks, 32 * ((u0 + t) >> 1), t & 1, c, q);
+                    }
+                    mma(z, a, oq[ks]);
+                    mma(z, b, ok[ks]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) S[u0 + t] = z[t];
+                    if constexpr (kSz == 4) __builtin_amdgcn_sched_barrier(0);     // 128 columns: no registers to read ahead
+                }
+            // the sums over this wave's 16 rows (the 16 lanes of a row group)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    xe[t][r] = row16_sum(dU[t][r] * Ev[t][r]);
+                    vd[t][r] = row16_sum(dv[t][r] * to_f32<IO>(rv[4 * t + r]));
+                }
+        } else {
+            ahead(std::integral_constant<int, 0>{});
+            ahead(std::integral_constant<int, 1>{});
+            ahead(std::integral_constant<int, 2>{});
+            ahead(std::integral_constant<int, 3>{});
+        }
+        if constexpr (T::kBufs == 1) {
+            __syncthreads();
+            if (ch > 0) fetch_all(ch - 1, lds0);
+        }
+        copies_done();
+        __syncthreads();
+        if (live) {
+            const size_t at = ((size_t(bh) * nc + ch) * ptiles + p0 / 16) * kC + 8 * q;
+            if (c == 0)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    *reinterpret_cast<f32x4 *>(sums.xe + at + 32 * (t >> 1) + 4 * (t & 1)) = xe[t];
+                    *reinterpret_cast<f32x4 *>(sums.vdv + at + 32 * (t >> 1) + 4 * (t & 1)) = vd[t];
+                }
+            const __amdgpu_buffer_rsrc_t view = buffer_rsrc(dvg + (size_t(bi) * L + t0) * hp + size_t(h) * P, uint32_t(rows - 1) * tok + uint32_t(P) * kSz);
+            const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int o = int(off + uint32_t(32 * (t >> 1) + 4 * (t & 1) + r) * tok);
+                    if constexpr (kSz == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dv[t][r]), view, o, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(dv[t][r]), view, o, 0, 0);
+                }
+        }
+    }
+    if (d_init && live)
+#pragma unroll
+        for (int t = 0; t < N / 16; ++t)
+            *reinterpret_cast<f32x4 *>(d_init + (size_t(bh) * P + p) * N + 32 * (t >> 1) + 8 * q + 4 * (t & 1)) = S[t];
+}
+
+// Kernel 4.  Block = (batch, chunk, group); wave w holds dq^T and dk^T of 16 tokens (tile
+// columns; rows n in registers, 8 consecutive ones a lane).  Per head and 64 rows p, dY, dv,
+// U and both states go through LDS.  Operands rounded to bf16 are the states and dv, as
+// stored; U and the matrices W and G, which are formed here, keep 16 bits (kP planes).
+template <typename IO, int N>
+struct GradTile {
+    static constexpr int kSz = int(sizeof(IO)), kP = kSz == 4 ? 1 : 2;
+    static constexpr int RP = 64 * kSz, RB = N * kSz;       // bytes per row of 64 p's / of N
+    static constexpr int kTok = kC * RP, kState = 64 * RB;  // bytes of a [64][64] / [64][N] tile
+    static constexpr int kY = 0, kV = kTok, kU = 2 * kTok, kS = kU + kP * kTok, kD = kS + kState, kHead = kD + kState;
+    // after the heads: W and G (kP planes each), k, q
+    static constexpr int kWm = 0, kGm = kP * kTok, kK = 2 * kP * kTok, kQ = kK + kState, kTail = kQ + kState;
+    static constexpr int kLds = kHead > kTail ? kHead : kTail;
+};
+
+template <typename IO, int N>
+__global__ __launch_bounds__(256, (2 * GradTile<IO, N>::kLds <= 159 * 1024 && N <= 128) ? 2 : 1) void k_delta_grads(const IO *__restrict__ qg, const IO *__restrict__ kg,
+                                                     const float *__restrict__ ag, const IO *__restrict__ dyg,
+                                                     const IO *__restrict__ dvg, const char *__restrict__ images,
+                                                     const f32x4 *__restrict__ E, const IO *__restrict__ Sg,
+                                                     const IO *__restrict__ dSg, IO *__restrict__ dqg, IO *__restrict__ dkg,
+                                                     int L, int H, int P, int G, int nc, float scale) {
+    using T = GradTile<IO, N>;
+    using Img = typename ChainTile<IO, N, kW, true>::Img;
+    constexpr int kSz = T::kSz, kP = T::kP, E16 = 16 / kSz;     // elements per 16 bytes
+    extern __shared__ __align__(16) char lds[];
+    __shared__ double gd[kC];
+    const uint32_t lds0 = lds_address(lds);
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
+    const int ch = blockIdx.x % nc, bg = blockIdx.x / nc, g = bg % G, bi = bg / G, r = H / G;
+    const int t0 = ch * kC, rows = min(kC, L - t0), ptiles = P / 16;
+    const size_t hp = size_t(H) * P, gn = size_t(G) * N;
+    const int tok = tile_row(w >> 1, w & 1, c);             // this lane's token
+
+    f32x4 dq[N / 16], dk[N / 16], Wm[4], Fm[4];
+#pragma unroll
+    for (int t = 0; t < N / 16; ++t) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 4; ++t) Wm[t] = Fm[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    {
+        const int pbs = (P + 63) / 64;
+        for (int turn = 0; turn < r * pbs; ++turn) {    // head h, rows pb .. pb + 63 of its state
+            const int h = g * r + turn / pbs, pb = turn % pbs * 64;
+            const size_t unit = (size_t(bi) * H + h) * nc + ch;
+            const float *gates = reinterpret_cast<const float *>(images + unit * Img::kBytes + Img::kGates);
+            const float fs = gates[tok], te = gates[kC + tok];
+            __syncthreads();        // the tiles' last readers
+            // thread numbers the compiler does not know: addresses are formed here again
+            // rather than kept over the loops, for which there are not the registers
+            int tid = threadIdx.x;
+            asm volatile("" : "+v"(tid));
+            const int lane = tid & 63, c = lane & 15, q = lane >> 4;
+            if (pb == 0 && w == 0) {
+                double s = lane < rows ? gate(ag[(size_t(bi) * L + t0 + lane) * H + h]) : 0.0;
+#pragma unroll
+                for (int off = 1; off < 64; off <<= 1) {
+                    const double o = __shfl_up(s, off, 64);
+                    if (lane >= off) s += o;
+                }
+                gd[lane] = s;
+            }
+            // dY, dv: rows of tokens (past the end: the last one, masked below); S, dS: rows p
+            const size_t src = (size_t(bi) * L + t0) * hp + size_t(h) * P + pb;
+            const int pchunks = min(64, P - pb) / E16;
+            copy_rows<T::RP, kC, kW, 0, 1>(dyg + src, uint32_t(hp) * kSz, rows - 1, pchunks, lds0 + T::kY);
+            copy_rows<T::RP, kC, kW, 0, 1>(dvg + src, uint32_t(hp) * kSz, rows - 1, pchunks, lds0 + T::kV);
+            copy_rows<T::RB, kC, kW, 0, 1>(Sg + (unit * P + pb) * N, T::RB, P - pb - 1, T::RB / 16, lds0 + T::kS);
+            copy_rows<T::RB, kC, kW, 0, 1>(dSg + (unit * P + pb) * N, T::RB, P - pb - 1, T::RB / 16, lds0 + T::kD);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {       // U = beta E, from wave w's chain tile: column p, 4 tokens a lane
+                const int t = i, row = 32 * (t >> 1) + 8 * q + 4 * (t & 1), col = (16 * w + c) * kSz;
+                f32x4 u = {0.f, 0.f, 0.f, 0.f};
+                if (pb + 16 * w < P) {
+                    const f32x4 bt = *reinterpret_cast<const f32x4 *>(gates + 2 * kC + row);
+                    u = bt * E[(unit * ptiles + pb / 16 + w) * 256 + 64 * t + lane];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    char *dst = lds + T::kU + (row + j) * T::RP + (((col >> 4) ^ place<T::RP>(row + j)) << 4) + (col & 15);
+                    if constexpr (kSz == 4) {
+                        *reinterpret_cast<float *>(dst) = u[j];
+                    } else {
+                        const bf16_bits hi = f32_to_bf16(u[j]);
+                        *reinterpret_cast<bf16_bits *>(dst) = hi;
+                        *reinterpret_cast<bf16_bits *>(dst + T::kTok) = f32_to_bf16(u[j] - bf16_to_f32(hi));
+                    }
+                }
+            }
+            copies_done();
+            __syncthreads();
+            if (P - pb < 64) {      // rows p past the head: the copies hold others there
+                for (int i = tid + (P - pb) * (T::RB / 16); i < T::kState / 16; i += 256)
+                    *reinterpret_cast<u32x4 *>(lds + T::kS + i * 16) = u32x4{0, 0, 0, 0};
+                __syncthreads();
+            }
+            // the states' parts, and dY U^T and dv U^T (rows j, columns i: this lane's token)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                int l = lane;
+                asm volatile("" : "+v"(l));
+                const int c = l & 15, q = l >> 4, tok = tile_row(w >> 1, w & 1, c);
+                const Op<IO, 1> oy = read_row<IO, 1, T::RP>(lds + T::kY, 0, tok, ks, q), ov = read_row<IO, 1, T::RP>(lds + T::kV, 0, tok, ks, q);
+                const Op<IO, kP> ou = read_row<IO, kP, T::RP>(lds + T::kU, T::kTok, tok, ks, q);
+#pragma unroll
+                for (int t = 0; t < N / 16; ++t) {
+                    const Op<IO, 1> as[1] = {read_col<IO, 1, T::RB>(lds + T::kS, 0, 32 * ks, 32 * (t >> 1), t & 1, c, q)};
+                    const Op<IO, 1> ad[1] = {read_col<IO, 1, T::RB>(lds + T::kD, 0, 32 * ks, 32 * (t >> 1), t & 1, c, q)};
+                    f32x4 zq[1] = {{0.f, 0.f, 0.f, 0.f}}, zv[1] = {{0.f, 0.f, 0.f, 0.f}}, zu[1] = {{0.f, 0.f, 0.f, 0.f}};
+                    mma(zq, as, oy);
+                    mma(zv, as, ov);
+                    mma(zu, ad, ou);
+                    dq[t] += (scale * fs) * zq[0];
+                    dk[t] += te * zu[0] - fs * zv[0];
+                    // the tiles' operands are not all read ahead: there are not the registers
+                    if (t & 1) __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            const double gt = gd[tok];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                f32x4 zw[1] = {{0.f, 0.f, 0.f, 0.f}}, zf[1] = {{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    const Op<IO, kP> au[1] = {read_row<IO, kP, T::RP>(lds + T::kU, T::kTok, tile_row(t >> 1, t & 1, c), ks, q)};
+                    mma(zw, au, read_row<IO, 1, T::RP>(lds + T::kY, 0, tok, ks, q));
+                    mma(zf, au, read_row<IO, 1, T::RP>(lds + T::kV, 0, tok, ks, q));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + i;
+                    const float x = float(gt - gd[j]), d = expf(j <= tok ? x : 0.f);
+                    const float wv = scale * d * zw[0][i], fv = -d * zf[0][i];
+                    Wm[t][i] += j <= tok && tok < rows ? wv : 0.f;
+                    Fm[t][i] += j < tok && tok < rows ? fv : 0.f;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+    __syncthreads();
+    // k and q into LDS, W [i][j] and G [i][j] = G [j][i] beside them
+    const size_t src = (size_t(bi) * L + t0) * gn + size_t(g) * N;
+    copy_rows<T::RB, kC, kW, 0, 1>(kg + src, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kK);
+    copy_rows<T::RB, kC, kW, 0, 1>(qg + src, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kQ);
+    auto put = [&](char *m, int row, int col, float v) {
+        char *dst = m + row * T::RP + (((col * kSz >> 4) ^ place<T::RP>(row)) << 4) + (col * kSz & 15);
+        if constexpr (kSz == 4) {
+            *reinterpret_cast<float *>(dst) = v;
+        } else {
+            const bf16_bits hi = f32_to_bf16(v);
+            *reinterpret_cast<bf16_bits *>(dst) = hi;
+            *reinterpret_cast<bf16_bits *>(dst + T::kTok) = f32_to_bf16(v - bf16_to_f32(hi));
+        }
+    };
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + i;
+            put(lds + T::kWm, tok, j, Wm[t][i]);        // 0 above the diagonal
+            if (j < tok) {
+                put(lds + T::kGm, tok, j, Fm[t][i]);
+                put(lds + T::kGm, j, tok, Fm[t][i]);
+            } else if (j == tok) {
+                put(lds + T::kGm, j, j, 0.f);
+            }
+        }
+    copies_done();
+    __syncthreads();
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        const Op<IO, kP> wr = read_row<IO, kP, T::RP>(lds + T::kWm, T::kTok, tok, ks, q);
+        const Op<IO, kP> gr = read_row<IO, kP, T::RP>(lds + T::kGm, T::kTok, tok, ks, q);
+        const Op<IO, kP> wc = read_col<IO, kP, T::RP>(lds + T::kWm, T::kTok, 32 * ks, 32 * (w >> 1), w & 1, c, q);
+#pragma unroll
+        for (int t = 0; t < N / 16; ++t) {
+            const Op<IO, 1> ak[1] = {read_col<IO, 1, T::RB>(lds + T::kK, 0, 32 * ks, 32 * (t >> 1), t & 1, c, q)};
+            const Op<IO, 1> aq[1] = {read_col<IO, 1, T::RB>(lds + T::kQ, 0, 32 * ks, 32 * (t >> 1), t & 1, c, q)};
+            f32x4 z[1] = {dq[t]};
+            mma(z, ak, wr);
+            dq[t] = z[0];
+            z[0] = dk[t];
+            mma(z, ak, gr);
+            mma(z, aq, wc);
+            dk[t] = z[0];
+            if (t & 1) __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    if (tok < rows) {
+        const size_t dst = (size_t(bi) * L + t0 + tok) * gn + size_t(g) * N + 8 * q;
+#pragma unroll
+        for (int s = 0; s < N / 32; ++s) {
+            if constexpr (kSz == 4) {
+                *reinterpret_cast<f32x4 *>(dqg + dst + 32 * s) = dq[2 * s];
+                *reinterpret_cast<f32x4 *>(dqg + dst + 32 * s + 4) = dq[2 * s + 1];
+                *reinterpret_cast<f32x4 *>(dkg + dst + 32 * s) = dk[2 * s];
+                *reinterpret_cast<f32x4 *>(dkg + dst + 32 * s + 4) = dk[2 * s + 1];
+            } else {
+                *reinterpret_cast<bf16x8 *>(dqg + dst + 32 * s) = to_op<IO, 1>(dq[2 * s], dq[2 * s + 1]).p[0];
+                *reinterpret_cast<bf16x8 *>(dkg + dst + 32 * s) = to_op<IO, 1>(dk[2 * s], dk[2 * s + 1]).p[0];
+            }
+        }
+    }
+}
+
+// Kernel 5.  Block = (batch, head, segment), one wave per chunk of it, lane = token.  The
+// sum from a token to the segment's end is taken in 64 bits: it is the sum of up to 256
+// terms that largely cancel.
+__global__ __launch_bounds__(64 * kSegment) void k_delta_gates(const float *__restrict__ ydy, const float *__restrict__ vdv,
+                                                               const float *__restrict__ xe, const float *__restrict__ lam,
+                                                               float *__restrict__ da, float *__restrict__ dbeta, int L, int H,
+                                                               int nc, int ptiles, int segs) {
+    __shared__ double total[kSegment];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int seg = blockIdx.x % segs, bh = blockIdx.x / segs, h = bh % H, bi = bh / H;
+    const int ch = seg * kSegment + w, t = ch * kC + lane;
+    double d = 0.0;
+    float b = 0.f;
+    if (ch < nc)
+        for (int i = 0; i < ptiles; ++i) {
+            const size_t at = ((size_t(bh) * nc + ch) * ptiles + i) * kC + lane;
+            d += double(ydy[at]) - double(vdv[at]);
+            b += xe[at];
+        }
+    if (t >= L) d = 0.0;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const double o = __shfl_down(d, off, 64);
+        if (lane + off < 64) d += o;
+    }
+    if (lane == 0) total[w] = d;
+    __syncthreads();
+    for (int i = w + 1; i < kSegment; ++i) d += total[i];
+    for (int i = 0; i < ptiles; ++i) d += double(lam[(size_t(bh) * ptiles + i) * segs + seg]);
+    if (ch < nc && t < L) {
+        const size_t at = (size_t(bi) * L + t) * H + h;
+        da[at] = float(d);
+        dbeta[at] = b;
+    }
+}
+
+template <typename IO, int N>
+hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t stream) {
+    using Pl = DeltaPlanes<true>;
+    using T = ChainTile<IO, N, kW, true>;
+    const int nc = (a.L + kC - 1) / kC, segs = (nc + kSegment - 1) / kSegment, ptiles = a.P / 16;
+    char *ws = static_cast<char *>(a.workspace);
+    char *images = ws;
+    const auto *q = static_cast<const IO *>(a.q), *k = static_cast<const IO *>(a.k), *v = static_cast<const IO *>(a.v);
+    const auto *dy = static_cast<const IO *>(a.dy);
+    auto *dv = static_cast<IO *>(a.dv);
+    DeltaSaved saved{reinterpret_cast<float *>(ws + pl.off_e), ws + pl.off_s, reinterpret_cast<float *>(ws + pl.off_anchor),
+                     reinterpret_cast<float *>(ws + pl.off_ydy)};
+    BackSums sums{reinterpret_cast<float *>(ws + pl.off_xe), reinterpret_cast<float *>(ws + pl.off_vdv), reinterpret_cast<float *>(ws + pl.off_lam)};
+    auto *dS = reinterpret_cast<IO *>(ws + pl.off_ds);
+
+    hipError_t e = launch_delta_prep<IO, N, Pl::kM, Pl::kQ>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
+    if (e != hipSuccess) return e;
+    const int pblocks = (a.P + 16 * kW - 1) / (16 * kW);
+    const dim3 grid(unsigned(a.b * a.H * pblocks));
+    auto chain = k_delta_chain<IO, N, kW, true>;
+    e = hipFuncSetAttribute(reinterpret_cast<const void *>(chain), hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(chain, grid, dim3(64 * kW), T::kLds, stream, q, k, v, images, a.init_state, nullptr, nullptr, dy, saved, a.L, a.H,
+                       a.P, a.G, nc, pblocks, a.scale);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    auto back = k_delta_chain_back<IO, N, kW>;
+    e = hipFuncSetAttribute(reinterpret_cast<const void *>(back), hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(back, grid, dim3(64 * kW), T::kLds, stream, q, k, v, dy, images, a.d_final, reinterpret_cast<const f32x4 *>(saved.E),
+                       reinterpret_cast<const f32x4 *>(saved.anchor), dv, dS, a.d_init, sums, a.L, a.H, a.P, a.G, nc, pblocks, a.scale);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    auto grads = k_delta_grads<IO, N>;
+    constexpr int lds = GradTile<IO, N>::kLds;
+    e = hipFuncSetAttribute(reinterpret_cast<const void *>(grads), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(grads, dim3(unsigned(int64_t(a.b) * a.G * nc)), dim3(256), lds, stream, q, k, a.a, dy, dv, images,
+                       reinterpret_cast<const f32x4 *>(saved.E), static_cast<const IO *>(saved.S), dS, static_cast<IO *>(a.dq),
+                       static_cast<IO *>(a.dk), a.L, a.H, a.P, a.G, nc, a.scale);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL(k_delta_gates, dim3(unsigned(int64_t(a.b) * a.H * segs)), dim3(64 * kSegment), 0, stream, saved.ydy, sums.vdv, sums.xe,
+                       sums.lam, a.da, a.dbeta, a.L, a.H, nc, ptiles, segs);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16) {
+    DeltaBwdPlan pl;
+    if (b <= 0 || L <= 0 || !delta_chunk_supported(b, L, H, P, N, G, bf16)) return pl;
+    using Pl = DeltaPlanes<true>;
+    const size_t nc = (size_t(L) + kC - 1) / kC, segs = (nc + kSegment - 1) / kSegment, bh = size_t(b) * H, units = bh * nc;
+    const size_t sz = bf16 ? 2 : 4, state = size_t(P) * N, ptiles = size_t(P) / 16;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t off = at;
+        at += (bytes + 255) / 256 * 256;
+        return off;
+    };
+    take(units * (bf16 ? ChunkImage<bf16_bits, Pl::kM, Pl::kQ>::kBytes : ChunkImage<float, Pl::kM, Pl::kQ>::kBytes));
+    pl.off_e = take(units * kC * P * 4);
+    pl.off_s = take(units * state * sz);
+    pl.off_ds = take(units * state * sz);
+    pl.off_anchor = take(bh * segs * state * 4);
+    pl.off_ydy = take(units * ptiles * kC * 4);
+    pl.off_xe = take(units * ptiles * kC * 4);
+    pl.off_vdv = take(units * ptiles * kC * 4);
+    pl.off_lam = take(bh * ptiles * segs * 4);
+    pl.total = at;
+    pl.supported = true;
+    return pl;
+}
+
+hipError_t launch_delta_bwd(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t stream) {
+    switch (a.N) {
+        case 32: return a.bf16 ? launch_n<bf16_bits, 32>(a, pl, stream) : launch_n<float, 32>(a, pl, stream);
+        case 64: return a.bf16 ? launch_n<bf16_bits, 64>(a, pl, stream) : launch_n<float, 64>(a, pl, stream);
+        case 128: return a.bf16 ? launch_n<bf16_bits, 128>(a, pl, stream) : launch_n<float, 128>(a, pl, stream);
+        case 256: return a.bf16 ? launch_n<bf16_bits, 256>(a, pl, stream) : hipErrorInvalidValue;
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace ssd

@@ -42,6 +42,9 @@ FWD = Call("ssd_gated_delta_fwd", ["q", "k", "v", "a", "beta", "init", "y", "fin
            ["q", "k", "v", "a", "beta", "init", "y", "final", "b", "L", "H", "P", "N", "G", "scale", "io", "ws", "ws_bytes"])
 STEPC = Call("ssd_gated_delta_step", ["state", "q", "k", "v", "a", "beta", "accept", "y", "out", "err"], dict(DIMS, L=4),
              ["state", "q", "k", "v", "a", "beta", "accept", "y", "out", "err", "b", "L", "H", "P", "N", "G", "scale", "io"])
+BWD = Call("ssd_gated_delta_bwd", ["q", "k", "v", "a", "beta", "init", "dy", "dfinal", "dq", "dk", "dv", "da", "dbeta", "dinit", "ws"],
+           dict(DIMS, ws_bytes=BIG), ["q", "k", "v", "a", "beta", "init", "dy", "dfinal", "dq", "dk", "dv", "da", "dbeta", "dinit",
+                                      "b", "L", "H", "P", "N", "G", "scale", "io", "ws", "ws_bytes"])
 ROWS = dict(rows=10, D=256, group=64, eps=1e-5, gate_first=0, io=1)
 GATE = Call("ssd_norm_gate_fwd", ["x", "z", "w", "y"], ROWS, ["x", "z", "w", "y", "rows", "D", "group", "eps", "gate_first", "io"])
 GATE_B = Call("ssd_norm_gate_bwd", ["x", "z", "w", "dy", "dx", "dz", "dw", "ws"], dict(ROWS, ws_bytes=BIG),
@@ -55,6 +58,7 @@ ADD_B = Call("ssd_norm_add_bwd", ["x", "sum", "scale", "w", "dy", "dsum", "dx", 
 
 @pytest.mark.parametrize("call,names", [
     (FWD, ["q", "k", "v", "a", "beta", "y"]), (STEPC, ["state", "q", "k", "v", "a", "beta", "y", "out"]),
+    (BWD, ["q", "k", "v", "a", "beta", "dy", "dq", "dk", "dv", "da", "dbeta"]),
     (GATE, ["x", "w", "y"]), (GATE_B, ["x", "z", "w", "dy", "dx", "dz", "dw"]), (ADD, ["x", "res", "w", "sum", "y"]),
     (ADD_B, ["x", "sum", "scale", "w", "dy", "dx", "dres", "dscale", "dw"])])
 def test_null_pointers(lib, call, names):
@@ -62,13 +66,18 @@ def test_null_pointers(lib, call, names):
         assert call(lib, **{n: None}) == NULL, n
 
 
-@pytest.mark.parametrize("call", [FWD, STEPC])
+@pytest.mark.parametrize("call", [FWD, STEPC, BWD])
 @pytest.mark.parametrize("over,code", [
     (dict(b=-1), DIM), (dict(L=-1), DIM), (dict(H=0), DIM), (dict(P=0), DIM), (dict(N=0), DIM), (dict(G=0), DIM), (dict(G=-2), DIM),
     (dict(G=3), GROUPS), (dict(N=24), UNSUP), (dict(N=48), UNSUP), (dict(N=512), UNSUP), (dict(io=2), UNSUP), (dict(io=-1), UNSUP),
     (dict(b=65536), UNSUP), (dict(H=65536), UNSUP)])
 def test_delta_dimensions(lib, call, over, code):
     assert call(lib, **over) == code
+
+
+@pytest.mark.parametrize("over", [dict(P=24), dict(P=1), dict(N=16), dict(N=256, io=0), dict(H=65534, G=65534, P=256)])
+def test_backward_shapes(lib, over):
+    assert BWD(lib, **over) == UNSUP
 
 
 @pytest.mark.parametrize("K", [0, 17, 100])
@@ -79,6 +88,7 @@ def test_step_token_counts(lib, K):
 @pytest.mark.parametrize("call,off", [
     (FWD, dict(q=8, k=2, v=8, y=4, init=8, final=4, a=2, beta=1, ws=8)),
     (STEPC, dict(state=8, out=8, q=8, k=4, v=1, y=1, a=2, beta=2, accept=2, err=1)),
+    (BWD, dict(q=8, k=4, v=2, a=2, beta=1, init=8, dy=8, dfinal=4, dq=8, dk=2, dv=4, da=2, dbeta=2, dinit=8, ws=8)),
     (GATE, dict(x=8, z=2, w=4, y=8)), (GATE_B, dict(x=8, z=2, w=4, dy=8, dx=4, dz=2, dw=8, ws=8)),
     (ADD, dict(x=8, res=4, scale=4, w=8, sum=8, y=2)),
     (ADD_B, dict(x=8, sum=4, scale=8, w=4, dy=2, dsum=8, dx=8, dres=4, dscale=4, dw=8, ws=4))])
@@ -90,6 +100,7 @@ def test_alignment(lib, call, off):
 @pytest.mark.parametrize("call,pairs", [
     (FWD, [("y", "q"), ("y", "v"), ("y", "a"), ("final", "init"), ("final", "k"), ("final", "y"), ("y", "init")]),
     (STEPC, [("y", "v"), ("out", "q"), ("y", "state"), ("out", "y"), ("err", "accept"), ("err", "state"), ("out", "beta")]),
+    (BWD, [("dq", "q"), ("dk", "dq"), ("dv", "v"), ("dv", "dy"), ("da", "a"), ("dbeta", "da"), ("dinit", "dfinal"), ("dinit", "init"), ("ws", "k"), ("ws", "dv")]),
     (GATE, [("y", "x"), ("y", "z"), ("y", "w")]), (GATE_B, [("dx", "x"), ("dz", "dx"), ("dw", "w"), ("ws", "dy"), ("ws", "dx"), ("dx", "dy")]),
     (ADD, [("sum", "x"), ("y", "x"), ("y", "res"), ("y", "sum"), ("sum", "w"), ("y", "scale")]),
     (ADD_B, [("dx", "x"), ("dx", "sum"), ("dres", "dsum"), ("dres", "dx"), ("dw", "dscale"), ("ws", "sum"), ("dscale", "scale")])])
@@ -129,6 +140,9 @@ def test_delta_workspace(lib):
     assert need > 0 and FWD(lib, ws_bytes=need - 1) == WS
     for name in ("q", "v", "y", "final"):
         assert FWD(lib, ws=FWD.address(name)) == ALIAS
+    assert BWD(lib, ws=None) == WS
+    need = bd.ssd_gated_delta_bwd_workspace_bytes(2, 100, 4, 64, 64, 2, 1)
+    assert need > 0 and BWD(lib, ws_bytes=need - 1) == WS
 
 
 def test_workspace_sizes():
@@ -142,8 +156,8 @@ def test_workspace_sizes():
 
 
 def test_nothing_to_do(lib):
-    assert STEPC(lib, b=0) == OK and FWD(lib, b=0) == OK
-    assert FWD(lib, L=0, final=None) == OK
+    assert STEPC(lib, b=0) == OK and FWD(lib, b=0) == OK and BWD(lib, b=0) == OK
+    assert FWD(lib, L=0, final=None) == OK and BWD(lib, L=0, dinit=None) == OK
     assert GATE(lib, rows=0) == OK and ADD(lib, rows=0) == OK
 
 
