@@ -50,7 +50,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
     const int pb = blockIdx.x % pblocks, bh = blockIdx.x / pblocks;
     const int h = bh % H, bi = bh / H, g = h / (H / G);
-    const int p0 = (pb * W + w) * 16, p = p0 + c, ptiles = P / 16, segs = (nc + kSegment - 1) / kSegment;
+    const int p0 = (pb * W + w) * 16, p = p0 + c, ptiles = P / 16, segs = (nc + kSegment<IO> - 1) / kSegment<IO>;
     const bool live = p0 < P;
     const size_t hp = size_t(H) * P, gn = size_t(G) * N;
     const char *img = images + size_t(bh) * nc * Img::kBytes;
@@ -115,8 +115,8 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
                         else rv[4 * t + r] = __builtin_amdgcn_raw_buffer_load_b16(view, at, 0, 0);
                     }
             }
-            if (ch % kSegment == kSegment - 1 || ch == nc - 1) {
-                const size_t at = (size_t(bh) * ptiles + p0 / 16) * segs + ch / kSegment;
+            if (ch % kSegment<IO> == kSegment<IO> - 1 || ch == nc - 1) {
+                const size_t at = (size_t(bh) * ptiles + p0 / 16) * segs + ch / kSegment<IO>;
                 const f32x4 *src = anchor + at * (N / 16) * 64 + lane;
                 float dot = 0.f;
 #pragma unroll
@@ -490,16 +490,17 @@ __global__ __launch_bounds__(256, (2 * GradTile<IO, N>::kLds <= 159 * 1024 && N 
 }
 
 // Kernel 5.  Block = (batch, head, segment), one wave per chunk of it, lane = token.  The
-// sum from a token to the segment's end is taken in 64 bits: it is the sum of up to 256
+// sum from a token to the segment's end is taken in 64 bits: it is the sum of up to 128
 // terms that largely cancel.
-__global__ __launch_bounds__(64 * kSegment) void k_delta_gates(const float *__restrict__ ydy, const float *__restrict__ vdv,
+template <int SEG>
+__global__ __launch_bounds__(64 * SEG) void k_delta_gates(const float *__restrict__ ydy, const float *__restrict__ vdv,
                                                                const float *__restrict__ xe, const float *__restrict__ lam,
                                                                float *__restrict__ da, float *__restrict__ dbeta, int L, int H,
                                                                int nc, int ptiles, int segs) {
-    __shared__ double total[kSegment];
+    __shared__ double total[SEG];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int seg = blockIdx.x % segs, bh = blockIdx.x / segs, h = bh % H, bi = bh / H;
-    const int ch = seg * kSegment + w, t = ch * kC + lane;
+    const int ch = seg * SEG + w, t = ch * kC + lane;
     double d = 0.0;
     float b = 0.f;
     if (ch < nc)
@@ -516,7 +517,7 @@ __global__ __launch_bounds__(64 * kSegment) void k_delta_gates(const float *__re
     }
     if (lane == 0) total[w] = d;
     __syncthreads();
-    for (int i = w + 1; i < kSegment; ++i) d += total[i];
+    for (int i = w + 1; i < SEG; ++i) d += total[i];
     for (int i = 0; i < ptiles; ++i) d += double(lam[(size_t(bh) * ptiles + i) * segs + seg]);
     if (ch < nc && t < L) {
         const size_t at = (size_t(bi) * L + t) * H + h;
@@ -529,7 +530,7 @@ template <typename IO, int N>
 hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t stream) {
     using Pl = DeltaPlanes<true>;
     using T = ChainTile<IO, N, kW, true>;
-    const int nc = (a.L + kC - 1) / kC, segs = (nc + kSegment - 1) / kSegment, ptiles = a.P / 16;
+    const int nc = (a.L + kC - 1) / kC, segs = (nc + kSegment<IO> - 1) / kSegment<IO>, ptiles = a.P / 16;
     char *ws = static_cast<char *>(a.workspace);
     char *images = ws;
     const auto *q = static_cast<const IO *>(a.q), *k = static_cast<const IO *>(a.k), *v = static_cast<const IO *>(a.v);
@@ -564,7 +565,7 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
                        reinterpret_cast<const f32x4 *>(saved.E), static_cast<const IO *>(saved.S), dS, static_cast<IO *>(a.dq),
                        static_cast<IO *>(a.dk), a.L, a.H, a.P, a.G, nc, a.scale);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(k_delta_gates, dim3(unsigned(int64_t(a.b) * a.H * segs)), dim3(64 * kSegment), 0, stream, saved.ydy, sums.vdv, sums.xe,
+    hipLaunchKernelGGL((k_delta_gates<kSegment<IO>>), dim3(unsigned(int64_t(a.b) * a.H * segs)), dim3(64 * kSegment<IO>), 0, stream, saved.ydy, sums.vdv, sums.xe,
                        sums.lam, a.da, a.dbeta, a.L, a.H, nc, ptiles, segs);
     return hipGetLastError();
 }
@@ -575,7 +576,7 @@ DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16)
     DeltaBwdPlan pl;
     if (b <= 0 || L <= 0 || !delta_chunk_supported(b, L, H, P, N, G, bf16)) return pl;
     using Pl = DeltaPlanes<true>;
-    const size_t nc = (size_t(L) + kC - 1) / kC, segs = (nc + kSegment - 1) / kSegment, bh = size_t(b) * H, units = bh * nc;
+    const size_t nc = (size_t(L) + kC - 1) / kC, segs = bf16 ? (nc + kSegment<bf16_bits> - 1) / kSegment<bf16_bits> : (nc + kSegment<float> - 1) / kSegment<float>, bh = size_t(b) * H, units = bh * nc;
     const size_t sz = bf16 ? 2 : 4, state = size_t(P) * N, ptiles = size_t(P) / 16;
     size_t at = 0;
     auto take = [&](size_t bytes) {

@@ -27,6 +27,7 @@ namespace ssd {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int kBwdBlocks = 1024;    // blocks of a backward pass, at the most
 
 // VEC elements of the I/O type, loaded and stored as one access.
 template <typename IO, int VEC>
@@ -80,8 +81,16 @@ __device__ __forceinline__ float team_sum(float v, float *tmp) {
     return v;
 }
 
-// act(z) and its slope.  e^-z overflows to inf for z below -88, where the gate is -0.
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+// act(z) = z sigmoid(z).  e^-z overflows to inf for z below -88, where the gate is -0.
+// With bf16 I/O the exponential is the hardware's of z log2(e) and the quotient its
+// reciprocal (relative errors of a few 2^-24 (1 + |z|), against 2^-9 of the rounding to
+// come).  That, one evaluation per element instead of three, and the order of gate and norm
+// as a template argument took the backward pass of 8192 x 4096 from 114 to 70 us (336 MB).
+template <typename IO>
+__device__ __forceinline__ float sigmoid(float z) {
+    if constexpr (std::is_same_v<IO, float>) return 1.f / (1.f + expf(-z));
+    else return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * kLog2e));
+}
 
 // ------------------------------------------------------------------- after the mixer
 template <typename IO, int VEC, int TPS, int NV>
@@ -112,7 +121,7 @@ __global__ __launch_bounds__(kBlock) void k_norm_gate_fwd(const IO *__restrict__
         if (!(live && c < group)) continue;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            const float act = z ? g[i][j] * sigmoid(g[i][j]) : 1.f;
+            const float act = z ? g[i][j] * sigmoid<IO>(g[i][j]) : 1.f;
             if (gate_first) u[i][j] *= act;
             g[i][j] = gate_first ? 1.f : act;
             ss += u[i][j] * u[i][j];
@@ -133,12 +142,12 @@ __global__ __launch_bounds__(kBlock) void k_norm_gate_fwd(const IO *__restrict__
 
 // One team keeps one group of channels and walks the rows of its slice; its sums for dw
 // stay in registers until the end.
-template <typename IO, int VEC, int TPS, int NV>
+template <typename IO, bool FIRST, int VEC, int TPS, int NV>
 __global__ __launch_bounds__(kBlock) void k_norm_gate_bwd(const IO *__restrict__ x, const IO *__restrict__ z,
                                                           const float *__restrict__ w, const IO *__restrict__ dy,
                                                           IO *__restrict__ dx, IO *__restrict__ dz,
                                                           float *__restrict__ dwp, int64_t rows, int D, int group,
-                                                          int slices, float eps, bool gate_first) {
+                                                          int slices, float eps) {
     __shared__ float tmp[4];
     constexpr int kTeams = kBlock / TPS;
     const int lane = threadIdx.x % TPS;
@@ -163,7 +172,6 @@ __global__ __launch_bounds__(kBlock) void k_norm_gate_bwd(const IO *__restrict__
         const bool on = live && row < rows;
         const int64_t at = (on ? row : 0) * D + col;
         float u[NV][VEC], g[NV][VEC], d[NV][VEC];
-        float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPS + lane) * VEC;
@@ -175,11 +183,15 @@ __global__ __launch_bounds__(kBlock) void k_norm_gate_bwd(const IO *__restrict__
                 load_vec<IO, VEC>(dy + at + c, d[i]);
             }
         }
+        float act[NV][VEC], ss = 0.f;       // the gate; g becomes its slope
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const float v = gate_first && z ? u[i][j] * (g[i][j] * sigmoid(g[i][j])) : u[i][j];
+                const float sg = sigmoid<IO>(g[i][j]);
+                act[i][j] = z ? g[i][j] * sg : 1.f;
+                g[i][j] = sg + act[i][j] * (1.f - sg);
+                const float v = FIRST ? u[i][j] * act[i][j] : u[i][j];
                 ss += v * v;
             }
         const float r = 1.f / sqrtf(team_sum<TPS>(ss, tmp) / float(group) + eps);
@@ -188,9 +200,8 @@ __global__ __launch_bounds__(kBlock) void k_norm_gate_bwd(const IO *__restrict__
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const float act = z ? g[i][j] * sigmoid(g[i][j]) : 1.f;
-                const float n = u[i][j] * (gate_first ? act : 1.f) * r;
-                const float up = gate_first ? d[i][j] : d[i][j] * act;     // gradient of n w
+                const float n = (FIRST ? u[i][j] * act[i][j] : u[i][j]) * r;
+                const float up = FIRST ? d[i][j] : d[i][j] * act[i][j];     // gradient of n w
                 dw[i][j] += up * n;
                 dot += up * wv[i][j] * n;
             }
@@ -202,13 +213,10 @@ __global__ __launch_bounds__(kBlock) void k_norm_gate_bwd(const IO *__restrict__
             float ox[VEC], oz[VEC];
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const float zz = g[i][j], sg = z ? sigmoid(zz) : 1.f;
-                const float act = z ? zz * sg : 1.f, slope = sg * (1.f + zz * (1.f - sg));
-                const float n = u[i][j] * (gate_first ? act : 1.f) * r;
-                const float dn = (gate_first ? d[i][j] : d[i][j] * act) * wv[i][j];
-                const float du = r * (dn - n * mean);
-                ox[j] = gate_first ? du * act : du;
-                oz[j] = (gate_first ? du * u[i][j] : d[i][j] * n * wv[i][j]) * slope;
+                const float n = (FIRST ? u[i][j] * act[i][j] : u[i][j]) * r;
+                const float du = r * ((FIRST ? d[i][j] : d[i][j] * act[i][j]) * wv[i][j] - n * mean);
+                ox[j] = FIRST ? du * act[i][j] : du;
+                oz[j] = (FIRST ? du * u[i][j] : d[i][j] * n * wv[i][j]) * g[i][j];
             }
             store_vec<IO, VEC>(dx + at + c, ox);
             if (z) store_vec<IO, VEC>(dz + at + c, oz);
@@ -365,14 +373,14 @@ __global__ __launch_bounds__(kBlock) void k_norm_gate_fwd_loop(const IO *__restr
         float u = to_f32<IO>(x[at + c]);
         if (z && gate_first) {
             const float zz = to_f32<IO>(z[at + c]);
-            u *= zz * sigmoid(zz);
+            u *= zz * sigmoid<IO>(zz);
         }
         ss += u * u;
     }
     const float r = 1.f / sqrtf(team_sum<256>(ss, tmp) / float(group) + eps);
     for (int c = threadIdx.x; c < group; c += kBlock) {
         const float zz = z ? to_f32<IO>(z[at + c]) : 0.f;
-        const float act = z ? zz * sigmoid(zz) : 1.f;
+        const float act = z ? zz * sigmoid<IO>(zz) : 1.f;
         y[at + c] = from_f32<IO>(to_f32<IO>(x[at + c]) * act * r * w[col + c]);
     }
 }
@@ -396,14 +404,14 @@ __global__ __launch_bounds__(kBlock) void k_norm_gate_bwd_loop(const IO *__restr
             float u = to_f32<IO>(x[at + c]);
             if (z && gate_first) {
                 const float zz = to_f32<IO>(z[at + c]);
-                u *= zz * sigmoid(zz);
+                u *= zz * sigmoid<IO>(zz);
             }
             ss += u * u;
         }
         const float r = 1.f / sqrtf(team_sum<256>(ss, tmp) / float(group) + eps);
         float dot = 0.f;
         for (int c = threadIdx.x; c < group; c += kBlock) {
-            const float zz = z ? to_f32<IO>(z[at + c]) : 0.f, act = z ? zz * sigmoid(zz) : 1.f;
+            const float zz = z ? to_f32<IO>(z[at + c]) : 0.f, act = z ? zz * sigmoid<IO>(zz) : 1.f;
             const float d = to_f32<IO>(dy[at + c]), u = to_f32<IO>(x[at + c]);
             const float n = u * (gate_first ? act : 1.f) * r, up = gate_first ? d : d * act;
             dw[c] += up * n;
@@ -411,7 +419,7 @@ __global__ __launch_bounds__(kBlock) void k_norm_gate_bwd_loop(const IO *__restr
         }
         const float mean = team_sum<256>(dot, tmp) / float(group);
         for (int c = threadIdx.x; c < group; c += kBlock) {
-            const float zz = z ? to_f32<IO>(z[at + c]) : 0.f, sg = z ? sigmoid(zz) : 1.f;
+            const float zz = z ? to_f32<IO>(z[at + c]) : 0.f, sg = z ? sigmoid<IO>(zz) : 1.f;
             const float act = z ? zz * sg : 1.f, slope = sg * (1.f + zz * (1.f - sg));
             const float d = to_f32<IO>(dy[at + c]), u = to_f32<IO>(x[at + c]), wc = w[col + c];
             const float n = u * (gate_first ? act : 1.f) * r;
@@ -481,21 +489,27 @@ __global__ __launch_bounds__(kBlock) void k_norm_add_bwd_loop(const IO *__restri
     }
 }
 
-// out[p][c] = the sum over slices of part[p][slice][c], slices in a fixed order: 4 waves
-// take a quarter of the slices each, 64 channels per block.
-__global__ __launch_bounds__(kBlock) void k_norm_reduce(const float *__restrict__ part, float *out0, float *out1,
-                                                        int slices, int D) {
-    __shared__ float tmp[4][64];
-    const int c = blockIdx.x * 64 + (threadIdx.x & 63), wv = threadIdx.x >> 6;
-    const float *p = part + size_t(blockIdx.y) * slices * D;
-    float s = 0.f;
-    if (c < D)
-        for (int i = wv; i < slices; i += 4) s += p[size_t(i) * D + c];
-    tmp[wv][threadIdx.x & 63] = s;
+// out[p][c] = the sum over slices of part[p][slice][c] in a fixed order: 64 channels per
+// block, 16 waves with every 16th slice each, 8 loads in flight.
+constexpr int kReduceWaves = 16;
+__global__ __launch_bounds__(64 * kReduceWaves) void k_norm_reduce(const float *__restrict__ part, float *out0, float *out1,
+                                                                   int slices, int D) {
+    __shared__ float tmp[kReduceWaves][64];
+    const int lane = threadIdx.x & 63, c = blockIdx.x * 64 + lane, wv = threadIdx.x >> 6;
+    const float *p = part + size_t(blockIdx.y) * slices * D + min(c, D - 1);
+    float s[8] = {};
+    int i = wv;
+    for (; i + 7 * kReduceWaves < slices; i += 8 * kReduceWaves)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += p[size_t(i + j * kReduceWaves) * D];
+    for (; i < slices; i += kReduceWaves) s[0] += p[size_t(i) * D];
+    tmp[wv][lane] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     __syncthreads();
     if (wv == 0 && c < D) {
-        float *out = blockIdx.y ? out1 : out0;
-        out[c] = (tmp[0][threadIdx.x] + tmp[1][threadIdx.x]) + (tmp[2][threadIdx.x] + tmp[3][threadIdx.x]);
+        float t = 0.f;
+#pragma unroll
+        for (int j = 0; j < kReduceWaves; ++j) t += tmp[j][lane];
+        (blockIdx.y ? out1 : out0)[c] = t;
     }
 }
 
@@ -575,8 +589,13 @@ hipError_t gate_bwd(const NormGateArgs &a, const NormBwdPlan &plan, hipStream_t 
         return hipGetLastError();
     }
     return with_team<IO>(t, [&](auto v, auto tps, auto nv) {
-        hipLaunchKernelGGL((k_norm_gate_bwd<IO, v(), tps(), nv()>), dim3(blocks_of(int64_t(ngroups) * plan.slices, kBlock / tps())),
-                           dim3(kBlock), 0, stream, x, z, a.w, dy, dx, dz, part, a.rows, a.D, a.group, plan.slices, a.eps, a.gate_first);
+        const dim3 grid(blocks_of(int64_t(ngroups) * plan.slices, kBlock / tps()));
+        if (a.gate_first)
+            hipLaunchKernelGGL((k_norm_gate_bwd<IO, true, v(), tps(), nv()>), grid, dim3(kBlock), 0, stream, x, z, a.w, dy, dx, dz, part,
+                               a.rows, a.D, a.group, plan.slices, a.eps);
+        else
+            hipLaunchKernelGGL((k_norm_gate_bwd<IO, false, v(), tps(), nv()>), grid, dim3(kBlock), 0, stream, x, z, a.w, dy, dx, dz, part,
+                               a.rows, a.D, a.group, plan.slices, a.eps);
         return hipGetLastError();
     });
 }
@@ -621,7 +640,7 @@ hipError_t add_bwd(const NormAddArgs &a, const NormBwdPlan &plan, hipStream_t st
 }
 
 hipError_t reduce(const float *part, float *out0, float *out1, int slices, int D, hipStream_t stream) {
-    hipLaunchKernelGGL(k_norm_reduce, dim3((D + 63) / 64, out1 ? 2 : 1), dim3(kBlock), 0, stream, part, out0, out1, slices, D);
+    hipLaunchKernelGGL(k_norm_reduce, dim3((D + 63) / 64, out1 ? 2 : 1), dim3(64 * kReduceWaves), 0, stream, part, out0, out1, slices, D);
     return hipGetLastError();
 }
 
@@ -632,8 +651,8 @@ NormBwdPlan plan_norm_bwd(int64_t rows, int D, int group, int params, bool bf16)
     if (rows <= 0) return p;
     const Team t = pick_team(group, bf16);
     const int ngroups = D / group, teams = t.nv ? kBlock / t.tps : 1;
-    // 512 blocks (two per CU): enough loads in flight, and few partials to add up
-    const int64_t want = (int64_t(512) * teams + ngroups - 1) / ngroups;
+    // enough blocks for the loads in flight, few enough for the partials to add up
+    const int64_t want = (int64_t(kBwdBlocks) * teams + ngroups - 1) / ngroups;
     p.slices = int(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(rows, 32768), want)));
     p.total = size_t(params) * p.slices * D * sizeof(float);
     return p;

@@ -3,7 +3,7 @@
 
 da, dbeta and d_init are carried in 32 bits in both types.  With bfloat16, dq, dk and dv
 are rounded once; the states and dv enter dq and dk rounded to bfloat16 as stored, each
-once per product: up to 4 roundings.  da is a sum over up to 256 tokens of differences of
+once per product: up to 4 roundings.  da is a sum over up to 128 tokens of differences of
 terms whose errors are those of 32-bit sums; it is compared with the terms' size.
 """
 import math
@@ -26,7 +26,7 @@ def cpu(c):
 
 def gate_terms(c, scale):
     """2-norm, per token, of what da's formula adds up: y . dy and v . dv of the tokens up to
-    256 further on, and <dS, S> at the segment's end, each with its elements' absolute values."""
+    128 further on, and <dS, S> at the segment's end, each with its elements' absolute values."""
     x = cpu(c)
     y, states = delta.delta_f64(*inputs_of(x), scale, x["init_state"])
     dv = delta.delta_grads_f64(*inputs_of(x), scale, x["dy"], x["init_state"], x["d_final"])[2]
@@ -35,7 +35,7 @@ def gate_terms(c, scale):
     L = y.shape[1]
     out = torch.zeros_like(per_token)
     for t in range(L):
-        out[:, t] = per_token[:, t:min(L, t + 256)].sum(1) + end
+        out[:, t] = per_token[:, t:min(L, t + 128)].sum(1) + end
     return float(out.sum().sqrt())
 
 
@@ -57,7 +57,7 @@ def check(c, scale, L, N, dtype, amplified=1.0):
     return got
 
 
-# lengths of one, about the chunk (64) and the segment (256) and beyond; heads per group;
+# lengths of one, about the chunk (64) and the segment (128) and beyond; heads per group;
 # head sizes that blocks of 32 and 64 rows do not divide; every state width
 CASES = [(1, 1, 1, 1, 16, 32), (2, 5, 4, 2, 16, 32), (1, 63, 2, 1, 32, 64), (1, 64, 2, 2, 64, 64), (2, 65, 3, 1, 48, 64), (1, 130, 4, 2, 64, 128),
          (1, 200, 2, 1, 128, 128), (1, 256, 1, 1, 16, 32), (1, 257, 2, 1, 80, 32), (2, 330, 2, 1, 32, 64), (1, 100, 5, 5, 96, 32), (1, 90, 6, 1, 16, 64)]
