@@ -41,6 +41,12 @@ COMMON_FLAGS = [
 ]
 
 
+# matrix products of the chains keep their accumulators in the registers the vector
+# instructions between them use (the heuristic's other choice copies them back and forth)
+SOURCE_FLAGS = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+                for src in ("ssd_delta_chunk.hip", "ssd_delta_bwd.hip")}
+
+
 def _hipcc() -> str:
     for cand in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc")):
         if cand and os.path.exists(cand):
@@ -67,7 +73,7 @@ def _resources(stderr: str) -> list[dict]:
 
 def _compile(src: str) -> tuple[str, list[dict]]:
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [_hipcc(), *COMMON_FLAGS, "-Rpass-analysis=kernel-resource-usage", "-c",
+    cmd = [_hipcc(), *COMMON_FLAGS, *SOURCE_FLAGS.get(src, []), "-Rpass-analysis=kernel-resource-usage", "-c",
            os.path.join(CSRC, src), "-o", obj]
     proc = subprocess.run(cmd, capture_output=True, text=True)
     if proc.returncode != 0:

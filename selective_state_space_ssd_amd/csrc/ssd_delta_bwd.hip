@@ -25,16 +25,14 @@
 namespace ssd {
 namespace {
 
-constexpr int kW = 4;       // waves per chain block
-
-// Sums over a chain wave's 16 rows, per token: fp32 [nc][P / 16][64] each.
+// Sums over 16 rows of the state, per token: fp32 [nc][P / 16][64] each.
 struct BackSums {
     float *xe, *vdv;
-    float *lam;         // [P / 16][segments]: <dS, S> at the end of each segment
+    float *lam;         // [P / 16][segments][X]: <dS, S> at the end of each segment, in parts
 };
 
-// Kernel 3.
-template <typename IO, int N, int W>
+// Kernel 3.  Waves, tiles and LDS as in the forward chain; dy is read by every wave.
+template <typename IO, int N, int W, int X>
 __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restrict__ qg, const IO *__restrict__ kg,
                                                              const IO *__restrict__ vg, const IO *__restrict__ dyg,
                                                              const char *__restrict__ images, const float *__restrict__ d_final,
@@ -42,97 +40,117 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
                                                              IO *__restrict__ dvg, IO *__restrict__ dSg,
                                                              float *__restrict__ d_init, BackSums sums, int L, int H, int P,
                                                              int G, int nc, int pblocks, float scale) {
-    using T = ChainTile<IO, N, W, true>;
-    using Img = typename T::Img;
     using Pl = DeltaPlanes<true>;
+    using T = ChainLds<IO, N, W, X, Pl::kQ, false>;
+    using Img = typename T::Img;
     extern __shared__ __align__(16) char lds[];
-    constexpr int KS = N / 32, kSz = int(sizeof(IO));
+    constexpr int kSz = int(sizeof(IO)), KS = N / 32 / X, NT = 2 * KS;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
-    const int pb = blockIdx.x % pblocks, bh = blockIdx.x / pblocks;
+    const int x = w % X, n0 = x * KS;
+    const int blk = xcd_neighbours(), pb = blk % pblocks, bh = blk / pblocks;
     const int h = bh % H, bi = bh / H, g = h / (H / G);
-    const int p0 = (pb * W + w) * 16, p = p0 + c, ptiles = P / 16, segs = (nc + kSegment<IO> - 1) / kSegment<IO>;
+    const int p0 = (pb * (W / X) + w / X) * 16, p = p0 + c, ptiles = P / 16, segs = (nc + kSegment<IO> - 1) / kSegment<IO>;
     const bool live = p0 < P;
     const size_t hp = size_t(H) * P, gn = size_t(G) * N;
     const char *img = images + size_t(bh) * nc * Img::kBytes;
     const IO *k0 = kg + size_t(bi) * L * gn + size_t(g) * N, *q0 = qg + size_t(bi) * L * gn + size_t(g) * N;
-    const IO *y0 = dyg + size_t(bi) * L * hp + size_t(h) * P + size_t(pb) * W * 16;
-    const int ychunks = min(16 * W, P - pb * W * 16) * kSz / 16;
+    const size_t vy0 = size_t(bi) * L * hp + size_t(h) * P;
     const uint32_t lds0 = lds_address(lds), tok = uint32_t(hp) * kSz;
+    char *xe = lds + T::kE + w * 4096;
 
     auto fetch = [&](int ch, uint32_t buf, auto part) {
         constexpr int kPart = decltype(part)::value;
         const int t0 = ch * kC, last = min(kC, L - t0) - 1;
         copy_rows<T::RB, kC, W, kPart, 4>(k0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf);
-        copy_rows<T::RB, kC, W, kPart, 4>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf + T::kQt);
-        copy_rows<T::RV, kC, W, kPart, 4>(y0 + size_t(t0) * hp, tok, last, ychunks, buf + T::kVt);
         copy_image<Img::kBytes, W, kPart, 4>(img + size_t(ch) * Img::kBytes, buf + T::kImg);
+        if constexpr (T::kQMain) copy_rows<T::RB, kC, W, kPart, 4>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf + T::kRows);
     };
-    auto fetch_all = [&](int ch, uint32_t buf) {
+    auto fetch_q = [&](int ch) {
+        if constexpr (T::kQMain) return;
+        const int t0 = ch * kC, last = min(kC, L - t0) - 1;
+        copy_rows<T::RB, kC, W, 0, 1>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, lds0 + T::kQt);
+    };
+    auto fetch_main = [&](int ch, uint32_t buf) {
         fetch(ch, buf, std::integral_constant<int, 0>{});
         fetch(ch, buf, std::integral_constant<int, 1>{});
         fetch(ch, buf, std::integral_constant<int, 2>{});
         fetch(ch, buf, std::integral_constant<int, 3>{});
     };
-
-    f32x4 S[N / 16];        // dS
+    // dy of chunk ch, accumulator layout; 0 past the sequence
+    IO ry[16];
+    auto fetch_dy = [&](int ch) {
+        if (!live) return;
+        const int t0 = ch * kC;
+        const __amdgpu_buffer_rsrc_t view = chunk_view(dyg + vy0 + size_t(t0) * hp, min(kC, L - t0), tok, P);
+        const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
 #pragma unroll
-    for (int t = 0; t < N / 16; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ry[4 * t + r] = load_checked<IO>(view, off + uint32_t(32 * (t >> 1) + 4 * (t & 1) + r) * tok);
+    };
+    auto dy_of = [&](int t) {
+        return f32x4{to_f32<IO>(ry[4 * t]), to_f32<IO>(ry[4 * t + 1]), to_f32<IO>(ry[4 * t + 2]), to_f32<IO>(ry[4 * t + 3])};
+    };
+    // of the 4 token tiles this wave finishes kOwn, from its x'th on
+    constexpr int kOwn = 4 / X;
+    auto own = [&](const f32x4 (&a)[4], int i) {
+        f32x4 v = a[i];
+#pragma unroll
+        for (int o = 1; o < X; ++o)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = x == o ? float(a[o * kOwn + i][r]) : float(v[r]);
+        return v;
+    };
+    auto state_at = [&](int t) { return (size_t(bh) * P + p) * N + 32 * (n0 + (t >> 1)) + 8 * q + 4 * (t & 1); };
+
+    f32x4 S[NT];        // dS
+#pragma unroll
+    for (int t = 0; t < NT; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (d_final && live)
 #pragma unroll
-        for (int t = 0; t < N / 16; ++t)
-            S[t] = *reinterpret_cast<const f32x4 *>(d_final + (size_t(bh) * P + p) * N + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
-    fetch_all(nc - 1, lds0);
+        for (int t = 0; t < NT; ++t) S[t] = *reinterpret_cast<const f32x4 *>(d_final + state_at(t));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ry[i] = IO(0);
+    fetch_main(nc - 1, lds0);
+    fetch_q(nc - 1);
+    fetch_dy(nc - 1);
     copies_done();
     __syncthreads();
 
     for (int i = 0; i < nc; ++i) {
-        const int ch = nc - 1 - i, t0 = ch * kC, rows = min(kC, L - t0);
-        const char *buf = lds + (T::kBufs == 2 ? (i & 1) * T::kBytes : 0);
-        auto ahead = [&](auto part) {       // past the first chunk: that one again
-            if constexpr (T::kBufs == 2) fetch(max(ch - 1, 0), lds0 + ((i + 1) & 1) * T::kBytes, part);
+        const int ch = nc - 1 - i, t0 = ch * kC, rows = min(kC, L - t0), next = max(ch - 1, 0);   // past the first: that one again
+        const char *buf = lds + (T::kBufs == 2 ? (i & 1) * T::kMain : 0);
+        const char *tk = buf, *tq = T::kQMain ? buf + T::kRows : lds + T::kQt, *tm = buf + T::kImg + Img::kM, *ts = buf + T::kImg + Img::kQ;
+        const float *gates = reinterpret_cast<const float *>(buf + T::kImg + Img::kGates);
+        const size_t unit = size_t(bh) * nc + ch;
+        auto ahead = [&](auto part) {
+            if constexpr (T::kBufs == 2) fetch(next, lds0 + ((i + 1) & 1) * T::kMain, part);
         };
-        f32x4 dv[4];
-        f32x4 xe[4], vd[4];
+        auto gate_of = [&](int which, int t) {
+            return *reinterpret_cast<const f32x4 *>(gates + which * kC + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
+        };
         if (live) {
-            const char *tk = buf, *tq = buf + T::kQt, *tm = buf + T::kImg + Img::kM, *ts = buf + T::kImg + Img::kQ;
-            const float *gates = reinterpret_cast<const float *>(buf + T::kImg + Img::kGates);
-            const size_t unit = size_t(bh) * nc + ch;
-            // what the end of the chunk needs, asked for first
-            f32x4 Ev[4];
-            IO rv[16];
-            {
-                const f32x4 *src = E + (unit * ptiles + p0 / 16) * 256 + lane;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) Ev[t] = src[64 * t];
-                const __amdgpu_buffer_rsrc_t view = buffer_rsrc(vg + (size_t(bi) * L + t0) * hp + size_t(h) * P, uint32_t(rows - 1) * tok + uint32_t(P) * kSz);
-                const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int at = int(off + uint32_t(32 * (t >> 1) + 4 * (t & 1) + r) * tok);
-                        if constexpr (kSz == 4) rv[4 * t + r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(view, at, 0, 0));
-                        else rv[4 * t + r] = __builtin_amdgcn_raw_buffer_load_b16(view, at, 0, 0);
-                    }
-            }
             if (ch % kSegment<IO> == kSegment<IO> - 1 || ch == nc - 1) {
                 const size_t at = (size_t(bh) * ptiles + p0 / 16) * segs + ch / kSegment<IO>;
-                const f32x4 *src = anchor + at * (N / 16) * 64 + lane;
+                const f32x4 *a0 = anchor + (at * (N / 16) + x * NT) * 64 + lane;
                 float dot = 0.f;
 #pragma unroll
-                for (int t = 0; t < N / 16; ++t) {
-                    const f32x4 a = src[64 * t];
+                for (int t = 0; t < NT; ++t) {
+                    const f32x4 a = a0[64 * t];
                     dot += S[t][0] * a[0] + S[t][1] * a[1] + S[t][2] * a[2] + S[t][3] * a[3];
                 }
                 dot = wave_sum(dot);
-                if (lane == 0) sums.lam[at] = dot;
+                if (lane == 0) sums.lam[at * X + x] = dot;
             }
-            ahead(std::integral_constant<int, 0>{});
+        }
+        f32x4 dU[4], dv[4], xs[kOwn], vd[kOwn], Ev[kOwn];
+        IO rv[4 * kOwn];
+        if (live) {
             Op<IO, Pl::kS> so[KS];
 #pragma unroll
             for (int s = 0; s < KS; ++s) so[s] = to_op<IO, Pl::kS>(S[2 * s], S[2 * s + 1]);
             {
-                IO *dst = dSg + (unit * P + p) * N + 8 * q;
+                IO *dst = dSg + (unit * P + p) * N + 32 * n0 + 8 * q;
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
                     if constexpr (kSz == 4) {
@@ -143,53 +161,61 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
                     }
                 }
             }
-            f32x4 fs[4], te[4], bt[4], dy[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const float *at = gates + 32 * (t >> 1) + 8 * q + 4 * (t & 1);
-                fs[t] = *reinterpret_cast<const f32x4 *>(at);
-                te[t] = *reinterpret_cast<const f32x4 *>(at + kC);
-                bt[t] = *reinterpret_cast<const f32x4 *>(at + 2 * kC);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {   // rows past the sequence hold its last one: not theirs
-                    const int row = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + r, col = (16 * w + c) * kSz;
-                    const float d = to_f32<IO>(*reinterpret_cast<const IO *>(buf + T::kVt + row * T::RV + (((col >> 4) ^ place<T::RV>(row)) << 4) + (col & 15)));
-                    dy[t][r] = row < rows ? d : 0.f;
-                }
-            }
-            // dU = e^{g_C - g} K dS^T + scores^T dY
-            f32x4 dU[4];
+            // this wave's part of dU = e^{g_C - g} K dS^T + scores^T dY: its columns of dS, and
+            // token half x of dY (both halves with one wave, none for waves past the second)
 #pragma unroll
             for (int t = 0; t < 4; ++t) dU[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 Op<IO, 1> a[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tk, 0, tile_row(t >> 1, t & 1, c), ks, q);
+                for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tk, 0, tile_row(t >> 1, t & 1, c), n0 + ks, q);
                 mma(dU, a, so[ks]);
             }
-            ahead(std::integral_constant<int, 1>{});
 #pragma unroll
-            for (int t = 0; t < 4; ++t) dU[t] *= te[t];
-            {
+            for (int t = 0; t < 4; ++t) dU[t] *= gate_of(1, t);
+            if (X == 1 || x == 1) {
                 Op<IO, Pl::kQ> a[4];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) a[t] = tri_col<IO, Pl::kQ>(ts, 1, t >> 1, t & 1, c, q);
-                mma(dU, a, to_op<IO, 1>(dy[2], dy[3]));
+                mma(dU, a, to_op<IO, 1>(dy_of(2), dy_of(3)));
             }
-            {
+            if (x == 0) {
                 f32x4 upper[2] = {dU[0], dU[1]};
                 Op<IO, Pl::kQ> a[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) a[e] = tri_col<IO, Pl::kQ>(ts, 0, 0, e, c, q);
-                mma(upper, a, to_op<IO, 1>(dy[0], dy[1]));
+                mma(upper, a, to_op<IO, 1>(dy_of(0), dy_of(1)));
                 dU[0] = upper[0];
                 dU[1] = upper[1];
             }
+            if constexpr (X > 1)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) reinterpret_cast<f32x4 *>(xe)[64 * t + lane] = dU[t];
+        }
+        if constexpr (X > 1) {
+            copies_done();      // q, asked for at the chunk's beginning
+            __syncthreads();    // and the parts are written
+        }
+        if (live) {     // what the end of the chunk needs: E and v of this wave's token tiles
+            const f32x4 *src = E + (unit * ptiles + p0 / 16) * 256 + lane;
+            const __amdgpu_buffer_rsrc_t view = chunk_view(vg + vy0 + size_t(t0) * hp, rows, tok, P);
+            const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) {
+                const int t = x * kOwn + j;
+                Ev[j] = src[64 * t];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) rv[4 * j + r] = load_checked<IO>(view, off + uint32_t(32 * (t >> 1) + 4 * (t & 1) + r) * tok);
+            }
+        }
+        ahead(std::integral_constant<int, 0>{});
+        ahead(std::integral_constant<int, 1>{});
+        if (live) {
+            if constexpr (X > 1) sum_of_parts<X>(lds + T::kE + (w - x) * 4096, lane, dU);
             // X = dU + M^T (beta dU), in place
-            const Op<IO, Pl::kM> br0 = to_op<IO, Pl::kM>(bt[0] * dU[0], bt[1] * dU[1]);
-            const Op<IO, Pl::kM> br1 = to_op<IO, Pl::kM>(bt[2] * dU[2], bt[3] * dU[3]);
-            ahead(std::integral_constant<int, 2>{});
+            const Op<IO, Pl::kM> br0 = to_op<IO, Pl::kM>(gate_of(2, 0) * dU[0], gate_of(2, 1) * dU[1]);
+            const Op<IO, Pl::kM> br1 = to_op<IO, Pl::kM>(gate_of(2, 2) * dU[2], gate_of(2, 3) * dU[3]);
             {
                 Op<IO, Pl::kM> a[4];
 #pragma unroll
@@ -206,81 +232,85 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
                 dU[1] = upper[1];
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) dv[t] = bt[t] * dU[t];
+            for (int t = 0; t < 4; ++t) dv[t] = gate_of(2, t) * dU[t];
+        }
+        ahead(std::integral_constant<int, 2>{});
+        ahead(std::integral_constant<int, 3>{});
+        if (live) {
             // dS <- e^{g_C} dS + Q^T (scale e^g dY) - K^T (e^g dv)
-            Op<IO, Pl::kS> oq[2], ok[2];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                oq[s] = to_op<IO, Pl::kS>(scale * fs[2 * s] * dy[2 * s], scale * fs[2 * s + 1] * dy[2 * s + 1]);
-                ok[s] = to_op<IO, Pl::kS>(-fs[2 * s] * dv[2 * s], -fs[2 * s + 1] * dv[2 * s + 1]);
-            }
-            ahead(std::integral_constant<int, 3>{});
             const float alpha = gates[kC - 1];
 #pragma unroll
-            for (int t = 0; t < N / 16; ++t) S[t] *= alpha;
+            for (int t = 0; t < NT; ++t) S[t] *= alpha;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
+            for (int ks = 0; ks < 2; ++ks) {
+                const f32x4 f0 = gate_of(0, 2 * ks), f1 = gate_of(0, 2 * ks + 1);
+                const Op<IO, Pl::kS> oq = to_op<IO, Pl::kS>(scale * f0 * dy_of(2 * ks), scale * f1 * dy_of(2 * ks + 1));
+                const Op<IO, Pl::kS> ok = to_op<IO, Pl::kS>(-f0 * dv[2 * ks], -f1 * dv[2 * ks + 1]);
+                if (ks == 1) fetch_dy(next);
 #pragma unroll
-                for (int u0 = 0; u0 < N / 16; u0 += 4) {
-                    constexpr int NT = N / 16 < 4 ? N / 16 : 4;
-                    f32x4 z[NT];
-                    Op<IO, 1> a[NT], b[NT];
+                for (int u0 = 0; u0 < NT; u0 += 4) {
+                    constexpr int M = NT < 4 ? NT : 4;
+                    f32x4 z[M];
+                    Op<IO, 1> a[M], b[M];
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
+                    for (int t = 0; t < M; ++t) {
                         z[t] = S[u0 + t];
-                        a[t] = read_col<IO, 1, T::RB>(tq, 0, 32 * ks, 32 * ((u0 + t) >> 1), t & 1, c, q);
-                        b[t] = read_col<IO, 1, T::RB>(tk, 0, 32 * ks, 32 * ((u0 + t) >> 1), t & 1, c, q);
+                        a[t] = read_col<IO, 1, T::RB>(tq, 0, 32 * ks, 32 * (n0 + ((u0 + t) >> 1)), t & 1, c, q);
+                        b[t] = read_col<IO, 1, T::RB>(tk, 0, 32 * ks, 32 * (n0 + ((u0 + t) >> 1)), t & 1, c, q);
                     }
-                    mma(z, a, oq[ks]);
-                    mma(z, b, ok[ks]);
+                    mma(z, a, oq);
+                    mma(z, b, ok);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) S[u0 + t] = z[t];
-                    if constexpr (kSz == 4) __builtin_amdgcn_sched_barrier(0);     // 128 columns: no registers to read ahead
+                    for (int t = 0; t < M; ++t) S[u0 + t] = z[t];
+                    if constexpr (kSz == 4) __builtin_amdgcn_sched_barrier(0);     // no registers to read ahead
                 }
-            // the sums over this wave's 16 rows (the 16 lanes of a row group)
+            }
+            // the sums over the 16 rows (the 16 lanes of a row group), of this wave's token tiles
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int j = 0; j < kOwn; ++j) {
+                const f32x4 du = own(dU, j), dvj = own(dv, j);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    xe[t][r] = row16_sum(dU[t][r] * Ev[t][r]);
-                    vd[t][r] = row16_sum(dv[t][r] * to_f32<IO>(rv[4 * t + r]));
+                    xs[j][r] = row16_sum(du[r] * Ev[j][r]);
+                    vd[j][r] = row16_sum(dvj[r] * to_f32<IO>(rv[4 * j + r]));
                 }
-        } else {
-            ahead(std::integral_constant<int, 0>{});
-            ahead(std::integral_constant<int, 1>{});
-            ahead(std::integral_constant<int, 2>{});
-            ahead(std::integral_constant<int, 3>{});
+            }
         }
         if constexpr (T::kBufs == 1) {
             __syncthreads();
-            if (ch > 0) fetch_all(ch - 1, lds0);
+            if (ch > 0) {
+                fetch_main(ch - 1, lds0);
+                fetch_q(ch - 1);
+            }
         }
         copies_done();
         __syncthreads();
+        if constexpr (T::kBufs == 2) fetch_q(next);     // this chunk's is read
         if (live) {
-            const size_t at = ((size_t(bh) * nc + ch) * ptiles + p0 / 16) * kC + 8 * q;
-            if (c == 0)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    *reinterpret_cast<f32x4 *>(sums.xe + at + 32 * (t >> 1) + 4 * (t & 1)) = xe[t];
-                    *reinterpret_cast<f32x4 *>(sums.vdv + at + 32 * (t >> 1) + 4 * (t & 1)) = vd[t];
-                }
-            const __amdgpu_buffer_rsrc_t view = buffer_rsrc(dvg + (size_t(bi) * L + t0) * hp + size_t(h) * P, uint32_t(rows - 1) * tok + uint32_t(P) * kSz);
+            const size_t at = (unit * ptiles + p0 / 16) * kC + 8 * q;
+            const __amdgpu_buffer_rsrc_t view = chunk_view(dvg + vy0 + size_t(t0) * hp, rows, tok, P);
             const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int j = 0; j < kOwn; ++j) {
+                const int t = x * kOwn + j, row = 32 * (t >> 1) + 4 * (t & 1);
+                const f32x4 dvj = own(dv, j);
+                if (c == 0) {
+                    *reinterpret_cast<f32x4 *>(sums.xe + at + row) = xs[j];
+                    *reinterpret_cast<f32x4 *>(sums.vdv + at + row) = vd[j];
+                }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int o = int(off + uint32_t(32 * (t >> 1) + 4 * (t & 1) + r) * tok);
-                    if constexpr (kSz == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dv[t][r]), view, o, 0, 0);
-                    else __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(dv[t][r]), view, o, 0, 0);
+                    const int o = int(off + uint32_t(row + r) * tok);
+                    if constexpr (kSz == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dvj[r]), view, o, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(dvj[r]), view, o, 0, 0);
                 }
+            }
         }
     }
+    copies_done();      // of the last chunk's q, asked for once more
     if (d_init && live)
 #pragma unroll
-        for (int t = 0; t < N / 16; ++t)
-            *reinterpret_cast<f32x4 *>(d_init + (size_t(bh) * P + p) * N + 32 * (t >> 1) + 8 * q + 4 * (t & 1)) = S[t];
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(d_init + state_at(t)) = S[t];
 }
 
 // Kernel 4.  Block = (batch, chunk, group); wave w holds dq^T and dk^T of 16 tokens (tile
@@ -306,7 +336,7 @@ __global__ __launch_bounds__(256, (2 * GradTile<IO, N>::kLds <= 159 * 1024 && N 
                                                      const IO *__restrict__ dSg, IO *__restrict__ dqg, IO *__restrict__ dkg,
                                                      int L, int H, int P, int G, int nc, float scale) {
     using T = GradTile<IO, N>;
-    using Img = typename ChainTile<IO, N, kW, true>::Img;
+    using Img = ChunkImage<IO, DeltaPlanes<true>::kM, DeltaPlanes<true>::kQ>;
     constexpr int kSz = T::kSz, kP = T::kP, E16 = 16 / kSz;     // elements per 16 bytes
     extern __shared__ __align__(16) char lds[];
     __shared__ double gd[kC];
@@ -348,10 +378,10 @@ __global__ __launch_bounds__(256, (2 * GradTile<IO, N>::kLds <= 159 * 1024 && N 
             // dY, dv: rows of tokens (past the end: the last one, masked below); S, dS: rows p
             const size_t src = (size_t(bi) * L + t0) * hp + size_t(h) * P + pb;
             const int pchunks = min(64, P - pb) / E16;
-            copy_rows<T::RP, kC, kW, 0, 1>(dyg + src, uint32_t(hp) * kSz, rows - 1, pchunks, lds0 + T::kY);
-            copy_rows<T::RP, kC, kW, 0, 1>(dvg + src, uint32_t(hp) * kSz, rows - 1, pchunks, lds0 + T::kV);
-            copy_rows<T::RB, kC, kW, 0, 1>(Sg + (unit * P + pb) * N, T::RB, P - pb - 1, T::RB / 16, lds0 + T::kS);
-            copy_rows<T::RB, kC, kW, 0, 1>(dSg + (unit * P + pb) * N, T::RB, P - pb - 1, T::RB / 16, lds0 + T::kD);
+            copy_rows<T::RP, kC, 4, 0, 1>(dyg + src, uint32_t(hp) * kSz, rows - 1, pchunks, lds0 + T::kY);
+            copy_rows<T::RP, kC, 4, 0, 1>(dvg + src, uint32_t(hp) * kSz, rows - 1, pchunks, lds0 + T::kV);
+            copy_rows<T::RB, kC, 4, 0, 1>(Sg + (unit * P + pb) * N, T::RB, P - pb - 1, T::RB / 16, lds0 + T::kS);
+            copy_rows<T::RB, kC, 4, 0, 1>(dSg + (unit * P + pb) * N, T::RB, P - pb - 1, T::RB / 16, lds0 + T::kD);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {       // U = beta E, from wave w's chain tile: column p, 4 tokens a lane
                 const int t = i, row = 32 * (t >> 1) + 8 * q + 4 * (t & 1), col = (16 * w + c) * kSz;
@@ -426,8 +456,8 @@ __global__ __launch_bounds__(256, (2 * GradTile<IO, N>::kLds <= 159 * 1024 && N 
     __syncthreads();
     // k and q into LDS, W [i][j] and G [i][j] = G [j][i] beside them
     const size_t src = (size_t(bi) * L + t0) * gn + size_t(g) * N;
-    copy_rows<T::RB, kC, kW, 0, 1>(kg + src, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kK);
-    copy_rows<T::RB, kC, kW, 0, 1>(qg + src, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kQ);
+    copy_rows<T::RB, kC, 4, 0, 1>(kg + src, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kK);
+    copy_rows<T::RB, kC, 4, 0, 1>(qg + src, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kQ);
     auto put = [&](char *m, int row, int col, float v) {
         char *dst = m + row * T::RP + (((col * kSz >> 4) ^ place<T::RP>(row)) << 4) + (col * kSz & 15);
         if constexpr (kSz == 4) {
@@ -496,7 +526,7 @@ template <int SEG>
 __global__ __launch_bounds__(64 * SEG) void k_delta_gates(const float *__restrict__ ydy, const float *__restrict__ vdv,
                                                                const float *__restrict__ xe, const float *__restrict__ lam,
                                                                float *__restrict__ da, float *__restrict__ dbeta, int L, int H,
-                                                               int nc, int ptiles, int segs) {
+                                                               int nc, int ptiles, int segs, int parts) {
     __shared__ double total[SEG];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int seg = blockIdx.x % segs, bh = blockIdx.x / segs, h = bh % H, bi = bh / H;
@@ -505,8 +535,9 @@ __global__ __launch_bounds__(64 * SEG) void k_delta_gates(const float *__restric
     float b = 0.f;
     if (ch < nc)
         for (int i = 0; i < ptiles; ++i) {
-            const size_t at = ((size_t(bh) * nc + ch) * ptiles + i) * kC + lane;
-            d += double(ydy[at]) - double(vdv[at]);
+            const size_t unit = size_t(bh) * nc + ch, at = (unit * ptiles + i) * kC + lane;
+            for (int x = 0; x < parts; ++x) d += double(ydy[((unit * parts + x) * ptiles + i) * kC + lane]);
+            d -= double(vdv[at]);
             b += xe[at];
         }
     if (t >= L) d = 0.0;
@@ -518,7 +549,8 @@ __global__ __launch_bounds__(64 * SEG) void k_delta_gates(const float *__restric
     if (lane == 0) total[w] = d;
     __syncthreads();
     for (int i = w + 1; i < SEG; ++i) d += total[i];
-    for (int i = 0; i < ptiles; ++i) d += double(lam[(size_t(bh) * ptiles + i) * segs + seg]);
+    for (int i = 0; i < ptiles; ++i)
+        for (int x = 0; x < parts; ++x) d += double(lam[((size_t(bh) * ptiles + i) * segs + seg) * parts + x]);
     if (ch < nc && t < L) {
         const size_t at = (size_t(bi) * L + t) * H + h;
         da[at] = float(d);
@@ -529,7 +561,6 @@ __global__ __launch_bounds__(64 * SEG) void k_delta_gates(const float *__restric
 template <typename IO, int N>
 hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t stream) {
     using Pl = DeltaPlanes<true>;
-    using T = ChainTile<IO, N, kW, true>;
     const int nc = (a.L + kC - 1) / kC, segs = (nc + kSegment<IO> - 1) / kSegment<IO>, ptiles = a.P / 16;
     char *ws = static_cast<char *>(a.workspace);
     char *images = ws;
@@ -543,20 +574,27 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
 
     hipError_t e = launch_delta_prep<IO, N, Pl::kM, Pl::kQ>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
     if (e != hipSuccess) return e;
-    const int pblocks = (a.P + 16 * kW - 1) / (16 * kW);
-    const dim3 grid(unsigned(a.b * a.H * pblocks));
-    auto chain = k_delta_chain<IO, N, kW, true>;
-    e = hipFuncSetAttribute(reinterpret_cast<const void *>(chain), hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(chain, grid, dim3(64 * kW), T::kLds, stream, q, k, v, images, a.init_state, nullptr, nullptr, dy, saved, a.L, a.H,
-                       a.P, a.G, nc, pblocks, a.scale);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    auto back = k_delta_chain_back<IO, N, kW>;
-    e = hipFuncSetAttribute(reinterpret_cast<const void *>(back), hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(back, grid, dim3(64 * kW), T::kLds, stream, q, k, v, dy, images, a.d_final, reinterpret_cast<const f32x4 *>(saved.E),
-                       reinterpret_cast<const f32x4 *>(saved.anchor), dv, dS, a.d_init, sums, a.L, a.H, a.P, a.G, nc, pblocks, a.scale);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    int parts = 1;
+    auto chains = [&](auto w_, auto x_) {
+        constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
+        constexpr int lds = ChainLds<IO, N, W, X, Pl::kQ, false>::kBytes;
+        const int per = 16 * W / X, pblocks = (a.P + per - 1) / per;
+        const dim3 grid(unsigned(a.b * a.H * pblocks));
+        parts = X;
+        auto chain = k_delta_chain<IO, N, W, X, true>;
+        e = hipFuncSetAttribute(reinterpret_cast<const void *>(chain), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(chain, grid, dim3(64 * W), lds, stream, q, k, v, images, a.init_state, nullptr, nullptr, dy, saved, a.L, a.H,
+                           a.P, a.G, nc, pblocks, a.scale);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        auto back = k_delta_chain_back<IO, N, W, X>;
+        e = hipFuncSetAttribute(reinterpret_cast<const void *>(back), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(back, grid, dim3(64 * W), lds, stream, q, k, v, dy, images, a.d_final, reinterpret_cast<const f32x4 *>(saved.E),
+                           reinterpret_cast<const f32x4 *>(saved.anchor), dv, dS, a.d_init, sums, a.L, a.H, a.P, a.G, nc, pblocks, a.scale);
+        return hipGetLastError();
+    };
+    if ((e = with_chain_shape<IO, N>(a.b, a.H, a.P, chains)) != hipSuccess) return e;
     auto grads = k_delta_grads<IO, N>;
     constexpr int lds = GradTile<IO, N>::kLds;
     e = hipFuncSetAttribute(reinterpret_cast<const void *>(grads), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -566,7 +604,7 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
                        static_cast<IO *>(a.dk), a.L, a.H, a.P, a.G, nc, a.scale);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL((k_delta_gates<kSegment<IO>>), dim3(unsigned(int64_t(a.b) * a.H * segs)), dim3(64 * kSegment<IO>), 0, stream, saved.ydy, sums.vdv, sums.xe,
-                       sums.lam, a.da, a.dbeta, a.L, a.H, nc, ptiles, segs);
+                       sums.lam, a.da, a.dbeta, a.L, a.H, nc, ptiles, segs, parts);
     return hipGetLastError();
 }
 
@@ -589,10 +627,10 @@ DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16)
     pl.off_s = take(units * state * sz);
     pl.off_ds = take(units * state * sz);
     pl.off_anchor = take(bh * segs * state * 4);
-    pl.off_ydy = take(units * ptiles * kC * 4);
+    pl.off_ydy = take(units * kMaxShare * ptiles * kC * 4);
     pl.off_xe = take(units * ptiles * kC * 4);
     pl.off_vdv = take(units * ptiles * kC * 4);
-    pl.off_lam = take(bh * ptiles * segs * 4);
+    pl.off_lam = take(bh * ptiles * segs * kMaxShare * 4);
     pl.total = at;
     pl.supported = true;
     return pl;

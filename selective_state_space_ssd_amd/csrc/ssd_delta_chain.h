@@ -4,13 +4,20 @@
 
 #include "ssd_delta_chunk.h"
 
+#ifndef SSD_FEW
+#define SSD_FEW 256
+#endif
+#ifndef SSD_SOME
+#define SSD_SOME 512
+#endif
 namespace ssd {
 
 // What the forward chain leaves for the backward pass, per (batch, head):
 //   E       [nc][P / 16][4][64] f32x4: a wave's accumulators of the brackets, as held
 //   S       [nc][P][N] io: the state that enters each chunk
-//   anchor  [P / 16][segments][N / 16][64] f32x4: the state after each segment of chunks
-//   ydy     [nc][P / 16][64] fp32: y . dy of each token over the wave's 16 rows
+//   anchor  [P / 16][segments][N / 16][64] f32x4: the state after each segment of chunks,
+//           as held
+//   ydy     [nc][X][P / 16][64] fp32: parts of y . dy of each token over 16 rows, to be added
 // Chunks per segment.  The gate gradients' error grows with the root of it: da of the
 // 4 x 2048-token layer 5.3e-7 of its norm with 1, 1.05e-6 with 4, which saves 47 of 725 us.
 // In fp32 the anchors cost nothing measurable.
@@ -34,19 +41,26 @@ struct DeltaPlanes {
     static constexpr int kS = 3, kM = 3, kQ = SAVE ? 3 : 2;
 };
 
-// LDS buffer of one chunk: k, q, the block's 16 W columns of v, the image.
-template <typename IO, int N, int W, bool SAVE>
-struct ChainTile {
-    using Pl = DeltaPlanes<SAVE>;
-    using Img = ChunkImage<IO, Pl::kM, Pl::kQ>;
+// A block's W waves are W / X tiles of 16 state rows, each shared by X waves that hold
+// N / X of its columns.  The sums over all columns (K S^T, Q S^T) are added up through LDS;
+// what only depends on those is computed by every one of the X waves, bit for bit alike.
+// Sharing shortens a chunk's steps where there are fewer tiles than SIMDs.
+//
+// LDS: k, M, the scores and gates of two chunks, the next one's copied in meanwhile (one
+// chunk where two do not fit).  With X = 1 q beside them; with more, q of one chunk, which is
+// done with halfway through it, and the exchanged sums (YX: those of Q S^T too).
+template <typename IO, int N, int W, int X, int NQ, bool YX>
+struct ChainLds {
+    using Img = ChunkImage<IO, 3, NQ>;
     static constexpr int kSz = int(sizeof(IO));
     static constexpr int RB = N * kSz;                      // bytes per row of k or q
-    static constexpr int RV = 16 * W * kSz;                 // bytes per row of v
-    static constexpr int kRows = kC * RB, kVals = kC * RV;  // bytes of the tiles
-    static constexpr int kQt = kRows, kVt = 2 * kRows, kImg = 2 * kRows + kVals;
-    static constexpr int kBytes = kImg + Img::kBytes;
-    static constexpr int kBufs = 2 * kBytes <= 160 * 1024 ? 2 : 1;
-    static constexpr int kLds = kBufs * kBytes;
+    static constexpr int kRows = kC * RB;                   // bytes of such a tile
+    static constexpr bool kQMain = X == 1;                  // q beside k, in both buffers
+    static constexpr int kImg = kQMain ? 2 * kRows : kRows, kMain = kImg + Img::kBytes, kQOwn = kQMain ? 0 : kRows;
+    static constexpr int kXe = X > 1 ? W * 4096 : 0, kXy = X > 1 && YX ? W * (4096 - 4096 / X) : 0;
+    static constexpr int kBufs = 2 * kMain + kQOwn + kXe + kXy <= 160 * 1024 ? 2 : 1;
+    static constexpr int kQt = kBufs * kMain, kE = kQt + kQOwn, kY = kE + kXe, kBytes = kY + kXy;
+    static_assert(kBytes <= 160 * 1024 && N / 32 % X == 0 && W % X == 0);
 };
 
 // Start the copies of ROWS rows of RB bytes (row r at base + r * stride bytes; rows
@@ -75,7 +89,12 @@ __device__ __forceinline__ void copy_image(const char *img, uint32_t dst) {
     }
 }
 
-// 4 consecutive elements of a range-checked view; past its end: 0.
+// One element / 4 consecutive ones of a range-checked view; past its end: 0.
+template <typename IO>
+__device__ __forceinline__ IO load_checked(__amdgpu_buffer_rsrc_t v, uint32_t off) {
+    if constexpr (std::is_same_v<IO, float>) return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(v, int(off), 0, 0));
+    else return __builtin_amdgcn_raw_buffer_load_b16(v, int(off), 0, 0);
+}
 template <typename IO>
 using Raw4 = std::conditional_t<std::is_same_v<IO, float>, f32x4, u32x2>;
 template <typename IO>
@@ -94,84 +113,134 @@ __device__ __forceinline__ Raw4<IO> narrow(f32x4 v) {
     else return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
-// block = (batch, head, W * 16 rows of the state), one wave per 16 rows.  k, q, v and the
-// chunk's image go through LDS; the next chunk's are copied into the other buffer
-// meanwhile, a part of them between any two steps (one buffer where two do not fit).
+// A range-checked view of one chunk of a [b, L, H, P] tensor, from its first token's row of
+// head h on (`base`), `rows` tokens.
+template <typename IO>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_view(const IO *base, int rows, uint32_t tok, int P) {
+    return buffer_rsrc(base, uint32_t(rows - 1) * tok + uint32_t(P) * uint32_t(sizeof(IO)));
+}
+
+// The sum of the X waves' accumulators (16-byte pieces [4][64] per wave), in their order.
+template <int X>
+__device__ __forceinline__ void sum_of_parts(const char *first, int lane, f32x4 (&out)[4]) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        out[t] = reinterpret_cast<const f32x4 *>(first)[64 * t + lane];
+#pragma unroll
+        for (int x = 1; x < X; ++x) out[t] += reinterpret_cast<const f32x4 *>(first + x * 4096)[64 * t + lane];
+    }
+}
+
 // SAVE: instead of y and the final state, what the backward pass needs (dyg is read).
-template <typename IO, int N, int W, bool SAVE>
-__global__ __launch_bounds__(64 * W, (SAVE && N * int(sizeof(IO)) > 256) ? 1 : 2) void k_delta_chain(const IO *__restrict__ qg, const IO *__restrict__ kg,
+template <typename IO, int N, int W, int X, bool SAVE>
+__global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ qg, const IO *__restrict__ kg,
                                                         const IO *__restrict__ vg, const char *__restrict__ images,
                                                         const float *__restrict__ init, IO *__restrict__ yg,
                                                         float *__restrict__ fin, const IO *__restrict__ dyg,
                                                         DeltaSaved saved, int L, int H, int P, int G, int nc, int pblocks,
                                                         float scale) {
-    using T = ChainTile<IO, N, W, SAVE>;
-    using Img = typename T::Img;
     using Pl = DeltaPlanes<SAVE>;
+    using T = ChainLds<IO, N, W, X, Pl::kQ, !SAVE>;
+    using Img = typename T::Img;
     extern __shared__ __align__(16) char lds[];
-    constexpr int KS = N / 32, kSz = int(sizeof(IO));
+    constexpr int kSz = int(sizeof(IO)), KS = N / 32 / X, NT = 2 * KS;  // this wave's column blocks and tiles
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
-    const int pb = blockIdx.x % pblocks, bh = blockIdx.x / pblocks;
+    const int x = w % X, n0 = x * KS;           // first column block
+    const int blk = xcd_neighbours(), pb = blk % pblocks, bh = blk / pblocks;
     const int h = bh % H, bi = bh / H, g = h / (H / G);
-    const int p0 = (pb * W + w) * 16, p = p0 + c, ptiles = P / 16;
-    const bool live = p0 < P;       // the same for a whole wave
+    const int p0 = (pb * (W / X) + w / X) * 16, p = p0 + c, ptiles = P / 16;
+    const bool live = p0 < P;       // the same for a whole wave, and for the waves of a tile
     const size_t hp = size_t(H) * P, gn = size_t(G) * N;
     const char *img = images + size_t(bh) * nc * Img::kBytes;
     const IO *k0 = kg + size_t(bi) * L * gn + size_t(g) * N, *q0 = qg + size_t(bi) * L * gn + size_t(g) * N;
-    const IO *v0 = vg + size_t(bi) * L * hp + size_t(h) * P + size_t(pb) * W * 16;
-    const int vchunks = min(16 * W, P - pb * W * 16) * kSz / 16;
+    const size_t vy0 = size_t(bi) * L * hp + size_t(h) * P;
     const uint32_t lds0 = lds_address(lds), tok = uint32_t(hp) * kSz;
+    char *xe = lds + T::kE + w * 4096;
 
-    // the copies of chunk ch into the buffer at `buf`, in 4 parts
+    // the copies of chunk ch: k and the image into the buffer at `buf` in 4 parts; q
     auto fetch = [&](int ch, uint32_t buf, auto part) {
         constexpr int kPart = decltype(part)::value;
         const int t0 = ch * kC, last = min(kC, L - t0) - 1;
         copy_rows<T::RB, kC, W, kPart, 4>(k0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf);
-        copy_rows<T::RB, kC, W, kPart, 4>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf + T::kQt);
-        copy_rows<T::RV, kC, W, kPart, 4>(v0 + size_t(t0) * hp, tok, last, vchunks, buf + T::kVt);
         copy_image<Img::kBytes, W, kPart, 4>(img + size_t(ch) * Img::kBytes, buf + T::kImg);
+        if constexpr (T::kQMain) copy_rows<T::RB, kC, W, kPart, 4>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf + T::kRows);
     };
-    auto fetch_all = [&](int ch, uint32_t buf) {
+    auto fetch_q = [&](int ch) {
+        if constexpr (T::kQMain) return;
+        const int t0 = ch * kC, last = min(kC, L - t0) - 1;
+        copy_rows<T::RB, kC, W, 0, 1>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, lds0 + T::kQt);
+    };
+    auto fetch_main = [&](int ch, uint32_t buf) {
         fetch(ch, buf, std::integral_constant<int, 0>{});
         fetch(ch, buf, std::integral_constant<int, 1>{});
         fetch(ch, buf, std::integral_constant<int, 2>{});
         fetch(ch, buf, std::integral_constant<int, 3>{});
     };
-
-    f32x4 S[N / 16];
+    // v of chunk ch, by one wave of a tile: accumulator layout
+    IO rv[16];
+    auto fetch_v = [&](int ch) {
+        if (!live || x != 0) return;
+        const int t0 = ch * kC;
+        const __amdgpu_buffer_rsrc_t view = chunk_view(vg + vy0 + size_t(t0) * hp, min(kC, L - t0), tok, P);
+        const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
 #pragma unroll
-    for (int t = 0; t < N / 16; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) rv[4 * t + r] = load_checked<IO>(view, off + uint32_t(32 * (t >> 1) + 4 * (t & 1) + r) * tok);
+    };
+    f32x4 V[4];
+    auto take_v = [&]() {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) V[t][r] = x == 0 ? to_f32<IO>(rv[4 * t + r]) : 0.f;
+    };
+    // row p of the state, this wave's columns 32 (n0 + t / 2) + 8 q + 4 (t & 1) ..
+    auto state_at = [&](int t) { return (size_t(bh) * P + p) * N + 32 * (n0 + (t >> 1)) + 8 * q + 4 * (t & 1); };
+
+    f32x4 S[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (init && live)
 #pragma unroll
-        for (int t = 0; t < N / 16; ++t)
-            S[t] = *reinterpret_cast<const f32x4 *>(init + (size_t(bh) * P + p) * N + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
-    fetch_all(0, lds0);
+        for (int t = 0; t < NT; ++t) S[t] = *reinterpret_cast<const f32x4 *>(init + state_at(t));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) rv[i] = IO(0);
+    fetch_main(0, lds0);
+    fetch_q(0);
+    fetch_v(0);
     copies_done();
+    take_v();
     __syncthreads();
 
     for (int ch = 0; ch < nc; ++ch) {
-        const int t0 = ch * kC, rows = min(kC, L - t0);
-        const char *buf = lds + (T::kBufs == 2 ? (ch & 1) * T::kBytes : 0);
-        auto ahead = [&](auto part) {       // past the last chunk: that one again
-            if constexpr (T::kBufs == 2) fetch(min(ch + 1, nc - 1), lds0 + ((ch + 1) & 1) * T::kBytes, part);
+        const int t0 = ch * kC, rows = min(kC, L - t0), next = min(ch + 1, nc - 1);     // past the last: that one again
+        const char *buf = lds + (T::kBufs == 2 ? (ch & 1) * T::kMain : 0);
+        const char *tk = buf, *tq = T::kQMain ? buf + T::kRows : lds + T::kQt, *tm = buf + T::kImg + Img::kM, *ts = buf + T::kImg + Img::kQ;
+        const float *gates = reinterpret_cast<const float *>(buf + T::kImg + Img::kGates);
+        auto ahead = [&](auto part) {
+            if constexpr (T::kBufs == 2) fetch(next, lds0 + ((ch + 1) & 1) * T::kMain, part);
         };
-        ahead(std::integral_constant<int, 0>{});
+        auto gate_of = [&](int which, int t) {
+            return *reinterpret_cast<const f32x4 *>(gates + which * kC + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
+        };
         Raw4<IO> yo[4];
-        f32x4 E[4];
-        if (live) {
-            const char *tk = buf, *tq = buf + T::kQt, *tm = buf + T::kImg + Img::kM, *ts = buf + T::kImg + Img::kQ;
-            const float *gates = reinterpret_cast<const float *>(buf + T::kImg + Img::kGates);
-            if constexpr (SAVE) {
-                const __amdgpu_buffer_rsrc_t view = buffer_rsrc(dyg + (size_t(bi) * L + t0) * hp + size_t(h) * P, uint32_t(rows - 1) * tok + uint32_t(P) * kSz);
+        f32x4 E[4], Y[4];
+        if constexpr (SAVE)
+            if (live) {
+                const __amdgpu_buffer_rsrc_t view = chunk_view(dyg + vy0 + size_t(t0) * hp, rows, tok, P);
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     yo[t] = load4_checked<IO>(view, uint32_t(tile_row(t >> 1, t & 1, c)) * tok + uint32_t(p0 + 4 * q) * kSz);
             }
+        fetch_v(next);
+        ahead(std::integral_constant<int, 0>{});
+        if (live) {
             Op<IO, Pl::kS> so[KS];
 #pragma unroll
             for (int s = 0; s < KS; ++s) so[s] = to_op<IO, Pl::kS>(S[2 * s], S[2 * s + 1]);
             if constexpr (SAVE) {
-                IO *dst = static_cast<IO *>(saved.S) + ((size_t(bh) * nc + ch) * P + p) * N + 8 * q;
+                IO *dst = static_cast<IO *>(saved.S) + ((size_t(bh) * nc + ch) * P + p) * N + 32 * n0 + 8 * q;
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
                     if constexpr (kSz == 4) {
@@ -182,48 +251,48 @@ __global__ __launch_bounds__(64 * W, (SAVE && N * int(sizeof(IO)) > 256) ? 1 : 2
                     }
                 }
             }
-            auto gate_of = [&](int which, int t) {
-                return *reinterpret_cast<const f32x4 *>(gates + which * kC + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
-            };
-            // R = V - e^g K S^T, and the state's part of Y (its rows p in registers)
-            f32x4 Y[4];
+            // this wave's part of R = V - e^g K S^T, and of the state's part of Y (rows p in
+            // registers: 4 consecutive ones of one token per lane)
 #pragma unroll
             for (int t = 0; t < 4; ++t) E[t] = Y[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 Op<IO, 1> a[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tk, 0, tile_row(t >> 1, t & 1, c), ks, q);
+                for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tk, 0, tile_row(t >> 1, t & 1, c), n0 + ks, q);
                 mma(E, a, so[ks]);
-            }
-            ahead(std::integral_constant<int, 1>{});
-            Op<IO, Pl::kM> br[2];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                f32x4 b[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = 2 * s + e;
-                    f32x4 V;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = 32 * s + 8 * q + 4 * e + r, at = (16 * w + c) * kSz;
-                        V[r] = to_f32<IO>(*reinterpret_cast<const IO *>(buf + T::kVt + row * T::RV + (((at >> 4) ^ place<T::RV>(row)) << 4) + (at & 15)));
-                    }
-                    E[t] = V - gate_of(0, t) * E[t];
-                    b[e] = gate_of(2, t) * E[t];
-                }
-                br[s] = to_op<IO, Pl::kM>(b[0], b[1]);
             }
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 Op<IO, 1> a[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tq, 0, tile_row(t >> 1, t & 1, c), ks, q);
+                for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tq, 0, tile_row(t >> 1, t & 1, c), n0 + ks, q);
                 mma(Y, first_planes<Pl::kQ>(so[ks]), a);
             }
-            ahead(std::integral_constant<int, 2>{});
+#pragma unroll
+            for (int t = 0; t < 4; ++t) E[t] = V[t] - gate_of(0, t) * E[t];
+            if constexpr (X > 1) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) reinterpret_cast<f32x4 *>(xe)[64 * t + lane] = E[t];
+                if constexpr (!SAVE) {      // token tiles t of Y go to wave t / (4 / X)
+                    f32x4 *xy = reinterpret_cast<f32x4 *>(lds + T::kY + w * (T::kXy / W));
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const int to = t / (4 / X);
+                        if (to != x) xy[64 * (to < x ? t : t - 4 / X) + lane] = Y[t];
+                    }
+                }
+            }
+        }
+        if constexpr (X > 1) __syncthreads();       // the parts are written, q is read
+        if constexpr (T::kBufs == 2) fetch_q(next);
+        ahead(std::integral_constant<int, 1>{});
+        if (live) {
+            if constexpr (X > 1) sum_of_parts<X>(lds + T::kE + (w - x) * 4096, lane, E);
             // E = R + M (beta R), U = beta E
+            Op<IO, Pl::kM> br[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) br[s] = to_op<IO, Pl::kM>(gate_of(2, 2 * s) * E[2 * s], gate_of(2, 2 * s + 1) * E[2 * s + 1]);
             {
                 Op<IO, Pl::kM> a[4];
 #pragma unroll
@@ -247,83 +316,91 @@ __global__ __launch_bounds__(64 * W, (SAVE && N * int(sizeof(IO)) > 256) ? 1 : 2
                 ud[s] = to_op<IO, Pl::kS>(gate_of(1, 2 * s) * u0, gate_of(1, 2 * s + 1) * u1);
                 uy[s] = to_op<IO, Pl::kQ>(u0, u1);
             }
-            ahead(std::integral_constant<int, 3>{});
+            ahead(std::integral_constant<int, 2>{});
             // S <- e^{g_C} S + K^T (e^{g_C - g} U)
             const float alpha = gates[kC - 1];
 #pragma unroll
-            for (int t = 0; t < N / 16; ++t) S[t] *= alpha;
+            for (int t = 0; t < NT; ++t) S[t] *= alpha;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                for (int t0 = 0; t0 < N / 16; t0 += 4) {     // 4 tiles a turn (N = 32 has 2)
-                    constexpr int NT = N / 16 < 4 ? N / 16 : 4;
-                    f32x4 z[NT];
-                    Op<IO, 1> a[NT];
+                for (int u0 = 0; u0 < NT; u0 += 4) {     // 4 tiles a turn (or all 2)
+                    constexpr int M = NT < 4 ? NT : 4;
+                    f32x4 z[M];
+                    Op<IO, 1> a[M];
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        z[t] = S[t0 + t];
-                        a[t] = read_col<IO, 1, T::RB>(tk, 0, 32 * ks, 32 * ((t0 + t) >> 1), t & 1, c, q);
+                    for (int t = 0; t < M; ++t) {
+                        z[t] = S[u0 + t];
+                        a[t] = read_col<IO, 1, T::RB>(tk, 0, 32 * ks, 32 * (n0 + ((u0 + t) >> 1)), t & 1, c, q);
                     }
                     mma(z, a, ud[ks]);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) S[t0 + t] = z[t];
+                    for (int t = 0; t < M; ++t) S[u0 + t] = z[t];
                 }
-            // Y = scale e^g Q S^T + scores U: 4 consecutive rows p of one token per lane
-#pragma unroll
-            for (int t = 0; t < 4; ++t) Y[t] *= scale * gates[tile_row(t >> 1, t & 1, c)];
-            {
-                Op<IO, Pl::kQ> a[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) a[t] = tri_row<IO, Pl::kQ>(ts, t >> 1, t & 1, 0, c, q);
-                mma(Y, uy[0], a);
-            }
-            {
-                f32x4 lower[2] = {Y[2], Y[3]};
-                Op<IO, Pl::kQ> a[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) a[e] = tri_row<IO, Pl::kQ>(ts, 1, e, 1, c, q);
-                mma(lower, uy[1], a);
-                Y[2] = lower[0];
-                Y[3] = lower[1];
-            }
+            ahead(std::integral_constant<int, 3>{});
+            // Y = scale e^g Q S^T + scores U; wave x finishes the token tiles t of t / (4 / X) = x
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
+                const bool mine = t / (4 / X) == x;     // the same for a whole wave
+                if constexpr (X > 1 && !SAVE) {
+                    if (!mine) continue;
+#pragma unroll
+                    for (int o = 1; o < X; ++o) {
+                        const int from = (x + o) % X;   // any order: two parts only, or a fixed rotation
+                        Y[t] += reinterpret_cast<const f32x4 *>(lds + T::kY + (w - x + from) * (T::kXy / W))[64 * (x < from ? t : t - 4 / X) + lane];
+                    }
+                }
+                Y[t] *= scale * gates[tile_row(t >> 1, t & 1, c)];
+                if (mine) {
+                    f32x4 z[1] = {Y[t]};
+#pragma unroll
+                    for (int ks = 0; ks <= (t >> 1); ++ks) {
+                        const Op<IO, Pl::kQ> a[1] = {tri_row<IO, Pl::kQ>(ts, t >> 1, t & 1, ks, c, q)};
+                        mma(z, uy[ks], a);
+                    }
+                    Y[t] = z[0];
+                }
                 if constexpr (SAVE) {
                     const f32x4 d = widen<IO>(yo[t]);
                     const float dot = group4_sum(Y[t][0] * d[0] + Y[t][1] * d[1] + Y[t][2] * d[2] + Y[t][3] * d[3]);
-                    if (q == 0) saved.ydy[((size_t(bh) * nc + ch) * ptiles + p0 / 16) * kC + tile_row(t >> 1, t & 1, c)] = dot;
+                    if (q == 0) saved.ydy[(((size_t(bh) * nc + ch) * X + x) * ptiles + p0 / 16) * kC + tile_row(t >> 1, t & 1, c)] = dot;
                 } else {
                     yo[t] = narrow<IO>(Y[t]);
                 }
             }
         } else {
-            ahead(std::integral_constant<int, 1>{});
             ahead(std::integral_constant<int, 2>{});
             ahead(std::integral_constant<int, 3>{});
         }
         if constexpr (T::kBufs == 1) {
             __syncthreads();
-            if (ch + 1 < nc) fetch_all(ch + 1, lds0);
+            if (ch + 1 < nc) {
+                fetch_main(ch + 1, lds0);
+                fetch_q(ch + 1);
+            }
         }
         copies_done();
+        take_v();
         __syncthreads();
         // stores last: nothing waits for them before the next chunk's copies
         if (live) {
             if constexpr (SAVE) {
                 f32x4 *dst = reinterpret_cast<f32x4 *>(saved.E) + ((size_t(bh) * nc + ch) * ptiles + p0 / 16) * 256 + lane;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) dst[64 * t] = E[t];
+                for (int t = 0; t < 4; ++t)
+                    if (t / (4 / X) == x) dst[64 * t] = E[t];
                 if (ch % kSegment<IO> == kSegment<IO> - 1 || ch == nc - 1) {
                     const int segs = (nc + kSegment<IO> - 1) / kSegment<IO>;
                     f32x4 *at = reinterpret_cast<f32x4 *>(saved.anchor) +
-                                ((size_t(bh) * ptiles + p0 / 16) * segs + ch / kSegment<IO>) * (N / 16) * 64 + lane;
+                                (((size_t(bh) * ptiles + p0 / 16) * segs + ch / kSegment<IO>) * (N / 16) + x * NT) * 64 + lane;
 #pragma unroll
-                    for (int t = 0; t < N / 16; ++t) at[64 * t] = S[t];
+                    for (int t = 0; t < NT; ++t) at[64 * t] = S[t];
                 }
             } else {
-                const __amdgpu_buffer_rsrc_t view = buffer_rsrc(yg + (size_t(bi) * L + t0) * hp + size_t(h) * P, uint32_t(rows - 1) * tok + uint32_t(P) * kSz);
+                const __amdgpu_buffer_rsrc_t view = chunk_view(yg + vy0 + size_t(t0) * hp, rows, tok, P);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
+                    if (t / (4 / X) != x) continue;
                     const int off = int(uint32_t(tile_row(t >> 1, t & 1, c)) * tok + uint32_t(p0 + 4 * q) * kSz);
                     if constexpr (kSz == 4) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, yo[t]), view, off, 0, 0);
                     else __builtin_amdgcn_raw_buffer_store_b64(yo[t], view, off, 0, 0);
@@ -333,8 +410,29 @@ __global__ __launch_bounds__(64 * W, (SAVE && N * int(sizeof(IO)) > 256) ? 1 : 2
     }
     if (!SAVE && fin && live)
 #pragma unroll
-        for (int t = 0; t < N / 16; ++t)
-            *reinterpret_cast<f32x4 *>(fin + (size_t(bh) * P + p) * N + 32 * (t >> 1) + 8 * q + 4 * (t & 1)) = S[t];
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(fin + state_at(t)) = S[t];
+}
+
+constexpr int kMaxShare = 4;    // waves per tile, at the most
+
+// Calls f(W, X) with the waves per block and per tile for a chain over b * H * P / 16 tiles.
+template <typename IO, int N, class F>
+hipError_t with_chain_shape(int b, int H, int P, F &&f) {
+    using std::integral_constant;
+    constexpr integral_constant<int, 1> one{};
+    constexpr integral_constant<int, 2> two{};
+    constexpr integral_constant<int, 4> four{};
+    [[maybe_unused]] constexpr integral_constant<int, 8> eight{};
+    const int64_t tiles = int64_t(b) * H * (P / 16);
+    if constexpr (N == 32) {
+        return f(four, one);
+    } else if constexpr (N == 64) {
+        return tiles <= SSD_SOME ? f(four, two) : f(four, one);
+    } else if constexpr (N * int(sizeof(IO)) == 256) {
+        return tiles <= SSD_FEW ? f(four, four) : tiles <= SSD_SOME ? f(four, two) : f(four, one);
+    } else {
+        return tiles <= SSD_FEW ? f(four, four) : f(eight, four);
+    }
 }
 
 }  // namespace ssd

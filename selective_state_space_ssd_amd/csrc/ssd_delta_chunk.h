@@ -45,6 +45,14 @@ __device__ __forceinline__ int place(int r) {
     else return (r & 8) >> 2;
 }
 
+// Workgroups go round the 8 XCDs in launch order; this numbers them so that neighbours run
+// on one XCD and find what they share in its L2.
+__device__ __forceinline__ int xcd_neighbours() {
+    constexpr int kXcds = 8;
+    const int n = gridDim.x, x = blockIdx.x % kXcds;
+    return x * (n / kXcds) + min(x, n % kXcds) + blockIdx.x / kXcds;
+}
+
 // The tile row of lane c: index 32 s + 8 (c >> 2) + 4 e + (c & 3).
 __device__ __forceinline__ int tile_row(int s, int e, int c) { return 32 * s + 8 * (c >> 2) + 4 * e + (c & 3); }
 

@@ -18,15 +18,19 @@ hipError_t launch_n(const DeltaChunkArgs &a, hipStream_t stream) {
     const auto *q = static_cast<const IO *>(a.q), *k = static_cast<const IO *>(a.k), *v = static_cast<const IO *>(a.v);
     hipError_t e = launch_delta_prep<IO, N, Pl::kM, Pl::kQ>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
     if (e != hipSuccess) return e;
-    constexpr int W = 4;
-    using T = ChainTile<IO, N, W, false>;
-    const int pblocks = (a.P + 16 * W - 1) / (16 * W);
-    auto kern = k_delta_chain<IO, N, W, false>;
-    e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3(unsigned(a.b * a.H * pblocks)), dim3(64 * W), T::kLds, stream, q, k, v, images, a.init_state,
-                       static_cast<IO *>(a.y), a.final_state, nullptr, DeltaSaved{}, a.L, a.H, a.P, a.G, nc, pblocks, a.scale);
-    return hipGetLastError();
+    // waves per block and waves per tile of 16 rows
+    auto chain = [&](auto w_, auto x_) {
+        constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
+        using T = ChainLds<IO, N, W, X, Pl::kQ, true>;
+        const int per = 16 * W / X, pblocks = (a.P + per - 1) / per;
+        auto kern = k_delta_chain<IO, N, W, X, false>;
+        e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, T::kBytes);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(kern, dim3(unsigned(a.b * a.H * pblocks)), dim3(64 * W), T::kBytes, stream, q, k, v, images, a.init_state,
+                           static_cast<IO *>(a.y), a.final_state, nullptr, DeltaSaved{}, a.L, a.H, a.P, a.G, nc, pblocks, a.scale);
+        return hipGetLastError();
+    };
+    return with_chain_shape<IO, N>(a.b, a.H, a.P, chain);
 }
 
 }  // namespace
