@@ -66,6 +66,8 @@ struct DeltaBwdArgs {
 struct DeltaBwdPlan {
     bool supported = false;
     size_t off_e = 0, off_s = 0, off_ds = 0, off_anchor = 0, off_ydy = 0, off_xe = 0, off_vdv = 0, off_lam = 0;
+    size_t off_parts = 0;   // sums of dq and dk in `splits` parts, if more than 1
+    int splits = 1;
     size_t total = 0;
 };
 DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16);

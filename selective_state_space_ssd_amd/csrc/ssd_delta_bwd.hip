@@ -8,7 +8,8 @@
 //        dU = scores^T dY + e^{g_C - g} (K dS^T),   X = dU + M^T (beta dU)
 //        dv = beta X,   dbeta_i = X_i . E_i
 //        dS <- e^{g_C} dS + (scale e^g dY)^T Q - (e^g dv)^T K
-//   4 grads      per chunk, all heads of a group in one block (dq and dk are their sums):
+//   4 grads      per chunk; dq and dk are sums over a group's heads, taken in one block, or
+//                in a few whose fp32 sums a further kernel adds:
 //        dq = scale e^g dY S + W K,                      W_ij = scale (dy_i . u_j) D_ij, j <= i
 //        dk = -e^g dv S + e^{g_C - g} U dS + W^T Q + G K,  G = F + F^T, F_ij = -(dv_i . u_j) D_ij, j < i
 //   5 gates      da.  The gates only scale v going in and y coming out of an ungated rule,
@@ -313,7 +314,8 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
         for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(d_init + state_at(t)) = S[t];
 }
 
-// Kernel 4.  Block = (batch, chunk, group); wave w holds dq^T and dk^T of 16 tokens (tile
+// Kernel 4.  Block = (batch, chunk, group, one of `splits` parts of its heads' state rows);
+// wave w holds dq^T and dk^T of 16 tokens (tile
 // columns; rows n in registers, 8 consecutive ones a lane).  Per head and 64 rows p, dY, dv,
 // U and both states go through LDS.  Operands rounded to bf16 are the states and dv, as
 // stored; U and the matrices W and G, which are formed here, keep 16 bits (kP planes).
@@ -326,15 +328,17 @@ struct GradTile {
     // after the heads: W and G (kP planes each), k, q
     static constexpr int kWm = 0, kGm = kP * kTok, kK = 2 * kP * kTok, kQ = kK + kState, kTail = kQ + kState;
     static constexpr int kLds = kHead > kTail ? kHead : kTail;
+    static constexpr int kPerCu = 2 * kLds <= 159 * 1024 && N <= 128 ? 2 : 1;       // blocks: LDS, and registers at N = 256
 };
 
 template <typename IO, int N>
-__global__ __launch_bounds__(256, (2 * GradTile<IO, N>::kLds <= 159 * 1024 && N <= 128) ? 2 : 1) void k_delta_grads(const IO *__restrict__ qg, const IO *__restrict__ kg,
+__global__ __launch_bounds__(256, (GradTile<IO, N>::kPerCu)) void k_delta_grads(const IO *__restrict__ qg, const IO *__restrict__ kg,
                                                      const float *__restrict__ ag, const IO *__restrict__ dyg,
                                                      const IO *__restrict__ dvg, const char *__restrict__ images,
                                                      const f32x4 *__restrict__ E, const IO *__restrict__ Sg,
                                                      const IO *__restrict__ dSg, IO *__restrict__ dqg, IO *__restrict__ dkg,
-                                                     int L, int H, int P, int G, int nc, float scale) {
+                                                     float *__restrict__ parts, int splits, int L, int H, int P, int G, int nc,
+                                                     float scale) {
     using T = GradTile<IO, N>;
     using Img = ChunkImage<IO, DeltaPlanes<true>::kM, DeltaPlanes<true>::kQ>;
     constexpr int kSz = T::kSz, kP = T::kP, E16 = 16 / kSz;     // elements per 16 bytes
@@ -342,7 +346,7 @@ __global__ __launch_bounds__(256, (2 * GradTile<IO, N>::kLds <= 159 * 1024 && N 
     __shared__ double gd[kC];
     const uint32_t lds0 = lds_address(lds);
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
-    const int ch = blockIdx.x % nc, bg = blockIdx.x / nc, g = bg % G, bi = bg / G, r = H / G;
+    const int split = blockIdx.x % splits, cell = blockIdx.x / splits, ch = cell % nc, bg = cell / nc, g = bg % G, bi = bg / G, r = H / G;
     const int t0 = ch * kC, rows = min(kC, L - t0), ptiles = P / 16;
     const size_t hp = size_t(H) * P, gn = size_t(G) * N;
     const int tok = tile_row(w >> 1, w & 1, c);             // this lane's token
@@ -354,8 +358,9 @@ __global__ __launch_bounds__(256, (2 * GradTile<IO, N>::kLds <= 159 * 1024 && N 
     for (int t = 0; t < 4; ++t) Wm[t] = Fm[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     {
-        const int pbs = (P + 63) / 64;
-        for (int turn = 0; turn < r * pbs; ++turn) {    // head h, rows pb .. pb + 63 of its state
+        const int pbs = (P + 63) / 64, turns = r * pbs;
+        const int first = int(int64_t(turns) * split / splits), end = int(int64_t(turns) * (split + 1) / splits);
+        for (int turn = first; turn < end; ++turn) {    // head h, rows pb .. pb + 63 of its state
             const int h = g * r + turn / pbs, pb = turn % pbs * 64;
             const size_t unit = (size_t(bi) * H + h) * nc + ch;
             const float *gates = reinterpret_cast<const float *>(images + unit * Img::kBytes + Img::kGates);
@@ -366,7 +371,7 @@ __global__ __launch_bounds__(256, (2 * GradTile<IO, N>::kLds <= 159 * 1024 && N 
             int tid = threadIdx.x;
             asm volatile("" : "+v"(tid));
             const int lane = tid & 63, c = lane & 15, q = lane >> 4;
-            if (pb == 0 && w == 0) {
+            if ((pb == 0 || turn == first) && w == 0) {
                 double s = lane < rows ? gate(ag[(size_t(bi) * L + t0 + lane) * H + h]) : 0.0;
 #pragma unroll
                 for (int off = 1; off < 64; off <<= 1) {
@@ -504,9 +509,16 @@ __global__ __launch_bounds__(256, (2 * GradTile<IO, N>::kLds <= 159 * 1024 && N 
     }
     if (tok < rows) {
         const size_t dst = (size_t(bi) * L + t0 + tok) * gn + size_t(g) * N + 8 * q;
+        const size_t all = size_t(gridDim.x / (splits * nc * G)) * L * gn;
+        float *pq = parts + 2 * split * all + dst, *pk = pq + all;
 #pragma unroll
         for (int s = 0; s < N / 32; ++s) {
-            if constexpr (kSz == 4) {
+            if (splits > 1) {
+                *reinterpret_cast<f32x4 *>(pq + 32 * s) = dq[2 * s];
+                *reinterpret_cast<f32x4 *>(pq + 32 * s + 4) = dq[2 * s + 1];
+                *reinterpret_cast<f32x4 *>(pk + 32 * s) = dk[2 * s];
+                *reinterpret_cast<f32x4 *>(pk + 32 * s + 4) = dk[2 * s + 1];
+            } else if constexpr (kSz == 4) {
                 *reinterpret_cast<f32x4 *>(dqg + dst + 32 * s) = dq[2 * s];
                 *reinterpret_cast<f32x4 *>(dqg + dst + 32 * s + 4) = dq[2 * s + 1];
                 *reinterpret_cast<f32x4 *>(dkg + dst + 32 * s) = dk[2 * s];
@@ -516,6 +528,28 @@ __global__ __launch_bounds__(256, (2 * GradTile<IO, N>::kLds <= 159 * 1024 && N 
                 *reinterpret_cast<bf16x8 *>(dkg + dst + 32 * s) = to_op<IO, 1>(dk[2 * s], dk[2 * s + 1]).p[0];
             }
         }
+    }
+}
+
+// The parts of dq and dk added in their order: parts [splits][dq, dk][all] fp32, 8 elements
+// per thread.
+template <typename IO>
+__global__ __launch_bounds__(256) void k_delta_join(const float *__restrict__ parts, IO *__restrict__ dqg, IO *__restrict__ dkg,
+                                                    int splits, size_t all) {
+    const size_t at = (size_t(blockIdx.x) * 256 + threadIdx.x) * 8;
+    if (at >= 2 * all) return;
+    f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+    for (int i = 0; i < splits; ++i) {
+        const float *p = parts + 2 * i * all + at;
+        s0 += *reinterpret_cast<const f32x4 *>(p);
+        s1 += *reinterpret_cast<const f32x4 *>(p + 4);
+    }
+    IO *dst = at < all ? dqg + at : dkg + (at - all);
+    if constexpr (sizeof(IO) == 4) {
+        *reinterpret_cast<f32x4 *>(dst) = s0;
+        *reinterpret_cast<f32x4 *>(dst + 4) = s1;
+    } else {
+        *reinterpret_cast<bf16x8 *>(dst) = to_op<IO, 1>(s0, s1).p[0];
     }
 }
 
@@ -571,16 +605,17 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
                      reinterpret_cast<float *>(ws + pl.off_ydy)};
     BackSums sums{reinterpret_cast<float *>(ws + pl.off_xe), reinterpret_cast<float *>(ws + pl.off_vdv), reinterpret_cast<float *>(ws + pl.off_lam)};
     auto *dS = reinterpret_cast<IO *>(ws + pl.off_ds);
+    auto *parts = reinterpret_cast<float *>(ws + pl.off_parts);
 
     hipError_t e = launch_delta_prep<IO, N, Pl::kM, Pl::kQ>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
     if (e != hipSuccess) return e;
-    int parts = 1;
+    int share = 1;
     auto chains = [&](auto w_, auto x_) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
         constexpr int lds = ChainLds<IO, N, W, X, Pl::kQ, false>::kBytes;
         const int per = 16 * W / X, pblocks = (a.P + per - 1) / per;
         const dim3 grid(unsigned(a.b * a.H * pblocks));
-        parts = X;
+        share = X;
         auto chain = k_delta_chain<IO, N, W, X, true>;
         e = hipFuncSetAttribute(reinterpret_cast<const void *>(chain), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
@@ -599,13 +634,31 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
     constexpr int lds = GradTile<IO, N>::kLds;
     e = hipFuncSetAttribute(reinterpret_cast<const void *>(grads), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(grads, dim3(unsigned(int64_t(a.b) * a.G * nc)), dim3(256), lds, stream, q, k, a.a, dy, dv, images,
+    hipLaunchKernelGGL(grads, dim3(unsigned(int64_t(a.b) * a.G * nc * pl.splits)), dim3(256), lds, stream, q, k, a.a, dy, dv, images,
                        reinterpret_cast<const f32x4 *>(saved.E), static_cast<const IO *>(saved.S), dS, static_cast<IO *>(a.dq),
-                       static_cast<IO *>(a.dk), a.L, a.H, a.P, a.G, nc, a.scale);
+                       static_cast<IO *>(a.dk), parts, pl.splits, a.L, a.H, a.P, a.G, nc, a.scale);
     if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (pl.splits > 1) {
+        const size_t all = size_t(a.b) * a.L * a.G * N;
+        hipLaunchKernelGGL(k_delta_join<IO>, dim3(unsigned((2 * all + 2047) / 2048)), dim3(256), 0, stream, parts,
+                           static_cast<IO *>(a.dq), static_cast<IO *>(a.dk), pl.splits, all);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     hipLaunchKernelGGL((k_delta_gates<kSegment<IO>>), dim3(unsigned(int64_t(a.b) * a.H * segs)), dim3(64 * kSegment<IO>), 0, stream, saved.ydy, sums.vdv, sums.xe,
-                       sums.lam, a.da, a.dbeta, a.L, a.H, nc, ptiles, segs, parts);
+                       sums.lam, a.da, a.dbeta, a.L, a.H, nc, ptiles, segs, share);
     return hipGetLastError();
+}
+
+// Parts to split a group's `turns` (of up to 64 state rows) into, where the chunks alone
+// leave CUs idle: as many as keep every block resident.  bf16, N = 128, one group: 64 heads
+// x 512 tokens 478 -> 140 us, 80 x 4096 1269 -> 840; twice the blocks 137 and 856, half of
+// them 132 and 885.  fp32, N = 64, one block per CU: 763 -> 164 us and 1703 -> 1068.
+int grad_splits(size_t cells, size_t turns, int N, bool bf16) {
+    const int per_cu = N == 32    ? bf16 ? GradTile<bf16_bits, 32>::kPerCu : GradTile<float, 32>::kPerCu
+                       : N == 64  ? bf16 ? GradTile<bf16_bits, 64>::kPerCu : GradTile<float, 64>::kPerCu
+                       : N == 128 ? bf16 ? GradTile<bf16_bits, 128>::kPerCu : GradTile<float, 128>::kPerCu
+                                  : GradTile<bf16_bits, 256>::kPerCu;
+    return int(std::max<size_t>(1, std::min(turns, 256 * per_cu / cells)));
 }
 
 }  // namespace
@@ -631,6 +684,8 @@ DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16)
     pl.off_xe = take(units * ptiles * kC * 4);
     pl.off_vdv = take(units * ptiles * kC * 4);
     pl.off_lam = take(bh * ptiles * segs * kMaxShare * 4);
+    pl.splits = grad_splits(size_t(b) * G * nc, size_t(H / G) * ((P + 63) / 64), N, bf16);
+    pl.off_parts = take(pl.splits > 1 ? size_t(pl.splits) * 2 * b * L * G * N * 4 : 0);
     pl.total = at;
     pl.supported = true;
     return pl;

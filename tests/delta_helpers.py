@@ -48,3 +48,10 @@ def tol_out(dtype, L, N, roundings):
     if dtype == torch.float32:
         return tol32(L, N)
     return roundings * torch.finfo(dtype).eps / 2 + tol32(L, N)
+
+
+# b, L, H, G, P, N with so many heads that a wave has 16 rows of the state to itself or
+# shares them with one other (the small cases share them among four), blocks whose last
+# rows lie past the head, and many chunks
+MANY = [(1, 70, 132, 1, 64, 64), (1, 70, 40, 1, 208, 64), (1, 70, 70, 2, 64, 128), (1, 70, 18, 2, 240, 128), (1, 70, 132, 2, 64, 128),
+        (1, 66, 70, 2, 64, 256), (1, 66, 18, 3, 240, 256), (9, 900, 8, 4, 16, 32)]

@@ -11,7 +11,7 @@ import math
 import pytest
 import torch
 
-from delta_helpers import U32, inputs_of, make, rel, tol32, tol_out
+from delta_helpers import MANY, U32, inputs_of, make, rel, tol32, tol_out
 from oracle import delta
 from selective_state_space_ssd_amd import binding as bd
 
@@ -68,6 +68,14 @@ CASES = [(1, 1, 1, 1, 16, 32), (2, 5, 4, 2, 16, 32), (1, 63, 2, 1, 32, 64), (1, 
 @pytest.mark.parametrize("init", [False, True])
 def test_gradients(b, L, H, G, P, N, dtype, init):
     check(make(b, L, H, G, P, N, dtype, seed=L + N, init=init), N ** -0.5, L, N, dtype)
+
+
+@pytest.mark.parametrize("b,L,H,G,P,N", MANY)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_heads_or_chunks(b, L, H, G, P, N, dtype):
+    if N == 256 and dtype == F32:
+        pytest.skip("fp32 gradients go up to N = 128")
+    check(make(b, L, H, G, P, N, dtype, seed=L + N), N ** -0.5, L, N, dtype)
 
 
 def test_widest_state():
