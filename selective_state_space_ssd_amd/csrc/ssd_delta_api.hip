@@ -20,12 +20,17 @@ ssd_status_t check_dims(int b, int L, int H, int P, int N, int G, ssd_dtype_t io
     return SSD_OK;
 }
 
-// Sequences up to this length go token by token.
-constexpr int kShort = 16;
+// Sequences up to this length go token by token, in one launch that keeps no workspace.
+// Both sides, us, token by token / in chunks, at P = 64 and one group:
+//   bf16, N = 64:   32 x 80 heads, 24 tokens 84 / 94, 32 tokens 105 / 96;  8 heads, 24 tokens 19 / 26
+//   bf16, N = 128:  32 x 80 heads, 24 tokens 110 / 119, 32 tokens 136 / 127;  8 heads, 32 tokens 23 / 25
+//   fp32, N = 64:   32 x 80 heads, 32 tokens 92 / 135, 48 tokens 130 / 138;  8 heads, 32 tokens 19 / 25, 64 tokens 31 / 26
+//   fp32, N = 128:  32 x 80 heads, 32 tokens 139 / 242;  8 heads, 32 tokens 21 / 26, 48 tokens 29 / 26
+int most_by_token(ssd_dtype_t io) { return io == SSD_DTYPE_BF16 ? 24 : 32; }
 
 // The chunked path of a sequence, unless it is short or no chunk kernel runs its shape.
 ssd::DeltaChunkPlan sequence_plan(int b, int L, int H, int P, int N, int G, ssd_dtype_t io) {
-    if (b == 0 || L <= kShort) return {};
+    if (b == 0 || L <= most_by_token(io)) return {};
     return ssd::plan_delta_chunk(b, L, H, P, N, G, io == SSD_DTYPE_BF16);
 }
 

@@ -4,12 +4,6 @@
 
 #include "ssd_delta_chunk.h"
 
-#ifndef SSD_FEW
-#define SSD_FEW 256
-#endif
-#ifndef SSD_SOME
-#define SSD_SOME 512
-#endif
 namespace ssd {
 
 // What the forward chain leaves for the backward pass, per (batch, head):
@@ -416,6 +410,16 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
 constexpr int kMaxShare = 4;    // waves per tile, at the most
 
 // Calls f(W, X) with the waves per block and per tile for a chain over b * H * P / 16 tiles.
+// A tile is shared by X waves as long as each wave still has one of the 1024 SIMDs to itself
+// (the chain waits for its own results, so that two waves on a SIMD cost one of them little,
+// but more waves than SIMDs cost every block its exchange).  512 tokens, one group, waves per
+// tile before -> after, us of the backward pass at 128, 256, 384, 512 and 640 tiles:
+//   bf16, N = 64,  1 -> 2:  256 -> 247, 424 -> 417, 592 -> 584, 761 -> 754, 933 -> 986
+//   fp32, N = 64,  1 -> 2:  470 -> 436, 792 -> 758, 1114 -> 1082, 1441 -> 1408, 1762 -> 1817
+//   bf16, N = 128, 1 -> 2:  302 -> 287, 494 -> 482, 688 -> 672, 884 -> 872, 1077 -> 1133
+//   bf16, N = 128, 1 -> 4:  302 -> 280, 494 -> 472, 688 -> 726
+// and of the forward pass with one tile per block (4, 4) for two (8, 4):
+//   fp32, N = 128:  76 -> 58, 86 -> 69, 94 -> 112;   bf16, N = 256:  60 -> 49, 70 -> 59, 78 -> 94
 template <typename IO, int N, class F>
 hipError_t with_chain_shape(int b, int H, int P, F &&f) {
     using std::integral_constant;
@@ -423,15 +427,16 @@ hipError_t with_chain_shape(int b, int H, int P, F &&f) {
     constexpr integral_constant<int, 2> two{};
     constexpr integral_constant<int, 4> four{};
     [[maybe_unused]] constexpr integral_constant<int, 8> eight{};
+    constexpr int kSimds = 1024;
     const int64_t tiles = int64_t(b) * H * (P / 16);
     if constexpr (N == 32) {
         return f(four, one);
     } else if constexpr (N == 64) {
-        return tiles <= SSD_SOME ? f(four, two) : f(four, one);
+        return tiles <= kSimds / 2 ? f(four, two) : f(four, one);
     } else if constexpr (N * int(sizeof(IO)) == 256) {
-        return tiles <= SSD_FEW ? f(four, four) : tiles <= SSD_SOME ? f(four, two) : f(four, one);
+        return tiles <= kSimds / 4 ? f(four, four) : tiles <= kSimds / 2 ? f(four, two) : f(four, one);
     } else {
-        return tiles <= SSD_FEW ? f(four, four) : f(eight, four);
+        return tiles <= kSimds / 4 ? f(four, four) : f(eight, four);
     }
 }
 

@@ -9,7 +9,7 @@ import math
 import pytest
 import torch
 
-from delta_helpers import U32, inputs_of, make, rel, tol32, tol_out
+from delta_helpers import MANY, U32, inputs_of, make, rel, tol32, tol_out
 from oracle import delta
 from selective_state_space_ssd_amd import binding as bd
 
@@ -39,6 +39,18 @@ FWD = [(1, 1, 1, 1, 16, 16), (2, 3, 4, 2, 16, 32), (1, 16, 2, 1, 32, 32), (1, 17
 @pytest.mark.parametrize("init", [False, True])
 def test_sequence(b, L, H, G, P, N, dtype, init):
     check_fwd(make(b, L, H, G, P, N, dtype, seed=L + N, init=init), N ** -0.5, L, N, dtype)
+
+
+@pytest.mark.parametrize("b,L,H,G,P,N", MANY)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_heads_or_chunks(b, L, H, G, P, N, dtype):
+    check_fwd(make(b, L, H, G, P, N, dtype, seed=L + N), N ** -0.5, L, N, dtype)
+
+
+@pytest.mark.parametrize("L", [16, 17, 24, 25, 32, 33])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_where_chunks_begin(L, dtype):
+    check_fwd(make(2, L, 4, 2, 48, 64, dtype, seed=L), 0.125, L, 64, dtype)
 
 
 def test_long_sequence():
