@@ -402,6 +402,8 @@ def _tensor(t, name, shape, dtype, device) -> Optional[int]:
     """The device pointer of ``t`` after checking what the C call cannot see; None stays None."""
     if t is None:
         return None
+    if t.device == device and t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.device != device:
@@ -410,23 +412,23 @@ def _tensor(t, name, shape, dtype, device) -> Optional[int]:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _enqueue(name, device, stream, *args) -> None:
     """Call the C entry point ``name`` with ``args`` and a stream of ``device`` (default:
     its current one)."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
+    if stream is None:      # the handle alone: 0.2 us where a Stream object takes 1.9
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
     elif stream.device != device:
         raise ValueError(f"{name}: the stream is on {stream.device}, the tensors are on {device}")
+    else:
+        handle = stream.cuda_stream
     if device.index == torch.cuda.current_device():
-        st = getattr(lib(), name)(*args, stream.cuda_stream)
+        st = getattr(lib(), name)(*args, handle)
     else:
         with torch.cuda.device(device):
-            st = getattr(lib(), name)(*args, stream.cuda_stream)
+            st = getattr(lib(), name)(*args, handle)
     if st != 0:
         raise SSDError(st, name)
 
