@@ -38,13 +38,26 @@ struct DeltaChunkArgs {
     void *workspace;
 };
 
+// A sequence of nc chunks run in segments of `per`, all at once (ssd_delta_chain.h).
+struct DeltaCut {
+    int segments = 1, per = 0;
+};
+DeltaCut cut_sequence(int64_t bh, int nc, int P, int N, bool bf16);
+
+// fp32 [b, H, segments - 1, P + N, N]: what the segments but the last do to a state, and
+// [b, H, segments, P, N]: the states that enter them; none for one segment.
+inline size_t map_bytes(size_t bh, int P, int N, const DeltaCut &c) { return bh * (c.segments - 1) * (P + N) * N * 4; }
+inline size_t entering_bytes(size_t bh, int P, int N, const DeltaCut &c) { return c.segments > 1 ? bh * c.segments * P * N * 4 : 0; }
+
 struct DeltaChunkPlan {
     bool supported = false;
-    size_t total = 0;           // workspace bytes: one image per (batch, head, chunk)
+    DeltaCut cut;
+    size_t off_map = 0, off_init = 0;   // behind the images: map and entering states of the segments
+    size_t total = 0;                   // workspace bytes
 };
 bool delta_chunk_supported(int b, int L, int H, int P, int N, int G, bool bf16);
 DeltaChunkPlan plan_delta_chunk(int b, int L, int H, int P, int N, int G, bool bf16);
-hipError_t launch_delta_chunk(const DeltaChunkArgs &a, hipStream_t stream);
+hipError_t launch_delta_chunk(const DeltaChunkArgs &a, const DeltaChunkPlan &plan, hipStream_t stream);
 
 // Gradients (ssd_delta_bwd.hip); the shapes of the chunked path.
 struct DeltaBwdArgs {
@@ -66,6 +79,8 @@ struct DeltaBwdArgs {
 struct DeltaBwdPlan {
     bool supported = false;
     size_t off_e = 0, off_s = 0, off_ds = 0, off_anchor = 0, off_ydy = 0, off_xe = 0, off_vdv = 0, off_lam = 0;
+    DeltaCut cut;
+    size_t off_map = 0, off_init = 0, off_dmap = 0, off_dinit = 0;      // of the segments, and of their gradients
     size_t off_parts = 0;   // sums of dq and dk in `splits` parts, if more than 1
     int splits = 1;
     size_t total = 0;

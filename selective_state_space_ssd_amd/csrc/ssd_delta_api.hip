@@ -106,7 +106,7 @@ ssd_status_t ssd_gated_delta_fwd(const void *q, const void *k, const void *v, co
         c.q = q; c.k = k; c.v = v; c.a = a; c.beta = beta; c.init_state = init_state;
         c.y = y; c.final_state = final_state; c.workspace = workspace;
         c.b = b; c.L = L; c.H = H; c.P = P; c.N = N; c.G = G; c.scale = scale; c.bf16 = bf16;
-        return done(ssd::launch_delta_chunk(c, stream));
+        return done(ssd::launch_delta_chunk(c, plan, stream));
     }
     ssd::DeltaStepArgs s{};
     s.state_in = init_state; s.q = q; s.k = k; s.v = v; s.a = a; s.beta = beta;

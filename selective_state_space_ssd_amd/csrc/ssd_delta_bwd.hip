@@ -616,12 +616,9 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
         const int per = 16 * W / X, pblocks = (a.P + per - 1) / per;
         const dim3 grid(unsigned(a.b * a.H * pblocks));
         share = X;
-        auto chain = k_delta_chain<IO, N, W, X, true>;
-        e = hipFuncSetAttribute(reinterpret_cast<const void *>(chain), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        e = launch_chain<IO, N, W, X, Chain::save, Pl::kQ>(q, k, v, images, a.init_state, nullptr, nullptr, dy, saved, a.b, a.L, a.H, a.P, a.G, nc, 1,
+                                                           a.scale, stream);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(chain, grid, dim3(64 * W), lds, stream, q, k, v, images, a.init_state, nullptr, nullptr, dy, saved, a.L, a.H,
-                           a.P, a.G, nc, pblocks, a.scale);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
         auto back = k_delta_chain_back<IO, N, W, X>;
         e = hipFuncSetAttribute(reinterpret_cast<const void *>(back), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
@@ -629,7 +626,7 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
                            reinterpret_cast<const f32x4 *>(saved.anchor), dv, dS, a.d_init, sums, a.L, a.H, a.P, a.G, nc, pblocks, a.scale);
         return hipGetLastError();
     };
-    if ((e = with_chain_shape<IO, N>(a.b, a.H, a.P, chains)) != hipSuccess) return e;
+    if ((e = with_chain_shape<IO, N>(int64_t(a.b) * a.H * ptiles, chains)) != hipSuccess) return e;
     auto grads = k_delta_grads<IO, N>;
     constexpr int lds = GradTile<IO, N>::kLds;
     e = hipFuncSetAttribute(reinterpret_cast<const void *>(grads), hipFuncAttributeMaxDynamicSharedMemorySize, lds);

@@ -2,6 +2,7 @@
 // ssd_delta_chunk.h for the formulas and the tile layout).
 #pragma once
 
+#include "ssd_delta.h"
 #include "ssd_delta_chunk.h"
 
 namespace ssd {
@@ -125,25 +126,37 @@ __device__ __forceinline__ void sum_of_parts(const char *first, int lane, f32x4 
     }
 }
 
-// SAVE: instead of y and the final state, what the backward pass needs (dyg is read).
-template <typename IO, int N, int W, int X, bool SAVE>
+// What a chain is run for.
+//   run   y and the final state
+//   save  what the backward pass needs (dyg is read)
+//   map   what a segment of the sequence does to the state that enters it, S -> S A + B: the
+//         states after it of P rows that enter as 0 (B) and, with v = 0, of the N rows of the
+//         identity (A).  The first segment's P rows enter as they are, without the others.
+enum class Chain { run, save, map };
+
+// One chain per (batch, head, segment of `per` chunks); `init` has a state for each, `fin`
+// for each (map: [P + N][N]) or for each (batch, head).
+template <typename IO, int N, int W, int X, Chain MODE, int NQ>
 __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ qg, const IO *__restrict__ kg,
                                                         const IO *__restrict__ vg, const char *__restrict__ images,
                                                         const float *__restrict__ init, IO *__restrict__ yg,
                                                         float *__restrict__ fin, const IO *__restrict__ dyg,
-                                                        DeltaSaved saved, int L, int H, int P, int G, int nc, int pblocks,
-                                                        float scale) {
-    using Pl = DeltaPlanes<SAVE>;
-    using T = ChainLds<IO, N, W, X, Pl::kQ, !SAVE>;
+                                                        DeltaSaved saved, int L, int H, int P, int G, int nc, int per, int segs,
+                                                        int pblocks, float scale) {
+    constexpr bool SAVE = MODE == Chain::save, MAP = MODE == Chain::map;
+    using Pl = DeltaPlanes<NQ == 3>;
+    using T = ChainLds<IO, N, W, X, NQ, MODE == Chain::run>;
     using Img = typename T::Img;
     extern __shared__ __align__(16) char lds[];
     constexpr int kSz = int(sizeof(IO)), KS = N / 32 / X, NT = 2 * KS;  // this wave's column blocks and tiles
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
     const int x = w % X, n0 = x * KS;           // first column block
-    const int blk = xcd_neighbours(), pb = blk % pblocks, bh = blk / pblocks;
+    const int blk = xcd_neighbours(), pb = blk % pblocks, unit = blk / pblocks, seg = unit % segs, bh = unit / segs;
     const int h = bh % H, bi = bh / H, g = h / (H / G);
     const int p0 = (pb * (W / X) + w / X) * 16, p = p0 + c, ptiles = P / 16;
-    const bool live = p0 < P;       // the same for a whole wave, and for the waves of a tile
+    const int first = seg * per, end = min(first + per, nc), prows = MAP && seg > 0 ? P + N : P;
+    if (pb * (W / X) * 16 >= prows) return;
+    const bool live = p0 < prows;   // the same for a whole wave, and for the waves of a tile
     const size_t hp = size_t(H) * P, gn = size_t(G) * N;
     const char *img = images + size_t(bh) * nc * Img::kBytes;
     const IO *k0 = kg + size_t(bi) * L * gn + size_t(g) * N, *q0 = qg + size_t(bi) * L * gn + size_t(g) * N;
@@ -157,10 +170,10 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
         const int t0 = ch * kC, last = min(kC, L - t0) - 1;
         copy_rows<T::RB, kC, W, kPart, 4>(k0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf);
         copy_image<Img::kBytes, W, kPart, 4>(img + size_t(ch) * Img::kBytes, buf + T::kImg);
-        if constexpr (T::kQMain) copy_rows<T::RB, kC, W, kPart, 4>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf + T::kRows);
+        if constexpr (T::kQMain && !MAP) copy_rows<T::RB, kC, W, kPart, 4>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf + T::kRows);
     };
     auto fetch_q = [&](int ch) {
-        if constexpr (T::kQMain) return;
+        if constexpr (T::kQMain || MAP) return;
         const int t0 = ch * kC, last = min(kC, L - t0) - 1;
         copy_rows<T::RB, kC, W, 0, 1>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, lds0 + T::kQt);
     };
@@ -173,7 +186,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
     // v of chunk ch, by one wave of a tile: accumulator layout
     IO rv[16];
     auto fetch_v = [&](int ch) {
-        if (!live || x != 0) return;
+        if (!live || x != 0 || (MAP && p0 >= P)) return;
         const int t0 = ch * kC;
         const __amdgpu_buffer_rsrc_t view = chunk_view(vg + vy0 + size_t(t0) * hp, min(kC, L - t0), tok, P);
         const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
@@ -190,30 +203,36 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
             for (int r = 0; r < 4; ++r) V[t][r] = x == 0 ? to_f32<IO>(rv[4 * t + r]) : 0.f;
     };
     // row p of the state, this wave's columns 32 (n0 + t / 2) + 8 q + 4 (t & 1) ..
-    auto state_at = [&](int t) { return (size_t(bh) * P + p) * N + 32 * (n0 + (t >> 1)) + 8 * q + 4 * (t & 1); };
+    auto state_at = [&](size_t of, int rows, int t) { return (of * rows + p) * N + 32 * (n0 + (t >> 1)) + 8 * q + 4 * (t & 1); };
 
     f32x4 S[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (init && live)
+    if (MAP && p0 >= P) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) S[t] = *reinterpret_cast<const f32x4 *>(init + state_at(t));
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[t][r] = p - P == 32 * (n0 + (t >> 1)) + 8 * q + 4 * (t & 1) + r ? 1.f : 0.f;
+    } else if (init && live && (!MAP || seg == 0)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) S[t] = *reinterpret_cast<const f32x4 *>(init + state_at(MAP ? bh : unit, P, t));
+    }
 #pragma unroll
     for (int i = 0; i < 16; ++i) rv[i] = IO(0);
-    fetch_main(0, lds0);
-    fetch_q(0);
-    fetch_v(0);
+    fetch_main(first, lds0);
+    fetch_q(first);
+    fetch_v(first);
     copies_done();
     take_v();
     __syncthreads();
 
-    for (int ch = 0; ch < nc; ++ch) {
-        const int t0 = ch * kC, rows = min(kC, L - t0), next = min(ch + 1, nc - 1);     // past the last: that one again
-        const char *buf = lds + (T::kBufs == 2 ? (ch & 1) * T::kMain : 0);
+    for (int ch = first; ch < end; ++ch) {
+        const int t0 = ch * kC, rows = min(kC, L - t0), next = min(ch + 1, end - 1);    // past the last: that one again
+        const char *buf = lds + (T::kBufs == 2 ? ((ch - first) & 1) * T::kMain : 0);
         const char *tk = buf, *tq = T::kQMain ? buf + T::kRows : lds + T::kQt, *tm = buf + T::kImg + Img::kM, *ts = buf + T::kImg + Img::kQ;
         const float *gates = reinterpret_cast<const float *>(buf + T::kImg + Img::kGates);
         auto ahead = [&](auto part) {
-            if constexpr (T::kBufs == 2) fetch(next, lds0 + ((ch + 1) & 1) * T::kMain, part);
+            if constexpr (T::kBufs == 2) fetch(next, lds0 + ((ch - first + 1) & 1) * T::kMain, part);
         };
         auto gate_of = [&](int which, int t) {
             return *reinterpret_cast<const f32x4 *>(gates + which * kC + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
@@ -257,7 +276,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                 mma(E, a, so[ks]);
             }
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
+            for (int ks = 0; ks < (MAP ? 0 : KS); ++ks) {
                 Op<IO, 1> a[4];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tq, 0, tile_row(t >> 1, t & 1, c), n0 + ks, q);
@@ -268,7 +287,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
             if constexpr (X > 1) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) reinterpret_cast<f32x4 *>(xe)[64 * t + lane] = E[t];
-                if constexpr (!SAVE) {      // token tiles t of Y go to wave t / (4 / X)
+                if constexpr (MODE == Chain::run) {     // token tiles t of Y go to wave t / (4 / X)
                     f32x4 *xy = reinterpret_cast<f32x4 *>(lds + T::kY + w * (T::kXy / W));
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
@@ -334,7 +353,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
             ahead(std::integral_constant<int, 3>{});
             // Y = scale e^g Q S^T + scores U; wave x finishes the token tiles t of t / (4 / X) = x
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int t = 0; t < (MAP ? 0 : 4); ++t) {
                 const bool mine = t / (4 / X) == x;     // the same for a whole wave
                 if constexpr (X > 1 && !SAVE) {
                     if (!mine) continue;
@@ -368,7 +387,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
         }
         if constexpr (T::kBufs == 1) {
             __syncthreads();
-            if (ch + 1 < nc) {
+            if (ch + 1 < end) {
                 fetch_main(ch + 1, lds0);
                 fetch_q(ch + 1);
             }
@@ -390,7 +409,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
 #pragma unroll
                     for (int t = 0; t < NT; ++t) at[64 * t] = S[t];
                 }
-            } else {
+            } else if constexpr (!MAP) {
                 const __amdgpu_buffer_rsrc_t view = chunk_view(yg + vy0 + size_t(t0) * hp, rows, tok, P);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
@@ -402,14 +421,15 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
             }
         }
     }
-    if (!SAVE && fin && live)
+    if (!SAVE && fin && live && (MAP || seg == segs - 1))
 #pragma unroll
-        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(fin + state_at(t)) = S[t];
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(fin + state_at(MAP ? unit : bh, MAP ? P + N : P, t)) = S[t];
 }
 
 constexpr int kMaxShare = 4;    // waves per tile, at the most
+constexpr int kSimds = 1024;
 
-// Calls f(W, X) with the waves per block and per tile for a chain over b * H * P / 16 tiles.
+// Calls f(W, X) with the waves per block and per tile for `tiles` chains of 16 state rows.
 // A tile is shared by X waves as long as each wave still has one of the 1024 SIMDs to itself
 // (the chain waits for its own results, so that two waves on a SIMD cost one of them little,
 // but more waves than SIMDs cost every block its exchange).  512 tokens, one group, waves per
@@ -421,14 +441,12 @@ constexpr int kMaxShare = 4;    // waves per tile, at the most
 // and of the forward pass with one tile per block (4, 4) for two (8, 4):
 //   fp32, N = 128:  76 -> 58, 86 -> 69, 94 -> 112;   bf16, N = 256:  60 -> 49, 70 -> 59, 78 -> 94
 template <typename IO, int N, class F>
-hipError_t with_chain_shape(int b, int H, int P, F &&f) {
+hipError_t with_chain_shape(int64_t tiles, F &&f) {
     using std::integral_constant;
     constexpr integral_constant<int, 1> one{};
     constexpr integral_constant<int, 2> two{};
     constexpr integral_constant<int, 4> four{};
     [[maybe_unused]] constexpr integral_constant<int, 8> eight{};
-    constexpr int kSimds = 1024;
-    const int64_t tiles = int64_t(b) * H * (P / 16);
     if constexpr (N == 32) {
         return f(four, one);
     } else if constexpr (N == 64) {
@@ -440,4 +458,117 @@ hipError_t with_chain_shape(int b, int H, int P, F &&f) {
     }
 }
 
+template <typename IO, int N, int W, int X, Chain MODE, int NQ>
+hipError_t launch_chain(const IO *q, const IO *k, const IO *v, const char *images, const float *init, IO *y, float *fin, const IO *dy,
+                        const DeltaSaved &saved, int b, int L, int H, int P, int G, int per, int segs, float scale, hipStream_t stream) {
+    constexpr int lds = ChainLds<IO, N, W, X, NQ, MODE == Chain::run>::kBytes;
+    const int rows = 16 * W / X, pblocks = ((MODE == Chain::map ? P + N : P) + rows - 1) / rows, nc = (L + kC - 1) / kC;
+    auto kern = k_delta_chain<IO, N, W, X, MODE, NQ>;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3(unsigned(int64_t(b) * H * segs * pblocks)), dim3(64 * W), lds, stream, q, k, v, images, init, y, fin, dy,
+                       saved, L, H, P, G, nc, per, segs, pblocks, scale);
+    return hipGetLastError();
+}
+
+namespace {
+
+// The states at the segments' borders, one after the other.  Block = (batch, head, 16 rows
+// of the state), wave w = 16 of its columns, on the fp32 matrix instruction; A is read ahead
+// by one segment where there are registers for it.
+//   !BACK  S_0 = init_state, S_1 = the first segment's rows, S_{i+1} = S_i A_i + B_i
+//   BACK   from the last segment down: dS that leaves segment i - 1 = dS_i A_i^T + D_i; `map`
+//          holds the A's as before, `add` the D's [segments][P][N] and `init` is unused
+template <int N, bool BACK>
+__global__ __launch_bounds__(4 * N) void k_delta_carry(const float *__restrict__ map, const float *__restrict__ add,
+                                                       const float *__restrict__ init_state, float *__restrict__ out, int P, int segs) {
+    __shared__ __align__(16) float rows[16][N + 4];
+    constexpr bool kAhead = N <= 128;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
+    const int pt = blockIdx.x % (P / 16), bh = blockIdx.x / (P / 16), col = 16 * w + c;
+    const size_t pn = size_t(P) * N, step = pn + size_t(N) * N, at = size_t(16 * pt + 4 * q) * N + col;
+    const float *m = map + size_t(bh) * (segs - 1) * step;
+    float *o = out + size_t(bh) * segs * pn + at;
+    f32x4 s, a[N / 16], an[kAhead ? N / 16 : 1];
+    // a product's k = 16 j + 4 q + r, r = 0 .. 3 in the elements of a[j]
+    auto fetch = [&](f32x4 (&to)[N / 16], int seg) {
+        const float *A = m + size_t(seg) * step + pn;
+#pragma unroll
+        for (int j = 0; j < N / 16; ++j) {
+            if constexpr (BACK) {
+                to[j] = *reinterpret_cast<const f32x4 *>(A + size_t(col) * N + 16 * j + 4 * q);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) to[j][r] = A[(16 * j + 4 * q + r) * N + col];
+            }
+        }
+    };
+    auto added = [&](int seg) {     // B or D of a segment
+        f32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = BACK ? add[(size_t(bh) * segs + seg) * pn + at + r * N] : m[size_t(seg) * step + at + r * N];
+        return v;
+    };
+    auto put = [&](int seg, const f32x4 &v) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[seg * pn + r * N] = v[r];
+    };
+    if constexpr (!BACK) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (init_state)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = init_state[size_t(bh) * pn + at + r * N];
+        put(0, v);
+    }
+    const int turns = segs - 2;         // the segments 1 .. segs - 2 that are passed through
+    auto segment = [&](int i) { return BACK ? segs - 2 - i : i + 1; };
+    s = added(BACK ? segs - 1 : 0);
+    put(BACK ? segs - 2 : 1, s);
+    if (turns > 0) fetch(a, segment(0));
+    for (int i = 0; i < turns; ++i) {
+        __syncthreads();                // the last product's readers
+#pragma unroll
+        for (int r = 0; r < 4; ++r) rows[4 * q + r][col] = s[r];
+        s = added(segment(i));
+        if constexpr (kAhead) fetch(an, segment(min(i + 1, turns - 1)));
+        __syncthreads();
+        f32x4 odd = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < N / 16; ++j) {
+            const f32x4 row = *reinterpret_cast<const f32x4 *>(&rows[c][16 * j + 4 * q]);
+            s = mfma_f32(row[0], a[j][0], s);
+            odd = mfma_f32(row[1], a[j][1], odd);
+            s = mfma_f32(row[2], a[j][2], s);
+            odd = mfma_f32(row[3], a[j][3], odd);
+        }
+        s += odd;
+        put(BACK ? segment(i) - 1 : segment(i) + 1, s);
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int j = 0; j < N / 16; ++j) a[j] = an[j];
+        } else {
+            fetch(a, segment(min(i + 1, turns - 1)));
+        }
+    }
+}
+
+// The states that enter the segments, if there are more than one.
+template <typename IO, int N, int NQ>
+hipError_t enter_segments(const IO *q, const IO *k, const IO *v, const char *images, const float *init_state, float *map, float *init, int b,
+                          int L, int H, int P, int G, const DeltaCut &cut, float scale, hipStream_t stream) {
+    if (cut.segments == 1) return hipSuccess;
+    const int64_t bh = int64_t(b) * H;
+    auto go = [&](auto w_, auto x_) {
+        constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
+        return launch_chain<IO, N, W, X, Chain::map, NQ>(q, k, v, images, init_state, static_cast<IO *>(nullptr), map, nullptr, DeltaSaved{}, b,
+                                                         L, H, P, G, cut.per, cut.segments - 1, scale, stream);
+    };
+    const hipError_t e = with_chain_shape<IO, N>(bh * (cut.segments - 1) * ((P + N) / 16), go);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_delta_carry<N, false>), dim3(unsigned(bh * (P / 16))), dim3(4 * N), 0, stream, map, nullptr, init_state, init, P,
+                       cut.segments);
+    return hipGetLastError();
+}
+
+}  // namespace
 }  // namespace ssd

@@ -11,29 +11,57 @@ namespace ssd {
 namespace {
 
 template <typename IO, int N>
-hipError_t launch_n(const DeltaChunkArgs &a, hipStream_t stream) {
+hipError_t launch_n(const DeltaChunkArgs &a, const DeltaChunkPlan &pl, hipStream_t stream) {
     using Pl = DeltaPlanes<false>;
-    const int nc = (a.L + kC - 1) / kC;
     char *images = static_cast<char *>(a.workspace);
+    auto *map = reinterpret_cast<float *>(images + pl.off_map), *init = reinterpret_cast<float *>(images + pl.off_init);
     const auto *q = static_cast<const IO *>(a.q), *k = static_cast<const IO *>(a.k), *v = static_cast<const IO *>(a.v);
     hipError_t e = launch_delta_prep<IO, N, Pl::kM, Pl::kQ>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
     if (e != hipSuccess) return e;
-    // waves per block and waves per tile of 16 rows
-    auto chain = [&](auto w_, auto x_) {
+    if ((e = enter_segments<IO, N, Pl::kQ>(q, k, v, images, a.init_state, map, init, a.b, a.L, a.H, a.P, a.G, pl.cut, a.scale, stream)) != hipSuccess)
+        return e;
+    auto go = [&](auto w_, auto x_) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
-        using T = ChainLds<IO, N, W, X, Pl::kQ, true>;
-        const int per = 16 * W / X, pblocks = (a.P + per - 1) / per;
-        auto kern = k_delta_chain<IO, N, W, X, false>;
-        e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, T::kBytes);
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(kern, dim3(unsigned(a.b * a.H * pblocks)), dim3(64 * W), T::kBytes, stream, q, k, v, images, a.init_state,
-                           static_cast<IO *>(a.y), a.final_state, nullptr, DeltaSaved{}, a.L, a.H, a.P, a.G, nc, pblocks, a.scale);
-        return hipGetLastError();
+        return launch_chain<IO, N, W, X, Chain::run, Pl::kQ>(q, k, v, images, pl.cut.segments > 1 ? init : a.init_state, static_cast<IO *>(a.y),
+                                                             a.final_state, nullptr, DeltaSaved{}, a.b, a.L, a.H, a.P, a.G, pl.cut.per,
+                                                             pl.cut.segments, a.scale, stream);
     };
-    return with_chain_shape<IO, N>(a.b, a.H, a.P, chain);
+    return with_chain_shape<IO, N>(int64_t(a.b) * a.H * pl.cut.segments * (a.P / 16), go);
 }
 
 }  // namespace
+
+// Chains wait for their own results, chunk after chunk; with few (batch, head)s most of the
+// device is idle meanwhile.  A sequence cut into segments needs each chunk twice, once to see
+// what its segment does to any state (P + N rows instead of P) and once with the state that
+// enters it, but all segments run at once.  The cut is the cheapest by the measured cost of a
+// chunk, in units of one step of a chain that has its SIMD to itself (3.3 us in bf16, N =
+// 128).  One segment -> this rule -> the best of 1, 2, 3, 4, 6, 8, 11, 16, 24, 32, 64, us, b = 1:
+//   bf16, P = N = 128:  3 heads, 4096 tokens 196 -> 82 -> 81, 16384: 730 -> 155 -> 161;
+//                       32 heads, 4096: 220 -> 196 -> 197, 16384: 864 -> 696 -> 692
+//   fp32, P = N = 64:   24 heads, 1600 tokens 140 -> 92 -> 84, 16384: 1228 -> 502 -> 497
+// and over 360 shapes of 1 to 64 heads and 256 to 16384 tokens as fast as that best in the
+// mean, 1.27 times as long at the most.
+DeltaCut cut_sequence(int64_t bh, int nc, int P, int N, bool bf16) {
+    const bool wide = N * (bf16 ? 2 : 4) > 256;     // blocks of 8 waves for 2 tiles
+    auto step = [&](int64_t tiles) {
+        if (wide) return tiles <= kSimds / 4 ? 1.0 : 1.75 * double((tiles + kSimds / 2 - 1) / (kSimds / 2));
+        return tiles <= kSimds / 4 ? 0.85 : double((tiles + kSimds - 1) / kSimds);
+    };
+    const double carry = N == 256 ? 1.5 : N == 128 ? 0.35 : 0.2, launches = 2.0;
+    DeltaCut best{1, nc};
+    double least = 0.95 * nc * step(bh * (P / 16));      // no cut for less than a twentieth
+    for (int s = 2; s <= std::min(nc / 2, 64); ++s) {
+        const int per = (nc + s - 1) / s;
+        if ((nc + per - 1) / per != s) continue;
+        const double c = per * (step(bh * s * (P / 16)) + 0.8 * step(bh * (s - 1) * ((P + N) / 16))) + carry * s + launches;
+        if (c < least) {
+            least = c;
+            best = {s, per};
+        }
+    }
+    return best;
+}
 
 bool delta_chunk_supported(int b, int L, int H, int P, int N, int G, bool bf16) {
     const bool n_ok = N == 32 || N == 64 || N == 128 || (bf16 && N == 256);
@@ -48,16 +76,22 @@ DeltaChunkPlan plan_delta_chunk(int b, int L, int H, int P, int N, int G, bool b
     if (!delta_chunk_supported(b, L, H, P, N, G, bf16)) return pl;
     using Pl = DeltaPlanes<false>;
     pl.supported = true;
-    pl.total = size_t(b) * H * ((L + kC - 1) / kC) * (bf16 ? ChunkImage<bf16_bits, Pl::kM, Pl::kQ>::kBytes : ChunkImage<float, Pl::kM, Pl::kQ>::kBytes);
+    const int nc = (L + kC - 1) / kC;
+    const size_t bh = size_t(b) * H;
+    pl.total = bh * nc * (bf16 ? ChunkImage<bf16_bits, Pl::kM, Pl::kQ>::kBytes : ChunkImage<float, Pl::kM, Pl::kQ>::kBytes);
+    pl.cut = cut_sequence(int64_t(bh), nc, P, N, bf16);
+    pl.off_map = pl.total;
+    pl.off_init = pl.off_map + map_bytes(bh, P, N, pl.cut);
+    pl.total = pl.off_init + entering_bytes(bh, P, N, pl.cut);
     return pl;
 }
 
-hipError_t launch_delta_chunk(const DeltaChunkArgs &a, hipStream_t stream) {
+hipError_t launch_delta_chunk(const DeltaChunkArgs &a, const DeltaChunkPlan &pl, hipStream_t stream) {
     switch (a.N) {
-        case 32: return a.bf16 ? launch_n<bf16_bits, 32>(a, stream) : launch_n<float, 32>(a, stream);
-        case 64: return a.bf16 ? launch_n<bf16_bits, 64>(a, stream) : launch_n<float, 64>(a, stream);
-        case 128: return a.bf16 ? launch_n<bf16_bits, 128>(a, stream) : launch_n<float, 128>(a, stream);
-        case 256: return a.bf16 ? launch_n<bf16_bits, 256>(a, stream) : hipErrorInvalidValue;
+        case 32: return a.bf16 ? launch_n<bf16_bits, 32>(a, pl, stream) : launch_n<float, 32>(a, pl, stream);
+        case 64: return a.bf16 ? launch_n<bf16_bits, 64>(a, pl, stream) : launch_n<float, 64>(a, pl, stream);
+        case 128: return a.bf16 ? launch_n<bf16_bits, 128>(a, pl, stream) : launch_n<float, 128>(a, pl, stream);
+        case 256: return a.bf16 ? launch_n<bf16_bits, 256>(a, pl, stream) : hipErrorInvalidValue;
         default: return hipErrorInvalidValue;
     }
 }

@@ -238,3 +238,46 @@ def test_two_streams_at_once():
         s.synchronize()
     for g, w in zip(got, want):
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+# b, L, H, G, P, N of sequences long enough for their few heads to be cut into segments: a
+# ragged last segment, blocks that end in the middle of a head's rows, every state width
+CUT = [(1, 64 * 16, 1, 1, 16, 32), (1, 64 * 40 - 63, 2, 1, 48, 64), (2, 64 * 30 + 1, 1, 1, 80, 128), (1, 2500, 3, 1, 32, 128), (1, 1600, 1, 1, 64, 256),
+       (1, 64 * 100, 1, 1, 16, 64)]
+
+
+@pytest.mark.parametrize("b,L,H,G,P,N", CUT)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("init", [False, True])
+def test_cut_into_segments(b, L, H, G, P, N, dtype, init):
+    if N >= 32 and (N < 256 or dtype == BF):    # the workspace holds more than each chunk's image: the segments' states
+        of = lambda tokens: bd.ssd_gated_delta_fwd_workspace_bytes(b, tokens, H, P, N, G, bd.SSD_DTYPE_BF16 if dtype == BF else bd.SSD_DTYPE_F32)
+        assert of(L) > of(128) // 2 * ((L + 63) // 64)
+    check_fwd(make(b, L, H, G, P, N, dtype, seed=L + N, init=init), N ** -0.5, L, N, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_cut_reflections_and_closed_gates(dtype):
+    """beta = 2 (the map of a segment is a reflection after the other, which shortens no
+    state) and a gate that closes in the middle (it is 0 from there on)."""
+    c = make(1, 1500, 2, 1, 32, 64, dtype, seed=4)
+    c["beta"][:, :, 0] = 2.0
+    c["a"][:, :, 0] = 0.0
+    c["a"][:, 700, 1] = -float("inf")
+    # as in test_equal_keys: M_ij beta_j is what token i reads of the reflections of 2 k_j, at
+    # most 2, so that a chunk's brackets take up 2 sqrt(63) < 16 times one rounding's error;
+    # the map from segment to segment is an isometry
+    check_fwd(c, 0.5, 1500, 64, dtype, amplified=16)
+
+
+def test_cut_rows_apart_from_nan_in_others():
+    c = make(1, 2000, 2, 1, 64, 128, BF, seed=2)
+    y, S = bd.gated_delta_fwd(*inputs_of(c), 1.0, init_state=c["init_state"])
+    c["v"][:, 1100, 0, 5] = float("nan")
+    c["init_state"][:, 1, 7] = float("inf")
+    y2, S2 = bd.gated_delta_fwd(*inputs_of(c), 1.0, init_state=c["init_state"])
+    keep = torch.ones(2, 64, dtype=torch.bool, device="cuda")
+    keep[0, 5] = keep[1, 7] = False
+    assert torch.equal(y2[:, :, keep], y[:, :, keep]) and torch.equal(S2[:, keep], S[:, keep])
+    assert torch.equal(y2[:, :1088, 0], y[:, :1088, 0])        # earlier chunks
+    assert torch.isnan(y2[:, 1100:, 0, 5]).all() and not torch.isfinite(S2[:, 1, 7]).any()
