@@ -42,7 +42,7 @@ struct DeltaChunkArgs {
 struct DeltaCut {
     int segments = 1, per = 0;
 };
-DeltaCut cut_sequence(int64_t bh, int nc, int P, int N, bool bf16);
+DeltaCut cut_sequence(int64_t bh, int nc, int P, int N, bool bf16, bool back);   // back: for the backward pass
 
 // fp32 [b, H, segments - 1, P + N, N]: what the segments but the last do to a state, and
 // [b, H, segments, P, N]: the states that enter them; none for one segment.

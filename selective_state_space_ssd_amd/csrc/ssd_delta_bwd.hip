@@ -32,15 +32,20 @@ struct BackSums {
     float *lam;         // [P / 16][segments][X]: <dS, S> at the end of each segment, in parts
 };
 
-// Kernel 3.  Waves, tiles and LDS as in the forward chain; dy is read by every wave.
-template <typename IO, int N, int W, int X>
+// Kernel 3.  Waves, tiles and LDS as in the forward chain; dy is read by every wave.  One
+// chain per (batch, head, segment of `per` chunks).  What leaves the last segment is d_final,
+// what leaves the others is in `d_enter`.  MAP: of the segments 1 .. segs - 1, only the
+// gradient of the state that enters each, into d_out [segs], with 0 for what leaves the
+// others; the forward maps tell what d_enter adds to it.
+template <typename IO, int N, int W, int X, bool MAP>
 __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restrict__ qg, const IO *__restrict__ kg,
                                                              const IO *__restrict__ vg, const IO *__restrict__ dyg,
                                                              const char *__restrict__ images, const float *__restrict__ d_final,
-                                                             const f32x4 *__restrict__ E, const f32x4 *__restrict__ anchor,
-                                                             IO *__restrict__ dvg, IO *__restrict__ dSg,
-                                                             float *__restrict__ d_init, BackSums sums, int L, int H, int P,
-                                                             int G, int nc, int pblocks, float scale) {
+                                                             const float *__restrict__ d_enter, const f32x4 *__restrict__ E,
+                                                             const f32x4 *__restrict__ anchor, IO *__restrict__ dvg,
+                                                             IO *__restrict__ dSg, float *__restrict__ d_out, BackSums sums, int L,
+                                                             int H, int P, int G, int nc, int per, int segs, int pblocks,
+                                                             float scale) {
     using Pl = DeltaPlanes<true>;
     using T = ChainLds<IO, N, W, X, Pl::kQ, false>;
     using Img = typename T::Img;
@@ -48,9 +53,10 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
     constexpr int kSz = int(sizeof(IO)), KS = N / 32 / X, NT = 2 * KS;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
     const int x = w % X, n0 = x * KS;
-    const int blk = xcd_neighbours(), pb = blk % pblocks, bh = blk / pblocks;
+    const int blk = xcd_neighbours(), pb = blk % pblocks, chain = blk / pblocks, skip = MAP ? 1 : 0;
+    const int seg = chain % (segs - skip) + skip, bh = chain / (segs - skip), first = seg * per, last = min(first + per, nc) - 1;
     const int h = bh % H, bi = bh / H, g = h / (H / G);
-    const int p0 = (pb * (W / X) + w / X) * 16, p = p0 + c, ptiles = P / 16, segs = (nc + kSegment<IO> - 1) / kSegment<IO>;
+    const int p0 = (pb * (W / X) + w / X) * 16, p = p0 + c, ptiles = P / 16, anchors = (nc + kSegment<IO> - 1) / kSegment<IO>;
     const bool live = p0 < P;
     const size_t hp = size_t(H) * P, gn = size_t(G) * N;
     const char *img = images + size_t(bh) * nc * Img::kBytes;
@@ -102,24 +108,25 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
             for (int r = 0; r < 4; ++r) v[r] = x == o ? float(a[o * kOwn + i][r]) : float(v[r]);
         return v;
     };
-    auto state_at = [&](int t) { return (size_t(bh) * P + p) * N + 32 * (n0 + (t >> 1)) + 8 * q + 4 * (t & 1); };
+    auto state_at = [&](int of, int t) { return (size_t(of) * P + p) * N + 32 * (n0 + (t >> 1)) + 8 * q + 4 * (t & 1); };
 
     f32x4 S[NT];        // dS
 #pragma unroll
     for (int t = 0; t < NT; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (d_final && live)
+    const float *from = seg == segs - 1 ? d_final : MAP ? nullptr : d_enter;
+    if (from && live)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) S[t] = *reinterpret_cast<const f32x4 *>(d_final + state_at(t));
+        for (int t = 0; t < NT; ++t) S[t] = *reinterpret_cast<const f32x4 *>(from + state_at(seg == segs - 1 ? bh : bh * segs + seg, t));
 #pragma unroll
     for (int i = 0; i < 16; ++i) ry[i] = IO(0);
-    fetch_main(nc - 1, lds0);
-    fetch_q(nc - 1);
-    fetch_dy(nc - 1);
+    fetch_main(last, lds0);
+    fetch_q(last);
+    fetch_dy(last);
     copies_done();
     __syncthreads();
 
-    for (int i = 0; i < nc; ++i) {
-        const int ch = nc - 1 - i, t0 = ch * kC, rows = min(kC, L - t0), next = max(ch - 1, 0);   // past the first: that one again
+    for (int i = 0; i <= last - first; ++i) {
+        const int ch = last - i, t0 = ch * kC, rows = min(kC, L - t0), next = max(ch - 1, first);     // past the first: that one again
         const char *buf = lds + (T::kBufs == 2 ? (i & 1) * T::kMain : 0);
         const char *tk = buf, *tq = T::kQMain ? buf + T::kRows : lds + T::kQt, *tm = buf + T::kImg + Img::kM, *ts = buf + T::kImg + Img::kQ;
         const float *gates = reinterpret_cast<const float *>(buf + T::kImg + Img::kGates);
@@ -130,9 +137,9 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
         auto gate_of = [&](int which, int t) {
             return *reinterpret_cast<const f32x4 *>(gates + which * kC + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
         };
-        if (live) {
+        if (!MAP && live) {
             if (ch % kSegment<IO> == kSegment<IO> - 1 || ch == nc - 1) {
-                const size_t at = (size_t(bh) * ptiles + p0 / 16) * segs + ch / kSegment<IO>;
+                const size_t at = (size_t(bh) * ptiles + p0 / 16) * anchors + ch / kSegment<IO>;
                 const f32x4 *a0 = anchor + (at * (N / 16) + x * NT) * 64 + lane;
                 float dot = 0.f;
 #pragma unroll
@@ -150,7 +157,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
             Op<IO, Pl::kS> so[KS];
 #pragma unroll
             for (int s = 0; s < KS; ++s) so[s] = to_op<IO, Pl::kS>(S[2 * s], S[2 * s + 1]);
-            {
+            if constexpr (!MAP) {
                 IO *dst = dSg + (unit * P + p) * N + 32 * n0 + 8 * q;
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
@@ -198,7 +205,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
             copies_done();      // q, asked for at the chunk's beginning
             __syncthreads();    // and the parts are written
         }
-        if (live) {     // what the end of the chunk needs: E and v of this wave's token tiles
+        if (!MAP && live) {     // what the end of the chunk needs: E and v of this wave's token tiles
             const f32x4 *src = E + (unit * ptiles + p0 / 16) * 256 + lane;
             const __amdgpu_buffer_rsrc_t view = chunk_view(vg + vy0 + size_t(t0) * hp, rows, tok, P);
             const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
@@ -268,7 +275,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
             }
             // the sums over the 16 rows (the 16 lanes of a row group), of this wave's token tiles
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) {
+            for (int j = 0; j < (MAP ? 0 : kOwn); ++j) {
                 const f32x4 du = own(dU, j), dvj = own(dv, j);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -279,7 +286,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
         }
         if constexpr (T::kBufs == 1) {
             __syncthreads();
-            if (ch > 0) {
+            if (ch > first) {
                 fetch_main(ch - 1, lds0);
                 fetch_q(ch - 1);
             }
@@ -287,7 +294,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
         copies_done();
         __syncthreads();
         if constexpr (T::kBufs == 2) fetch_q(next);     // this chunk's is read
-        if (live) {
+        if (!MAP && live) {
             const size_t at = (unit * ptiles + p0 / 16) * kC + 8 * q;
             const __amdgpu_buffer_rsrc_t view = chunk_view(dvg + vy0 + size_t(t0) * hp, rows, tok, P);
             const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
@@ -309,9 +316,9 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
         }
     }
     copies_done();      // of the last chunk's q, asked for once more
-    if (d_init && live)
+    if (d_out && live && (MAP || seg == 0))
 #pragma unroll
-        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(d_init + state_at(t)) = S[t];
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(d_out + state_at(MAP ? bh * segs + seg : bh, t)) = S[t];
 }
 
 // Kernel 4.  Block = (batch, chunk, group, one of `splits` parts of its heads' state rows);
@@ -609,24 +616,41 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
 
     hipError_t e = launch_delta_prep<IO, N, Pl::kM, Pl::kQ>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
     if (e != hipSuccess) return e;
-    int share = 1;
-    auto chains = [&](auto w_, auto x_) {
+    auto *map = reinterpret_cast<float *>(ws + pl.off_map), *init = reinterpret_cast<float *>(ws + pl.off_init);
+    auto *dmap = reinterpret_cast<float *>(ws + pl.off_dmap), *dinit = reinterpret_cast<float *>(ws + pl.off_dinit);
+    const DeltaCut &cut = pl.cut;
+    e = enter_segments<IO, N, Pl::kQ>(q, k, v, images, a.init_state, map, init, a.b, a.L, a.H, a.P, a.G, cut, a.scale, stream);
+    if (e != hipSuccess) return e;
+    auto back = [&](auto w_, auto x_, auto map_, float *to) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
+        constexpr bool MAP = decltype(map_)::value;
         constexpr int lds = ChainLds<IO, N, W, X, Pl::kQ, false>::kBytes;
-        const int per = 16 * W / X, pblocks = (a.P + per - 1) / per;
-        const dim3 grid(unsigned(a.b * a.H * pblocks));
-        share = X;
-        e = launch_chain<IO, N, W, X, Chain::save, Pl::kQ>(q, k, v, images, a.init_state, nullptr, nullptr, dy, saved, a.b, a.L, a.H, a.P, a.G, nc, 1,
-                                                           a.scale, stream);
+        const int rows = 16 * W / X, pblocks = (a.P + rows - 1) / rows;
+        auto kern = k_delta_chain_back<IO, N, W, X, MAP>;
+        e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
-        auto back = k_delta_chain_back<IO, N, W, X>;
-        e = hipFuncSetAttribute(reinterpret_cast<const void *>(back), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(back, grid, dim3(64 * W), lds, stream, q, k, v, dy, images, a.d_final, reinterpret_cast<const f32x4 *>(saved.E),
-                           reinterpret_cast<const f32x4 *>(saved.anchor), dv, dS, a.d_init, sums, a.L, a.H, a.P, a.G, nc, pblocks, a.scale);
+        hipLaunchKernelGGL(kern, dim3(unsigned(int64_t(a.b) * a.H * (cut.segments - (MAP ? 1 : 0)) * pblocks)), dim3(64 * W), lds, stream, q, k,
+                           v, dy, images, a.d_final, dinit, reinterpret_cast<const f32x4 *>(saved.E),
+                           reinterpret_cast<const f32x4 *>(saved.anchor), dv, dS, to, sums, a.L, a.H, a.P, a.G, nc, cut.per, cut.segments,
+                           pblocks, a.scale);
         return hipGetLastError();
     };
-    if ((e = with_chain_shape<IO, N>(int64_t(a.b) * a.H * ptiles, chains)) != hipSuccess) return e;
+    const int64_t tiles = int64_t(a.b) * a.H * ptiles;
+    if (cut.segments > 1) {
+        auto go = [&](auto w, auto x) { return back(w, x, std::true_type{}, dmap); };
+        if ((e = with_chain_shape<IO, N>(tiles * (cut.segments - 1), go)) != hipSuccess) return e;
+        hipLaunchKernelGGL((k_delta_carry<N, true>), dim3(unsigned(tiles)), dim3(4 * N), 0, stream, map, dmap, nullptr, dinit, a.P, cut.segments);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    int share = 1;      // waves per tile, each with its own part of the sums
+    auto chains = [&](auto w_, auto x_) {
+        constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
+        share = X;
+        e = launch_chain<IO, N, W, X, Chain::save, Pl::kQ>(q, k, v, images, cut.segments > 1 ? init : a.init_state, nullptr, nullptr, dy, saved,
+                                                           a.b, a.L, a.H, a.P, a.G, cut.per, cut.segments, a.scale, stream);
+        return e != hipSuccess ? e : back(w_, x_, std::false_type{}, a.d_init);
+    };
+    if ((e = with_chain_shape<IO, N>(tiles * cut.segments, chains)) != hipSuccess) return e;
     auto grads = k_delta_grads<IO, N>;
     constexpr int lds = GradTile<IO, N>::kLds;
     e = hipFuncSetAttribute(reinterpret_cast<const void *>(grads), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -682,6 +706,11 @@ DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16)
     pl.off_vdv = take(units * ptiles * kC * 4);
     pl.off_lam = take(bh * ptiles * segs * kMaxShare * 4);
     pl.splits = grad_splits(size_t(b) * G * nc, size_t(H / G) * ((P + 63) / 64), N, bf16);
+    pl.cut = cut_sequence(int64_t(bh), int(nc), P, N, bf16, true);
+    pl.off_map = take(map_bytes(bh, P, N, pl.cut));
+    pl.off_init = take(entering_bytes(bh, P, N, pl.cut));
+    pl.off_dmap = take(entering_bytes(bh, P, N, pl.cut));
+    pl.off_dinit = take(entering_bytes(bh, P, N, pl.cut));
     pl.off_parts = take(pl.splits > 1 ? size_t(pl.splits) * 2 * b * L * G * N * 4 : 0);
     pl.total = at;
     pl.supported = true;

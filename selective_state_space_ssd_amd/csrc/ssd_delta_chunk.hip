@@ -41,8 +41,10 @@ hipError_t launch_n(const DeltaChunkArgs &a, const DeltaChunkPlan &pl, hipStream
 //                       32 heads, 4096: 220 -> 196 -> 197, 16384: 864 -> 696 -> 692
 //   fp32, P = N = 64:   24 heads, 1600 tokens 140 -> 92 -> 84, 16384: 1228 -> 502 -> 497
 // and over 360 shapes of 1 to 64 heads and 256 to 16384 tokens as fast as that best in the
-// mean, 1.27 times as long at the most.
-DeltaCut cut_sequence(int64_t bh, int nc, int P, int N, bool bf16) {
+// mean, 1.27 times as long at the most.  Backward, 144 shapes: the same, 1.25 at the most;
+//   bf16, P = 64, N = 128:  24 heads, 2048 tokens 304 -> 213 -> 213, 6000: 804 -> 431 -> 429
+//   fp32, P = N = 64:   4 heads, 777 tokens 190 -> 127 -> 126, 6000: 1062 -> 199 -> 199
+DeltaCut cut_sequence(int64_t bh, int nc, int P, int N, bool bf16, bool back) {
     const bool wide = N * (bf16 ? 2 : 4) > 256;     // blocks of 8 waves for 2 tiles
     auto step = [&](int64_t tiles) {
         if (wide) return tiles <= kSimds / 4 ? 1.0 : 1.75 * double((tiles + kSimds / 2 - 1) / (kSimds / 2));
@@ -50,11 +52,13 @@ DeltaCut cut_sequence(int64_t bh, int nc, int P, int N, bool bf16) {
     };
     const double carry = N == 256 ? 1.5 : N == 128 ? 0.35 : 0.2, launches = 2.0;
     DeltaCut best{1, nc};
-    double least = 0.95 * nc * step(bh * (P / 16));      // no cut for less than a twentieth
+    // backward: a chain each way, and the chain back over zeros for its map
+    const double passes = back ? 2.0 : 1.0, extra = back ? 0.8 : 0.0;
+    double least = 0.95 * nc * passes * step(bh * (P / 16));      // no cut for less than a twentieth
     for (int s = 2; s <= std::min(nc / 2, 64); ++s) {
         const int per = (nc + s - 1) / s;
         if ((nc + per - 1) / per != s) continue;
-        const double c = per * (step(bh * s * (P / 16)) + 0.8 * step(bh * (s - 1) * ((P + N) / 16))) + carry * s + launches;
+        const double c = per * ((passes + extra) * step(bh * s * (P / 16)) + 0.8 * step(bh * (s - 1) * ((P + N) / 16))) + passes * (carry * s + launches);
         if (c < least) {
             least = c;
             best = {s, per};
@@ -79,7 +83,7 @@ DeltaChunkPlan plan_delta_chunk(int b, int L, int H, int P, int N, int G, bool b
     const int nc = (L + kC - 1) / kC;
     const size_t bh = size_t(b) * H;
     pl.total = bh * nc * (bf16 ? ChunkImage<bf16_bits, Pl::kM, Pl::kQ>::kBytes : ChunkImage<float, Pl::kM, Pl::kQ>::kBytes);
-    pl.cut = cut_sequence(int64_t(bh), nc, P, N, bf16);
+    pl.cut = cut_sequence(int64_t(bh), nc, P, N, bf16, false);
     pl.off_map = pl.total;
     pl.off_init = pl.off_map + map_bytes(bh, P, N, pl.cut);
     pl.total = pl.off_init + entering_bytes(bh, P, N, pl.cut);

@@ -55,3 +55,8 @@ def tol_out(dtype, L, N, roundings):
 # rows lie past the head, and many chunks
 MANY = [(1, 70, 132, 1, 64, 64), (1, 70, 40, 1, 208, 64), (1, 70, 70, 2, 64, 128), (1, 70, 18, 2, 240, 128), (1, 70, 132, 2, 64, 128),
         (1, 66, 70, 2, 64, 256), (1, 66, 18, 3, 240, 256), (9, 900, 8, 4, 16, 32)]
+
+# b, L, H, G, P, N of sequences long enough for their few heads to be cut into segments: a
+# ragged last segment, blocks that end in the middle of a head's rows, every state width
+CUT = [(1, 64 * 16, 1, 1, 16, 32), (1, 64 * 40 - 63, 2, 1, 48, 64), (2, 64 * 30 + 1, 1, 1, 80, 128), (1, 2500, 3, 1, 32, 128), (1, 1600, 1, 1, 64, 256),
+       (1, 64 * 100, 1, 1, 16, 64)]

@@ -9,7 +9,7 @@ import math
 import pytest
 import torch
 
-from delta_helpers import MANY, U32, inputs_of, make, rel, tol32, tol_out
+from delta_helpers import CUT, MANY, U32, inputs_of, make, rel, tol32, tol_out
 from oracle import delta
 from selective_state_space_ssd_amd import binding as bd
 
@@ -201,7 +201,7 @@ def test_prefill_then_decode():
     assert rel(state, S) <= 2 * tol32(100, 64)
 
 
-@pytest.mark.parametrize("L", [8, 200])
+@pytest.mark.parametrize("L", [8, 200, 2000])
 def test_captured_and_replayed(L):
     c = make(2, L, 4, 2, 64, 128, BF, seed=21)
     n = bd.ssd_gated_delta_fwd_workspace_bytes(2, L, 4, 64, 128, 2, bd.SSD_DTYPE_BF16)
@@ -238,12 +238,6 @@ def test_two_streams_at_once():
         s.synchronize()
     for g, w in zip(got, want):
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
-
-
-# b, L, H, G, P, N of sequences long enough for their few heads to be cut into segments: a
-# ragged last segment, blocks that end in the middle of a head's rows, every state width
-CUT = [(1, 64 * 16, 1, 1, 16, 32), (1, 64 * 40 - 63, 2, 1, 48, 64), (2, 64 * 30 + 1, 1, 1, 80, 128), (1, 2500, 3, 1, 32, 128), (1, 1600, 1, 1, 64, 256),
-       (1, 64 * 100, 1, 1, 16, 64)]
 
 
 @pytest.mark.parametrize("b,L,H,G,P,N", CUT)

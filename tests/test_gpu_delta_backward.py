@@ -11,7 +11,7 @@ import math
 import pytest
 import torch
 
-from delta_helpers import MANY, U32, inputs_of, make, rel, tol32, tol_out
+from delta_helpers import CUT, MANY, U32, inputs_of, make, rel, tol32, tol_out
 from oracle import delta
 from selective_state_space_ssd_amd import binding as bd
 
@@ -76,6 +76,18 @@ def test_many_heads_or_chunks(b, L, H, G, P, N, dtype):
     if N == 256 and dtype == F32:
         pytest.skip("fp32 gradients go up to N = 128")
     check(make(b, L, H, G, P, N, dtype, seed=L + N), N ** -0.5, L, N, dtype)
+
+
+@pytest.mark.parametrize("b,L,H,G,P,N", CUT)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("init", [False, True])
+def test_cut_into_segments(b, L, H, G, P, N, dtype, init):
+    if N == 256 and dtype == F32:
+        pytest.skip("fp32 gradients go up to N = 128")
+    c = make(b, L, H, G, P, N, dtype, seed=L + N, init=init)
+    if not init:
+        c["d_final"] = None
+    check(c, N ** -0.5, L, N, dtype)
 
 
 def test_widest_state():
@@ -180,10 +192,11 @@ def test_no_tokens():
     assert torch.equal(got[5], c["d_final"]) and got[0].shape == (2, 0, 1, 32)
 
 
-def test_captured_and_replayed():
-    c = make(1, 150, 4, 2, 64, 128, BF, seed=21)
+@pytest.mark.parametrize("L", [150, 1600])
+def test_captured_and_replayed(L):
+    c = make(1, L, 4, 2, 64, 128, BF, seed=21)
     outs = [torch.empty_like(c[n]) for n in ("q", "k", "v", "a", "beta", "init_state")]
-    ws = torch.empty(bd.ssd_gated_delta_bwd_workspace_bytes(1, 150, 4, 64, 128, 2, bd.SSD_DTYPE_BF16), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(bd.ssd_gated_delta_bwd_workspace_bytes(1, L, 4, 64, 128, 2, bd.SSD_DTYPE_BF16), dtype=torch.uint8, device="cuda")
 
     def step():
         bd.ssd_gated_delta_bwd(*inputs_of(c), c["init_state"], c["dy"], c["d_final"], *outs, 0.5, ws)
@@ -194,7 +207,7 @@ def test_captured_and_replayed():
     with torch.cuda.graph(graph):
         step()
     for seed in range(3):
-        c["dy"].copy_(make(1, 150, 4, 2, 64, 128, BF, seed=30 + seed)["dy"])
+        c["dy"].copy_(make(1, L, 4, 2, 64, 128, BF, seed=30 + seed)["dy"])
         graph.replay()
         torch.cuda.synchronize()
         got = [t.clone() for t in outs]
