@@ -385,7 +385,7 @@ __global__ __launch_bounds__(256, (GradTile<IO, N>::kPerCu)) void k_delta_grads(
                     const double o = __shfl_up(s, off, 64);
                     if (lane >= off) s += o;
                 }
-                gd[lane] = s * kLog2e;
+                gd[lane] = s;
             }
             // dY, dv: rows of tokens (past the end: the last one, masked below); S, dS: rows p
             const size_t src = (size_t(bi) * L + t0) * hp + size_t(h) * P + pb;
@@ -456,7 +456,7 @@ __global__ __launch_bounds__(256, (GradTile<IO, N>::kPerCu)) void k_delta_grads(
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + i;
-                    const float d = decay(j <= tok ? gt - gd[j] : 0.0);
+                    const float x = float(gt - gd[j]), d = expf(j <= tok ? x : 0.f);
                     const float wv = scale * d * zw[0][i], fv = -d * zf[0][i];
                     Wm[t][i] += j <= tok && tok < rows ? wv : 0.f;
                     Fm[t][i] += j < tok && tok < rows ? fv : 0.f;

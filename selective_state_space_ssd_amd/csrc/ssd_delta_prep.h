@@ -66,7 +66,7 @@ __global__ __launch_bounds__(256, 3) void k_delta_prep(const IO *__restrict__ qg
     __shared__ float sbs[kPrepHeads][kC];
     __shared__ __align__(16) float mm[kC * kLd], sc[kC * kLd];  // Lo, then M over it; scores
     float *yt = sc;                                             // later [32][33] of it
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, q = lane >> 4;
     const int r = H / G, hblocks = (r + hb - 1) / hb;
     const int ch = blockIdx.x % nc, hblk = blockIdx.x / nc % hblocks, bg = blockIdx.x / nc / hblocks;
     const int g = bg % G, bi = bg / G;
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256, 3) void k_delta_prep(const IO *__restrict__ qg
             if (lane >= off) s += o;
         }
         const double end = __shfl(s, 63, 64);
-        gd[w][lane] = s * kLog2e;
+        gd[w][lane] = s;
         sbs[w][lane] = bt;
         float *gates = reinterpret_cast<float *>(image(w) + Img::kGates);
         gates[lane] = expf(float(s));
@@ -125,28 +125,15 @@ __global__ __launch_bounds__(256, 3) void k_delta_prep(const IO *__restrict__ qg
         const float *sb = sbs[j];
         char *img = image(j);
         __syncthreads();            // the gates; the last head's matrices are written out
-        double gk[4], gq[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            gk[i] = gd[j][16 * w + 4 * q + i];
-            gq[i] = gd[j][16 * wq + 4 * q + i];
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int col = 16 * t + c;
-            const double gc = gd[j][col];
-            // above the diagonal: zeros, and no decay is taken in the tiles there
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int rk = 16 * w + 4 * q + i;
-                mm[rk * kLd + col] = t <= w ? col < rk ? kk[t][i] * decay(gk[i] - gc) : 0.f : 0.f;
+                // above the diagonal: zeros (the tiles there are zero, their decay unused)
+                const int col = 16 * t + c, rk = 16 * w + 4 * q + i, rq = 16 * wq + 4 * q + i;
+                mm[rk * kLd + col] = col < rk ? kk[t][i] * expf(float(gd[j][rk] - gd[j][col])) : 0.f;
+                sc[rq * kLd + col] = col <= rq ? scale * qk[t][i] * expf(float(gd[j][rq] - gd[j][col])) : 0.f;
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int rq = 16 * wq + 4 * q + i;
-                sc[rq * kLd + col] = t <= wq ? col <= rq ? scale * qk[t][i] * decay(gq[i] - gc) : 0.f : 0.f;
-            }
-        }
         __syncthreads();
         if (w > 0) {    // the other waves write the scores out meanwhile
             write_image<IO, Img::kPlanesQ>(sc, img + Img::kQ, tid - 64, 192);
