@@ -372,6 +372,7 @@ __global__ __launch_bounds__(256, (GradTile<IO, N>::kPerCu)) void k_delta_grads(
 
     {
         const int pbs = (P + 63) / 64, turns = r * pbs;
+        constexpr int kWarm = (2 * T::kState / 128 + 255) / 256;
         const int first = int(int64_t(turns) * split / splits), end = int(int64_t(turns) * (split + 1) / splits);
         for (int turn = first; turn < end; ++turn) {    // head h, rows pb .. pb + 63 of its state
             const int h = g * r + turn / pbs, pb = turn % pbs * 64;
@@ -422,6 +423,24 @@ __global__ __launch_bounds__(256, (GradTile<IO, N>::kPerCu)) void k_delta_grads(
             }
             copies_done();
             __syncthreads();
+            // one word of each 128 bytes of what the next turn reads, so that it is in the L2
+            // by then: the states, E, dY and dv
+            uint32_t warm[kWarm + 1];
+            {
+                const int nt = min(turn + 1, end - 1), nh = g * r + nt / pbs, npb = nt % pbs * 64;
+                const size_t nu = (size_t(bi) * H + nh) * nc + ch;
+#pragma unroll
+                for (int i = 0; i < kWarm; ++i) {
+                    const int at = (i * 256 + tid) * 128 % T::kState, row = min(at / T::RB, P - npb - 1);
+                    const IO *of = (i * 256 + tid) * 128 < T::kState ? Sg : dSg;
+                    warm[i] = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const char *>(of + (nu * P + npb + row) * N) + at % T::RB);
+                }
+                const int row = min(tid & 63, rows - 1);
+                const size_t src = (size_t(bi) * L + t0 + row) * hp + size_t(nh) * P + npb;
+                const char *of = w < 2 ? reinterpret_cast<const char *>(E + (nu * ptiles + min(npb / 16 + (tid >> 5), ptiles - 1)) * 256) + (tid & 31) * 128
+                                       : reinterpret_cast<const char *>((w == 2 ? dyg : dvg) + src);
+                warm[kWarm] = *reinterpret_cast<const uint32_t *>(of);
+            }
             if (P - pb < 64) {      // rows p past the head: the copies hold others there
                 for (int i = tid + (P - pb) * (T::RB / 16); i < T::kState / 16; i += 256)
                     *reinterpret_cast<u32x4 *>(lds + T::kS + i * 16) = u32x4{0, 0, 0, 0};
@@ -469,6 +488,8 @@ __global__ __launch_bounds__(256, (GradTile<IO, N>::kPerCu)) void k_delta_grads(
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
+#pragma unroll
+            for (int i = 0; i <= kWarm; ++i) asm volatile("" : : "v"(warm[i]));
         }
     }
     __syncthreads();
