@@ -31,6 +31,12 @@ constexpr int kC = 64;      // tokens per chunk
 // in any case, and the sums (in 64 bits) keep the digits of the small ones beside it.
 __device__ __forceinline__ double gate(float a) { return a < -1e5f ? -1e5 : double(a); }
 
+// The decay of a difference of gate sums that are kept in units of ln 2: one exp2 of the
+// hardware (one unit in the last place) where e^x takes a dozen instructions; the difference
+// loses what it loses in rounding to 32 bits either way.  Below 2^-126 it is 0.
+constexpr double kPerLn2 = 1.4426950408889634;
+__device__ __forceinline__ float decay(double x) { return __builtin_amdgcn_exp2f(float(x)); }
+
 // LDS tiles: rows of RB bytes in chunks of 16; chunk `ch` of row r lies at ch ^ place(r).
 // A 128-bit read serves 16 lanes a cycle, lanes {0-3, 12-15, 20-27} and {4-11, 16-19,
 // 28-31} and the same 32 further on, from 64 banks; a 64-bit read the 32 lanes of a half.

@@ -8,9 +8,10 @@
 // for the blocks below the diagonal, 16 then 32 wide, on the fp32 matrix instruction.  No
 // power of Lo is formed, so keys that repeat do not make the terms grow.
 //
-// 4096 chunks of a head (4 x 2048 tokens, 32 heads in 8 groups, bf16, N = 128) take 49 us and
-// write 130 MB of images, 2.65 TB/s: half of what a copy reads and writes in that time, and
-// the decays at a twelfth of their instructions do not change it.
+// 4096 chunks of a head (4 x 2048 tokens, 32 heads in 8 groups, bf16, N = 128) take 43 us and
+// write 130 MB of images, 3.0 TB/s (a fill reaches 7): a head is seven steps between
+// barriers, and 4 blocks a CU cover for each other.  With registers for 3, 52; 49 with a
+// library e^x and decays above the diagonal too.
 #pragma once
 
 #include <algorithm>
@@ -61,7 +62,7 @@ __device__ __forceinline__ void write_image(const float *m, char *dst, int first
 constexpr int kPrepHeads = 4;
 
 template <typename IO, int N, int NM, int NQ>
-__global__ __launch_bounds__(256, 3) void k_delta_prep(const IO *__restrict__ qg, const IO *__restrict__ kg,
+__global__ __launch_bounds__(256, 4) void k_delta_prep(const IO *__restrict__ qg, const IO *__restrict__ kg,
                                                     const float *__restrict__ a, const float *__restrict__ beta,
                                                     char *__restrict__ images, int L, int H, int G, int nc, int hb,
                                                     float scale) {
@@ -70,7 +71,7 @@ __global__ __launch_bounds__(256, 3) void k_delta_prep(const IO *__restrict__ qg
     __shared__ float sbs[kPrepHeads][kC];
     __shared__ __align__(16) float mm[kC * kLd], sc[kC * kLd];  // Lo, then M over it; scores
     float *yt = sc;                                             // later [32][33] of it
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, q = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
     const int r = H / G, hblocks = (r + hb - 1) / hb;
     const int ch = blockIdx.x % nc, hblk = blockIdx.x / nc % hblocks, bg = blockIdx.x / nc / hblocks;
     const int g = bg % G, bi = bg / G;
@@ -88,7 +89,7 @@ __global__ __launch_bounds__(256, 3) void k_delta_prep(const IO *__restrict__ qg
             if (lane >= off) s += o;
         }
         const double end = __shfl(s, 63, 64);
-        gd[w][lane] = s;
+        gd[w][lane] = s * kPerLn2;
         sbs[w][lane] = bt;
         float *gates = reinterpret_cast<float *>(image(w) + Img::kGates);
         gates[lane] = expf(float(s));
@@ -129,15 +130,28 @@ __global__ __launch_bounds__(256, 3) void k_delta_prep(const IO *__restrict__ qg
         const float *sb = sbs[j];
         char *img = image(j);
         __syncthreads();            // the gates; the last head's matrices are written out
+        double gk[4], gq[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int i = 0; i < 4; ++i) {
+            gk[i] = gd[j][16 * w + 4 * q + i];
+            gq[i] = gd[j][16 * wq + 4 * q + i];
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int col = 16 * t + c;
+            const double gc = gd[j][col];
+            // above the diagonal: zeros, and no decay is taken in the tiles there
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                // above the diagonal: zeros (the tiles there are zero, their decay unused)
-                const int col = 16 * t + c, rk = 16 * w + 4 * q + i, rq = 16 * wq + 4 * q + i;
-                mm[rk * kLd + col] = col < rk ? kk[t][i] * expf(float(gd[j][rk] - gd[j][col])) : 0.f;
-                sc[rq * kLd + col] = col <= rq ? scale * qk[t][i] * expf(float(gd[j][rq] - gd[j][col])) : 0.f;
+                const int rk = 16 * w + 4 * q + i;
+                mm[rk * kLd + col] = t <= w ? col < rk ? kk[t][i] * decay(gk[i] - gc) : 0.f : 0.f;
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int rq = 16 * wq + 4 * q + i;
+                sc[rq * kLd + col] = t <= wq ? col <= rq ? scale * qk[t][i] * decay(gq[i] - gc) : 0.f : 0.f;
+            }
+        }
         __syncthreads();
         if (w > 0) {    // the other waves write the scores out meanwhile
             write_image<IO, Img::kPlanesQ>(sc, img + Img::kQ, tid - 64, 192);
