@@ -20,7 +20,7 @@
 
 namespace ssd {
 
-constexpr int kLd = kC + 1;     // LDS row of the fp32 work matrices
+constexpr int kLd = kC + 4;     // LDS row of the fp32 work matrices: 16-byte pieces, rows 4 banks apart
 
 template <typename IO>
 __device__ __forceinline__ Op<IO, 1> load_row8(const IO *p) {
@@ -48,9 +48,9 @@ __device__ __forceinline__ void write_image(const float *m, char *dst, int first
         const int col = (pos ^ (top ? place<kRowTop>(r) : place<kRow>(r))) * E;
         const float *s = m + (top ? r : 32 + r) * kLd + col;
         if constexpr (std::is_same_v<IO, float>) {
-            *reinterpret_cast<float4 *>(dst + i * 16) = make_float4(s[0], s[1], s[2], s[3]);
+            *reinterpret_cast<f32x4 *>(dst + i * 16) = *reinterpret_cast<const f32x4 *>(s);
         } else {
-            const Op<IO, NP> o = to_op<IO, NP>(f32x4{s[0], s[1], s[2], s[3]}, f32x4{s[4], s[5], s[6], s[7]});
+            const Op<IO, NP> o = to_op<IO, NP>(*reinterpret_cast<const f32x4 *>(s), *reinterpret_cast<const f32x4 *>(s + 4));
 #pragma unroll
             for (int p = 0; p < NP; ++p)
                 *reinterpret_cast<uint4 *>(dst + p * Img::kPlane + i * 16) = __builtin_bit_cast(uint4, o.p[p]);
@@ -162,15 +162,13 @@ __global__ __launch_bounds__(256, 4) void k_delta_prep(const IO *__restrict__ qg
 #pragma unroll
             for (int i = 1; i < 16; ++i) m[i] = -l0[i * kLd + c];
 #pragma unroll
-            for (int k0 = 0; k0 < 16; k0 += 4) {    // 4 columns of Lo in registers at a time
-                float lo[16][4];
+            for (int k0 = 0; k0 < 16; k0 += 2) {    // 2 columns of Lo in registers at a time
+                f32x2 lo[16];
 #pragma unroll
-                for (int i = k0 + 1; i < 16; ++i)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) lo[i][k] = l0[i * kLd + k0 + k];
+                for (int i = k0 + 1; i < 16; ++i) lo[i] = *reinterpret_cast<const f32x2 *>(l0 + i * kLd + k0);
                 asm volatile("" ::: "memory");
 #pragma unroll
-                for (int k = k0 == 0 ? 1 : 0; k < 4; ++k) {
+                for (int k = k0 == 0 ? 1 : 0; k < 2; ++k) {
                     const float bm = m[k0 + k] * sb[16 * q + k0 + k];
 #pragma unroll
                     for (int i = k0 + k + 1; i < 16; ++i) m[i] -= lo[i][k] * bm;
