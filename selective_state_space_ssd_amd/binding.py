@@ -441,9 +441,12 @@ class _NoSwitch:
         return False
 
 
+_NO_SWITCH = _NoSwitch()
+
+
 def _allocating_on(stream):
     """What a wrapper allocates for work on ``stream`` is allocated on that stream."""
-    return _NoSwitch() if stream is None else torch.cuda.stream(stream)
+    return _NO_SWITCH if stream is None else torch.cuda.stream(stream)
 
 
 def _scratch(nbytes, device) -> Optional[torch.Tensor]:
@@ -457,9 +460,11 @@ def _workspace_arg(workspace, device):
 
 
 def _delta_dims(k, v):
-    if k.dim() != 4 or v.dim() != 4:
-        raise ValueError("q and k are [b, L, G, N], v is [b, L, H, P]")
-    return (*v.shape, k.shape[3], k.shape[2])
+    try:
+        (b, L, H, P), (_, _, G, N) = v.shape, k.shape
+    except ValueError:
+        raise ValueError("q and k are [b, L, G, N], v is [b, L, H, P]") from None
+    return b, L, H, P, N, G
 
 
 def ssd_gated_delta_step(state_in, q, k, v, a, beta, accept_len, y, state_out, scale, err_flag=None,
@@ -677,7 +682,7 @@ def gated_delta_fwd(q, k, v, a, beta, scale, init_state=None, workspace=None, st
     b, L, H, P, N, G = _delta_dims(k, v)
     with _allocating_on(stream):
         y = torch.empty_like(v)
-        final_state = torch.empty((b, H, P, N), dtype=torch.float32, device=v.device)
+        final_state = torch.empty((b, H, P, N), dtype=torch.float32, device=v.device) if init_state is None else torch.empty_like(init_state)
         if workspace is None:
             workspace = _scratch(ssd_gated_delta_fwd_workspace_bytes(b, L, H, P, N, G, _io_code(v)), v.device)
     ssd_gated_delta_fwd(q, k, v, a, beta, init_state, y, final_state, scale, workspace, stream)
