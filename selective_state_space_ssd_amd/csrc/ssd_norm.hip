@@ -199,7 +199,8 @@ __global__ __launch_bounds__(kBlock) void k_norm_gate_bwd(const IO *__restrict__
                 const float v = FIRST ? u[i][j] * act[i][j] : u[i][j];
                 ss += v * v;
             }
-        const float r = 1.f / sqrtf(team_sum<TPS>(ss, tmp) / float(group) + eps);
+        const float sq = team_sum<TPS>(ss, tmp);
+        const float r = on ? 1.f / sqrtf(sq / float(group) + eps) : 0.f;    // no row: its zeros add nothing, eps = 0 too
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -324,7 +325,8 @@ __global__ __launch_bounds__(kBlock) void k_norm_add_bwd(const IO *__restrict__ 
 #pragma unroll
             for (int j = 0; j < VEC; ++j) ss += s[i][j] * s[i][j];
         }
-        const float r = 1.f / sqrtf(team_sum<TPS>(ss, tmp) / float(D) + eps);
+        const float sq = team_sum<TPS>(ss, tmp);
+        const float r = on ? 1.f / sqrtf(sq / float(D) + eps) : 0.f;    // no row: its zeros add nothing, eps = 0 too
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)

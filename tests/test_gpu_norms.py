@@ -181,3 +181,19 @@ def test_on_another_stream():
     got = bd.norm_gate_fwd(x, z, w, 640, EPS, stream=side)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_parameter_gradients_without_eps(dtype):
+    """eps = 0 and more rows than the backward pass has blocks, not a multiple of them: the
+    blocks without a row in the last turn add nothing."""
+    rows, D = 1500, 520
+    x, z, dy = (draw((rows, D), dtype, s) for s in (1, 2, 3))
+    w = draw((D,), F32, 4, 0.2, 1.0)
+    for gate_first in (False, True):
+        _, _, dw = bd.norm_gate_bwd(x, z, w, dy, D, 0.0, gate_first)
+        assert rel(dw, norms.norm_gate_grads_f64(x, z, w, dy, D, 0.0, gate_first)[2]) <= par_tol(D, rows)
+    scale = draw((D,), F32, 6, 0.1, 0.5)
+    _, _, dw, dscale = bd.norm_add_bwd(x, x, w, dy, None, 0.0, scale=scale)
+    _, _, ew, escale = norms.norm_add_grads_f64(x, x, w, dy, None, 0.0, scale)
+    assert rel(dw, ew) <= par_tol(D, rows) and rel(dscale, escale) <= 2 * par_tol(D, rows)
