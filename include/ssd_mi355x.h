@@ -463,7 +463,8 @@ ssd_status_t ssd_chunk_scan_bwd(const void *x, const float *dt, const float *A, 
  *   (NULL = skip) is the state after the last token.  N in {16, 32, 64, 128, 256}, any
  *   P >= 1.  workspace: ssd_gated_delta_fwd_workspace_bytes bytes ((size_t)-1: dimensions
  *   this build does not run), 16-byte aligned, scratch without preparation; calls that
- *   overlap in time need one each.  L = 0 copies init_state (or zeros) to final_state.
+ *   overlap in time need one each.  Short sequences, P that is no multiple of 16, N = 16, and
+ *   N = 256 with fp32 I/O go token by token, the others in chunks.  L = 0 copies init_state (or zeros) to final_state.
  *   q, k, v, y, states 16-byte aligned, a and beta 4-byte.
  *
  * ssd_gated_delta_bwd: from dy (of y) and d_final (of final_state; NULL = zero) the

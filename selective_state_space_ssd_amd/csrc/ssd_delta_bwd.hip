@@ -18,11 +18,12 @@
 // 2 and 3 are chains over the chunks whose waves keep 16 rows of the state each, as in the
 // forward pass: 32-bit values throughout, since da and dbeta come out of differences.
 //
-// 4 x 2048 tokens, 32 heads of 128 x 128, bf16, us: prep 64, chain 197, chain back 250, grads
-// 177, gates 15.  The chains are bound by a wave's steps (ssd_delta_chain.h); grads reads
-// 540 MB (E, both states, dy, dv), 3.0 TB/s: a block waits for each turn's copies, and only
+// 4 x 2048 tokens, 32 heads of 128 x 128, bf16, us: prep 46, chain 197, chain back 250, grads
+// 163, gates 15.  The chains are bound by a wave's steps (ssd_delta_chain.h); grads reads
+// 540 MB (E, both states, dy, dv), 3.3 TB/s: a block waits for each turn's copies, and only
 // the other block of its CU works meanwhile (a second set of tiles does not fit the LDS, the
-// states' copies a turn ahead do not fit the registers).
+// states' copies a turn ahead do not fit the registers; what fits is asking them into the
+// L2, 175 us without).
 #include <algorithm>
 
 #include "ssd_delta.h"
