@@ -19,7 +19,7 @@
 // forward pass: 32-bit values throughout, since da and dbeta come out of differences.
 //
 // 4 x 2048 tokens, 32 heads of 128 x 128, bf16, us: prep 46, chain 197, chain back 250, grads
-// 163, gates 15.  The chains are bound by a wave's steps (ssd_delta_chain.h); grads reads
+// 163, gates 9.  The chains are bound by a wave's steps (ssd_delta_chain.h); grads reads
 // 540 MB (E, both states, dy, dv), 3.3 TB/s: a block waits for each turn's copies, and only
 // the other block of its CU works meanwhile (a second set of tiles does not fit the LDS, the
 // states' copies a turn ahead do not fit the registers; what fits is asking them into the
@@ -602,13 +602,17 @@ __global__ __launch_bounds__(64 * SEG) void k_delta_gates(const float *__restric
     const int ch = seg * SEG + w, t = ch * kC + lane;
     double d = 0.0;
     float b = 0.f;
-    if (ch < nc)
+    if (ch < nc) {
+        const size_t unit = size_t(bh) * nc + ch, at = unit * ptiles * kC + lane;
+        const float *y = ydy + unit * parts * ptiles * kC + lane;
+#pragma unroll 8
+        for (int i = 0; i < parts * ptiles; ++i) d += double(y[i * kC]);
+#pragma unroll 8
         for (int i = 0; i < ptiles; ++i) {
-            const size_t unit = size_t(bh) * nc + ch, at = (unit * ptiles + i) * kC + lane;
-            for (int x = 0; x < parts; ++x) d += double(ydy[((unit * parts + x) * ptiles + i) * kC + lane]);
-            d -= double(vdv[at]);
-            b += xe[at];
+            d -= double(vdv[at + i * kC]);
+            b += xe[at + i * kC];
         }
+    }
     if (t >= L) d = 0.0;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -618,8 +622,11 @@ __global__ __launch_bounds__(64 * SEG) void k_delta_gates(const float *__restric
     if (lane == 0) total[w] = d;
     __syncthreads();
     for (int i = w + 1; i < SEG; ++i) d += total[i];
-    for (int i = 0; i < ptiles; ++i)
-        for (int x = 0; x < parts; ++x) d += double(lam[((size_t(bh) * ptiles + i) * segs + seg) * parts + x]);
+    double dot = 0.0;       // <dS, S>, lane i one part of it
+    for (int i = lane; i < ptiles * parts; i += 64) dot += double(lam[((size_t(bh) * ptiles + i / parts) * segs + seg) * parts + i % parts]);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) dot += __shfl_xor(dot, off, 64);
+    d += dot;
     if (ch < nc && t < L) {
         const size_t at = (size_t(bi) * L + t) * H + h;
         da[at] = float(d);
