@@ -44,7 +44,7 @@ struct BackSums {
 // what leaves the others is in `d_enter`.  MAP: of the segments 1 .. segs - 1, only the
 // gradient of the state that enters each, into d_out [segs], with 0 for what leaves the
 // others; the forward maps tell what d_enter adds to it.
-template <typename IO, int N, int W, int X, bool MAP>
+template <typename IO, int N, int W, int X, bool MAP, bool ONE>
 __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restrict__ qg, const IO *__restrict__ kg,
                                                              const IO *__restrict__ vg, const IO *__restrict__ dyg,
                                                              const char *__restrict__ images, const float *__restrict__ d_final,
@@ -54,7 +54,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
                                                              int H, int P, int G, int nc, int per, int segs, int pblocks,
                                                              float scale) {
     using Pl = DeltaPlanes<true>;
-    using T = ChainLds<IO, N, W, X, Pl::kQ, false>;
+    using T = ChainLds<IO, N, W, X, Pl::kQ, false, ONE>;
     using Img = typename T::Img;
     extern __shared__ __align__(16) char lds[];
     constexpr int kSz = int(sizeof(IO)), KS = N / 32 / X, NT = 2 * KS;
@@ -656,12 +656,12 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
     const DeltaCut &cut = pl.cut;
     e = enter_segments<IO, N, Pl::kQ>(q, k, v, images, a.init_state, map, init, a.b, a.L, a.H, a.P, a.G, cut, a.scale, stream);
     if (e != hipSuccess) return e;
-    auto back = [&](auto w_, auto x_, auto map_, float *to) {
+    auto back = [&](auto w_, auto x_, auto one_, auto map_, float *to) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
-        constexpr bool MAP = decltype(map_)::value;
-        constexpr int lds = ChainLds<IO, N, W, X, Pl::kQ, false>::kBytes;
+        constexpr bool MAP = decltype(map_)::value, ONE = decltype(one_)::value;
+        constexpr int lds = ChainLds<IO, N, W, X, Pl::kQ, false, ONE>::kBytes;
         const int rows = 16 * W / X, pblocks = (a.P + rows - 1) / rows;
-        auto kern = k_delta_chain_back<IO, N, W, X, MAP>;
+        auto kern = k_delta_chain_back<IO, N, W, X, MAP, ONE>;
         e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(kern, dim3(unsigned(int64_t(a.b) * a.H * (cut.segments - (MAP ? 1 : 0)) * pblocks)), dim3(64 * W), lds, stream, q, k,
@@ -672,20 +672,20 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
     };
     const int64_t tiles = int64_t(a.b) * a.H * ptiles;
     if (cut.segments > 1) {
-        auto go = [&](auto w, auto x) { return back(w, x, std::true_type{}, dmap); };
-        if ((e = with_chain_shape<IO, N>(tiles * (cut.segments - 1), go)) != hipSuccess) return e;
+        auto go = [&](auto w, auto x, auto one) { return back(w, x, one, std::true_type{}, dmap); };
+        if ((e = with_chain_shape<IO, N, Pl::kQ>(tiles * (cut.segments - 1), go)) != hipSuccess) return e;
         hipLaunchKernelGGL((k_delta_carry<N, true>), dim3(unsigned(tiles)), dim3(4 * N), 0, stream, map, dmap, nullptr, dinit, a.P, cut.segments);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     int share = 1;      // waves per tile, each with its own part of the sums
-    auto chains = [&](auto w_, auto x_) {
+    auto chains = [&](auto w_, auto x_, auto one_) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
         share = X;
-        e = launch_chain<IO, N, W, X, Chain::save, Pl::kQ>(q, k, v, images, cut.segments > 1 ? init : a.init_state, nullptr, nullptr, dy, saved,
+        e = launch_chain<IO, N, W, X, Chain::save, Pl::kQ, decltype(one_)::value>(q, k, v, images, cut.segments > 1 ? init : a.init_state, nullptr, nullptr, dy, saved,
                                                            a.b, a.L, a.H, a.P, a.G, cut.per, cut.segments, a.scale, stream);
-        return e != hipSuccess ? e : back(w_, x_, std::false_type{}, a.d_init);
+        return e != hipSuccess ? e : back(w_, x_, one_, std::false_type{}, a.d_init);
     };
-    if ((e = with_chain_shape<IO, N>(tiles * cut.segments, chains)) != hipSuccess) return e;
+    if ((e = with_chain_shape<IO, N, Pl::kQ>(tiles * cut.segments, chains)) != hipSuccess) return e;
     auto grads = k_delta_grads<IO, N>;
     constexpr int lds = GradTile<IO, N>::kLds;
     e = hipFuncSetAttribute(reinterpret_cast<const void *>(grads), hipFuncAttributeMaxDynamicSharedMemorySize, lds);

@@ -42,9 +42,9 @@ struct DeltaPlanes {
 // Sharing shortens a chunk's steps where there are fewer tiles than SIMDs.
 //
 // LDS: k, M, the scores and gates of two chunks, the next one's copied in meanwhile (one
-// chunk where two do not fit).  With X = 1 q beside them; with more, q of one chunk, which is
+// chunk where two do not fit, or, ONE, where two blocks a CU gain more than copies ahead).  With X = 1 q beside them; with more, q of one chunk, which is
 // done with halfway through it, and the exchanged sums (YX: those of Q S^T too).
-template <typename IO, int N, int W, int X, int NQ, bool YX>
+template <typename IO, int N, int W, int X, int NQ, bool YX, bool ONE>
 struct ChainLds {
     using Img = ChunkImage<IO, 3, NQ>;
     static constexpr int kSz = int(sizeof(IO));
@@ -53,7 +53,7 @@ struct ChainLds {
     static constexpr bool kQMain = X == 1;                  // q beside k, in both buffers
     static constexpr int kImg = kQMain ? 2 * kRows : kRows, kMain = kImg + Img::kBytes, kQOwn = kQMain ? 0 : kRows;
     static constexpr int kXe = X > 1 ? W * 4096 : 0, kXy = X > 1 && YX ? W * (4096 - 4096 / X) : 0;
-    static constexpr int kBufs = 2 * kMain + kQOwn + kXe + kXy <= 160 * 1024 ? 2 : 1;
+    static constexpr int kBufs = !ONE && 2 * kMain + kQOwn + kXe + kXy <= 160 * 1024 ? 2 : 1;
     static constexpr int kQt = kBufs * kMain, kE = kQt + kQOwn, kY = kE + kXe, kBytes = kY + kXy;
     static_assert(kBytes <= 160 * 1024 && N / 32 % X == 0 && W % X == 0);
 };
@@ -145,7 +145,7 @@ enum class Chain { run, save, map };
 
 // One chain per (batch, head, segment of `per` chunks); `init` has a state for each, `fin`
 // for each (map: [P + N][N]) or for each (batch, head).
-template <typename IO, int N, int W, int X, Chain MODE, int NQ>
+template <typename IO, int N, int W, int X, Chain MODE, int NQ, bool ONE>
 __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ qg, const IO *__restrict__ kg,
                                                         const IO *__restrict__ vg, const char *__restrict__ images,
                                                         const float *__restrict__ init, IO *__restrict__ yg,
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                                                         int pblocks, float scale) {
     constexpr bool SAVE = MODE == Chain::save, MAP = MODE == Chain::map;
     using Pl = DeltaPlanes<NQ == 3>;
-    using T = ChainLds<IO, N, W, X, NQ, MODE == Chain::run>;
+    using T = ChainLds<IO, N, W, X, NQ, MODE == Chain::run, ONE>;
     using Img = typename T::Img;
     extern __shared__ __align__(16) char lds[];
     constexpr int kSz = int(sizeof(IO)), KS = N / 32 / X, NT = 2 * KS;  // this wave's column blocks and tiles
@@ -449,30 +449,46 @@ constexpr int kSimds = 1024;
 //   bf16, N = 128, 1 -> 4:  302 -> 280, 494 -> 472, 688 -> 726
 // and of the forward pass with one tile per block (4, 4) for two (8, 4):
 //   fp32, N = 128:  76 -> 58, 86 -> 69, 94 -> 112;   bf16, N = 256:  60 -> 49, 70 -> 59, 78 -> 94
-template <typename IO, int N, class F>
+//
+// With more tiles than SIMDs, one chunk's buffer instead of two lets a second block onto a CU,
+// whose waves fill the waits, where the registers allow it too (the backward pass of wide
+// rows has none).  2048 tokens, two buffers -> one, us at 1024, 1280, 2048 and 4096 tiles:
+//   bf16, N = 64,  backward:  520 -> 557, 843 -> 730, 1000 -> 908, 1926 -> 1764
+//   bf16, N = 128, forward:   172 -> 184, 308 -> 271, 349 -> 329, 680 -> 627
+//   fp32, N = 64,  forward:   251 -> 272, 462 -> 392, 486 -> 430, 961 -> 840
+//   fp32, N = 64,  backward:  977 -> 1065, 1603 -> 1650, 1947 -> 2010, 3852 -> 4000 (not done)
+//   bf16, N = 32,  forward:   130 -> 132, 187 -> 190, 230 -> 234, 445 -> 454 (two blocks fit as it is)
+template <typename IO, int N, int NQ, class F>
 hipError_t with_chain_shape(int64_t tiles, F &&f) {
     using std::integral_constant;
     constexpr integral_constant<int, 1> one{};
     constexpr integral_constant<int, 2> two{};
     constexpr integral_constant<int, 4> four{};
     [[maybe_unused]] constexpr integral_constant<int, 8> eight{};
+    constexpr int kRow = N * int(sizeof(IO));
+    [[maybe_unused]] auto alone = [&]() {       // a wave per tile
+        constexpr bool kGains = 4 * ChainLds<IO, N, 4, 1, NQ, false, false>::kMain > 160 * 1024 && (NQ < 3 || kRow <= 128);
+        if constexpr (kGains)
+            if (tiles > kSimds) return f(four, one, std::true_type{});
+        return f(four, one, std::false_type{});
+    };
     if constexpr (N == 32) {
-        return f(four, one);
+        return alone();
     } else if constexpr (N == 64) {
-        return tiles <= kSimds / 2 ? f(four, two) : f(four, one);
-    } else if constexpr (N * int(sizeof(IO)) == 256) {
-        return tiles <= kSimds / 4 ? f(four, four) : tiles <= kSimds / 2 ? f(four, two) : f(four, one);
+        return tiles <= kSimds / 2 ? f(four, two, std::false_type{}) : alone();
+    } else if constexpr (kRow == 256) {
+        return tiles <= kSimds / 4 ? f(four, four, std::false_type{}) : tiles <= kSimds / 2 ? f(four, two, std::false_type{}) : alone();
     } else {
-        return tiles <= kSimds / 4 ? f(four, four) : f(eight, four);
+        return tiles <= kSimds / 4 ? f(four, four, std::false_type{}) : f(eight, four, std::false_type{});
     }
 }
 
-template <typename IO, int N, int W, int X, Chain MODE, int NQ>
+template <typename IO, int N, int W, int X, Chain MODE, int NQ, bool ONE>
 hipError_t launch_chain(const IO *q, const IO *k, const IO *v, const char *images, const float *init, IO *y, float *fin, const IO *dy,
                         const DeltaSaved &saved, int b, int L, int H, int P, int G, int per, int segs, float scale, hipStream_t stream) {
-    constexpr int lds = ChainLds<IO, N, W, X, NQ, MODE == Chain::run>::kBytes;
+    constexpr int lds = ChainLds<IO, N, W, X, NQ, MODE == Chain::run, ONE>::kBytes;
     const int rows = 16 * W / X, pblocks = ((MODE == Chain::map ? P + N : P) + rows - 1) / rows, nc = (L + kC - 1) / kC;
-    auto kern = k_delta_chain<IO, N, W, X, MODE, NQ>;
+    auto kern = k_delta_chain<IO, N, W, X, MODE, NQ, ONE>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, dim3(unsigned(int64_t(b) * H * segs * pblocks)), dim3(64 * W), lds, stream, q, k, v, images, init, y, fin, dy,
@@ -567,12 +583,12 @@ hipError_t enter_segments(const IO *q, const IO *k, const IO *v, const char *ima
                           int L, int H, int P, int G, const DeltaCut &cut, float scale, hipStream_t stream) {
     if (cut.segments == 1) return hipSuccess;
     const int64_t bh = int64_t(b) * H;
-    auto go = [&](auto w_, auto x_) {
+    auto go = [&](auto w_, auto x_, auto one_) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
-        return launch_chain<IO, N, W, X, Chain::map, NQ>(q, k, v, images, init_state, static_cast<IO *>(nullptr), map, nullptr, DeltaSaved{}, b,
+        return launch_chain<IO, N, W, X, Chain::map, NQ, decltype(one_)::value>(q, k, v, images, init_state, static_cast<IO *>(nullptr), map, nullptr, DeltaSaved{}, b,
                                                          L, H, P, G, cut.per, cut.segments - 1, scale, stream);
     };
-    const hipError_t e = with_chain_shape<IO, N>(bh * (cut.segments - 1) * ((P + N) / 16), go);
+    const hipError_t e = with_chain_shape<IO, N, NQ>(bh * (cut.segments - 1) * ((P + N) / 16), go);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((k_delta_carry<N, false>), dim3(unsigned(bh * (P / 16))), dim3(4 * N), 0, stream, map, nullptr, init_state, init, P,
                        cut.segments);

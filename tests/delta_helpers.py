@@ -52,10 +52,11 @@ def tol_out(dtype, L, N, roundings):
 
 # b, L, H, G, P, N with so many heads that a wave has 16 rows of the state to itself or
 # shares them with one other (the small cases share them among four), blocks whose last
-# rows lie past the head, and many chunks (the last: so many that the gradients' sums are
-# split in the middle of a head)
+# rows lie past the head, and many chunks (so many that the gradients' sums are split in the
+# middle of a head); last, more tiles of 16 rows than the device has SIMDs
 MANY = [(1, 70, 132, 1, 64, 64), (1, 70, 40, 1, 208, 64), (1, 70, 70, 2, 64, 128), (1, 70, 18, 2, 240, 128), (1, 70, 132, 2, 64, 128),
-        (1, 66, 70, 2, 64, 256), (1, 66, 18, 3, 240, 256), (9, 900, 8, 4, 16, 32), (8, 1000, 3, 1, 80, 32)]
+        (1, 66, 70, 2, 64, 256), (1, 66, 18, 3, 240, 256), (9, 900, 8, 4, 16, 32), (8, 1000, 3, 1, 80, 32),
+        (1, 66, 118, 1, 144, 64), (2, 100, 33, 3, 256, 32), (1, 66, 132, 2, 128, 128)]
 
 # b, L, H, G, P, N of sequences long enough for their few heads to be cut into segments: a
 # ragged last segment, blocks that end in the middle of a head's rows, every state width
