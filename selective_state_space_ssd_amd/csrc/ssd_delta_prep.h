@@ -10,8 +10,9 @@
 //
 // 4096 chunks of a head (4 x 2048 tokens, 32 heads in 8 groups, bf16, N = 128) take 43 us and
 // write 130 MB of images, 3.0 TB/s (a fill reaches 7): a head is seven steps between
-// barriers, and 4 blocks a CU cover for each other.  With registers for 3, 52; 49 with a
-// library e^x and decays above the diagonal too.
+// barriers, and 4 blocks a CU cover for each other; the vector units are busy half of the
+// time, the waves wait for LDS and barriers the rest (one barrier less: the same 43).  With
+// registers for 3 blocks, 52; 49 with a library e^x and decays above the diagonal too.
 #pragma once
 
 #include <algorithm>
