@@ -53,8 +53,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
                                                              IO *__restrict__ dSg, float *__restrict__ d_out, BackSums sums, int L,
                                                              int H, int P, int G, int nc, int per, int segs, int pblocks,
                                                              float scale) {
-    using Pl = DeltaPlanes<true>;
-    using T = ChainLds<IO, N, W, X, Pl::kQ, false, ONE>;
+    using T = ChainLds<IO, N, W, X, false, ONE>;
     using Img = typename T::Img;
     extern __shared__ __align__(16) char lds[];
     constexpr int kSz = int(sizeof(IO)), KS = N / 32 / X, NT = 2 * KS;
@@ -161,9 +160,9 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
         f32x4 dU[4], dv[4], xs[kOwn], vd[kOwn], Ev[kOwn];
         IO rv[4 * kOwn];
         if (live) {
-            Op<IO, Pl::kS> so[KS];
+            Op<IO, kPlanes> so[KS];
 #pragma unroll
-            for (int s = 0; s < KS; ++s) so[s] = to_op<IO, Pl::kS>(S[2 * s], S[2 * s + 1]);
+            for (int s = 0; s < KS; ++s) so[s] = to_op<IO, kPlanes>(S[2 * s], S[2 * s + 1]);
             if constexpr (!MAP) {
                 IO *dst = dSg + (unit * P + p) * N + 32 * n0 + 8 * q;
 #pragma unroll
@@ -190,16 +189,16 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
 #pragma unroll
             for (int t = 0; t < 4; ++t) dU[t] *= gate_of(1, t);
             if (X == 1 || x == 1) {
-                Op<IO, Pl::kQ> a[4];
+                Op<IO, kPlanes> a[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) a[t] = tri_col<IO, Pl::kQ>(ts, 1, t >> 1, t & 1, c, q);
+                for (int t = 0; t < 4; ++t) a[t] = tri_col<IO, kPlanes>(ts, 1, t >> 1, t & 1, c, q);
                 mma(dU, a, to_op<IO, 1>(dy_of(2), dy_of(3)));
             }
             if (x == 0) {
                 f32x4 upper[2] = {dU[0], dU[1]};
-                Op<IO, Pl::kQ> a[2];
+                Op<IO, kPlanes> a[2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) a[e] = tri_col<IO, Pl::kQ>(ts, 0, 0, e, c, q);
+                for (int e = 0; e < 2; ++e) a[e] = tri_col<IO, kPlanes>(ts, 0, 0, e, c, q);
                 mma(upper, a, to_op<IO, 1>(dy_of(0), dy_of(1)));
                 dU[0] = upper[0];
                 dU[1] = upper[1];
@@ -229,19 +228,19 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
         if (live) {
             if constexpr (X > 1) sum_of_parts<X>(lds + T::kE + (w - x) * 4096, lane, dU);
             // X = dU + M^T (beta dU), in place
-            const Op<IO, Pl::kM> br0 = to_op<IO, Pl::kM>(gate_of(2, 0) * dU[0], gate_of(2, 1) * dU[1]);
-            const Op<IO, Pl::kM> br1 = to_op<IO, Pl::kM>(gate_of(2, 2) * dU[2], gate_of(2, 3) * dU[3]);
+            const Op<IO, kPlanes> br0 = to_op<IO, kPlanes>(gate_of(2, 0) * dU[0], gate_of(2, 1) * dU[1]);
+            const Op<IO, kPlanes> br1 = to_op<IO, kPlanes>(gate_of(2, 2) * dU[2], gate_of(2, 3) * dU[3]);
             {
-                Op<IO, Pl::kM> a[4];
+                Op<IO, kPlanes> a[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) a[t] = tri_col<IO, Pl::kM>(tm, 1, t >> 1, t & 1, c, q);
+                for (int t = 0; t < 4; ++t) a[t] = tri_col<IO, kPlanes>(tm, 1, t >> 1, t & 1, c, q);
                 mma(dU, a, br1);
             }
             {
                 f32x4 upper[2] = {dU[0], dU[1]};
-                Op<IO, Pl::kM> a[2];
+                Op<IO, kPlanes> a[2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) a[e] = tri_col<IO, Pl::kM>(tm, 0, 0, e, c, q);
+                for (int e = 0; e < 2; ++e) a[e] = tri_col<IO, kPlanes>(tm, 0, 0, e, c, q);
                 mma(upper, a, br0);
                 dU[0] = upper[0];
                 dU[1] = upper[1];
@@ -259,8 +258,8 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 const f32x4 f0 = gate_of(0, 2 * ks), f1 = gate_of(0, 2 * ks + 1);
-                const Op<IO, Pl::kS> oq = to_op<IO, Pl::kS>(scale * f0 * dy_of(2 * ks), scale * f1 * dy_of(2 * ks + 1));
-                const Op<IO, Pl::kS> ok = to_op<IO, Pl::kS>(-f0 * dv[2 * ks], -f1 * dv[2 * ks + 1]);
+                const Op<IO, kPlanes> oq = to_op<IO, kPlanes>(scale * f0 * dy_of(2 * ks), scale * f1 * dy_of(2 * ks + 1));
+                const Op<IO, kPlanes> ok = to_op<IO, kPlanes>(-f0 * dv[2 * ks], -f1 * dv[2 * ks + 1]);
                 if (ks == 1) fetch_dy(next);
 #pragma unroll
                 for (int u0 = 0; u0 < NT; u0 += 4) {
@@ -354,7 +353,7 @@ __global__ __launch_bounds__(256, (GradTile<IO, N>::kPerCu)) void k_delta_grads(
                                                      float *__restrict__ parts, int splits, int L, int H, int P, int G, int nc,
                                                      float scale) {
     using T = GradTile<IO, N>;
-    using Img = ChunkImage<IO, DeltaPlanes<true>::kM, DeltaPlanes<true>::kQ>;
+    using Img = ChunkImage<IO>;
     constexpr int kSz = T::kSz, kP = T::kP, E16 = 16 / kSz;     // elements per 16 bytes
     extern __shared__ __align__(16) char lds[];
     __shared__ double gd[kC];
@@ -636,7 +635,6 @@ __global__ __launch_bounds__(64 * SEG) void k_delta_gates(const float *__restric
 
 template <typename IO, int N>
 hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t stream) {
-    using Pl = DeltaPlanes<true>;
     const int nc = (a.L + kC - 1) / kC, segs = (nc + kSegment<IO> - 1) / kSegment<IO>, ptiles = a.P / 16;
     char *ws = static_cast<char *>(a.workspace);
     char *images = ws;
@@ -649,17 +647,17 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
     auto *dS = reinterpret_cast<IO *>(ws + pl.off_ds);
     auto *parts = reinterpret_cast<float *>(ws + pl.off_parts);
 
-    hipError_t e = launch_delta_prep<IO, N, Pl::kM, Pl::kQ>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
+    hipError_t e = launch_delta_prep<IO, N>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
     if (e != hipSuccess) return e;
     auto *map = reinterpret_cast<float *>(ws + pl.off_map), *init = reinterpret_cast<float *>(ws + pl.off_init);
     auto *dmap = reinterpret_cast<float *>(ws + pl.off_dmap), *dinit = reinterpret_cast<float *>(ws + pl.off_dinit);
     const DeltaCut &cut = pl.cut;
-    e = enter_segments<IO, N, Pl::kQ>(q, k, v, images, a.init_state, map, init, a.b, a.L, a.H, a.P, a.G, cut, a.scale, stream);
+    e = enter_segments<IO, N, true>(q, k, v, images, a.init_state, map, init, a.b, a.L, a.H, a.P, a.G, cut, a.scale, stream);
     if (e != hipSuccess) return e;
     auto back = [&](auto w_, auto x_, auto one_, auto map_, float *to) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
         constexpr bool MAP = decltype(map_)::value, ONE = decltype(one_)::value;
-        constexpr int lds = ChainLds<IO, N, W, X, Pl::kQ, false, ONE>::kBytes;
+        constexpr int lds = ChainLds<IO, N, W, X, false, ONE>::kBytes;
         const int rows = 16 * W / X, pblocks = (a.P + rows - 1) / rows;
         auto kern = k_delta_chain_back<IO, N, W, X, MAP, ONE>;
         e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -673,7 +671,7 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
     const int64_t tiles = int64_t(a.b) * a.H * ptiles;
     if (cut.segments > 1) {
         auto go = [&](auto w, auto x, auto one) { return back(w, x, one, std::true_type{}, dmap); };
-        if ((e = with_chain_shape<IO, N, Pl::kQ>(tiles * (cut.segments - 1), go)) != hipSuccess) return e;
+        if ((e = with_chain_shape<IO, N, true>(tiles * (cut.segments - 1), go)) != hipSuccess) return e;
         hipLaunchKernelGGL((k_delta_carry<N, true>), dim3(unsigned(tiles)), dim3(4 * N), 0, stream, map, dmap, nullptr, dinit, a.P, cut.segments);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
@@ -681,11 +679,11 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
     auto chains = [&](auto w_, auto x_, auto one_) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
         share = X;
-        e = launch_chain<IO, N, W, X, Chain::save, Pl::kQ, decltype(one_)::value>(q, k, v, images, cut.segments > 1 ? init : a.init_state, nullptr, nullptr, dy, saved,
+        e = launch_chain<IO, N, W, X, Chain::save, decltype(one_)::value>(q, k, v, images, cut.segments > 1 ? init : a.init_state, nullptr, nullptr, dy, saved,
                                                            a.b, a.L, a.H, a.P, a.G, cut.per, cut.segments, a.scale, stream);
         return e != hipSuccess ? e : back(w_, x_, one_, std::false_type{}, a.d_init);
     };
-    if ((e = with_chain_shape<IO, N, Pl::kQ>(tiles * cut.segments, chains)) != hipSuccess) return e;
+    if ((e = with_chain_shape<IO, N, true>(tiles * cut.segments, chains)) != hipSuccess) return e;
     auto grads = k_delta_grads<IO, N>;
     constexpr int lds = GradTile<IO, N>::kLds;
     e = hipFuncSetAttribute(reinterpret_cast<const void *>(grads), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -722,7 +720,6 @@ int grad_splits(size_t cells, size_t turns, int N, bool bf16) {
 DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16) {
     DeltaBwdPlan pl;
     if (b <= 0 || L <= 0 || !delta_chunk_supported(b, L, H, P, N, G, bf16)) return pl;
-    using Pl = DeltaPlanes<true>;
     const size_t nc = (size_t(L) + kC - 1) / kC, segs = bf16 ? (nc + kSegment<bf16_bits> - 1) / kSegment<bf16_bits> : (nc + kSegment<float> - 1) / kSegment<float>, bh = size_t(b) * H, units = bh * nc;
     const size_t sz = bf16 ? 2 : 4, state = size_t(P) * N, ptiles = size_t(P) / 16;
     size_t at = 0;
@@ -731,7 +728,7 @@ DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16)
         at += (bytes + 255) / 256 * 256;
         return off;
     };
-    take(units * (bf16 ? ChunkImage<bf16_bits, Pl::kM, Pl::kQ>::kBytes : ChunkImage<float, Pl::kM, Pl::kQ>::kBytes));
+    take(units * (bf16 ? ChunkImage<bf16_bits>::kBytes : ChunkImage<float>::kBytes));
     pl.off_e = take(units * kC * P * 4);
     pl.off_s = take(units * state * sz);
     pl.off_ds = take(units * state * sz);

@@ -26,27 +26,18 @@ struct DeltaSaved {
     float *ydy;
 };
 
-// Planes of the values that stay 32-bit on their way through the bf16 matrix products:
-// the state, what is added to it, M and the vectors M meets (3: 24 bits).  y is rounded to
-// bf16 at the end, but its terms may be much larger than it is (keys that repeat: each U
-// takes back most of the one before), so its operands keep 16 bits; for the backward
-// pass, whose gate gradients are differences of y . dy, all 24.
-template <bool SAVE>
-struct DeltaPlanes {
-    static constexpr int kS = 3, kM = 3, kQ = SAVE ? 3 : 2;
-};
-
 // A block's W waves are W / X tiles of 16 state rows, each shared by X waves that hold
 // N / X of its columns.  The sums over all columns (K S^T, Q S^T) are added up through LDS;
 // what only depends on those is computed by every one of the X waves, bit for bit alike.
 // Sharing shortens a chunk's steps where there are fewer tiles than SIMDs.
 //
 // LDS: k, M, the scores and gates of two chunks, the next one's copied in meanwhile (one
-// chunk where two do not fit, or, ONE, where two blocks a CU gain more than copies ahead).  With X = 1 q beside them; with more, q of one chunk, which is
-// done with halfway through it, and the exchanged sums (YX: those of Q S^T too).
-template <typename IO, int N, int W, int X, int NQ, bool YX, bool ONE>
+// chunk where two do not fit, or, ONE, where two blocks a CU gain more than copies ahead).
+// With X = 1 q beside them; with more, q of one chunk, which is done with halfway through it,
+// and the exchanged sums (YX: those of Q S^T too).
+template <typename IO, int N, int W, int X, bool YX, bool ONE>
 struct ChainLds {
-    using Img = ChunkImage<IO, 3, NQ>;
+    using Img = ChunkImage<IO>;
     static constexpr int kSz = int(sizeof(IO));
     static constexpr int RB = N * kSz;                      // bytes per row of k or q
     static constexpr int kRows = kC * RB;                   // bytes of such a tile
@@ -127,7 +118,7 @@ __device__ __forceinline__ void sum_of_parts(const char *first, int lane, f32x4 
 }
 
 // What bounds it: one wave's steps, not the matrix cores.  A chunk of a bf16 tile at N = 128
-// is 190 matrix instructions (3000 cycles) and 7500 cycles in between, of which splitting
+// is 216 matrix instructions (3500 cycles) and 7500 cycles in between, of which splitting
 // values into planes and the accumulators' scaling issue for 4000; the waves of the only
 // block that fits a CU find nobody to fill the rest.  4 x 2048 tokens, 32 heads of 128 x 128,
 // a wave on every SIMD: 141 us for 32 chunks in turn, 168 MB of inputs and outputs; without
@@ -145,7 +136,7 @@ enum class Chain { run, save, map };
 
 // One chain per (batch, head, segment of `per` chunks); `init` has a state for each, `fin`
 // for each (map: [P + N][N]) or for each (batch, head).
-template <typename IO, int N, int W, int X, Chain MODE, int NQ, bool ONE>
+template <typename IO, int N, int W, int X, Chain MODE, bool ONE>
 __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ qg, const IO *__restrict__ kg,
                                                         const IO *__restrict__ vg, const char *__restrict__ images,
                                                         const float *__restrict__ init, IO *__restrict__ yg,
@@ -153,8 +144,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                                                         DeltaSaved saved, int L, int H, int P, int G, int nc, int per, int segs,
                                                         int pblocks, float scale) {
     constexpr bool SAVE = MODE == Chain::save, MAP = MODE == Chain::map;
-    using Pl = DeltaPlanes<NQ == 3>;
-    using T = ChainLds<IO, N, W, X, NQ, MODE == Chain::run, ONE>;
+    using T = ChainLds<IO, N, W, X, MODE == Chain::run, ONE>;
     using Img = typename T::Img;
     extern __shared__ __align__(16) char lds[];
     constexpr int kSz = int(sizeof(IO)), KS = N / 32 / X, NT = 2 * KS;  // this wave's column blocks and tiles
@@ -258,9 +248,9 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
         fetch_v(next);
         ahead(std::integral_constant<int, 0>{});
         if (live) {
-            Op<IO, Pl::kS> so[KS];
+            Op<IO, kPlanes> so[KS];
 #pragma unroll
-            for (int s = 0; s < KS; ++s) so[s] = to_op<IO, Pl::kS>(S[2 * s], S[2 * s + 1]);
+            for (int s = 0; s < KS; ++s) so[s] = to_op<IO, kPlanes>(S[2 * s], S[2 * s + 1]);
             if constexpr (SAVE) {
                 IO *dst = static_cast<IO *>(saved.S) + ((size_t(bh) * nc + ch) * P + p) * N + 32 * n0 + 8 * q;
 #pragma unroll
@@ -289,7 +279,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                 Op<IO, 1> a[4];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tq, 0, tile_row(t >> 1, t & 1, c), n0 + ks, q);
-                mma(Y, first_planes<Pl::kQ>(so[ks]), a);
+                mma(Y, so[ks], a);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) E[t] = V[t] - gate_of(0, t) * E[t];
@@ -312,31 +302,31 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
         if (live) {
             if constexpr (X > 1) sum_of_parts<X>(lds + T::kE + (w - x) * 4096, lane, E);
             // E = R + M (beta R), U = beta E
-            Op<IO, Pl::kM> br[2];
+            Op<IO, kPlanes> br[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) br[s] = to_op<IO, Pl::kM>(gate_of(2, 2 * s) * E[2 * s], gate_of(2, 2 * s + 1) * E[2 * s + 1]);
+            for (int s = 0; s < 2; ++s) br[s] = to_op<IO, kPlanes>(gate_of(2, 2 * s) * E[2 * s], gate_of(2, 2 * s + 1) * E[2 * s + 1]);
             {
-                Op<IO, Pl::kM> a[4];
+                Op<IO, kPlanes> a[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) a[t] = tri_row<IO, Pl::kM>(tm, t >> 1, t & 1, 0, c, q);
+                for (int t = 0; t < 4; ++t) a[t] = tri_row<IO, kPlanes>(tm, t >> 1, t & 1, 0, c, q);
                 mma(E, a, br[0]);
             }
             {
                 f32x4 lower[2] = {E[2], E[3]};
-                Op<IO, Pl::kM> a[2];
+                Op<IO, kPlanes> a[2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) a[e] = tri_row<IO, Pl::kM>(tm, 1, e, 1, c, q);
+                for (int e = 0; e < 2; ++e) a[e] = tri_row<IO, kPlanes>(tm, 1, e, 1, c, q);
                 mma(lower, a, br[1]);
                 E[2] = lower[0];
                 E[3] = lower[1];
             }
-            Op<IO, Pl::kQ> uy[2];
-            Op<IO, Pl::kS> ud[2];
+            Op<IO, kPlanes> uy[2];
+            Op<IO, kPlanes> ud[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const f32x4 u0 = gate_of(2, 2 * s) * E[2 * s], u1 = gate_of(2, 2 * s + 1) * E[2 * s + 1];
-                ud[s] = to_op<IO, Pl::kS>(gate_of(1, 2 * s) * u0, gate_of(1, 2 * s + 1) * u1);
-                uy[s] = to_op<IO, Pl::kQ>(u0, u1);
+                ud[s] = to_op<IO, kPlanes>(gate_of(1, 2 * s) * u0, gate_of(1, 2 * s + 1) * u1);
+                uy[s] = to_op<IO, kPlanes>(u0, u1);
             }
             ahead(std::integral_constant<int, 2>{});
             // S <- e^{g_C} S + K^T (e^{g_C - g} U)
@@ -377,7 +367,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                     f32x4 z[1] = {Y[t]};
 #pragma unroll
                     for (int ks = 0; ks <= (t >> 1); ++ks) {
-                        const Op<IO, Pl::kQ> a[1] = {tri_row<IO, Pl::kQ>(ts, t >> 1, t & 1, ks, c, q)};
+                        const Op<IO, kPlanes> a[1] = {tri_row<IO, kPlanes>(ts, t >> 1, t & 1, ks, c, q)};
                         mma(z, uy[ks], a);
                     }
                     Y[t] = z[0];
@@ -458,7 +448,7 @@ constexpr int kSimds = 1024;
 //   fp32, N = 64,  forward:   251 -> 272, 462 -> 392, 486 -> 430, 961 -> 840
 //   fp32, N = 64,  backward:  977 -> 1065, 1603 -> 1650, 1947 -> 2010, 3852 -> 4000 (not done)
 //   bf16, N = 32,  forward:   130 -> 132, 187 -> 190, 230 -> 234, 445 -> 454 (two blocks fit as it is)
-template <typename IO, int N, int NQ, class F>
+template <typename IO, int N, bool BACK, class F>
 hipError_t with_chain_shape(int64_t tiles, F &&f) {
     using std::integral_constant;
     constexpr integral_constant<int, 1> one{};
@@ -467,7 +457,7 @@ hipError_t with_chain_shape(int64_t tiles, F &&f) {
     [[maybe_unused]] constexpr integral_constant<int, 8> eight{};
     constexpr int kRow = N * int(sizeof(IO));
     [[maybe_unused]] auto alone = [&]() {       // a wave per tile
-        constexpr bool kGains = 4 * ChainLds<IO, N, 4, 1, NQ, false, false>::kMain > 160 * 1024 && (NQ < 3 || kRow <= 128);
+        constexpr bool kGains = 4 * ChainLds<IO, N, 4, 1, false, false>::kMain > 160 * 1024 && (!BACK || kRow <= 128);
         if constexpr (kGains)
             if (tiles > kSimds) return f(four, one, std::true_type{});
         return f(four, one, std::false_type{});
@@ -483,12 +473,12 @@ hipError_t with_chain_shape(int64_t tiles, F &&f) {
     }
 }
 
-template <typename IO, int N, int W, int X, Chain MODE, int NQ, bool ONE>
+template <typename IO, int N, int W, int X, Chain MODE, bool ONE>
 hipError_t launch_chain(const IO *q, const IO *k, const IO *v, const char *images, const float *init, IO *y, float *fin, const IO *dy,
                         const DeltaSaved &saved, int b, int L, int H, int P, int G, int per, int segs, float scale, hipStream_t stream) {
-    constexpr int lds = ChainLds<IO, N, W, X, NQ, MODE == Chain::run, ONE>::kBytes;
+    constexpr int lds = ChainLds<IO, N, W, X, MODE == Chain::run, ONE>::kBytes;
     const int rows = 16 * W / X, pblocks = ((MODE == Chain::map ? P + N : P) + rows - 1) / rows, nc = (L + kC - 1) / kC;
-    auto kern = k_delta_chain<IO, N, W, X, MODE, NQ, ONE>;
+    auto kern = k_delta_chain<IO, N, W, X, MODE, ONE>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, dim3(unsigned(int64_t(b) * H * segs * pblocks)), dim3(64 * W), lds, stream, q, k, v, images, init, y, fin, dy,
@@ -578,17 +568,17 @@ __global__ __launch_bounds__(4 * N) void k_delta_carry(const float *__restrict__
 }
 
 // The states that enter the segments, if there are more than one.
-template <typename IO, int N, int NQ>
+template <typename IO, int N, bool BACK>
 hipError_t enter_segments(const IO *q, const IO *k, const IO *v, const char *images, const float *init_state, float *map, float *init, int b,
                           int L, int H, int P, int G, const DeltaCut &cut, float scale, hipStream_t stream) {
     if (cut.segments == 1) return hipSuccess;
     const int64_t bh = int64_t(b) * H;
     auto go = [&](auto w_, auto x_, auto one_) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
-        return launch_chain<IO, N, W, X, Chain::map, NQ, decltype(one_)::value>(q, k, v, images, init_state, static_cast<IO *>(nullptr), map, nullptr, DeltaSaved{}, b,
+        return launch_chain<IO, N, W, X, Chain::map, decltype(one_)::value>(q, k, v, images, init_state, static_cast<IO *>(nullptr), map, nullptr, DeltaSaved{}, b,
                                                          L, H, P, G, cut.per, cut.segments - 1, scale, stream);
     };
-    const hipError_t e = with_chain_shape<IO, N, NQ>(bh * (cut.segments - 1) * ((P + N) / 16), go);
+    const hipError_t e = with_chain_shape<IO, N, BACK>(bh * (cut.segments - 1) * ((P + N) / 16), go);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((k_delta_carry<N, false>), dim3(unsigned(bh * (P / 16))), dim3(4 * N), 0, stream, map, nullptr, init_state, init, P,
                        cut.segments);

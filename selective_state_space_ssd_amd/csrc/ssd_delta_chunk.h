@@ -158,20 +158,6 @@ __device__ __forceinline__ Op<IO, NP> to_op(f32x4 lo, f32x4 hi) {
     return o;
 }
 
-// The first NF planes alone.
-template <int NF, typename IO, int NP>
-__device__ __forceinline__ Op<IO, NF> first_planes(const Op<IO, NP> &o) {
-    Op<IO, NF> f;
-    if constexpr (std::is_same_v<IO, float>) {
-        f.v[0] = o.v[0];
-        f.v[1] = o.v[1];
-    } else {
-#pragma unroll
-        for (int i = 0; i < NF; ++i) f.p[i] = o.p[i];
-    }
-    return f;
-}
-
 // Row `row` of a tile, values 8 (4 ks + q) .. + 7, from NP planes `stride` bytes apart.
 template <typename IO, int NP, int RB>
 __device__ __forceinline__ Op<IO, NP> read_row(const char *tile, int stride, int row, int ks, int q) {
@@ -238,16 +224,24 @@ __device__ __forceinline__ uint32_t lds_address(const char *p) {
     return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char *)p));
 }
 
+// Planes of the values that stay 32-bit on their way through the bf16 matrix products (24
+// bits): the state, what is added to it, M, the vectors M meets, and the scores.  y too, though
+// it is rounded to bf16 in the end: where the chunk's updates erase a large state, or keys
+// repeat, its terms are much larger than it is.  With 16 bits of state, scores and updates y
+// was off by 2^-18 of those terms, and 1.2e-4 of the layer's y (2-norm) fell on the other side
+// of a rounding border than the exact value.
+constexpr int kPlanes = 3;
+
 // One chunk's image in the workspace and in LDS:
-//   M in NM planes and the scores in NQ (fp32 I/O: one fp32 plane each), both lower
+//   M and the scores in kPlanes planes (fp32 I/O: one fp32 plane each), both lower
 //   triangular: a plane holds rows 0 .. 31 of columns 0 .. 31, then rows 32 .. 63 whole;
 //   then [3][64] fp32: e^g, e^{g_C - g}, beta.
-template <typename IO, int NM, int NQ>
+template <typename IO>
 struct ChunkImage {
     static constexpr int kSz = int(sizeof(IO));
-    static constexpr int kPlanesM = kSz == 4 ? 1 : NM, kPlanesQ = kSz == 4 ? 1 : NQ;
     static constexpr int kTop = 32 * 32 * kSz, kPlane = kTop + 32 * 64 * kSz;
-    static constexpr int kM = 0, kQ = kPlanesM * kPlane, kGates = kQ + kPlanesQ * kPlane;
+    static constexpr int kOf = kSz == 4 ? 1 : kPlanes;      // planes a matrix has
+    static constexpr int kM = 0, kQ = kOf * kPlane, kGates = 2 * kOf * kPlane;
     static constexpr int kBytes = kGates + 1024;            // the gates rounded up to 1 KiB
 };
 
@@ -255,14 +249,14 @@ struct ChunkImage {
 // columns 32 ks + 8 q .. (ks <= s);
 template <typename IO, int NP>
 __device__ __forceinline__ Op<IO, NP> tri_row(const char *m, int s, int e, int ks, int c, int q) {
-    using Img = ChunkImage<IO, 1, 1>;
+    using Img = ChunkImage<IO>;
     if (s == 0) return read_row<IO, NP, 32 * Img::kSz>(m, Img::kPlane, tile_row(0, e, c), 0, q);
     return read_row<IO, NP, 64 * Img::kSz>(m + Img::kTop, Img::kPlane, tile_row(0, e, c), ks, q);
 }
 // columns tile_row(s, e, c), rows 32 ks + 8 q .. (ks >= s).
 template <typename IO, int NP>
 __device__ __forceinline__ Op<IO, NP> tri_col(const char *m, int ks, int s, int e, int c, int q) {
-    using Img = ChunkImage<IO, 1, 1>;
+    using Img = ChunkImage<IO>;
     if (ks == 0) return read_col<IO, NP, 32 * Img::kSz>(m, Img::kPlane, 0, 0, e, c, q);
     return read_col<IO, NP, 64 * Img::kSz>(m + Img::kTop, Img::kPlane, 0, 32 * s, e, c, q);
 }

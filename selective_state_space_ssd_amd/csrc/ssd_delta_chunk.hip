@@ -12,21 +12,20 @@ namespace {
 
 template <typename IO, int N>
 hipError_t launch_n(const DeltaChunkArgs &a, const DeltaChunkPlan &pl, hipStream_t stream) {
-    using Pl = DeltaPlanes<false>;
     char *images = static_cast<char *>(a.workspace);
     auto *map = reinterpret_cast<float *>(images + pl.off_map), *init = reinterpret_cast<float *>(images + pl.off_init);
     const auto *q = static_cast<const IO *>(a.q), *k = static_cast<const IO *>(a.k), *v = static_cast<const IO *>(a.v);
-    hipError_t e = launch_delta_prep<IO, N, Pl::kM, Pl::kQ>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
+    hipError_t e = launch_delta_prep<IO, N>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
     if (e != hipSuccess) return e;
-    if ((e = enter_segments<IO, N, Pl::kQ>(q, k, v, images, a.init_state, map, init, a.b, a.L, a.H, a.P, a.G, pl.cut, a.scale, stream)) != hipSuccess)
+    if ((e = enter_segments<IO, N, false>(q, k, v, images, a.init_state, map, init, a.b, a.L, a.H, a.P, a.G, pl.cut, a.scale, stream)) != hipSuccess)
         return e;
     auto go = [&](auto w_, auto x_, auto one_) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
-        return launch_chain<IO, N, W, X, Chain::run, Pl::kQ, decltype(one_)::value>(q, k, v, images, pl.cut.segments > 1 ? init : a.init_state, static_cast<IO *>(a.y),
+        return launch_chain<IO, N, W, X, Chain::run, decltype(one_)::value>(q, k, v, images, pl.cut.segments > 1 ? init : a.init_state, static_cast<IO *>(a.y),
                                                              a.final_state, nullptr, DeltaSaved{}, a.b, a.L, a.H, a.P, a.G, pl.cut.per,
                                                              pl.cut.segments, a.scale, stream);
     };
-    return with_chain_shape<IO, N, Pl::kQ>(int64_t(a.b) * a.H * pl.cut.segments * (a.P / 16), go);
+    return with_chain_shape<IO, N, false>(int64_t(a.b) * a.H * pl.cut.segments * (a.P / 16), go);
 }
 
 }  // namespace
@@ -78,11 +77,10 @@ bool delta_chunk_supported(int b, int L, int H, int P, int N, int G, bool bf16) 
 DeltaChunkPlan plan_delta_chunk(int b, int L, int H, int P, int N, int G, bool bf16) {
     DeltaChunkPlan pl;
     if (!delta_chunk_supported(b, L, H, P, N, G, bf16)) return pl;
-    using Pl = DeltaPlanes<false>;
     pl.supported = true;
     const int nc = (L + kC - 1) / kC;
     const size_t bh = size_t(b) * H;
-    pl.total = bh * nc * (bf16 ? ChunkImage<bf16_bits, Pl::kM, Pl::kQ>::kBytes : ChunkImage<float, Pl::kM, Pl::kQ>::kBytes);
+    pl.total = bh * nc * (bf16 ? ChunkImage<bf16_bits>::kBytes : ChunkImage<float>::kBytes);
     pl.cut = cut_sequence(int64_t(bh), nc, P, N, bf16, false);
     pl.off_map = pl.total;
     pl.off_init = pl.off_map + map_bytes(bh, P, N, pl.cut);

@@ -40,7 +40,7 @@ __device__ __forceinline__ Op<IO, 1> load_row8(const IO *p) {
 // the `first`.
 template <typename IO, int NP>
 __device__ __forceinline__ void write_image(const float *m, char *dst, int first, int threads) {
-    using Img = ChunkImage<IO, 1, 1>;
+    using Img = ChunkImage<IO>;
     constexpr int kRowTop = 32 * Img::kSz, kRow = 64 * Img::kSz, E = 16 / Img::kSz;
     for (int i = first; i < Img::kPlane / 16; i += threads) {
         const bool top = i < Img::kTop / 16;
@@ -62,12 +62,12 @@ __device__ __forceinline__ void write_image(const float *m, char *dst, int first
 // Heads of a group that one block takes, sharing the products of the group's keys.
 constexpr int kPrepHeads = 4;
 
-template <typename IO, int N, int NM, int NQ>
+template <typename IO, int N>
 __global__ __launch_bounds__(256, 4) void k_delta_prep(const IO *__restrict__ qg, const IO *__restrict__ kg,
                                                     const float *__restrict__ a, const float *__restrict__ beta,
                                                     char *__restrict__ images, int L, int H, int G, int nc, int hb,
                                                     float scale) {
-    using Img = ChunkImage<IO, NM, NQ>;
+    using Img = ChunkImage<IO>;
     __shared__ double gd[kPrepHeads][kC];
     __shared__ float sbs[kPrepHeads][kC];
     __shared__ __align__(16) float mm[kC * kLd], sc[kC * kLd];  // Lo, then M over it; scores
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(256, 4) void k_delta_prep(const IO *__restrict__ qg
         }
         __syncthreads();
         if (w > 0) {    // the other waves write the scores out meanwhile
-            write_image<IO, Img::kPlanesQ>(sc, img + Img::kQ, tid - 64, 192);
+            write_image<IO, kPlanes>(sc, img + Img::kQ, tid - 64, 192);
         } else {        // diagonal blocks of 16, lane = (block q, column c): each row found
                         // is taken out of all later ones
             float *l0 = mm + 16 * q * kLd + 16 * q;
@@ -222,19 +222,19 @@ __global__ __launch_bounds__(256, 4) void k_delta_prep(const IO *__restrict__ qg
             for (int i = 0; i < 4; ++i) mm[(r0 + 4 * q + i) * kLd + c0 + c] = -z[i];
         }
         __syncthreads();
-        write_image<IO, Img::kPlanesM>(mm, img + Img::kM, tid, 256);
+        write_image<IO, kPlanes>(mm, img + Img::kM, tid, 256);
     }
 }
 
 // One launch over all chunks.  A block per chunk, group and kPrepHeads heads where that
 // fills the device, per head where it does not.
-template <typename IO, int N, int NM, int NQ>
+template <typename IO, int N>
 hipError_t launch_delta_prep(const IO *q, const IO *k, const float *a, const float *beta, char *images, int b, int L, int H,
                              int G, float scale, hipStream_t stream) {
     const int nc = (L + kC - 1) / kC, r = H / G;
     const int hb = int64_t(b) * nc * G * ((r + kPrepHeads - 1) / kPrepHeads) >= 512 ? std::min(r, kPrepHeads) : 1;
     const unsigned blocks = unsigned(int64_t(b) * nc * G * ((r + hb - 1) / hb));
-    hipLaunchKernelGGL((k_delta_prep<IO, N, NM, NQ>), dim3(blocks), dim3(256), 0, stream, q, k, a, beta, images, L, H, G, nc, hb, scale);
+    hipLaunchKernelGGL((k_delta_prep<IO, N>), dim3(blocks), dim3(256), 0, stream, q, k, a, beta, images, L, H, G, nc, hb, scale);
     return hipGetLastError();
 }
 
