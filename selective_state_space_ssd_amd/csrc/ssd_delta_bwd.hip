@@ -12,18 +12,17 @@
 //                in a few whose fp32 sums a further kernel adds:
 //        dq = scale e^g dY S + W K,                      W_ij = scale (dy_i . u_j) D_ij, j <= i
 //        dk = -e^g dv S + e^{g_C - g} U dS + W^T Q + G K,  G = F + F^T, F_ij = -(dv_i . u_j) D_ij, j < i
+//      Both are differences where the chunk's updates erase a large state, or the gradient of
+//      one: states, U, dv, W and G keep 32 bits here too, and dq and dk are rounded once.
 //   5 gates      da.  The gates only scale v going in and y coming out of an ungated rule,
 //        so the gradient of the gate sum at token t is y_t . dy_t - v_t . dv_t, and
 //        da_t = sum of it from t to the end of a segment + <dS, S> at the segment's end.
 // 2 and 3 are chains over the chunks whose waves keep 16 rows of the state each, as in the
 // forward pass: 32-bit values throughout, since da and dbeta come out of differences.
 //
-// 4 x 2048 tokens, 32 heads of 128 x 128, bf16, us: prep 46, chain 197, chain back 250, grads
-// 163, gates 9.  The chains are bound by a wave's steps (ssd_delta_chain.h); grads reads
-// 540 MB (E, both states, dy, dv), 3.3 TB/s: a block waits for each turn's copies, and only
-// the other block of its CU works meanwhile (a second set of tiles does not fit the LDS, the
-// states' copies a turn ahead do not fit the registers; what fits is asking them into the
-// L2, 175 us without).
+// 4 x 2048 tokens, 32 heads of 128 x 128, bf16, us: prep 45, chain 216, chain back 287, grads
+// 325, gates 9.  The chains are bound by a wave's steps (ssd_delta_chain.h) and write 805 MB
+// (both states, E and X, in 32 bits); grads reads 870 MB, 2.7 TB/s.
 #include <algorithm>
 
 #include "ssd_delta.h"
@@ -50,7 +49,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
                                                              const char *__restrict__ images, const float *__restrict__ d_final,
                                                              const float *__restrict__ d_enter, const f32x4 *__restrict__ E,
                                                              const f32x4 *__restrict__ anchor, IO *__restrict__ dvg,
-                                                             IO *__restrict__ dSg, float *__restrict__ d_out, BackSums sums, int L,
+                                                             float *__restrict__ dSg, f32x4 *__restrict__ Xg, float *__restrict__ d_out, BackSums sums, int L,
                                                              int H, int P, int G, int nc, int per, int segs, int pblocks,
                                                              float scale) {
     using T = ChainLds<IO, N, W, X, false, ONE>;
@@ -164,16 +163,9 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
 #pragma unroll
             for (int s = 0; s < KS; ++s) so[s] = to_op<IO, kPlanes>(S[2 * s], S[2 * s + 1]);
             if constexpr (!MAP) {
-                IO *dst = dSg + (unit * P + p) * N + 32 * n0 + 8 * q;
+                float *dst = dSg + (unit * P + p) * N + 32 * n0 + 8 * q;
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    if constexpr (kSz == 4) {
-                        *reinterpret_cast<f32x4 *>(dst + 32 * s) = S[2 * s];
-                        *reinterpret_cast<f32x4 *>(dst + 32 * s + 4) = S[2 * s + 1];
-                    } else {
-                        *reinterpret_cast<bf16x8 *>(dst + 32 * s) = so[s].p[0];
-                    }
-                }
+                for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(dst + 32 * (t >> 1) + 4 * (t & 1)) = S[t];
             }
             // this wave's part of dU = e^{g_C - g} K dS^T + scores^T dY: its columns of dS, and
             // token half x of dY (both halves with one wave, none for waves past the second)
@@ -308,6 +300,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
             for (int j = 0; j < kOwn; ++j) {
                 const int t = x * kOwn + j, row = 32 * (t >> 1) + 4 * (t & 1);
                 const f32x4 dvj = own(dv, j);
+                Xg[(unit * ptiles + p0 / 16) * 256 + 64 * t + lane] = own(dU, j);
                 if (c == 0) {
                     *reinterpret_cast<f32x4 *>(sums.xe + at + row) = xs[j];
                     *reinterpret_cast<f32x4 *>(sums.vdv + at + row) = vd[j];
@@ -327,34 +320,38 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
         for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(d_out + state_at(MAP ? bh * segs + seg : bh, t)) = S[t];
 }
 
-// Kernel 4.  Block = (batch, chunk, group, one of `splits` parts of its heads' state rows);
-// wave w holds dq^T and dk^T of 16 tokens (tile
-// columns; rows n in registers, 8 consecutive ones a lane).  Per head and 64 rows p, dY, dv,
-// U and both states go through LDS.  Operands rounded to bf16 are the states and dv, as
-// stored; U and the matrices W and G, which are formed here, keep 16 bits (kP planes).
+// Kernel 4.  Block = (batch, chunk, group, one of `splits` parts of its heads' state rows).
+// Wave w holds dq^T and dk^T of 16 tokens (tile columns; rows n in registers, 4 consecutive
+// ones a tile), of one half of the N's: waves w and w + 4 share their tokens.  Per turn a
+// head's 32 rows p: dY, dv, U and both states go through LDS, 32-bit ones split into kPlanes
+// planes on the way there; the next turn's values are on their way into registers meanwhile.
 template <typename IO, int N>
 struct GradTile {
-    static constexpr int kSz = int(sizeof(IO)), kP = kSz == 4 ? 1 : 2;
-    static constexpr int RP = 64 * kSz, RB = N * kSz;       // bytes per row of 64 p's / of N
-    static constexpr int kTok = kC * RP, kState = 64 * RB;  // bytes of a [64][64] / [64][N] tile
-    static constexpr int kY = 0, kV = kTok, kU = 2 * kTok, kS = kU + kP * kTok, kD = kS + kState, kHead = kD + kState;
+    static constexpr int kSz = int(sizeof(IO)), kP = kSz == 4 ? 1 : kPlanes;
+    static constexpr int kRows = 32;                        // state rows a turn
+    static constexpr int RP = kRows * kSz, RB = N * kSz;    // bytes per row of p's / of N
+    static constexpr int kTok = kC * RP, kState = kRows * RB;       // bytes of a [64][32] / [32][N] tile
+    static constexpr int kS = 0, kD = kP * kState, kU = 2 * kP * kState, kV = kU + kP * kTok, kY = kV + kP * kTok, kHead = kY + kTok;
     // after the heads: W and G (kP planes each), k, q
-    static constexpr int kWm = 0, kGm = kP * kTok, kK = 2 * kP * kTok, kQ = kK + kState, kTail = kQ + kState;
+    static constexpr int RM = kC * kSz, kMat = kC * RM, kWm = 0, kGm = kP * kMat, kK = 2 * kP * kMat, kQ = kK + kC * RB, kTail = kQ + kC * RB;
     static constexpr int kLds = kHead > kTail ? kHead : kTail;
-    static constexpr int kPerCu = 2 * kLds <= 159 * 1024 && N <= 128 ? 2 : 1;       // blocks: LDS, and registers at N = 256
+    static constexpr int kThreads = 512, kEights = kRows * N / 8, kLoads = (kEights + kThreads - 1) / kThreads;     // 8 values a thread and load
+    static constexpr bool kTight = RB >= 512;       // as many accumulators as leave few registers
+    static constexpr bool kAhead = N <= 128;        // a turn's values are asked for a turn ahead
+    static_assert(kLds <= 159 * 1024);
 };
 
 template <typename IO, int N>
-__global__ __launch_bounds__(256, (GradTile<IO, N>::kPerCu)) void k_delta_grads(const IO *__restrict__ qg, const IO *__restrict__ kg,
+__global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, const IO *__restrict__ kg,
                                                      const float *__restrict__ ag, const IO *__restrict__ dyg,
-                                                     const IO *__restrict__ dvg, const char *__restrict__ images,
-                                                     const f32x4 *__restrict__ E, const IO *__restrict__ Sg,
-                                                     const IO *__restrict__ dSg, IO *__restrict__ dqg, IO *__restrict__ dkg,
+                                                     const char *__restrict__ images, const f32x4 *__restrict__ E,
+                                                     const f32x4 *__restrict__ Xg, const float *__restrict__ Sg,
+                                                     const float *__restrict__ dSg, IO *__restrict__ dqg, IO *__restrict__ dkg,
                                                      float *__restrict__ parts, int splits, int L, int H, int P, int G, int nc,
                                                      float scale) {
     using T = GradTile<IO, N>;
     using Img = ChunkImage<IO>;
-    constexpr int kSz = T::kSz, kP = T::kP, E16 = 16 / kSz;     // elements per 16 bytes
+    constexpr int kSz = T::kSz, kP = T::kP, NT = N / 32;    // column tiles of a wave
     extern __shared__ __align__(16) char lds[];
     __shared__ double gd[kC];
     const uint32_t lds0 = lds_address(lds);
@@ -362,183 +359,221 @@ __global__ __launch_bounds__(256, (GradTile<IO, N>::kPerCu)) void k_delta_grads(
     const int split = blockIdx.x % splits, cell = blockIdx.x / splits, ch = cell % nc, bg = cell / nc, g = bg % G, bi = bg / G, r = H / G;
     const int t0 = ch * kC, rows = min(kC, L - t0), ptiles = P / 16;
     const size_t hp = size_t(H) * P, gn = size_t(G) * N;
-    const int tok = tile_row(w >> 1, w & 1, c);             // this lane's token
+    const int tw = w & 3, half = w >> 2, tok = tile_row(tw >> 1, tw & 1, c);    // this lane's token
+    auto column = [&](int i) { return half * NT + i; };     // tile i of this wave, of the N / 16
 
-    f32x4 dq[N / 16], dk[N / 16], Wm[4], Fm[4];
+    f32x4 dq[NT], dk[NT], Wm[2], Fm[2];
 #pragma unroll
-    for (int t = 0; t < N / 16; ++t) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < NT; ++i) dq[i] = dk[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < 4; ++t) Wm[t] = Fm[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int e = 0; e < 2; ++e) Wm[e] = Fm[e] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    {
-        const int pbs = (P + 63) / 64, turns = r * pbs;
-        constexpr int kWarm = (2 * T::kState / 128 + 255) / 256;
-        const int first = int(int64_t(turns) * split / splits), end = int(int64_t(turns) * (split + 1) / splits);
-        for (int turn = first; turn < end; ++turn) {    // head h, rows pb .. pb + 63 of its state
-            const int h = g * r + turn / pbs, pb = turn % pbs * 64;
-            const size_t unit = (size_t(bi) * H + h) * nc + ch;
-            const float *gates = reinterpret_cast<const float *>(images + unit * Img::kBytes + Img::kGates);
-            const float fs = gates[tok], te = gates[kC + tok];
-            __syncthreads();        // the tiles' last readers
-            // thread numbers the compiler does not know: addresses are formed here again
-            // rather than kept over the loops, for which there are not the registers
-            int tid = threadIdx.x;
-            asm volatile("" : "+v"(tid));
-            const int lane = tid & 63, c = lane & 15, q = lane >> 4;
-            if ((pb == 0 || turn == first) && w == 0) {
-                double s = lane < rows ? gate(ag[(size_t(bi) * L + t0 + lane) * H + h]) : 0.0;
+    const int pbs = (P + T::kRows - 1) / T::kRows, turns = r * pbs;
+    const int first = int(int64_t(turns) * split / splits), end = int(int64_t(turns) * (split + 1) / splits);
+    // one turn's values, as loaded: rows and tokens past the end are zeros
+    struct {
+        f32x4 s[T::kLoads][2], d[T::kLoads][2], e, x, bt;
+        u32x4 y;
+        float a, fs, te;
+    } in;
+    auto fetch = [&](int turn) {
+        const int h = g * r + turn / pbs, pb = turn % pbs * T::kRows;
+        const size_t unit = (size_t(bi) * H + h) * nc + ch;
+        const float *gates = reinterpret_cast<const float *>(images + unit * Img::kBytes + Img::kGates);
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int off = 1; off < 64; off <<= 1) {
-                    const double o = __shfl_up(s, off, 64);
-                    if (lane >= off) s += o;
-                }
-                gd[lane] = s;
+        for (int i = 0; i < T::kLoads; ++i) {
+            const int u = i * T::kThreads + tid, row = u / (N / 8);
+            const bool on = u < T::kEights && pb + row < P;
+            const size_t at = (unit * P + pb + (on ? row : 0)) * N + u % (N / 8) * 8;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                in.s[i][e] = on ? *reinterpret_cast<const f32x4 *>(Sg + at + 4 * e) : zero;
+                in.d[i][e] = on ? *reinterpret_cast<const f32x4 *>(dSg + at + 4 * e) : zero;
             }
-            // dY, dv: rows of tokens (past the end: the last one, masked below); S, dS: rows p
-            const size_t src = (size_t(bi) * L + t0) * hp + size_t(h) * P + pb;
-            const int pchunks = min(64, P - pb) / E16;
-            copy_rows<T::RP, kC, 4, 0, 1>(dyg + src, uint32_t(hp) * kSz, rows - 1, pchunks, lds0 + T::kY);
-            copy_rows<T::RP, kC, 4, 0, 1>(dvg + src, uint32_t(hp) * kSz, rows - 1, pchunks, lds0 + T::kV);
-            copy_rows<T::RB, kC, 4, 0, 1>(Sg + (unit * P + pb) * N, T::RB, P - pb - 1, T::RB / 16, lds0 + T::kS);
-            copy_rows<T::RB, kC, 4, 0, 1>(dSg + (unit * P + pb) * N, T::RB, P - pb - 1, T::RB / 16, lds0 + T::kD);
+        }
+        // E and X: a chain wave's tile of 16 p's is 256 pieces, (tid & 255) >> 6 the token tile
+        const int pt = pb / 16 + (tid >> 8), t = (tid >> 6) & 3;
+        const size_t piece = (unit * ptiles + min(pt, ptiles - 1)) * 256 + (tid & 255);
+        in.e = pt < ptiles ? E[piece] : zero;
+        in.x = pt < ptiles ? Xg[piece] : zero;
+        in.bt = *reinterpret_cast<const f32x4 *>(gates + 2 * kC + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
+        constexpr int kPer = T::RP / 16;        // 16-byte pieces of a token's row of dY
+        const int ty = tid / kPer, py = pb + tid % kPer * (16 / kSz);
+        const bool on = ty < rows && py < P;
+        const IO *src = dyg + (size_t(bi) * L + t0 + (on ? ty : 0)) * hp + size_t(h) * P + (on ? py : 0);
+        in.y = on ? *reinterpret_cast<const u32x4 *>(src) : u32x4{0, 0, 0, 0};
+        in.a = lane < rows ? ag[(size_t(bi) * L + t0 + min(lane, rows - 1)) * H + h] : 0.f;
+        in.fs = gates[tok];
+        in.te = gates[kC + tok];
+    };
+    auto put = [&](char *tile, int stride, int row_bytes, int place_, int row, int col, float v) {
+        char *dst = tile + row * row_bytes + (((col * kSz >> 4) ^ place_) << 4) + (col * kSz & 15);
+        if constexpr (kSz == 4) {
+            *reinterpret_cast<float *>(dst) = v;
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {       // U = beta E, from wave w's chain tile: column p, 4 tokens a lane
-                const int t = i, row = 32 * (t >> 1) + 8 * q + 4 * (t & 1), col = (16 * w + c) * kSz;
-                f32x4 u = {0.f, 0.f, 0.f, 0.f};
-                if (pb + 16 * w < P) {
-                    const f32x4 bt = *reinterpret_cast<const f32x4 *>(gates + 2 * kC + row);
-                    u = bt * E[(unit * ptiles + pb / 16 + w) * 256 + 64 * t + lane];
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    char *dst = lds + T::kU + (row + j) * T::RP + (((col >> 4) ^ place<T::RP>(row + j)) << 4) + (col & 15);
-                    if constexpr (kSz == 4) {
-                        *reinterpret_cast<float *>(dst) = u[j];
-                    } else {
-                        const bf16_bits hi = f32_to_bf16(u[j]);
-                        *reinterpret_cast<bf16_bits *>(dst) = hi;
-                        *reinterpret_cast<bf16_bits *>(dst + T::kTok) = f32_to_bf16(u[j] - bf16_to_f32(hi));
-                    }
-                }
+            for (int p = 0; p < kP; ++p) {
+                const bf16_bits part = f32_to_bf16(v);
+                *reinterpret_cast<bf16_bits *>(dst + p * stride) = part;
+                v -= bf16_to_f32(part);
             }
-            copies_done();
-            __syncthreads();
-            // one word of each 128 bytes of what the next turn reads, so that it is in the L2
-            // by then: the states, E, dY and dv
-            uint32_t warm[kWarm + 1];
-            {
-                const int nt = min(turn + 1, end - 1), nh = g * r + nt / pbs, npb = nt % pbs * 64;
-                const size_t nu = (size_t(bi) * H + nh) * nc + ch;
+        }
+    };
+    auto put_state = [&](char *tile, int row, int eight, const f32x4 (&v)[2]) {
+        if constexpr (kSz == 4) {
 #pragma unroll
-                for (int i = 0; i < kWarm; ++i) {
-                    const int at = (i * 256 + tid) * 128 % T::kState, row = min(at / T::RB, P - npb - 1);
-                    const IO *of = (i * 256 + tid) * 128 < T::kState ? Sg : dSg;
-                    warm[i] = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const char *>(of + (nu * P + npb + row) * N) + at % T::RB);
-                }
-                const int row = min(tid & 63, rows - 1);
-                const size_t src = (size_t(bi) * L + t0 + row) * hp + size_t(nh) * P + npb;
-                const char *of = w < 2 ? reinterpret_cast<const char *>(E + (nu * ptiles + min(npb / 16 + (tid >> 5), ptiles - 1)) * 256) + (tid & 31) * 128
-                                       : reinterpret_cast<const char *>((w == 2 ? dyg : dvg) + src);
-                warm[kWarm] = *reinterpret_cast<const uint32_t *>(of);
-            }
-            if (P - pb < 64) {      // rows p past the head: the copies hold others there
-                for (int i = tid + (P - pb) * (T::RB / 16); i < T::kState / 16; i += 256)
-                    *reinterpret_cast<u32x4 *>(lds + T::kS + i * 16) = u32x4{0, 0, 0, 0};
-                __syncthreads();
-            }
-            // the states' parts, and dY U^T and dv U^T (rows j, columns i: this lane's token)
+            for (int e = 0; e < 2; ++e) *reinterpret_cast<f32x4 *>(tile + row * T::RB + (((2 * eight + e) ^ place<T::RB>(row)) * 16)) = v[e];
+        } else {
+            const Op<IO, kP> o = to_op<IO, kP>(v[0], v[1]);
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                int l = lane;
-                asm volatile("" : "+v"(l));
-                const int c = l & 15, q = l >> 4, tok = tile_row(w >> 1, w & 1, c);
-                const Op<IO, 1> oy = read_row<IO, 1, T::RP>(lds + T::kY, 0, tok, ks, q), ov = read_row<IO, 1, T::RP>(lds + T::kV, 0, tok, ks, q);
-                const Op<IO, kP> ou = read_row<IO, kP, T::RP>(lds + T::kU, T::kTok, tok, ks, q);
+            for (int p = 0; p < kP; ++p)
+                *reinterpret_cast<uint4 *>(tile + p * T::kState + row * T::RB + ((eight ^ place<T::RB>(row)) * 16)) = __builtin_bit_cast(uint4, o.p[p]);
+        }
+    };
+    float D[2][4] = {};         // decays from token j = 32 half + 8 q + 4 e + i to this lane's
+    if (T::kAhead && first < end) fetch(first);
+    for (int turn = first; turn < end; ++turn) {    // head h, rows pb .. pb + 31 of its state
+        const bool new_head = turn == first || turn % pbs == 0;
+        if constexpr (!T::kAhead) fetch(turn);
+        const float fs = in.fs, te = in.te;
+        __syncthreads();        // the tiles' last readers
+        // a thread number the compiler does not know: addresses are formed here again rather
+        // than kept over the turns, for which there may not be the registers
+        int tid = threadIdx.x;
+        if constexpr (T::kTight) asm volatile("" : "+v"(tid));
+        const int lane = tid & 63, c = lane & 15, q = lane >> 4, tok = tile_row(tw >> 1, tw & 1, c);
+        if (new_head && w == 0) {
+            double s = lane < rows ? gate(in.a) : 0.0;
 #pragma unroll
-                for (int t = 0; t < N / 16; ++t) {
-                    const Op<IO, 1> as[1] = {read_col<IO, 1, T::RB>(lds + T::kS, 0, 32 * ks, 32 * (t >> 1), t & 1, c, q)};
-                    const Op<IO, 1> ad[1] = {read_col<IO, 1, T::RB>(lds + T::kD, 0, 32 * ks, 32 * (t >> 1), t & 1, c, q)};
-                    f32x4 zq[1] = {{0.f, 0.f, 0.f, 0.f}}, zv[1] = {{0.f, 0.f, 0.f, 0.f}}, zu[1] = {{0.f, 0.f, 0.f, 0.f}};
-                    mma(zq, as, oy);
-                    mma(zv, as, ov);
-                    mma(zu, ad, ou);
-                    dq[t] += (scale * fs) * zq[0];
-                    dk[t] += te * zu[0] - fs * zv[0];
-                    // the tiles' operands are not all read ahead: there are not the registers
-                    if (t & 1) __builtin_amdgcn_sched_barrier(0);
-                }
+            for (int off = 1; off < 64; off <<= 1) {
+                const double o = __shfl_up(s, off, 64);
+                if (lane >= off) s += o;
             }
+            gd[lane] = s;
+        }
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) {
+            const int u = i * T::kThreads + tid;
+            if (u >= T::kEights) break;
+            put_state(lds + T::kS, u / (N / 8), u % (N / 8), in.s[i]);
+            put_state(lds + T::kD, u / (N / 8), u % (N / 8), in.d[i]);
+            if constexpr (T::kTight) __builtin_amdgcn_sched_barrier(0);
+        }
+        {
+            const int t = (tid >> 6) & 3, col = 16 * (tid >> 8) + c;
+            const f32x4 u = in.bt * in.e, v = in.bt * in.x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + j;
+                put(lds + T::kU, T::kTok, T::RP, place<T::RP>(row), row, col, u[j]);
+                put(lds + T::kV, T::kTok, T::RP, place<T::RP>(row), row, col, v[j]);
+                if constexpr (T::kTight) __builtin_amdgcn_sched_barrier(0);
+            }
+            constexpr int kPer = T::RP / 16;
+            if (const int row = tid / kPer; row < kC)
+                *reinterpret_cast<u32x4 *>(lds + T::kY + row * T::RP + (((tid % kPer) ^ place<T::RP>(row)) * 16)) = in.y;
+        }
+        if constexpr (T::kAhead) fetch(min(turn + 1, end - 1));
+        __syncthreads();
+        if (new_head) {
             const double gt = gd[tok];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                f32x4 zw[1] = {{0.f, 0.f, 0.f, 0.f}}, zf[1] = {{0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const Op<IO, kP> au[1] = {read_row<IO, kP, T::RP>(lds + T::kU, T::kTok, tile_row(t >> 1, t & 1, c), ks, q)};
-                    mma(zw, au, read_row<IO, 1, T::RP>(lds + T::kY, 0, tok, ks, q));
-                    mma(zf, au, read_row<IO, 1, T::RP>(lds + T::kV, 0, tok, ks, q));
-                }
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int j = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + i;
-                    const float x = float(gt - gd[j]), d = expf(j <= tok ? x : 0.f);
-                    const float wv = scale * d * zw[0][i], fv = -d * zf[0][i];
-                    Wm[t][i] += j <= tok && tok < rows ? wv : 0.f;
-                    Fm[t][i] += j < tok && tok < rows ? fv : 0.f;
+                    const int j = 32 * half + 8 * q + 4 * e + i;
+                    D[e][i] = expf(j <= tok ? float(gt - gd[j]) : 0.f);
                 }
-                __builtin_amdgcn_sched_barrier(0);
-            }
+        }
+        // the states' parts
+        const Op<IO, 1> oy = read_row<IO, 1, T::RP>(lds + T::kY, 0, tok, 0, q);
+        const Op<IO, kP> ov = read_row<IO, kP, T::RP>(lds + T::kV, T::kTok, tok, 0, q), ou = read_row<IO, kP, T::RP>(lds + T::kU, T::kTok, tok, 0, q);
+        constexpr int M = NT < 2 || T::kTight ? 1 : 2;
 #pragma unroll
-            for (int i = 0; i <= kWarm; ++i) asm volatile("" : : "v"(warm[i]));
+        for (int i0 = 0; i0 < NT; i0 += M) {
+            Op<IO, kP> as[M], ad[M];
+            f32x4 zq[M], zv[M], zu[M];
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                const int t = column(i0 + i);
+                as[i] = read_col<IO, kP, T::RB>(lds + T::kS, T::kState, 0, 32 * (t >> 1), t & 1, c, q);
+                ad[i] = read_col<IO, kP, T::RB>(lds + T::kD, T::kState, 0, 32 * (t >> 1), t & 1, c, q);
+                zq[i] = zv[i] = zu[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+            mma(zq, as, oy);
+            mma(zv, as, ov);
+            mma(zu, ad, ou);
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                dq[i0 + i] += (scale * fs) * zq[i];
+                dk[i0 + i] += te * zu[i] - fs * zv[i];
+            }
+            if constexpr (T::kTight) __builtin_amdgcn_sched_barrier(0);     // no registers to read ahead
+        }
+        // dY U^T and dv U^T (rows j, columns i: this lane's token), where some j <= i
+        if (half <= (tw >> 1)) {
+            Op<IO, kP> au[2];
+            f32x4 zw[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, zf[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) au[e] = read_row<IO, kP, T::RP>(lds + T::kU, T::kTok, tile_row(half, e, c), 0, q);
+            mma(zw, au, oy);
+            mma(zf, au, ov);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = 32 * half + 8 * q + 4 * e + i;
+                    const float wv = scale * D[e][i] * zw[e][i], fv = -D[e][i] * zf[e][i];
+                    Wm[e][i] += j <= tok && tok < rows ? wv : 0.f;
+                    Fm[e][i] += j < tok && tok < rows ? fv : 0.f;
+                }
         }
     }
     __syncthreads();
     // k and q into LDS, W [i][j] and G [i][j] = G [j][i] beside them
     const size_t src = (size_t(bi) * L + t0) * gn + size_t(g) * N;
-    copy_rows<T::RB, kC, 4, 0, 1>(kg + src, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kK);
-    copy_rows<T::RB, kC, 4, 0, 1>(qg + src, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kQ);
-    auto put = [&](char *m, int row, int col, float v) {
-        char *dst = m + row * T::RP + (((col * kSz >> 4) ^ place<T::RP>(row)) << 4) + (col * kSz & 15);
-        if constexpr (kSz == 4) {
-            *reinterpret_cast<float *>(dst) = v;
-        } else {
-            const bf16_bits hi = f32_to_bf16(v);
-            *reinterpret_cast<bf16_bits *>(dst) = hi;
-            *reinterpret_cast<bf16_bits *>(dst + T::kTok) = f32_to_bf16(v - bf16_to_f32(hi));
-        }
-    };
+    constexpr int kCopiers = kC * T::RB >= 8 * 1024 ? 8 : 4;    // waves: 1 KiB each at least
+    if (w < kCopiers) {
+        copy_rows<T::RB, kC, kCopiers, 0, 1>(kg + src, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kK);
+        copy_rows<T::RB, kC, kCopiers, 0, 1>(qg + src, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kQ);
+    }
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int j = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + i;
-            put(lds + T::kWm, tok, j, Wm[t][i]);        // 0 above the diagonal
+            const int j = 32 * half + 8 * q + 4 * e + i;
+            put(lds + T::kWm, T::kMat, T::RM, place<T::RM>(tok), tok, j, Wm[e][i]);     // 0 above the diagonal
             if (j < tok) {
-                put(lds + T::kGm, tok, j, Fm[t][i]);
-                put(lds + T::kGm, j, tok, Fm[t][i]);
+                put(lds + T::kGm, T::kMat, T::RM, place<T::RM>(tok), tok, j, Fm[e][i]);
+                put(lds + T::kGm, T::kMat, T::RM, place<T::RM>(j), j, tok, Fm[e][i]);
             } else if (j == tok) {
-                put(lds + T::kGm, j, j, 0.f);
+                put(lds + T::kGm, T::kMat, T::RM, place<T::RM>(j), j, j, 0.f);
             }
         }
     copies_done();
     __syncthreads();
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-        const Op<IO, kP> wr = read_row<IO, kP, T::RP>(lds + T::kWm, T::kTok, tok, ks, q);
-        const Op<IO, kP> gr = read_row<IO, kP, T::RP>(lds + T::kGm, T::kTok, tok, ks, q);
-        const Op<IO, kP> wc = read_col<IO, kP, T::RP>(lds + T::kWm, T::kTok, 32 * ks, 32 * (w >> 1), w & 1, c, q);
+        int l = lane;
+        if constexpr (T::kTight) asm volatile("" : "+v"(l));
+        const int c = l & 15, q = l >> 4, tok = tile_row(tw >> 1, tw & 1, c);
+        const Op<IO, kP> wr = read_row<IO, kP, T::RM>(lds + T::kWm, T::kMat, tok, ks, q);
+        const Op<IO, kP> gr = read_row<IO, kP, T::RM>(lds + T::kGm, T::kMat, tok, ks, q);
+        const Op<IO, kP> wc = read_col<IO, kP, T::RM>(lds + T::kWm, T::kMat, 32 * ks, 32 * (tw >> 1), tw & 1, c, q);
 #pragma unroll
-        for (int t = 0; t < N / 16; ++t) {
+        for (int i = 0; i < NT; ++i) {
+            const int t = column(i);
             const Op<IO, 1> ak[1] = {read_col<IO, 1, T::RB>(lds + T::kK, 0, 32 * ks, 32 * (t >> 1), t & 1, c, q)};
             const Op<IO, 1> aq[1] = {read_col<IO, 1, T::RB>(lds + T::kQ, 0, 32 * ks, 32 * (t >> 1), t & 1, c, q)};
-            f32x4 z[1] = {dq[t]};
+            f32x4 z[1] = {dq[i]};
             mma(z, ak, wr);
-            dq[t] = z[0];
-            z[0] = dk[t];
+            dq[i] = z[0];
+            z[0] = dk[i];
             mma(z, ak, gr);
             mma(z, aq, wc);
-            dk[t] = z[0];
-            if (t & 1) __builtin_amdgcn_sched_barrier(0);
+            dk[i] = z[0];
+            if constexpr (T::kTight) __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (tok < rows) {
@@ -546,20 +581,14 @@ __global__ __launch_bounds__(256, (GradTile<IO, N>::kPerCu)) void k_delta_grads(
         const size_t all = size_t(gridDim.x / (splits * nc * G)) * L * gn;
         float *pq = parts + 2 * split * all + dst, *pk = pq + all;
 #pragma unroll
-        for (int s = 0; s < N / 32; ++s) {
+        for (int i = 0; i < NT; ++i) {
+            const int at = 32 * (column(i) >> 1) + 4 * (column(i) & 1);
             if (splits > 1) {
-                *reinterpret_cast<f32x4 *>(pq + 32 * s) = dq[2 * s];
-                *reinterpret_cast<f32x4 *>(pq + 32 * s + 4) = dq[2 * s + 1];
-                *reinterpret_cast<f32x4 *>(pk + 32 * s) = dk[2 * s];
-                *reinterpret_cast<f32x4 *>(pk + 32 * s + 4) = dk[2 * s + 1];
-            } else if constexpr (kSz == 4) {
-                *reinterpret_cast<f32x4 *>(dqg + dst + 32 * s) = dq[2 * s];
-                *reinterpret_cast<f32x4 *>(dqg + dst + 32 * s + 4) = dq[2 * s + 1];
-                *reinterpret_cast<f32x4 *>(dkg + dst + 32 * s) = dk[2 * s];
-                *reinterpret_cast<f32x4 *>(dkg + dst + 32 * s + 4) = dk[2 * s + 1];
+                *reinterpret_cast<f32x4 *>(pq + at) = dq[i];
+                *reinterpret_cast<f32x4 *>(pk + at) = dk[i];
             } else {
-                *reinterpret_cast<bf16x8 *>(dqg + dst + 32 * s) = to_op<IO, 1>(dq[2 * s], dq[2 * s + 1]).p[0];
-                *reinterpret_cast<bf16x8 *>(dkg + dst + 32 * s) = to_op<IO, 1>(dk[2 * s], dk[2 * s + 1]).p[0];
+                *reinterpret_cast<Raw4<IO> *>(dqg + dst + at) = narrow<IO>(dq[i]);
+                *reinterpret_cast<Raw4<IO> *>(dkg + dst + at) = narrow<IO>(dk[i]);
             }
         }
     }
@@ -641,10 +670,11 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
     const auto *q = static_cast<const IO *>(a.q), *k = static_cast<const IO *>(a.k), *v = static_cast<const IO *>(a.v);
     const auto *dy = static_cast<const IO *>(a.dy);
     auto *dv = static_cast<IO *>(a.dv);
-    DeltaSaved saved{reinterpret_cast<float *>(ws + pl.off_e), ws + pl.off_s, reinterpret_cast<float *>(ws + pl.off_anchor),
+    DeltaSaved saved{reinterpret_cast<float *>(ws + pl.off_e), reinterpret_cast<float *>(ws + pl.off_s), reinterpret_cast<float *>(ws + pl.off_anchor),
                      reinterpret_cast<float *>(ws + pl.off_ydy)};
     BackSums sums{reinterpret_cast<float *>(ws + pl.off_xe), reinterpret_cast<float *>(ws + pl.off_vdv), reinterpret_cast<float *>(ws + pl.off_lam)};
-    auto *dS = reinterpret_cast<IO *>(ws + pl.off_ds);
+    auto *dS = reinterpret_cast<float *>(ws + pl.off_ds);
+    auto *kept_x = reinterpret_cast<f32x4 *>(ws + pl.off_x);
     auto *parts = reinterpret_cast<float *>(ws + pl.off_parts);
 
     hipError_t e = launch_delta_prep<IO, N>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
@@ -664,7 +694,7 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(kern, dim3(unsigned(int64_t(a.b) * a.H * (cut.segments - (MAP ? 1 : 0)) * pblocks)), dim3(64 * W), lds, stream, q, k,
                            v, dy, images, a.d_final, dinit, reinterpret_cast<const f32x4 *>(saved.E),
-                           reinterpret_cast<const f32x4 *>(saved.anchor), dv, dS, to, sums, a.L, a.H, a.P, a.G, nc, cut.per, cut.segments,
+                           reinterpret_cast<const f32x4 *>(saved.anchor), dv, dS, kept_x, to, sums, a.L, a.H, a.P, a.G, nc, cut.per, cut.segments,
                            pblocks, a.scale);
         return hipGetLastError();
     };
@@ -688,8 +718,8 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
     constexpr int lds = GradTile<IO, N>::kLds;
     e = hipFuncSetAttribute(reinterpret_cast<const void *>(grads), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(grads, dim3(unsigned(int64_t(a.b) * a.G * nc * pl.splits)), dim3(256), lds, stream, q, k, a.a, dy, dv, images,
-                       reinterpret_cast<const f32x4 *>(saved.E), static_cast<const IO *>(saved.S), dS, static_cast<IO *>(a.dq),
+    hipLaunchKernelGGL(grads, dim3(unsigned(int64_t(a.b) * a.G * nc * pl.splits)), dim3(GradTile<IO, N>::kThreads), lds, stream, q, k, a.a, dy, images,
+                       reinterpret_cast<const f32x4 *>(saved.E), kept_x, saved.S, dS, static_cast<IO *>(a.dq),
                        static_cast<IO *>(a.dk), parts, pl.splits, a.L, a.H, a.P, a.G, nc, a.scale);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (pl.splits > 1) {
@@ -703,17 +733,9 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
     return hipGetLastError();
 }
 
-// Parts to split a group's `turns` (of up to 64 state rows) into, where the chunks alone
-// leave CUs idle: as many as keep every block resident.  bf16, N = 128, one group: 64 heads
-// x 512 tokens 478 -> 140 us, 80 x 4096 1269 -> 840; twice the blocks 137 and 856, half of
-// them 132 and 885.  fp32, N = 64, one block per CU: 763 -> 164 us and 1703 -> 1068.
-int grad_splits(size_t cells, size_t turns, int N, bool bf16) {
-    const int per_cu = N == 32    ? bf16 ? GradTile<bf16_bits, 32>::kPerCu : GradTile<float, 32>::kPerCu
-                       : N == 64  ? bf16 ? GradTile<bf16_bits, 64>::kPerCu : GradTile<float, 64>::kPerCu
-                       : N == 128 ? bf16 ? GradTile<bf16_bits, 128>::kPerCu : GradTile<float, 128>::kPerCu
-                                  : GradTile<bf16_bits, 256>::kPerCu;
-    return int(std::max<size_t>(1, std::min(turns, 256 * per_cu / cells)));
-}
+// Parts to split a group's `turns` (of up to 32 state rows) into, where the chunks alone
+// leave CUs idle: as many as give each CU a block.
+int grad_splits(size_t cells, size_t turns) { return int(std::max<size_t>(1, std::min(turns, 256 / cells))); }
 
 }  // namespace
 
@@ -721,7 +743,7 @@ DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16)
     DeltaBwdPlan pl;
     if (b <= 0 || L <= 0 || !delta_chunk_supported(b, L, H, P, N, G, bf16)) return pl;
     const size_t nc = (size_t(L) + kC - 1) / kC, segs = bf16 ? (nc + kSegment<bf16_bits> - 1) / kSegment<bf16_bits> : (nc + kSegment<float> - 1) / kSegment<float>, bh = size_t(b) * H, units = bh * nc;
-    const size_t sz = bf16 ? 2 : 4, state = size_t(P) * N, ptiles = size_t(P) / 16;
+    const size_t state = size_t(P) * N, ptiles = size_t(P) / 16;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t off = at;
@@ -730,14 +752,15 @@ DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16)
     };
     take(units * (bf16 ? ChunkImage<bf16_bits>::kBytes : ChunkImage<float>::kBytes));
     pl.off_e = take(units * kC * P * 4);
-    pl.off_s = take(units * state * sz);
-    pl.off_ds = take(units * state * sz);
+    pl.off_x = take(units * kC * P * 4);
+    pl.off_s = take(units * state * 4);
+    pl.off_ds = take(units * state * 4);
     pl.off_anchor = take(bh * segs * state * 4);
     pl.off_ydy = take(units * kMaxShare * ptiles * kC * 4);
     pl.off_xe = take(units * ptiles * kC * 4);
     pl.off_vdv = take(units * ptiles * kC * 4);
     pl.off_lam = take(bh * ptiles * segs * kMaxShare * 4);
-    pl.splits = grad_splits(size_t(b) * G * nc, size_t(H / G) * ((P + 63) / 64), N, bf16);
+    pl.splits = grad_splits(size_t(b) * G * nc, size_t(H / G) * ((P + 31) / 32));
     pl.cut = cut_sequence(int64_t(bh), int(nc), P, N, bf16, true);
     pl.off_map = take(map_bytes(bh, P, N, pl.cut));
     pl.off_init = take(entering_bytes(bh, P, N, pl.cut));

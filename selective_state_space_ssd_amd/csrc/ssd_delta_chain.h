@@ -9,7 +9,7 @@ namespace ssd {
 
 // What the forward chain leaves for the backward pass, per (batch, head):
 //   E       [nc][P / 16][4][64] f32x4: a wave's accumulators of the brackets, as held
-//   S       [nc][P][N] io: the state that enters each chunk
+//   S       [nc][P][N] fp32: the state that enters each chunk
 //   anchor  [P / 16][segments][N / 16][64] f32x4: the state after each segment of chunks,
 //           as held
 //   ydy     [nc][X][P / 16][64] fp32: parts of y . dy of each token over 16 rows, to be added
@@ -21,7 +21,7 @@ constexpr int kSegment = std::is_same_v<IO, float> ? 1 : 2;
 
 struct DeltaSaved {
     float *E;
-    void *S;
+    float *S;
     float *anchor;
     float *ydy;
 };
@@ -56,6 +56,7 @@ template <int RB, int ROWS, int W, int PART, int PARTS>
 __device__ __forceinline__ void copy_rows(const void *base, uint32_t stride, int last, int chunks, uint32_t dst) {
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     constexpr int kIt = ROWS * RB / 1024 / W, kPer = (kIt + PARTS - 1) / PARTS;
+    static_assert(kIt * W * 1024 == ROWS * RB);
 #pragma unroll
     for (int i = PART * kPer; i < (PART + 1) * kPer && i < kIt; ++i) {
         const int at = (i * W + w) * 64 + lane, r = at / (RB / 16), col = min((at % (RB / 16)) ^ place<RB>(r), chunks - 1);
@@ -252,16 +253,9 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
 #pragma unroll
             for (int s = 0; s < KS; ++s) so[s] = to_op<IO, kPlanes>(S[2 * s], S[2 * s + 1]);
             if constexpr (SAVE) {
-                IO *dst = static_cast<IO *>(saved.S) + ((size_t(bh) * nc + ch) * P + p) * N + 32 * n0 + 8 * q;
+                float *dst = saved.S + ((size_t(bh) * nc + ch) * P + p) * N + 32 * n0 + 8 * q;
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    if constexpr (kSz == 4) {
-                        *reinterpret_cast<f32x4 *>(dst + 32 * s) = S[2 * s];
-                        *reinterpret_cast<f32x4 *>(dst + 32 * s + 4) = S[2 * s + 1];
-                    } else {
-                        *reinterpret_cast<bf16x8 *>(dst + 32 * s) = so[s].p[0];
-                    }
-                }
+                for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(dst + 32 * (t >> 1) + 4 * (t & 1)) = S[t];
             }
             // this wave's part of R = V - e^g K S^T, and of the state's part of Y (rows p in
             // registers: 4 consecutive ones of one token per lane)
