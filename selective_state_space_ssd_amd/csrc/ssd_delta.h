@@ -78,10 +78,10 @@ struct DeltaBwdArgs {
 // The workspace begins with the chunk images; byte offsets of what follows.
 struct DeltaBwdPlan {
     bool supported = false;
-    size_t off_e = 0, off_x = 0, off_s = 0, off_ds = 0, off_anchor = 0, off_ydy = 0, off_xe = 0, off_vdv = 0, off_lam = 0;
+    size_t off_e = 0, off_x = 0, off_s = 0, off_ds = 0;
     DeltaCut cut;
     size_t off_map = 0, off_init = 0, off_dmap = 0, off_dinit = 0;      // of the segments, and of their gradients
-    size_t off_parts = 0;   // sums of dq and dk in `splits` parts, if more than 1
+    size_t off_parts = 0, off_gate_parts = 0;   // sums of dq and dk, da and dbeta in `splits` parts, if more than 1
     int splits = 1;
     size_t total = 0;
 };

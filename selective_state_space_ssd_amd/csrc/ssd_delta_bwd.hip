@@ -1,12 +1,12 @@
 // ssd_delta_bwd.hip -- gradients of the gated delta rule, in chunks of 64 tokens (formulas,
 // names and tile layout of the forward pass: ssd_delta_chunk.h).
 //
-// Nothing is kept from the forward pass; five kernels:
+// Nothing is kept from the forward pass; four kernels:
 //   1 prep       M and the scores of every chunk (ssd_delta_prep.h)
-//   2 chain      forward over the chunks: E, the entering states, y . dy (ssd_delta_chain.h)
+//   2 chain      forward over the chunks: E and the entering states (ssd_delta_chain.h)
 //   3 chain back from d_final, with dS the gradient of the state a chunk leaves:
 //        dU = scores^T dY + e^{g_C - g} (K dS^T),   X = dU + M^T (beta dU)
-//        dv = beta X,   dbeta_i = X_i . E_i
+//        dv = beta X
 //        dS <- e^{g_C} dS + (scale e^g dY)^T Q - (e^g dv)^T K
 //   4 grads      per chunk; dq and dk are sums over a group's heads, taken in one block, or
 //                in a few whose fp32 sums a further kernel adds:
@@ -14,15 +14,18 @@
 //        dk = -e^g dv S + e^{g_C - g} U dS + W^T Q + G K,  G = F + F^T, F_ij = -(dv_i . u_j) D_ij, j < i
 //      Both are differences where the chunk's updates erase a large state, or the gradient of
 //      one: states, U, dv, W and G keep 32 bits here too, and dq and dk are rounded once.
-//   5 gates      da.  The gates only scale v going in and y coming out of an ungated rule,
-//        so the gradient of the gate sum at token t is y_t . dy_t - v_t . dv_t, and
-//        da_t = sum of it from t to the end of a segment + <dS, S> at the segment's end.
+//        dbeta_i = X_i . E_i
+//      da_t is the sum of what passes the gate of token t: from tokens j < t to i >= t in the
+//      chunk, from the entering state to i >= t, from j < t to the leaving state, and from
+//      state to state.  Every such term holds e^{a_t}.  (The difference y . dy - v . dv summed
+//      over the tokens from t on is the same number, with fewer products, but its terms do
+//      not shrink with the gate: with a = -8 it was off by 2e-3 of da, with -16 by 3 times da.)
 // 2 and 3 are chains over the chunks whose waves keep 16 rows of the state each, as in the
-// forward pass: 32-bit values throughout, since da and dbeta come out of differences.
+// forward pass: 32-bit values throughout.
 //
-// 4 x 2048 tokens, 32 heads of 128 x 128, bf16, us: prep 45, chain 216, chain back 287, grads
-// 325, gates 9.  The chains are bound by a wave's steps (ssd_delta_chain.h) and write 805 MB
-// (both states, E and X, in 32 bits); grads reads 870 MB, 2.7 TB/s.
+// 4 x 2048 tokens, 32 heads of 128 x 128, bf16, us: prep 45, chain 151, chain back 219, grads
+// 403.  The chains are bound by a wave's steps (ssd_delta_chain.h) and write 805 MB (both
+// states, E and X, in 32 bits); grads reads 870 MB.
 #include <algorithm>
 
 #include "ssd_delta.h"
@@ -32,12 +35,6 @@
 namespace ssd {
 namespace {
 
-// Sums over 16 rows of the state, per token: fp32 [nc][P / 16][64] each.
-struct BackSums {
-    float *xe, *vdv;
-    float *lam;         // [P / 16][segments][X]: <dS, S> at the end of each segment, in parts
-};
-
 // Kernel 3.  Waves, tiles and LDS as in the forward chain; dy is read by every wave.  One
 // chain per (batch, head, segment of `per` chunks).  What leaves the last segment is d_final,
 // what leaves the others is in `d_enter`.  MAP: of the segments 1 .. segs - 1, only the
@@ -45,14 +42,12 @@ struct BackSums {
 // others; the forward maps tell what d_enter adds to it.
 template <typename IO, int N, int W, int X, bool MAP, bool ONE>
 __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restrict__ qg, const IO *__restrict__ kg,
-                                                             const IO *__restrict__ vg, const IO *__restrict__ dyg,
-                                                             const char *__restrict__ images, const float *__restrict__ d_final,
-                                                             const float *__restrict__ d_enter, const f32x4 *__restrict__ E,
-                                                             const f32x4 *__restrict__ anchor, IO *__restrict__ dvg,
-                                                             float *__restrict__ dSg, f32x4 *__restrict__ Xg, float *__restrict__ d_out, BackSums sums, int L,
-                                                             int H, int P, int G, int nc, int per, int segs, int pblocks,
-                                                             float scale) {
-    using T = ChainLds<IO, N, W, X, false, ONE>;
+                                                             const IO *__restrict__ dyg, const char *__restrict__ images,
+                                                             const float *__restrict__ d_final, const float *__restrict__ d_enter,
+                                                             IO *__restrict__ dvg, float *__restrict__ dSg, f32x4 *__restrict__ Xg,
+                                                             float *__restrict__ d_out, int L, int H, int P, int G, int nc, int per,
+                                                             int segs, int pblocks, float scale) {
+    using T = ChainLds<IO, N, W, X, true, false, ONE>;
     using Img = typename T::Img;
     extern __shared__ __align__(16) char lds[];
     constexpr int kSz = int(sizeof(IO)), KS = N / 32 / X, NT = 2 * KS;
@@ -61,7 +56,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
     const int blk = xcd_neighbours(), pb = blk % pblocks, chain = blk / pblocks, skip = MAP ? 1 : 0;
     const int seg = chain % (segs - skip) + skip, bh = chain / (segs - skip), first = seg * per, last = min(first + per, nc) - 1;
     const int h = bh % H, bi = bh / H, g = h / (H / G);
-    const int p0 = (pb * (W / X) + w / X) * 16, p = p0 + c, ptiles = P / 16, anchors = (nc + kSegment<IO> - 1) / kSegment<IO>;
+    const int p0 = (pb * (W / X) + w / X) * 16, p = p0 + c, ptiles = P / 16;
     const bool live = p0 < P;
     const size_t hp = size_t(H) * P, gn = size_t(G) * N;
     const char *img = images + size_t(bh) * nc * Img::kBytes;
@@ -142,22 +137,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
         auto gate_of = [&](int which, int t) {
             return *reinterpret_cast<const f32x4 *>(gates + which * kC + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
         };
-        if (!MAP && live) {
-            if (ch % kSegment<IO> == kSegment<IO> - 1 || ch == nc - 1) {
-                const size_t at = (size_t(bh) * ptiles + p0 / 16) * anchors + ch / kSegment<IO>;
-                const f32x4 *a0 = anchor + (at * (N / 16) + x * NT) * 64 + lane;
-                float dot = 0.f;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const f32x4 a = a0[64 * t];
-                    dot += S[t][0] * a[0] + S[t][1] * a[1] + S[t][2] * a[2] + S[t][3] * a[3];
-                }
-                dot = wave_sum(dot);
-                if (lane == 0) sums.lam[at * X + x] = dot;
-            }
-        }
-        f32x4 dU[4], dv[4], xs[kOwn], vd[kOwn], Ev[kOwn];
-        IO rv[4 * kOwn];
+        f32x4 dU[4], dv[4];
         if (live) {
             Op<IO, kPlanes> so[KS];
 #pragma unroll
@@ -202,18 +182,6 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
         if constexpr (X > 1) {
             copies_done();      // q, asked for at the chunk's beginning
             __syncthreads();    // and the parts are written
-        }
-        if (!MAP && live) {     // what the end of the chunk needs: E and v of this wave's token tiles
-            const f32x4 *src = E + (unit * ptiles + p0 / 16) * 256 + lane;
-            const __amdgpu_buffer_rsrc_t view = chunk_view(vg + vy0 + size_t(t0) * hp, rows, tok, P);
-            const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
-#pragma unroll
-            for (int j = 0; j < kOwn; ++j) {
-                const int t = x * kOwn + j;
-                Ev[j] = src[64 * t];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) rv[4 * j + r] = load_checked<IO>(view, off + uint32_t(32 * (t >> 1) + 4 * (t & 1) + r) * tok);
-            }
         }
         ahead(std::integral_constant<int, 0>{});
         ahead(std::integral_constant<int, 1>{});
@@ -271,16 +239,6 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
                     if constexpr (kSz == 4) __builtin_amdgcn_sched_barrier(0);     // no registers to read ahead
                 }
             }
-            // the sums over the 16 rows (the 16 lanes of a row group), of this wave's token tiles
-#pragma unroll
-            for (int j = 0; j < (MAP ? 0 : kOwn); ++j) {
-                const f32x4 du = own(dU, j), dvj = own(dv, j);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    xs[j][r] = row16_sum(du[r] * Ev[j][r]);
-                    vd[j][r] = row16_sum(dvj[r] * to_f32<IO>(rv[4 * j + r]));
-                }
-            }
         }
         if constexpr (T::kBufs == 1) {
             __syncthreads();
@@ -293,7 +251,6 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
         __syncthreads();
         if constexpr (T::kBufs == 2) fetch_q(next);     // this chunk's is read
         if (!MAP && live) {
-            const size_t at = (unit * ptiles + p0 / 16) * kC + 8 * q;
             const __amdgpu_buffer_rsrc_t view = chunk_view(dvg + vy0 + size_t(t0) * hp, rows, tok, P);
             const uint32_t off = uint32_t(8 * q) * tok + uint32_t(p) * kSz;
 #pragma unroll
@@ -301,10 +258,6 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
                 const int t = x * kOwn + j, row = 32 * (t >> 1) + 4 * (t & 1);
                 const f32x4 dvj = own(dv, j);
                 Xg[(unit * ptiles + p0 / 16) * 256 + 64 * t + lane] = own(dU, j);
-                if (c == 0) {
-                    *reinterpret_cast<f32x4 *>(sums.xe + at + row) = xs[j];
-                    *reinterpret_cast<f32x4 *>(sums.vdv + at + row) = vd[j];
-                }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int o = int(off + uint32_t(row + r) * tok);
@@ -320,26 +273,39 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
         for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(d_out + state_at(MAP ? bh * segs + seg : bh, t)) = S[t];
 }
 
-// Kernel 4.  Block = (batch, chunk, group, one of `splits` parts of its heads' state rows).
-// Wave w holds dq^T and dk^T of 16 tokens (tile columns; rows n in registers, 4 consecutive
-// ones a tile), of one half of the N's: waves w and w + 4 share their tokens.  Per turn a
-// head's 32 rows p: dY, dv, U and both states go through LDS, 32-bit ones split into kPlanes
-// planes on the way there; the next turn's values are on their way into registers meanwhile.
+// Kernel 4.  Block = (batch, chunk, group, one of `splits` parts of its heads' state rows, NB
+// of the N columns: more have no room in registers).  Wave w holds dq^T and dk^T of 16
+// tokens (tile columns; rows n in registers, 4 consecutive ones a tile), of one half of the
+// columns: waves w and w + 4 share their tokens.  Per turn a
+// head's 32 rows p: dY, X, E and both states go through LDS, 32-bit ones split into kPlanes
+// planes on the way there; the next turn's values are asked for as soon as this one's have
+// left their registers.
 template <typename IO, int N>
 struct GradTile {
     static constexpr int kSz = int(sizeof(IO)), kP = kSz == 4 ? 1 : kPlanes;
     static constexpr int kRows = 32;                        // state rows a turn
-    static constexpr int RP = kRows * kSz, RB = N * kSz;    // bytes per row of p's / of N
-    static constexpr int kTok = kC * RP, kState = kRows * RB;       // bytes of a [64][32] / [32][N] tile
-    static constexpr int kS = 0, kD = kP * kState, kU = 2 * kP * kState, kV = kU + kP * kTok, kY = kV + kP * kTok, kHead = kY + kTok;
-    // after the heads: W and G (kP planes each), k, q
-    static constexpr int RM = kC * kSz, kMat = kC * RM, kWm = 0, kGm = kP * kMat, kK = 2 * kP * kMat, kQ = kK + kC * RB, kTail = kQ + kC * RB;
-    static constexpr int kLds = kHead > kTail ? kHead : kTail;
-    static constexpr int kThreads = 512, kEights = kRows * N / 8, kLoads = (kEights + kThreads - 1) / kThreads;     // 8 values a thread and load
-    static constexpr bool kTight = RB >= 512;       // as many accumulators as leave few registers
-    static constexpr bool kAhead = N <= 128;        // a turn's values are asked for a turn ahead
+    static constexpr int NB = N * kSz > 256 ? 256 / kSz : N, kCols = N / NB;
+    static constexpr int RT = kC * kSz, RP = kRows * kSz, RB = NB * kSz;    // bytes per row of tokens / of p's / of columns
+    static constexpr int kTok = kRows * RT, kState = kRows * RB;            // bytes of a tile of tokens / of the state
+    // S, dS [32][NB]; E, X [32][64] (kP planes each); dY [64][32]
+    static constexpr int kS = 0, kD = kP * kState, kE = 2 * kP * kState, kV = kE + kP * kTok, kY = kV + kP * kTok, kHead = kY + kTok;
+    // after the heads, over them: W and G [64][64] (kP planes each); beside them k, q [64][NB]
+    static constexpr int kMat = kC * RT, kWm = 0, kGm = kP * kMat, kTail = 2 * kP * kMat;
+    static constexpr int kK = kHead > kTail ? kHead : kTail, kQ = kK + kC * RB, kEnd = kQ + kC * RB;
+    // W and F, summed over the heads so far, as the 6 waves hold them that have any; the gates'
+    // part: sums down T's columns [8][64]; A, B [2][64], X . E [2][64], e^g, e^{g_C - g} and beta.
+    // T [64][65] lies over the tiles of the head's last turn.
+    static constexpr int kW = kEnd, kSums = kW + 6 * 4096, kA = kSums + 8 * kC * 4, kB = kA + 2 * kC * 4, kX = kB + 2 * kC * 4, kGates = kX + 2 * kC * 4;
+    static constexpr int kLds = kGates + 3 * kC * 4, LT = kC + 1;
+    static_assert(kC * LT * 4 <= kHead);
+    static constexpr int kThreads = 512, kEights = kRows * NB / 8, kLoads = (kEights + kThreads - 1) / kThreads;     // 8 values a thread and load
+    static constexpr bool kTight = RB >= 256;       // as many accumulators as leave few registers
     static_assert(kLds <= 159 * 1024);
 };
+
+// Portions of a head's state rows that different blocks take, where a group's turns are split:
+// block s takes the turns turns * s / splits .. turns * (s + 1) / splits - 1.
+__host__ __device__ __forceinline__ int split_of(int64_t turn, int64_t turns, int splits) { return int(((turn + 1) * splits - 1) / turns); }
 
 template <typename IO, int N>
 __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, const IO *__restrict__ kg,
@@ -347,80 +313,104 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
                                                      const char *__restrict__ images, const f32x4 *__restrict__ E,
                                                      const f32x4 *__restrict__ Xg, const float *__restrict__ Sg,
                                                      const float *__restrict__ dSg, IO *__restrict__ dqg, IO *__restrict__ dkg,
-                                                     float *__restrict__ parts, int splits, int L, int H, int P, int G, int nc,
-                                                     float scale) {
+                                                     float *__restrict__ dag, float *__restrict__ dbg, float *__restrict__ parts,
+                                                     float *__restrict__ gate_parts, int splits, int L, int H, int P, int G,
+                                                     int nc, float scale) {
     using T = GradTile<IO, N>;
     using Img = ChunkImage<IO>;
-    constexpr int kSz = T::kSz, kP = T::kP, NT = N / 32;    // column tiles of a wave
+    constexpr int kSz = T::kSz, kP = T::kP, NB = T::NB, kCols = T::kCols, NT = NB / 32;     // column tiles of a wave
     extern __shared__ __align__(16) char lds[];
     __shared__ double gd[kC];
+    __shared__ float zs[8];
     const uint32_t lds0 = lds_address(lds);
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
-    const int split = blockIdx.x % splits, cell = blockIdx.x / splits, ch = cell % nc, bg = cell / nc, g = bg % G, bi = bg / G, r = H / G;
+    const int tid0 = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid0 >> 6);
+    const int cb = blockIdx.x % kCols, split = blockIdx.x / kCols % splits, cell = blockIdx.x / kCols / splits, ch = cell % nc, bg = cell / nc, g = bg % G, bi = bg / G, r = H / G;
     const int t0 = ch * kC, rows = min(kC, L - t0), ptiles = P / 16;
     const size_t hp = size_t(H) * P, gn = size_t(G) * N;
-    const int tw = w & 3, half = w >> 2, tok = tile_row(tw >> 1, tw & 1, c);    // this lane's token
-    auto column = [&](int i) { return half * NT + i; };     // tile i of this wave, of the N / 16
+    const int tw = w & 3, half = w >> 2;
+    const bool below = half <= (tw >> 1);       // some of this wave's j's are not after its tokens
+    auto column = [&](int i) { return half * NT + i; };     // tile i of this wave, of the NB / 16
+    const IO *k0 = kg + (size_t(bi) * L + t0) * gn + size_t(g) * N, *q0 = qg + (size_t(bi) * L + t0) * gn + size_t(g) * N;
+    float *Tm = reinterpret_cast<float *>(lds), *sums = reinterpret_cast<float *>(lds + T::kSums);
+    float *As = reinterpret_cast<float *>(lds + T::kA), *Bs = reinterpret_cast<float *>(lds + T::kB), *Xs = reinterpret_cast<float *>(lds + T::kX);
+    float *gates = reinterpret_cast<float *>(lds + T::kGates);
+    f32x4 *held = reinterpret_cast<f32x4 *>(lds + T::kW) + (half ? tw + 2 : tw) * 256 + (tid0 & 63);     // W, F [2][64] each of a wave
 
-    f32x4 dq[NT], dk[NT], Wm[2], Fm[2];
+    f32x4 dq[NT], dk[NT];                   // sums over the heads
+    f32x4 Wh[2], Fh[2], xe;                 // of one head: dY E^T and X E^T; X . E
+    float accA, accB, accZ;                 // this lane's part of A_i, B_i, Z (below) of one head
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < NT; ++i) dq[i] = dk[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < NT; ++i) dq[i] = dk[i] = zero;
+    if (below)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) Wm[e] = Fm[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int e = 0; e < 4; ++e) held[64 * e] = zero;
+    auto clear_head = [&]() {
+        Wh[0] = Wh[1] = Fh[0] = Fh[1] = xe = zero;
+        accA = accB = accZ = 0.f;
+    };
+    clear_head();
 
+    constexpr int kCopiers = kC * T::RB >= 8 * 1024 ? 8 : 4;    // waves: 1 KiB each at least
+    auto copy_keys = [&]() {
+        if (w < kCopiers) {
+            copy_rows<T::RB, kC, kCopiers, 0, 1>(k0 + cb * NB, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kK);
+            copy_rows<T::RB, kC, kCopiers, 0, 1>(q0 + cb * NB, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kQ);
+        }
+    };
     const int pbs = (P + T::kRows - 1) / T::kRows, turns = r * pbs;
     const int first = int(int64_t(turns) * split / splits), end = int(int64_t(turns) * (split + 1) / splits);
     // one turn's values, as loaded: rows and tokens past the end are zeros
-    struct {
-        f32x4 s[T::kLoads][2], d[T::kLoads][2], e, x, bt;
-        u32x4 y;
-        float a, fs, te;
-    } in;
-    auto fetch = [&](int turn) {
+    f32x4 in_s[T::kLoads][2], in_d[T::kLoads][2], in_e, in_x;
+    u32x4 in_y;
+    float in_a, in_gate;
+    auto fetch_states = [&](int i, int turn, int tid) {     // the i'th load of each state
+        const int h = g * r + turn / pbs, pb = turn % pbs * T::kRows, u = i * T::kThreads + tid;
+        const size_t at = (((size_t(bi) * H + h) * nc + ch) * P + pb + u / (NB / 8)) * N + cb * NB + u % (NB / 8) * 8;
+        const bool on = u < T::kEights && pb + u / (NB / 8) < P;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            in_s[i][e] = on ? *reinterpret_cast<const f32x4 *>(Sg + at + 4 * e) : zero;
+            in_d[i][e] = on ? *reinterpret_cast<const f32x4 *>(dSg + at + 4 * e) : zero;
+        }
+    };
+    auto fetch_rest = [&](int turn, int tid) {
         const int h = g * r + turn / pbs, pb = turn % pbs * T::kRows;
         const size_t unit = (size_t(bi) * H + h) * nc + ch;
-        const float *gates = reinterpret_cast<const float *>(images + unit * Img::kBytes + Img::kGates);
-        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < T::kLoads; ++i) {
-            const int u = i * T::kThreads + tid, row = u / (N / 8);
-            const bool on = u < T::kEights && pb + row < P;
-            const size_t at = (unit * P + pb + (on ? row : 0)) * N + u % (N / 8) * 8;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                in.s[i][e] = on ? *reinterpret_cast<const f32x4 *>(Sg + at + 4 * e) : zero;
-                in.d[i][e] = on ? *reinterpret_cast<const f32x4 *>(dSg + at + 4 * e) : zero;
-            }
-        }
+        const float *from = reinterpret_cast<const float *>(images + unit * Img::kBytes + Img::kGates);
         // E and X: a chain wave's tile of 16 p's is 256 pieces, (tid & 255) >> 6 the token tile
-        const int pt = pb / 16 + (tid >> 8), t = (tid >> 6) & 3;
+        const int pt = pb / 16 + (tid >> 8);
         const size_t piece = (unit * ptiles + min(pt, ptiles - 1)) * 256 + (tid & 255);
-        in.e = pt < ptiles ? E[piece] : zero;
-        in.x = pt < ptiles ? Xg[piece] : zero;
-        in.bt = *reinterpret_cast<const f32x4 *>(gates + 2 * kC + 32 * (t >> 1) + 8 * q + 4 * (t & 1));
+        in_e = pt < ptiles ? E[piece] : zero;
+        in_x = pt < ptiles ? Xg[piece] : zero;
         constexpr int kPer = T::RP / 16;        // 16-byte pieces of a token's row of dY
         const int ty = tid / kPer, py = pb + tid % kPer * (16 / kSz);
         const bool on = ty < rows && py < P;
         const IO *src = dyg + (size_t(bi) * L + t0 + (on ? ty : 0)) * hp + size_t(h) * P + (on ? py : 0);
-        in.y = on ? *reinterpret_cast<const u32x4 *>(src) : u32x4{0, 0, 0, 0};
-        in.a = lane < rows ? ag[(size_t(bi) * L + t0 + min(lane, rows - 1)) * H + h] : 0.f;
-        in.fs = gates[tok];
-        in.te = gates[kC + tok];
+        in_y = on ? *reinterpret_cast<const u32x4 *>(src) : u32x4{0, 0, 0, 0};
+        in_a = ag[(size_t(bi) * L + t0 + min(tid & 63, rows - 1)) * H + h];
+        in_gate = from[min(tid, 3 * kC - 1)];
     };
-    auto put = [&](char *tile, int stride, int row_bytes, int place_, int row, int col, float v) {
-        char *dst = tile + row * row_bytes + (((col * kSz >> 4) ^ place_) << 4) + (col * kSz & 15);
+    auto fetch = [&](int turn, int tid) {
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) fetch_states(i, turn, tid);
+        fetch_rest(turn, tid);
+    };
+    // 4 / 8 consecutive values of row `row` of a tile, from element `col` (a multiple of 4 / 8) on
+    auto put4 = [&](char *tile, int row, int col, f32x4 v) {
+        char *dst = tile + row * T::RT + (((col * kSz >> 4) ^ place<T::RT>(row)) << 4) + (col * kSz & 15);
         if constexpr (kSz == 4) {
-            *reinterpret_cast<float *>(dst) = v;
+            *reinterpret_cast<f32x4 *>(dst) = v;
         } else {
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
-                const bf16_bits part = f32_to_bf16(v);
-                *reinterpret_cast<bf16_bits *>(dst + p * stride) = part;
-                v -= bf16_to_f32(part);
+                const u32x2 part = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                *reinterpret_cast<u32x2 *>(dst + p * T::kTok) = part;
+                v = f32x4{minus_lo(v[0], part[0]), minus_hi(v[1], part[0]), minus_lo(v[2], part[1]), minus_hi(v[3], part[1])};
             }
         }
     };
-    auto put_state = [&](char *tile, int row, int eight, const f32x4 (&v)[2]) {
+    auto put8 = [&](char *tile, int row, int eight, const f32x4 (&v)[2]) {
         if constexpr (kSz == 4) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) *reinterpret_cast<f32x4 *>(tile + row * T::RB + (((2 * eight + e) ^ place<T::RB>(row)) * 16)) = v[e];
@@ -431,20 +421,56 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
                 *reinterpret_cast<uint4 *>(tile + p * T::kState + row * T::RB + ((eight ^ place<T::RB>(row)) * 16)) = __builtin_bit_cast(uint4, o.p[p]);
         }
     };
-    float D[2][4] = {};         // decays from token j = 32 half + 8 q + 4 e + i to this lane's
-    if (T::kAhead && first < end) fetch(first);
+    // 4 values of row `tok` of k or q, columns 4 c4 .. of the block's
+    auto four_of = [&](const char *tile, int tok, int c4) {
+        const int at = c4 * 4 * kSz;
+        return widen<IO>(*reinterpret_cast<const Raw4<IO> *>(tile + tok * T::RB + (((at >> 4) ^ place<T::RB>(tok)) << 4) + (at & 15)));
+    };
+    // row `tok` of k or q as an operand, columns 32 ks + 8 q .. of all N
+    auto row_of = [&](const char *tile, const IO *src, int tok, int ks, int q) {
+        if constexpr (kCols == 1) return read_row<IO, 1, T::RB>(tile, 0, tok, ks, q);
+        else return load_row8<IO>(src + size_t(min(tok, rows - 1)) * gn + 32 * ks + 8 * q);
+    };
+
+    copy_keys();
+    fetch(first, tid0);
+    copies_done();
+    bool new_head = true;
     for (int turn = first; turn < end; ++turn) {    // head h, rows pb .. pb + 31 of its state
-        const bool new_head = turn == first || turn % pbs == 0;
-        if constexpr (!T::kAhead) fetch(turn);
-        const float fs = in.fs, te = in.te;
-        __syncthreads();        // the tiles' last readers
+        const bool last_of_head = turn == end - 1 || (turn + 1) % pbs == 0;
+        const int ahead = min(turn + 1, end - 1);
         // a thread number the compiler does not know: addresses are formed here again rather
         // than kept over the turns, for which there may not be the registers
         int tid = threadIdx.x;
-        if constexpr (T::kTight) asm volatile("" : "+v"(tid));
-        const int lane = tid & 63, c = lane & 15, q = lane >> 4, tok = tile_row(tw >> 1, tw & 1, c);
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63, c = lane & 15, q = lane >> 4, tok = tile_row(tw >> 1, tw & 1, c);    // this lane's token
+        __syncthreads();        // the tiles' last readers
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) {
+            const int u = i * T::kThreads + tid;
+            if (u < T::kEights) {
+                put8(lds + T::kS, u / (NB / 8), u % (NB / 8), in_s[i]);
+                put8(lds + T::kD, u / (NB / 8), u % (NB / 8), in_d[i]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) accZ += in_s[i][e][j] * in_d[i][e][j];
+            fetch_states(i, ahead, tid);
+            if constexpr (T::kTight) __builtin_amdgcn_sched_barrier(0);
+        }
+        {
+            const int t = (tid >> 6) & 3, row = 16 * (tid >> 8) + c, col = 32 * (t >> 1) + 8 * q + 4 * (t & 1);
+            put4(lds + T::kE, row, col, in_e);
+            put4(lds + T::kV, row, col, in_x);
+            xe += in_e * in_x;
+            constexpr int kPer = T::RP / 16;
+            if (const int y = tid / kPer; y < kC)
+                *reinterpret_cast<u32x4 *>(lds + T::kY + y * T::RP + (((tid % kPer) ^ place<T::RP>(y)) * 16)) = in_y;
+            if (tid < 3 * kC) gates[tid] = in_gate;
+        }
         if (new_head && w == 0) {
-            double s = lane < rows ? gate(in.a) : 0.0;
+            double s = lane < rows ? gate(in_a) : 0.0;
 #pragma unroll
             for (int off = 1; off < 64; off <<= 1) {
                 const double o = __shfl_up(s, off, 64);
@@ -452,43 +478,14 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
             }
             gd[lane] = s;
         }
-#pragma unroll
-        for (int i = 0; i < T::kLoads; ++i) {
-            const int u = i * T::kThreads + tid;
-            if (u >= T::kEights) break;
-            put_state(lds + T::kS, u / (N / 8), u % (N / 8), in.s[i]);
-            put_state(lds + T::kD, u / (N / 8), u % (N / 8), in.d[i]);
-            if constexpr (T::kTight) __builtin_amdgcn_sched_barrier(0);
-        }
-        {
-            const int t = (tid >> 6) & 3, col = 16 * (tid >> 8) + c;
-            const f32x4 u = in.bt * in.e, v = in.bt * in.x;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + j;
-                put(lds + T::kU, T::kTok, T::RP, place<T::RP>(row), row, col, u[j]);
-                put(lds + T::kV, T::kTok, T::RP, place<T::RP>(row), row, col, v[j]);
-                if constexpr (T::kTight) __builtin_amdgcn_sched_barrier(0);
-            }
-            constexpr int kPer = T::RP / 16;
-            if (const int row = tid / kPer; row < kC)
-                *reinterpret_cast<u32x4 *>(lds + T::kY + row * T::RP + (((tid % kPer) ^ place<T::RP>(row)) * 16)) = in.y;
-        }
-        if constexpr (T::kAhead) fetch(min(turn + 1, end - 1));
+        new_head = last_of_head;
+        fetch_rest(ahead, tid);
         __syncthreads();
-        if (new_head) {
-            const double gt = gd[tok];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = 32 * half + 8 * q + 4 * e + i;
-                    D[e][i] = expf(j <= tok ? float(gt - gd[j]) : 0.f);
-                }
-        }
         // the states' parts
+        const float fs = gates[tok], bt = gates[2 * kC + tok], te = gates[kC + tok] * bt, fv = fs * bt;
         const Op<IO, 1> oy = read_row<IO, 1, T::RP>(lds + T::kY, 0, tok, 0, q);
-        const Op<IO, kP> ov = read_row<IO, kP, T::RP>(lds + T::kV, T::kTok, tok, 0, q), ou = read_row<IO, kP, T::RP>(lds + T::kU, T::kTok, tok, 0, q);
+        const Op<IO, kP> ov = read_col<IO, kP, T::RT>(lds + T::kV, T::kTok, 0, 32 * (tw >> 1), tw & 1, c, q);
+        const Op<IO, kP> ou = read_col<IO, kP, T::RT>(lds + T::kE, T::kTok, 0, 32 * (tw >> 1), tw & 1, c, q);
         constexpr int M = NT < 2 || T::kTight ? 1 : 2;
 #pragma unroll
         for (int i0 = 0; i0 < NT; i0 += M) {
@@ -499,68 +496,167 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
                 const int t = column(i0 + i);
                 as[i] = read_col<IO, kP, T::RB>(lds + T::kS, T::kState, 0, 32 * (t >> 1), t & 1, c, q);
                 ad[i] = read_col<IO, kP, T::RB>(lds + T::kD, T::kState, 0, 32 * (t >> 1), t & 1, c, q);
-                zq[i] = zv[i] = zu[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                zq[i] = zv[i] = zu[i] = zero;
             }
             mma(zq, as, oy);
             mma(zv, as, ov);
             mma(zu, ad, ou);
 #pragma unroll
             for (int i = 0; i < M; ++i) {
-                dq[i0 + i] += (scale * fs) * zq[i];
-                dk[i0 + i] += te * zu[i] - fs * zv[i];
+                const int c4 = 8 * (column(i0 + i) >> 1) + 2 * q + (column(i0 + i) & 1);
+                const f32x4 kv = four_of(lds + T::kK, tok, c4), qv = four_of(lds + T::kQ, tok, c4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float a = (scale * fs) * zq[i][j], b = fv * zv[i][j], d = te * zu[i][j];
+                    dq[i0 + i][j] += a;
+                    dk[i0 + i][j] += d - b;
+                    accA += a * qv[j] - b * kv[j];
+                    accB += d * kv[j];
+                }
             }
             if constexpr (T::kTight) __builtin_amdgcn_sched_barrier(0);     // no registers to read ahead
         }
-        // dY U^T and dv U^T (rows j, columns i: this lane's token), where some j <= i
-        if (half <= (tw >> 1)) {
+        // dY E^T and X E^T (rows j, columns i: this lane's token)
+        __builtin_amdgcn_sched_barrier(0);
+        if (below) {
             Op<IO, kP> au[2];
-            f32x4 zw[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, zf[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) au[e] = read_row<IO, kP, T::RP>(lds + T::kU, T::kTok, tile_row(half, e, c), 0, q);
-            mma(zw, au, oy);
-            mma(zf, au, ov);
+            for (int e = 0; e < 2; ++e) au[e] = read_col<IO, kP, T::RT>(lds + T::kE, T::kTok, 0, 32 * half, e, c, q);
+            mma(Wh, au, oy);
+            mma(Fh, au, ov);
+        }
+        if (!last_of_head) continue;
+        __syncthreads();        // the tiles' last readers, T lies over them
+
+        // The head's W and F, and its gates' gradients:  with T_ij = W_ij (q_i . k_j) + F_ij (k_i . k_j),
+        //   A_i = scale e^{g_i} dy_i . S q_i - dv_i . e^{g_i} S k_i,  B_j = u_j . e^{g_C - g_j} dS k_j,  Z = e^{g_C} <S, dS>
+        //   da_t = sum of T_ij over j < t <= i + sum of A_i over i >= t + sum of B_j over j < t + Z
+        // all terms that pass the gate of token t, and no others: each holds e^{a_t}, so that none
+        // of them outgrows the result where that gate closes.
+        {
+            f32x4 kk[2] = {zero, zero}, qk[2] = {zero, zero};
+            if (below && cb == 0) {     // T once, not per part of the columns
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+                for (int ks = 0; ks < N / 32; ++ks) {
+                    Op<IO, 1> a[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) a[e] = row_of(lds + T::kK, k0, tile_row(half, e, c), ks, q);
+                    mma(kk, a, row_of(lds + T::kK, k0, tok, ks, q));
+                    mma(qk, a, row_of(lds + T::kQ, q0, tok, ks, q));
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            const double gt = gd[tok];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                f32x4 wv = zero, fv = zero;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = 32 * half + 8 * q + 4 * e + i;
-                    const float wv = scale * D[e][i] * zw[e][i], fv = -D[e][i] * zf[e][i];
-                    Wm[e][i] += j <= tok && tok < rows ? wv : 0.f;
-                    Fm[e][i] += j < tok && tok < rows ? fv : 0.f;
+                    const float D = expf(j <= tok ? float(gt - gd[j]) : 0.f);
+                    const float bj = gates[2 * kC + j];
+                    if (j <= tok && tok < rows) wv[i] = (scale * D) * (bj * Wh[e][i]);
+                    if (j < tok && tok < rows) fv[i] = (-D * bt) * (bj * Fh[e][i]);
+                    Tm[tok * T::LT + j] = j < tok && tok < rows ? wv[i] * qk[e][i] + fv[i] * kk[e][i] : 0.f;
                 }
+                if (below) {
+                    held[128 * e] += wv;
+                    held[128 * e + 64] += fv;
+                }
+            }
+        }
+        accA = group4_sum(accA);
+        accB = group4_sum(accB);
+        accZ = wave_sum(accZ);
+        if (q == 0) {
+            As[half * kC + tok] = tok < rows ? accA : 0.f;
+            Bs[half * kC + tok] = tok < rows ? accB : 0.f;
+        }
+        if (lane == 0) zs[w] = accZ;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xe[j] = row16_sum(xe[j]);
+        if (c == 0) *reinterpret_cast<f32x4 *>(Xs + (tid >> 8) * kC + 32 * ((tid >> 7) & 1) + 8 * q + 4 * ((tid >> 6) & 1)) = xe;
+        clear_head();
+        __syncthreads();
+        // wave w: the sums down the columns of T, from rows 8 w .. 8 w + 7 on; lane = column j
+        float v[8];
+#pragma unroll
+        for (int i = 7; i >= 0; --i) v[i] = Tm[(8 * w + i) * T::LT + lane] + (i < 7 ? v[i + 1] : 0.f);
+        sums[w * kC + lane] = v[0];
+        __syncthreads();
+        float lower = 0.f;
+#pragma unroll
+        for (int i = 1; i < 8; ++i) lower += w + i < 8 ? sums[((w + i) & 7) * kC + lane] : 0.f;
+        float da = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {       // row t = 8 w + i: its columns j < t
+            const float s = wave_sum(lane < 8 * w + i ? v[i] + lower : 0.f);
+            da = lane == 8 * w + i ? s : da;
+        }
+        float a = As[lane] + As[kC + lane], b = Bs[lane] + Bs[kC + lane];
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const float oa = __shfl_down(a, off, 64), ob = __shfl_up(b, off, 64);
+            if (lane + off < 64) a += oa;
+            if (lane >= off) b += ob;
+        }
+        b = __shfl_up(b, 1, 64);
+        const float z = ((zs[0] + zs[1]) + (zs[2] + zs[3])) + ((zs[4] + zs[5]) + (zs[6] + zs[7]));
+        da += a + (lane ? b : 0.f) + gates[kC - 1] * z;
+        if (lane >> 3 == w && lane < rows) {
+            const int hr = turn / pbs, h = g * r + hr;
+            const size_t all = size_t(gridDim.x / (kCols * splits * nc * G)) * L * H, at = (size_t(bi) * L + t0 + lane) * H + h;
+            const float db = cb == 0 ? Xs[lane] + Xs[kC + lane] : 0.f;
+            if (kCols > 1 || splits > 1) {
+                float *to = gate_parts + 2 * all * ((split - split_of(int64_t(hr) * pbs, turns, splits)) * kCols + cb) + at;
+                to[0] = da;
+                to[all] = db;
+            } else {
+                dag[at] = da;
+                dbg[at] = db;
+            }
         }
     }
     __syncthreads();
-    // k and q into LDS, W [i][j] and G [i][j] = G [j][i] beside them
-    const size_t src = (size_t(bi) * L + t0) * gn + size_t(g) * N;
-    constexpr int kCopiers = kC * T::RB >= 8 * 1024 ? 8 : 4;    // waves: 1 KiB each at least
-    if (w < kCopiers) {
-        copy_rows<T::RB, kC, kCopiers, 0, 1>(kg + src, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kK);
-        copy_rows<T::RB, kC, kCopiers, 0, 1>(qg + src, uint32_t(gn) * kSz, rows - 1, T::RB / 16, lds0 + T::kQ);
-    }
+    const int lane = tid0 & 63, c = lane & 15, q = lane >> 4, tok = tile_row(tw >> 1, tw & 1, c);
+    // W [i][j] and G [i][j] = G [j][i]
+    auto put = [&](char *tile, int row, int col, float v) {
+        char *dst = tile + row * T::RT + (((col * kSz >> 4) ^ place<T::RT>(row)) << 4) + (col * kSz & 15);
+        if constexpr (kSz == 4) {
+            *reinterpret_cast<float *>(dst) = v;
+        } else {
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+            for (int p = 0; p < kP; ++p) {
+                const bf16_bits part = f32_to_bf16(v);
+                *reinterpret_cast<bf16_bits *>(dst + p * T::kMat) = part;
+                v -= bf16_to_f32(part);
+            }
+        }
+    };
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const f32x4 wv = below ? held[128 * e] : zero, fv = below ? held[128 * e + 64] : zero;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int j = 32 * half + 8 * q + 4 * e + i;
-            put(lds + T::kWm, T::kMat, T::RM, place<T::RM>(tok), tok, j, Wm[e][i]);     // 0 above the diagonal
+            put(lds + T::kWm, tok, j, wv[i]);           // 0 above the diagonal
             if (j < tok) {
-                put(lds + T::kGm, T::kMat, T::RM, place<T::RM>(tok), tok, j, Fm[e][i]);
-                put(lds + T::kGm, T::kMat, T::RM, place<T::RM>(j), j, tok, Fm[e][i]);
+                put(lds + T::kGm, tok, j, fv[i]);
+                put(lds + T::kGm, j, tok, fv[i]);
             } else if (j == tok) {
-                put(lds + T::kGm, T::kMat, T::RM, place<T::RM>(j), j, j, 0.f);
+                put(lds + T::kGm, j, j, 0.f);
             }
         }
-    copies_done();
+    }
     __syncthreads();
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
         int l = lane;
         if constexpr (T::kTight) asm volatile("" : "+v"(l));
         const int c = l & 15, q = l >> 4, tok = tile_row(tw >> 1, tw & 1, c);
-        const Op<IO, kP> wr = read_row<IO, kP, T::RM>(lds + T::kWm, T::kMat, tok, ks, q);
-        const Op<IO, kP> gr = read_row<IO, kP, T::RM>(lds + T::kGm, T::kMat, tok, ks, q);
-        const Op<IO, kP> wc = read_col<IO, kP, T::RM>(lds + T::kWm, T::kMat, 32 * ks, 32 * (tw >> 1), tw & 1, c, q);
+        const Op<IO, kP> wr = read_row<IO, kP, T::RT>(lds + T::kWm, T::kMat, tok, ks, q);
+        const Op<IO, kP> gr = read_row<IO, kP, T::RT>(lds + T::kGm, T::kMat, tok, ks, q);
+        const Op<IO, kP> wc = read_col<IO, kP, T::RT>(lds + T::kWm, T::kMat, 32 * ks, 32 * (tw >> 1), tw & 1, c, q);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int t = column(i);
@@ -577,8 +673,8 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
         }
     }
     if (tok < rows) {
-        const size_t dst = (size_t(bi) * L + t0 + tok) * gn + size_t(g) * N + 8 * q;
-        const size_t all = size_t(gridDim.x / (splits * nc * G)) * L * gn;
+        const size_t dst = (size_t(bi) * L + t0 + tok) * gn + size_t(g) * N + cb * NB + 8 * q;
+        const size_t all = size_t(gridDim.x / (kCols * splits * nc * G)) * L * gn;
         float *pq = parts + 2 * split * all + dst, *pk = pq + all;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -594,11 +690,26 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
     }
 }
 
-// The parts of dq and dk added in their order: parts [splits][dq, dk][all] fp32, 8 elements
-// per thread.
+// The parts added in their order: of dq and dk, parts [splits][dq, dk][all] fp32, 8 elements
+// per thread; of da and dbeta, gate_parts [portions of a head][da, dbeta][b, L, H], one per
+// thread of the blocks from `blocks` on (`cols` of them per portion).
 template <typename IO>
 __global__ __launch_bounds__(256) void k_delta_join(const float *__restrict__ parts, IO *__restrict__ dqg, IO *__restrict__ dkg,
-                                                    int splits, size_t all) {
+                                                    const float *__restrict__ gate_parts, float *__restrict__ da,
+                                                    float *__restrict__ dbeta, int splits, size_t all, unsigned blocks, size_t tokens,
+                                                    int H, int r, int pbs, int cols) {
+    if (blockIdx.x >= blocks) {
+        const size_t i = size_t(blockIdx.x - blocks) * 256 + threadIdx.x, n = tokens * H;
+        if (i >= 2 * n) return;
+        const bool second = i >= n;
+        const int hr = int((second ? i - n : i) % H) % r;
+        const int64_t turn = int64_t(hr) * pbs, turns = int64_t(r) * pbs;
+        const int portions = split_of(turn + pbs - 1, turns, splits) - split_of(turn, turns, splits) + 1;
+        float s = 0.f;
+        for (int j = 0; j < portions * cols; ++j) s += gate_parts[2 * n * j + i];
+        (second ? dbeta : da)[second ? i - n : i] = s;
+        return;
+    }
     const size_t at = (size_t(blockIdx.x) * 256 + threadIdx.x) * 8;
     if (at >= 2 * all) return;
     f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
@@ -616,66 +727,22 @@ __global__ __launch_bounds__(256) void k_delta_join(const float *__restrict__ pa
     }
 }
 
-// Kernel 5.  Block = (batch, head, segment), one wave per chunk of it, lane = token.  The
-// sum from a token to the segment's end is taken in 64 bits: it is the sum of up to 128
-// terms that largely cancel.
-template <int SEG>
-__global__ __launch_bounds__(64 * SEG) void k_delta_gates(const float *__restrict__ ydy, const float *__restrict__ vdv,
-                                                               const float *__restrict__ xe, const float *__restrict__ lam,
-                                                               float *__restrict__ da, float *__restrict__ dbeta, int L, int H,
-                                                               int nc, int ptiles, int segs, int parts) {
-    __shared__ double total[SEG];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int seg = blockIdx.x % segs, bh = blockIdx.x / segs, h = bh % H, bi = bh / H;
-    const int ch = seg * SEG + w, t = ch * kC + lane;
-    double d = 0.0;
-    float b = 0.f;
-    if (ch < nc) {
-        const size_t unit = size_t(bh) * nc + ch, at = unit * ptiles * kC + lane;
-        const float *y = ydy + unit * parts * ptiles * kC + lane;
-#pragma unroll 8
-        for (int i = 0; i < parts * ptiles; ++i) d += double(y[i * kC]);
-#pragma unroll 8
-        for (int i = 0; i < ptiles; ++i) {
-            d -= double(vdv[at + i * kC]);
-            b += xe[at + i * kC];
-        }
-    }
-    if (t >= L) d = 0.0;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double o = __shfl_down(d, off, 64);
-        if (lane + off < 64) d += o;
-    }
-    if (lane == 0) total[w] = d;
-    __syncthreads();
-    for (int i = w + 1; i < SEG; ++i) d += total[i];
-    double dot = 0.0;       // <dS, S>, lane i one part of it
-    for (int i = lane; i < ptiles * parts; i += 64) dot += double(lam[((size_t(bh) * ptiles + i / parts) * segs + seg) * parts + i % parts]);
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) dot += __shfl_xor(dot, off, 64);
-    d += dot;
-    if (ch < nc && t < L) {
-        const size_t at = (size_t(bi) * L + t) * H + h;
-        da[at] = float(d);
-        dbeta[at] = b;
-    }
-}
+// Turns of a head in k_delta_grads, and the parts its columns are taken in.
+int grad_turns(int P) { return (P + 31) / 32; }
+int grad_columns(int N, bool bf16) { return N * (bf16 ? 2 : 4) > 256 ? N * (bf16 ? 2 : 4) / 256 : 1; }
 
 template <typename IO, int N>
 hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t stream) {
-    const int nc = (a.L + kC - 1) / kC, segs = (nc + kSegment<IO> - 1) / kSegment<IO>, ptiles = a.P / 16;
+    const int nc = (a.L + kC - 1) / kC, ptiles = a.P / 16;
     char *ws = static_cast<char *>(a.workspace);
     char *images = ws;
     const auto *q = static_cast<const IO *>(a.q), *k = static_cast<const IO *>(a.k), *v = static_cast<const IO *>(a.v);
     const auto *dy = static_cast<const IO *>(a.dy);
     auto *dv = static_cast<IO *>(a.dv);
-    DeltaSaved saved{reinterpret_cast<float *>(ws + pl.off_e), reinterpret_cast<float *>(ws + pl.off_s), reinterpret_cast<float *>(ws + pl.off_anchor),
-                     reinterpret_cast<float *>(ws + pl.off_ydy)};
-    BackSums sums{reinterpret_cast<float *>(ws + pl.off_xe), reinterpret_cast<float *>(ws + pl.off_vdv), reinterpret_cast<float *>(ws + pl.off_lam)};
+    DeltaSaved saved{reinterpret_cast<float *>(ws + pl.off_e), reinterpret_cast<float *>(ws + pl.off_s)};
     auto *dS = reinterpret_cast<float *>(ws + pl.off_ds);
     auto *kept_x = reinterpret_cast<f32x4 *>(ws + pl.off_x);
-    auto *parts = reinterpret_cast<float *>(ws + pl.off_parts);
+    auto *parts = reinterpret_cast<float *>(ws + pl.off_parts), *gate_parts = reinterpret_cast<float *>(ws + pl.off_gate_parts);
 
     hipError_t e = launch_delta_prep<IO, N>(q, k, a.a, a.beta, images, a.b, a.L, a.H, a.G, a.scale, stream);
     if (e != hipSuccess) return e;
@@ -687,15 +754,13 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
     auto back = [&](auto w_, auto x_, auto one_, auto map_, float *to) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
         constexpr bool MAP = decltype(map_)::value, ONE = decltype(one_)::value;
-        constexpr int lds = ChainLds<IO, N, W, X, false, ONE>::kBytes;
+        constexpr int lds = ChainLds<IO, N, W, X, true, false, ONE>::kBytes;
         const int rows = 16 * W / X, pblocks = (a.P + rows - 1) / rows;
         auto kern = k_delta_chain_back<IO, N, W, X, MAP, ONE>;
         e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(kern, dim3(unsigned(int64_t(a.b) * a.H * (cut.segments - (MAP ? 1 : 0)) * pblocks)), dim3(64 * W), lds, stream, q, k,
-                           v, dy, images, a.d_final, dinit, reinterpret_cast<const f32x4 *>(saved.E),
-                           reinterpret_cast<const f32x4 *>(saved.anchor), dv, dS, kept_x, to, sums, a.L, a.H, a.P, a.G, nc, cut.per, cut.segments,
-                           pblocks, a.scale);
+                           dy, images, a.d_final, dinit, dv, dS, kept_x, to, a.L, a.H, a.P, a.G, nc, cut.per, cut.segments, pblocks, a.scale);
         return hipGetLastError();
     };
     const int64_t tiles = int64_t(a.b) * a.H * ptiles;
@@ -705,12 +770,10 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
         hipLaunchKernelGGL((k_delta_carry<N, true>), dim3(unsigned(tiles)), dim3(4 * N), 0, stream, map, dmap, nullptr, dinit, a.P, cut.segments);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    int share = 1;      // waves per tile, each with its own part of the sums
     auto chains = [&](auto w_, auto x_, auto one_) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
-        share = X;
-        e = launch_chain<IO, N, W, X, Chain::save, decltype(one_)::value>(q, k, v, images, cut.segments > 1 ? init : a.init_state, nullptr, nullptr, dy, saved,
-                                                           a.b, a.L, a.H, a.P, a.G, cut.per, cut.segments, a.scale, stream);
+        e = launch_chain<IO, N, W, X, Chain::save, decltype(one_)::value>(q, k, v, images, cut.segments > 1 ? init : a.init_state, nullptr, nullptr,
+                                                           saved, a.b, a.L, a.H, a.P, a.G, cut.per, cut.segments, a.scale, stream);
         return e != hipSuccess ? e : back(w_, x_, one_, std::false_type{}, a.d_init);
     };
     if ((e = with_chain_shape<IO, N, true>(tiles * cut.segments, chains)) != hipSuccess) return e;
@@ -718,18 +781,15 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
     constexpr int lds = GradTile<IO, N>::kLds;
     e = hipFuncSetAttribute(reinterpret_cast<const void *>(grads), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(grads, dim3(unsigned(int64_t(a.b) * a.G * nc * pl.splits)), dim3(GradTile<IO, N>::kThreads), lds, stream, q, k, a.a, dy, images,
-                       reinterpret_cast<const f32x4 *>(saved.E), kept_x, saved.S, dS, static_cast<IO *>(a.dq),
-                       static_cast<IO *>(a.dk), parts, pl.splits, a.L, a.H, a.P, a.G, nc, a.scale);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (pl.splits > 1) {
-        const size_t all = size_t(a.b) * a.L * a.G * N;
-        hipLaunchKernelGGL(k_delta_join<IO>, dim3(unsigned((2 * all + 2047) / 2048)), dim3(256), 0, stream, parts,
-                           static_cast<IO *>(a.dq), static_cast<IO *>(a.dk), pl.splits, all);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL((k_delta_gates<kSegment<IO>>), dim3(unsigned(int64_t(a.b) * a.H * segs)), dim3(64 * kSegment<IO>), 0, stream, saved.ydy, sums.vdv, sums.xe,
-                       sums.lam, a.da, a.dbeta, a.L, a.H, nc, ptiles, segs, share);
+    constexpr int kCols = GradTile<IO, N>::kCols;
+    hipLaunchKernelGGL(grads, dim3(unsigned(int64_t(a.b) * a.G * nc * pl.splits * kCols)), dim3(GradTile<IO, N>::kThreads), lds, stream, q, k, a.a, dy, images,
+                       reinterpret_cast<const f32x4 *>(saved.E), kept_x, saved.S, dS, static_cast<IO *>(a.dq), static_cast<IO *>(a.dk), a.da,
+                       a.dbeta, parts, gate_parts, pl.splits, a.L, a.H, a.P, a.G, nc, a.scale);
+    if ((e = hipGetLastError()) != hipSuccess || pl.splits * kCols == 1) return e;
+    const size_t tokens = size_t(a.b) * a.L, all = tokens * a.G * N;
+    const unsigned blocks = pl.splits > 1 ? unsigned((2 * all + 2047) / 2048) : 0;
+    hipLaunchKernelGGL(k_delta_join<IO>, dim3(blocks + unsigned((2 * tokens * a.H + 255) / 256)), dim3(256), 0, stream, parts, static_cast<IO *>(a.dq),
+                       static_cast<IO *>(a.dk), gate_parts, a.da, a.dbeta, pl.splits, all, blocks, tokens, a.H, a.H / a.G, grad_turns(a.P), kCols);
     return hipGetLastError();
 }
 
@@ -742,8 +802,8 @@ int grad_splits(size_t cells, size_t turns) { return int(std::max<size_t>(1, std
 DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16) {
     DeltaBwdPlan pl;
     if (b <= 0 || L <= 0 || !delta_chunk_supported(b, L, H, P, N, G, bf16)) return pl;
-    const size_t nc = (size_t(L) + kC - 1) / kC, segs = bf16 ? (nc + kSegment<bf16_bits> - 1) / kSegment<bf16_bits> : (nc + kSegment<float> - 1) / kSegment<float>, bh = size_t(b) * H, units = bh * nc;
-    const size_t state = size_t(P) * N, ptiles = size_t(P) / 16;
+    const size_t nc = (size_t(L) + kC - 1) / kC, bh = size_t(b) * H, units = bh * nc;
+    const size_t state = size_t(P) * N;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t off = at;
@@ -755,18 +815,15 @@ DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16)
     pl.off_x = take(units * kC * P * 4);
     pl.off_s = take(units * state * 4);
     pl.off_ds = take(units * state * 4);
-    pl.off_anchor = take(bh * segs * state * 4);
-    pl.off_ydy = take(units * kMaxShare * ptiles * kC * 4);
-    pl.off_xe = take(units * ptiles * kC * 4);
-    pl.off_vdv = take(units * ptiles * kC * 4);
-    pl.off_lam = take(bh * ptiles * segs * kMaxShare * 4);
-    pl.splits = grad_splits(size_t(b) * G * nc, size_t(H / G) * ((P + 31) / 32));
+    const int cols = grad_columns(N, bf16);
+    pl.splits = grad_splits(size_t(b) * G * nc * cols, size_t(H / G) * grad_turns(P));
     pl.cut = cut_sequence(int64_t(bh), int(nc), P, N, bf16, true);
     pl.off_map = take(map_bytes(bh, P, N, pl.cut));
     pl.off_init = take(entering_bytes(bh, P, N, pl.cut));
     pl.off_dmap = take(entering_bytes(bh, P, N, pl.cut));
     pl.off_dinit = take(entering_bytes(bh, P, N, pl.cut));
     pl.off_parts = take(pl.splits > 1 ? size_t(pl.splits) * 2 * b * L * G * N * 4 : 0);
+    pl.off_gate_parts = take(pl.splits * cols > 1 ? size_t(pl.splits > 1 ? grad_turns(P) : 1) * cols * 2 * b * L * H * 4 : 0);
     pl.total = at;
     pl.supported = true;
     return pl;

@@ -7,23 +7,11 @@
 
 namespace ssd {
 
-// What the forward chain leaves for the backward pass, per (batch, head):
+// What the forward chain leaves for the backward pass, fp32, per (batch, head):
 //   E       [nc][P / 16][4][64] f32x4: a wave's accumulators of the brackets, as held
-//   S       [nc][P][N] fp32: the state that enters each chunk
-//   anchor  [P / 16][segments][N / 16][64] f32x4: the state after each segment of chunks,
-//           as held
-//   ydy     [nc][X][P / 16][64] fp32: parts of y . dy of each token over 16 rows, to be added
-// Chunks per segment.  The gate gradients' error grows with the root of it: da of the
-// 4 x 2048-token layer 5.3e-7 of its norm with 1, 1.05e-6 with 4, which saves 47 of 725 us.
-// In fp32 the anchors cost nothing measurable.
-template <typename IO>
-constexpr int kSegment = std::is_same_v<IO, float> ? 1 : 2;
-
+//   S       [nc][P][N]: the state that enters each chunk
 struct DeltaSaved {
-    float *E;
-    float *S;
-    float *anchor;
-    float *ydy;
+    float *E, *S;
 };
 
 // A block's W waves are W / X tiles of 16 state rows, each shared by X waves that hold
@@ -33,16 +21,18 @@ struct DeltaSaved {
 //
 // LDS: k, M, the scores and gates of two chunks, the next one's copied in meanwhile (one
 // chunk where two do not fit, or, ONE, where two blocks a CU gain more than copies ahead).
-// With X = 1 q beside them; with more, q of one chunk, which is done with halfway through it,
-// and the exchanged sums (YX: those of Q S^T too).
-template <typename IO, int N, int W, int X, bool YX, bool ONE>
+// Chains that read them (Q) have the scores, and q: with X = 1 beside them; with more, that of
+// one chunk, which is done with halfway through it.  Then the exchanged sums (YX: those of
+// Q S^T too).
+template <typename IO, int N, int W, int X, bool Q, bool YX, bool ONE>
 struct ChainLds {
     using Img = ChunkImage<IO>;
     static constexpr int kSz = int(sizeof(IO));
     static constexpr int RB = N * kSz;                      // bytes per row of k or q
     static constexpr int kRows = kC * RB;                   // bytes of such a tile
-    static constexpr bool kQMain = X == 1;                  // q beside k, in both buffers
-    static constexpr int kImg = kQMain ? 2 * kRows : kRows, kMain = kImg + Img::kBytes, kQOwn = kQMain ? 0 : kRows;
+    static constexpr bool kQMain = Q && X == 1;             // q beside k, in both buffers
+    static constexpr int kImg = kQMain ? 2 * kRows : kRows, kImgBytes = Q ? Img::kBytes : Img::kQ;
+    static constexpr int kMain = kImg + kImgBytes, kQOwn = Q && X > 1 ? kRows : 0;
     static constexpr int kXe = X > 1 ? W * 4096 : 0, kXy = X > 1 && YX ? W * (4096 - 4096 / X) : 0;
     static constexpr int kBufs = !ONE && 2 * kMain + kQOwn + kXe + kXy <= 160 * 1024 ? 2 : 1;
     static constexpr int kQt = kBufs * kMain, kE = kQt + kQOwn, kY = kE + kXe, kBytes = kY + kXy;
@@ -76,19 +66,15 @@ __device__ __forceinline__ void copy_image(const char *img, uint32_t dst) {
     }
 }
 
-// One element / 4 consecutive ones of a range-checked view; past its end: 0.
+// One element of a range-checked view; past its end: 0.
 template <typename IO>
 __device__ __forceinline__ IO load_checked(__amdgpu_buffer_rsrc_t v, uint32_t off) {
     if constexpr (std::is_same_v<IO, float>) return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(v, int(off), 0, 0));
     else return __builtin_amdgcn_raw_buffer_load_b16(v, int(off), 0, 0);
 }
+// 4 elements of the I/O type.
 template <typename IO>
 using Raw4 = std::conditional_t<std::is_same_v<IO, float>, f32x4, u32x2>;
-template <typename IO>
-__device__ __forceinline__ Raw4<IO> load4_checked(__amdgpu_buffer_rsrc_t v, uint32_t off) {
-    if constexpr (std::is_same_v<IO, float>) return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(v, int(off), 0, 0));
-    else return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(v, int(off), 0, 0));
-}
 template <typename IO>
 __device__ __forceinline__ f32x4 widen(Raw4<IO> v) {
     if constexpr (std::is_same_v<IO, float>) return v;
@@ -129,7 +115,7 @@ __device__ __forceinline__ void sum_of_parts(const char *first, int lane, f32x4 
 
 // What a chain is run for.
 //   run   y and the final state
-//   save  what the backward pass needs (dyg is read)
+//   save  what the backward pass needs
 //   map   what a segment of the sequence does to the state that enters it, S -> S A + B: the
 //         states after it of P rows that enter as 0 (B) and, with v = 0, of the N rows of the
 //         identity (A).  The first segment's P rows enter as they are, without the others.
@@ -141,11 +127,10 @@ template <typename IO, int N, int W, int X, Chain MODE, bool ONE>
 __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ qg, const IO *__restrict__ kg,
                                                         const IO *__restrict__ vg, const char *__restrict__ images,
                                                         const float *__restrict__ init, IO *__restrict__ yg,
-                                                        float *__restrict__ fin, const IO *__restrict__ dyg,
-                                                        DeltaSaved saved, int L, int H, int P, int G, int nc, int per, int segs,
+                                                        float *__restrict__ fin, DeltaSaved saved, int L, int H, int P, int G, int nc, int per, int segs,
                                                         int pblocks, float scale) {
-    constexpr bool SAVE = MODE == Chain::save, MAP = MODE == Chain::map;
-    using T = ChainLds<IO, N, W, X, MODE == Chain::run, ONE>;
+    constexpr bool RUN = MODE == Chain::run, SAVE = MODE == Chain::save, MAP = MODE == Chain::map;
+    using T = ChainLds<IO, N, W, X, RUN, RUN, ONE>;
     using Img = typename T::Img;
     extern __shared__ __align__(16) char lds[];
     constexpr int kSz = int(sizeof(IO)), KS = N / 32 / X, NT = 2 * KS;  // this wave's column blocks and tiles
@@ -165,15 +150,16 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
     char *xe = lds + T::kE + w * 4096;
 
     // the copies of chunk ch: k and the image into the buffer at `buf` in 4 parts; q
+    // (with it or alone)
     auto fetch = [&](int ch, uint32_t buf, auto part) {
         constexpr int kPart = decltype(part)::value;
         const int t0 = ch * kC, last = min(kC, L - t0) - 1;
         copy_rows<T::RB, kC, W, kPart, 4>(k0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf);
-        copy_image<Img::kBytes, W, kPart, 4>(img + size_t(ch) * Img::kBytes, buf + T::kImg);
-        if constexpr (T::kQMain && !MAP) copy_rows<T::RB, kC, W, kPart, 4>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf + T::kRows);
+        copy_image<T::kImgBytes, W, kPart, 4>(img + size_t(ch) * Img::kBytes, buf + T::kImg);
+        if constexpr (T::kQMain) copy_rows<T::RB, kC, W, kPart, 4>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, buf + T::kRows);
     };
     auto fetch_q = [&](int ch) {
-        if constexpr (T::kQMain || MAP) return;
+        if constexpr (T::kQMain || !RUN) return;
         const int t0 = ch * kC, last = min(kC, L - t0) - 1;
         copy_rows<T::RB, kC, W, 0, 1>(q0 + size_t(t0) * gn, uint32_t(gn) * kSz, last, T::RB / 16, lds0 + T::kQt);
     };
@@ -239,13 +225,6 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
         };
         Raw4<IO> yo[4];
         f32x4 E[4], Y[4];
-        if constexpr (SAVE)
-            if (live) {
-                const __amdgpu_buffer_rsrc_t view = chunk_view(dyg + vy0 + size_t(t0) * hp, rows, tok, P);
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    yo[t] = load4_checked<IO>(view, uint32_t(tile_row(t >> 1, t & 1, c)) * tok + uint32_t(p0 + 4 * q) * kSz);
-            }
         fetch_v(next);
         ahead(std::integral_constant<int, 0>{});
         if (live) {
@@ -269,7 +248,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                 mma(E, a, so[ks]);
             }
 #pragma unroll
-            for (int ks = 0; ks < (MAP ? 0 : KS); ++ks) {
+            for (int ks = 0; ks < (RUN ? KS : 0); ++ks) {
                 Op<IO, 1> a[4];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) a[t] = read_row<IO, 1, T::RB>(tq, 0, tile_row(t >> 1, t & 1, c), n0 + ks, q);
@@ -280,7 +259,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
             if constexpr (X > 1) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) reinterpret_cast<f32x4 *>(xe)[64 * t + lane] = E[t];
-                if constexpr (MODE == Chain::run) {     // token tiles t of Y go to wave t / (4 / X)
+                if constexpr (RUN) {     // token tiles t of Y go to wave t / (4 / X)
                     f32x4 *xy = reinterpret_cast<f32x4 *>(lds + T::kY + w * (T::kXy / W));
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
@@ -346,9 +325,9 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
             ahead(std::integral_constant<int, 3>{});
             // Y = scale e^g Q S^T + scores U; wave x finishes the token tiles t of t / (4 / X) = x
 #pragma unroll
-            for (int t = 0; t < (MAP ? 0 : 4); ++t) {
+            for (int t = 0; t < (RUN ? 4 : 0); ++t) {
                 const bool mine = t / (4 / X) == x;     // the same for a whole wave
-                if constexpr (X > 1 && !SAVE) {
+                if constexpr (X > 1) {
                     if (!mine) continue;
 #pragma unroll
                     for (int o = 1; o < X; ++o) {
@@ -356,23 +335,13 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                         Y[t] += reinterpret_cast<const f32x4 *>(lds + T::kY + (w - x + from) * (T::kXy / W))[64 * (x < from ? t : t - 4 / X) + lane];
                     }
                 }
-                Y[t] *= scale * gates[tile_row(t >> 1, t & 1, c)];
-                if (mine) {
-                    f32x4 z[1] = {Y[t]};
+                f32x4 z[1] = {(scale * gates[tile_row(t >> 1, t & 1, c)]) * Y[t]};
 #pragma unroll
-                    for (int ks = 0; ks <= (t >> 1); ++ks) {
-                        const Op<IO, kPlanes> a[1] = {tri_row<IO, kPlanes>(ts, t >> 1, t & 1, ks, c, q)};
-                        mma(z, uy[ks], a);
-                    }
-                    Y[t] = z[0];
+                for (int ks = 0; ks <= (t >> 1); ++ks) {
+                    const Op<IO, kPlanes> a[1] = {tri_row<IO, kPlanes>(ts, t >> 1, t & 1, ks, c, q)};
+                    mma(z, uy[ks], a);
                 }
-                if constexpr (SAVE) {
-                    const f32x4 d = widen<IO>(yo[t]);
-                    const float dot = group4_sum(Y[t][0] * d[0] + Y[t][1] * d[1] + Y[t][2] * d[2] + Y[t][3] * d[3]);
-                    if (q == 0) saved.ydy[(((size_t(bh) * nc + ch) * X + x) * ptiles + p0 / 16) * kC + tile_row(t >> 1, t & 1, c)] = dot;
-                } else {
-                    yo[t] = narrow<IO>(Y[t]);
-                }
+                yo[t] = narrow<IO>(z[0]);
             }
         } else {
             ahead(std::integral_constant<int, 2>{});
@@ -395,14 +364,7 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     if (t / (4 / X) == x) dst[64 * t] = E[t];
-                if (ch % kSegment<IO> == kSegment<IO> - 1 || ch == nc - 1) {
-                    const int segs = (nc + kSegment<IO> - 1) / kSegment<IO>;
-                    f32x4 *at = reinterpret_cast<f32x4 *>(saved.anchor) +
-                                (((size_t(bh) * ptiles + p0 / 16) * segs + ch / kSegment<IO>) * (N / 16) + x * NT) * 64 + lane;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) at[64 * t] = S[t];
-                }
-            } else if constexpr (!MAP) {
+            } else if constexpr (RUN) {
                 const __amdgpu_buffer_rsrc_t view = chunk_view(yg + vy0 + size_t(t0) * hp, rows, tok, P);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
@@ -419,7 +381,6 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
         for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(fin + state_at(MAP ? unit : bh, MAP ? P + N : P, t)) = S[t];
 }
 
-constexpr int kMaxShare = 4;    // waves per tile, at the most
 constexpr int kSimds = 1024;
 
 // Calls f(W, X) with the waves per block and per tile for `tiles` chains of 16 state rows.
@@ -451,7 +412,7 @@ hipError_t with_chain_shape(int64_t tiles, F &&f) {
     [[maybe_unused]] constexpr integral_constant<int, 8> eight{};
     constexpr int kRow = N * int(sizeof(IO));
     [[maybe_unused]] auto alone = [&]() {       // a wave per tile
-        constexpr bool kGains = 4 * ChainLds<IO, N, 4, 1, false, false>::kMain > 160 * 1024 && (!BACK || kRow <= 128);
+        constexpr bool kGains = 4 * ChainLds<IO, N, 4, 1, true, false, false>::kMain > 160 * 1024 && (!BACK || kRow <= 128);
         if constexpr (kGains)
             if (tiles > kSimds) return f(four, one, std::true_type{});
         return f(four, one, std::false_type{});
@@ -468,14 +429,15 @@ hipError_t with_chain_shape(int64_t tiles, F &&f) {
 }
 
 template <typename IO, int N, int W, int X, Chain MODE, bool ONE>
-hipError_t launch_chain(const IO *q, const IO *k, const IO *v, const char *images, const float *init, IO *y, float *fin, const IO *dy,
+hipError_t launch_chain(const IO *q, const IO *k, const IO *v, const char *images, const float *init, IO *y, float *fin,
                         const DeltaSaved &saved, int b, int L, int H, int P, int G, int per, int segs, float scale, hipStream_t stream) {
-    constexpr int lds = ChainLds<IO, N, W, X, MODE == Chain::run, ONE>::kBytes;
+    constexpr bool RUN = MODE == Chain::run;
+    constexpr int lds = ChainLds<IO, N, W, X, RUN, RUN, ONE>::kBytes;
     const int rows = 16 * W / X, pblocks = ((MODE == Chain::map ? P + N : P) + rows - 1) / rows, nc = (L + kC - 1) / kC;
     auto kern = k_delta_chain<IO, N, W, X, MODE, ONE>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3(unsigned(int64_t(b) * H * segs * pblocks)), dim3(64 * W), lds, stream, q, k, v, images, init, y, fin, dy,
+    hipLaunchKernelGGL(kern, dim3(unsigned(int64_t(b) * H * segs * pblocks)), dim3(64 * W), lds, stream, q, k, v, images, init, y, fin,
                        saved, L, H, P, G, nc, per, segs, pblocks, scale);
     return hipGetLastError();
 }
@@ -569,7 +531,7 @@ hipError_t enter_segments(const IO *q, const IO *k, const IO *v, const char *ima
     const int64_t bh = int64_t(b) * H;
     auto go = [&](auto w_, auto x_, auto one_) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
-        return launch_chain<IO, N, W, X, Chain::map, decltype(one_)::value>(q, k, v, images, init_state, static_cast<IO *>(nullptr), map, nullptr, DeltaSaved{}, b,
+        return launch_chain<IO, N, W, X, Chain::map, decltype(one_)::value>(q, k, v, images, init_state, static_cast<IO *>(nullptr), map, DeltaSaved{}, b,
                                                          L, H, P, G, cut.per, cut.segments - 1, scale, stream);
     };
     const hipError_t e = with_chain_shape<IO, N, BACK>(bh * (cut.segments - 1) * ((P + N) / 16), go);

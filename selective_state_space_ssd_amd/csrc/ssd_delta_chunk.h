@@ -233,16 +233,16 @@ __device__ __forceinline__ uint32_t lds_address(const char *p) {
 constexpr int kPlanes = 3;
 
 // One chunk's image in the workspace and in LDS:
-//   M and the scores in kPlanes planes (fp32 I/O: one fp32 plane each), both lower
-//   triangular: a plane holds rows 0 .. 31 of columns 0 .. 31, then rows 32 .. 63 whole;
-//   then [3][64] fp32: e^g, e^{g_C - g}, beta.
+//   M in kPlanes planes (fp32 I/O: one fp32 plane), lower triangular: a plane holds rows
+//   0 .. 31 of columns 0 .. 31, then rows 32 .. 63 whole; then [3][64] fp32: e^g,
+//   e^{g_C - g}, beta; then the scores, like M.
 template <typename IO>
 struct ChunkImage {
     static constexpr int kSz = int(sizeof(IO));
     static constexpr int kTop = 32 * 32 * kSz, kPlane = kTop + 32 * 64 * kSz;
     static constexpr int kOf = kSz == 4 ? 1 : kPlanes;      // planes a matrix has
-    static constexpr int kM = 0, kQ = kOf * kPlane, kGates = 2 * kOf * kPlane;
-    static constexpr int kBytes = kGates + 1024;            // the gates rounded up to 1 KiB
+    static constexpr int kM = 0, kGates = kOf * kPlane, kQ = kGates + 1024;     // the gates rounded up to 1 KiB
+    static constexpr int kBytes = kQ + kOf * kPlane;
 };
 
 // Operands from a lower triangular matrix of an image, blocks of 32: rows tile_row(s, e, c),

@@ -22,7 +22,7 @@ hipError_t launch_n(const DeltaChunkArgs &a, const DeltaChunkPlan &pl, hipStream
     auto go = [&](auto w_, auto x_, auto one_) {
         constexpr int W = decltype(w_)::value, X = decltype(x_)::value;
         return launch_chain<IO, N, W, X, Chain::run, decltype(one_)::value>(q, k, v, images, pl.cut.segments > 1 ? init : a.init_state, static_cast<IO *>(a.y),
-                                                             a.final_state, nullptr, DeltaSaved{}, a.b, a.L, a.H, a.P, a.G, pl.cut.per,
+                                                             a.final_state, DeltaSaved{}, a.b, a.L, a.H, a.P, a.G, pl.cut.per,
                                                              pl.cut.segments, a.scale, stream);
     };
     return with_chain_shape<IO, N, false>(int64_t(a.b) * a.H * pl.cut.segments * (a.P / 16), go);
