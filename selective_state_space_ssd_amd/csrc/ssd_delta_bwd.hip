@@ -23,9 +23,14 @@
 // 2 and 3 are chains over the chunks whose waves keep 16 rows of the state each, as in the
 // forward pass: 32-bit values throughout.
 //
-// 4 x 2048 tokens, 32 heads of 128 x 128, bf16, us: prep 45, chain 151, chain back 219, grads
-// 403.  The chains are bound by a wave's steps (ssd_delta_chain.h) and write 805 MB (both
-// states, E and X, in 32 bits); grads reads 870 MB.
+// 4 x 2048 tokens, 32 heads of 128 x 128, bf16, us: prep 46, chain 150, chain back 218, grads
+// 300.  The chains are bound by a wave's steps (ssd_delta_chain.h) and write 805 MB (both
+// states, E and X, in 32 bits).  grads reads 870 MB at 2.9 TB/s, for which it is not waiting
+// (every state from the caches: 265): a wave issues vector instructions 22 % of the time (a
+// third of them splits values into planes), its SIMD's matrix unit is busy 23 %, and two
+// waves a SIMD, all that the registers allow, leave gaps at LDS reads, barriers and the ends
+// of heads (a head's gates take 30 us of the 300, a block's beginning and end 35).  With the
+// states' planes in LDS, shared by all waves, it is the same time.
 #include <algorithm>
 
 #include "ssd_delta.h"
@@ -274,33 +279,30 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain_back(const IO *__restric
 }
 
 // Kernel 4.  Block = (batch, chunk, group, one of `splits` parts of its heads' state rows, NB
-// of the N columns: more have no room in registers).  Wave w holds dq^T and dk^T of 16
-// tokens (tile columns; rows n in registers, 4 consecutive ones a tile), of one half of the
-// columns: waves w and w + 4 share their tokens.  Per turn a
-// head's 32 rows p: dY, X, E and both states go through LDS, 32-bit ones split into kPlanes
-// planes on the way there; the next turn's values are asked for as soon as this one's have
-// left their registers.
+// of the N columns: more have no room in registers).  A turn takes 32 rows p of a head's
+// state.  The states are operands as loaded: wave w holds 16 of the columns, of 16 NTT tokens
+// dq^T and dk^T (rows n in registers, 4 consecutive ones; tile columns the tokens), and
+// splits its part of S and dS into planes in registers, once for all its tokens.  dY, E and X
+// go through LDS, the next turn's while this one is computed: one barrier a turn.
 template <typename IO, int N>
 struct GradTile {
     static constexpr int kSz = int(sizeof(IO)), kP = kSz == 4 ? 1 : kPlanes;
-    static constexpr int kRows = 32;                        // state rows a turn
+    static constexpr int kThreads = 512, kRows = 32;        // state rows a turn
     static constexpr int NB = N * kSz > 256 ? 256 / kSz : N, kCols = N / NB;
+    static constexpr int CT = NB / 16, TH = 8 / CT, NTT = 4 / TH;           // column tiles, waves that share one, token tiles of each
     static constexpr int RT = kC * kSz, RP = kRows * kSz, RB = NB * kSz;    // bytes per row of tokens / of p's / of columns
-    static constexpr int kTok = kRows * RT, kState = kRows * RB;            // bytes of a tile of tokens / of the state
-    // S, dS [32][NB]; E, X [32][64] (kP planes each); dY [64][32]
-    static constexpr int kS = 0, kD = kP * kState, kE = 2 * kP * kState, kV = kE + kP * kTok, kY = kV + kP * kTok, kHead = kY + kTok;
-    // after the heads, over them: W and G [64][64] (kP planes each); beside them k, q [64][NB]
-    static constexpr int kMat = kC * RT, kWm = 0, kGm = kP * kMat, kTail = 2 * kP * kMat;
-    static constexpr int kK = kHead > kTail ? kHead : kTail, kQ = kK + kC * RB, kEnd = kQ + kC * RB;
+    static constexpr int kTok = kRows * RT;                 // bytes of a tile of tokens
+    // of a turn: E, X [32][64] (kP planes each); dY [64][32]; e^g, e^{g_C - g} and beta.  Two of them
+    static constexpr int kE = 0, kV = kP * kTok, kY = 2 * kP * kTok, kGates = kY + kTok, kTurn = kGates + 1024;
+    // after the heads, over them: W and F [64][64] (kP planes each); beside them k, q [64][NB]
+    static constexpr int kMat = kC * RT, kWm = 0, kFm = kP * kMat, kTail = 2 * kP * kMat;
+    static constexpr int kK = 2 * kTurn > kTail ? 2 * kTurn : kTail, kQ = kK + kC * RB, kEnd = kQ + kC * RB;
     // W and F, summed over the heads so far, as the 6 waves hold them that have any; the gates'
-    // part: sums down T's columns [8][64]; A, B [2][64], X . E [2][64], e^g, e^{g_C - g} and beta.
-    // T [64][65] lies over the tiles of the head's last turn.
-    static constexpr int kW = kEnd, kSums = kW + 6 * 4096, kA = kSums + 8 * kC * 4, kB = kA + 2 * kC * 4, kX = kB + 2 * kC * 4, kGates = kX + 2 * kC * 4;
-    static constexpr int kLds = kGates + 3 * kC * 4, LT = kC + 1;
-    static_assert(kC * LT * 4 <= kHead);
-    static constexpr int kThreads = 512, kEights = kRows * NB / 8, kLoads = (kEights + kThreads - 1) / kThreads;     // 8 values a thread and load
-    static constexpr bool kTight = RB >= 256;       // as many accumulators as leave few registers
-    static_assert(kLds <= 159 * 1024);
+    // part: sums down T's columns [8][64]; A, B [CT][64], X . E [2][64].  T [64][65] lies over the
+    // head's last turn.
+    static constexpr int kW = kEnd, kSums = kW + 6 * 4096, kA = kSums + 8 * kC * 4, kB = kA + CT * kC * 4, kX = kB + CT * kC * 4;
+    static constexpr int kLds = kX + 2 * kC * 4, LT = kC + 1;
+    static_assert(kC * LT * 4 <= kGates && kLds <= 159 * 1024);
 };
 
 // Portions of a head's state rows that different blocks take, where a group's turns are split:
@@ -314,40 +316,43 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
                                                      const f32x4 *__restrict__ Xg, const float *__restrict__ Sg,
                                                      const float *__restrict__ dSg, IO *__restrict__ dqg, IO *__restrict__ dkg,
                                                      float *__restrict__ dag, float *__restrict__ dbg, float *__restrict__ parts,
-                                                     float *__restrict__ gate_parts, int splits, int L, int H, int P, int G,
-                                                     int nc, float scale) {
+                                                     float *__restrict__ gate_parts, int splits, int b, int L, int H, int P,
+                                                     int G, int nc, float scale) {
     using T = GradTile<IO, N>;
     using Img = ChunkImage<IO>;
-    constexpr int kSz = T::kSz, kP = T::kP, NB = T::NB, kCols = T::kCols, NT = NB / 32;     // column tiles of a wave
+    constexpr int kSz = T::kSz, kP = T::kP, NB = T::NB, kCols = T::kCols, NTT = T::NTT;
     extern __shared__ __align__(16) char lds[];
-    __shared__ double gd[kC];
+    __shared__ double gd[2][kC];        // this head's gate sums, in units of ln 2, and the next one's
     __shared__ float zs[8];
     const uint32_t lds0 = lds_address(lds);
-    const int tid0 = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid0 >> 6);
-    const int cb = blockIdx.x % kCols, split = blockIdx.x / kCols % splits, cell = blockIdx.x / kCols / splits, ch = cell % nc, bg = cell / nc, g = bg % G, bi = bg / G, r = H / G;
+    int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), cb = blockIdx.x % kCols, split = blockIdx.x / kCols % splits, cell = blockIdx.x / kCols / splits, ch = cell % nc, bg = cell / nc, g = bg % G, bi = bg / G, r = H / G;
     const int t0 = ch * kC, rows = min(kC, L - t0), ptiles = P / 16;
     const size_t hp = size_t(H) * P, gn = size_t(G) * N;
     const int tw = w & 3, half = w >> 2;
     const bool below = half <= (tw >> 1);       // some of this wave's j's are not after its tokens
-    auto column = [&](int i) { return half * NT + i; };     // tile i of this wave, of the NB / 16
+    // this wave's columns 32 (ct >> 1) + 8 (m >> 2) + 4 (ct & 1) + (m & 3), m = 0 .. 15, and token tiles th NTT ..
+    const int ct = w % T::CT, th = w / T::CT, nq = 32 * (ct >> 1) + 4 * (ct & 1);
+    auto tile_of = [&](int i) { return th * NTT + i; };
     const IO *k0 = kg + (size_t(bi) * L + t0) * gn + size_t(g) * N, *q0 = qg + (size_t(bi) * L + t0) * gn + size_t(g) * N;
-    float *Tm = reinterpret_cast<float *>(lds), *sums = reinterpret_cast<float *>(lds + T::kSums);
+    float *sums = reinterpret_cast<float *>(lds + T::kSums);
     float *As = reinterpret_cast<float *>(lds + T::kA), *Bs = reinterpret_cast<float *>(lds + T::kB), *Xs = reinterpret_cast<float *>(lds + T::kX);
-    float *gates = reinterpret_cast<float *>(lds + T::kGates);
-    f32x4 *held = reinterpret_cast<f32x4 *>(lds + T::kW) + (half ? tw + 2 : tw) * 256 + (tid0 & 63);     // W, F [2][64] each of a wave
+    f32x4 *held = reinterpret_cast<f32x4 *>(lds + T::kW) + (half ? tw + 2 : tw) * 256 + lane;     // W, F [2][64] each of a wave
 
-    f32x4 dq[NT], dk[NT];                   // sums over the heads
+    f32x4 dq[NTT], dk[NTT];                 // sums over the heads
     f32x4 Wh[2], Fh[2], xe;                 // of one head: dY E^T and X E^T; X . E
-    float accA, accB, accZ;                 // this lane's part of A_i, B_i, Z (below) of one head
+    float accQ[NTT], accV[NTT], accU[NTT], accZ;    // this lane's part of dy S q, X S k, E dS k per token and <S, dS> of one head
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < NT; ++i) dq[i] = dk[i] = zero;
+    for (int i = 0; i < NTT; ++i) dq[i] = dk[i] = zero;
     if (below)
 #pragma unroll
         for (int e = 0; e < 4; ++e) held[64 * e] = zero;
     auto clear_head = [&]() {
         Wh[0] = Wh[1] = Fh[0] = Fh[1] = xe = zero;
-        accA = accB = accZ = 0.f;
+        accZ = 0.f;
+#pragma unroll
+        for (int i = 0; i < NTT; ++i) accQ[i] = accV[i] = accU[i] = 0.f;
     };
     clear_head();
 
@@ -360,71 +365,114 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
     };
     const int pbs = (P + T::kRows - 1) / T::kRows, turns = r * pbs;
     const int first = int(int64_t(turns) * split / splits), end = int(int64_t(turns) * (split + 1) / splits);
+    // a turn: head g r + hr, rows 32 pi .. of its state
+    struct Turn {
+        int hr, pi;
+    };
+    auto following = [&](const Turn &t) { return t.pi + 1 < pbs ? Turn{t.hr, t.pi + 1} : Turn{t.hr + 1, 0}; };
     // one turn's values, as loaded: rows and tokens past the end are zeros
-    f32x4 in_s[T::kLoads][2], in_d[T::kLoads][2], in_e, in_x;
+    float in_s[8], in_d[8];         // column tile_row(0, 0, c) + nq, rows 8 q ..
+    f32x4 in_e, in_x;
     u32x4 in_y;
     float in_a, in_gate;
-    auto fetch_states = [&](int i, int turn, int tid) {     // the i'th load of each state
-        const int h = g * r + turn / pbs, pb = turn % pbs * T::kRows, u = i * T::kThreads + tid;
-        const size_t at = (((size_t(bi) * H + h) * nc + ch) * P + pb + u / (NB / 8)) * N + cb * NB + u % (NB / 8) * 8;
-        const bool on = u < T::kEights && pb + u / (NB / 8) < P;
+    // range-checked views, so that a load's address is a scalar base and the thread's own offset
+    auto view_of = [](const void *base, uint32_t bytes) { return buffer_rsrc(base, bytes); };
+    auto load16 = [](__amdgpu_buffer_rsrc_t v, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b128(v, int(off), 0, 0); };
+    const uint32_t off_state = (8 * q * N + tile_row(0, 0, c) + nq) * 4;
+    auto fetch_states = [&](const Turn &t) {
+        const int h = g * r + t.hr, pb = t.pi * T::kRows;
+        const size_t at = (((size_t(bi) * H + h) * nc + ch) * P + pb) * N + cb * NB;
+        const uint32_t bytes = (min(T::kRows, P - pb) * N - cb * NB) * 4, off = off_state;
+        const __amdgpu_buffer_rsrc_t vs = view_of(Sg + at, bytes), vd = view_of(dSg + at, bytes);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            in_s[i][e] = on ? *reinterpret_cast<const f32x4 *>(Sg + at + 4 * e) : zero;
-            in_d[i][e] = on ? *reinterpret_cast<const f32x4 *>(dSg + at + 4 * e) : zero;
+        for (int j = 0; j < 8; ++j) {
+            in_s[j] = load_checked<float>(vs, off + 4 * j * N);
+            in_d[j] = load_checked<float>(vd, off + 4 * j * N);
         }
     };
-    auto fetch_rest = [&](int turn, int tid) {
-        const int h = g * r + turn / pbs, pb = turn % pbs * T::kRows;
+    constexpr int kPer = T::RP / 16;            // 16-byte pieces of a token's row of dY
+    const int at_y = tid % kPer * (16 / kSz);
+    const uint32_t off_dy = tid / kPer * uint32_t(hp) * kSz + tid % kPer * 16;
+    auto fetch_rest = [&](const Turn &t) {
+        const int h = g * r + t.hr, pb = t.pi * T::kRows;
         const size_t unit = (size_t(bi) * H + h) * nc + ch;
-        const float *from = reinterpret_cast<const float *>(images + unit * Img::kBytes + Img::kGates);
         // E and X: a chain wave's tile of 16 p's is 256 pieces, (tid & 255) >> 6 the token tile
-        const int pt = pb / 16 + (tid >> 8);
-        const size_t piece = (unit * ptiles + min(pt, ptiles - 1)) * 256 + (tid & 255);
-        in_e = pt < ptiles ? E[piece] : zero;
-        in_x = pt < ptiles ? Xg[piece] : zero;
-        constexpr int kPer = T::RP / 16;        // 16-byte pieces of a token's row of dY
-        const int ty = tid / kPer, py = pb + tid % kPer * (16 / kSz);
-        const bool on = ty < rows && py < P;
-        const IO *src = dyg + (size_t(bi) * L + t0 + (on ? ty : 0)) * hp + size_t(h) * P + (on ? py : 0);
-        in_y = on ? *reinterpret_cast<const u32x4 *>(src) : u32x4{0, 0, 0, 0};
+        const size_t piece = (unit * ptiles + pb / 16) * 256;
+        const uint32_t bytes = min(T::kRows / 16, ptiles - pb / 16) * 4096;
+        in_e = __builtin_bit_cast(f32x4, load16(view_of(E + piece, bytes), tid * 16));
+        in_x = __builtin_bit_cast(f32x4, load16(view_of(Xg + piece, bytes), tid * 16));
+        const uint32_t past = at_y < P - pb ? 0 : 0x80000000u;
+        in_y = load16(chunk_view(dyg + (size_t(bi) * L + t0) * hp + size_t(h) * P + pb, rows, uint32_t(hp) * kSz, P - pb), off_dy | past);
         in_a = ag[(size_t(bi) * L + t0 + min(tid & 63, rows - 1)) * H + h];
-        in_gate = from[min(tid, 3 * kC - 1)];
+        in_gate = reinterpret_cast<const float *>(images + unit * Img::kBytes + Img::kGates)[min(tid, 3 * kC - 1)];
     };
-    auto fetch = [&](int turn, int tid) {
+    auto sum_gates = [&](double (&to)[kC], int lane) {      // by one wave, of the head fetched last
+        double s = lane < rows ? gate(in_a) : 0.0;
 #pragma unroll
-        for (int i = 0; i < T::kLoads; ++i) fetch_states(i, turn, tid);
-        fetch_rest(turn, tid);
+        for (int off = 1; off < 64; off <<= 1) {
+            const double o = __shfl_up(s, off, 64);
+            if (lane >= off) s += o;
+        }
+        to[lane] = s * kPerLn2;
     };
-    // 4 / 8 consecutive values of row `row` of a tile, from element `col` (a multiple of 4 / 8) on
-    auto put4 = [&](char *tile, int row, int col, f32x4 v) {
-        char *dst = tile + row * T::RT + (((col * kSz >> 4) ^ place<T::RT>(row)) << 4) + (col * kSz & 15);
+    auto put4 = [&](char *dst, int stride, f32x4 v) {       // 4 consecutive values, planes `stride` bytes apart
         if constexpr (kSz == 4) {
             *reinterpret_cast<f32x4 *>(dst) = v;
         } else {
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
                 const u32x2 part = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                *reinterpret_cast<u32x2 *>(dst + p * T::kTok) = part;
+                *reinterpret_cast<u32x2 *>(dst + p * stride) = part;
                 v = f32x4{minus_lo(v[0], part[0]), minus_hi(v[1], part[0]), minus_lo(v[2], part[1]), minus_hi(v[3], part[1])};
             }
         }
     };
-    auto put8 = [&](char *tile, int row, int eight, const f32x4 (&v)[2]) {
+    // Offsets formed once.  Chunks of a row lie at chunk ^ place(row), so that another token
+    // tile's, whose chunk numbers differ in bits of their own, is an exclusive or away.
+    constexpr int kJ = kSz == 4 ? 8 : 2;
+    int off_col[kJ];        // of a tile of tokens: rows 8 q .., column tile_row(0, 0, c), as read_col takes them
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+        const int row = kSz == 4 ? 8 * q + j : 8 * q + 4 * j + (c >> 2), n = tile_row(0, 0, c);
+        off_col[j] = row * T::RT + (((kSz == 4 ? n >> 2 : c & 3) ^ place<T::RT>(row)) * 16) + (kSz == 4 ? (n & 3) * 4 : 0);
+    }
+    auto token_operand = [&](const char *tile, int s, int e) {      // columns tile_row(s, e, c)
+        Op<IO, kP> o;
         if constexpr (kSz == 4) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) *reinterpret_cast<f32x4 *>(tile + row * T::RB + (((2 * eight + e) ^ place<T::RB>(row)) * 16)) = v[e];
+            for (int j = 0; j < 8; ++j) o.v[j >> 2][j & 3] = *reinterpret_cast<const float *>(tile + (off_col[j] ^ (128 * s + 16 * e)));
         } else {
-            const Op<IO, kP> o = to_op<IO, kP>(v[0], v[1]);
 #pragma unroll
-            for (int p = 0; p < kP; ++p)
-                *reinterpret_cast<uint4 *>(tile + p * T::kState + row * T::RB + ((eight ^ place<T::RB>(row)) * 16)) = __builtin_bit_cast(uint4, o.p[p]);
+            for (int i = 0; i < kP; ++i)
+                o.p[i] = read_tr8(tile + i * T::kTok + (off_col[0] ^ (64 * s)) + 8 * e, tile + i * T::kTok + (off_col[1] ^ (64 * s)) + 8 * e);
+        }
+        return o;
+    };
+    const int row0 = tile_row(0, 0, c);     // token tile 0's row of this lane
+    const int off_y = row0 * T::RP + ((kSz == 4 ? 0 : q ^ place<T::RP>(row0)) * 16);
+    auto dy_operand = [&](const char *tile, int s, int e) {         // row tile_row(s, e, c), p's 8 q ..
+        if constexpr (kSz == 4) {
+            return read_row<IO, 1, T::RP>(tile, 0, row0 + 32 * s + 4 * e, 0, q);
+        } else {
+            Op<IO, 1> o;        // place<64> sees neither the bit of s nor that of e
+            o.p[0] = as_bf16x8(*reinterpret_cast<const uint4 *>(tile + off_y + (32 * s + 4 * e) * T::RP));
+            return o;
         }
     };
-    // 4 values of row `tok` of k or q, columns 4 c4 .. of the block's
-    auto four_of = [&](const char *tile, int tok, int c4) {
-        const int at = c4 * 4 * kSz;
-        return widen<IO>(*reinterpret_cast<const Raw4<IO> *>(tile + tok * T::RB + (((at >> 4) ^ place<T::RB>(tok)) << 4) + (at & 15)));
+    // 4 values of row tile_row(s, e, c) of k or q, this lane's columns nq + 8 q ..
+    const int at_key = (nq + 8 * q) * kSz, off_key = row0 * T::RB + (((at_key >> 4) ^ place<T::RB>(row0)) << 4) + (at_key & 15);
+    auto four_of = [&](const char *tile, int s, int e) {
+        constexpr int kFlip = place<T::RB>(4) << 4;
+        return widen<IO>(*reinterpret_cast<const Raw4<IO> *>(tile + (e ? off_key ^ kFlip : off_key) + (32 * s + 4 * e) * T::RB));
+    };
+    const int put_row = 16 * (tid >> 8) + c, put_col = 32 * ((tid >> 7) & 1) + 8 * q + 4 * ((tid >> 6) & 1);
+    const int off_put = put_row * T::RT + (((put_col * kSz >> 4) ^ place<T::RT>(put_row)) << 4) + (put_col * kSz & 15);
+    const int off_puty = tid / (T::RP / 16) * T::RP + (((tid % (T::RP / 16)) ^ place<T::RP>(tid / (T::RP / 16))) * 16);
+    auto put_rest = [&](char *to) {
+        put4(to + T::kE + off_put, T::kTok, in_e);
+        put4(to + T::kV + off_put, T::kTok, in_x);
+        if (T::kTok == 16 * T::kThreads || tid < T::kTok / 16) *reinterpret_cast<u32x4 *>(to + T::kY + off_puty) = in_y;
+        if (tid < 3 * kC) reinterpret_cast<float *>(to + T::kGates)[tid] = in_gate;
     };
     // row `tok` of k or q as an operand, columns 32 ks + 8 q .. of all N
     auto row_of = [&](const char *tile, const IO *src, int tok, int ks, int q) {
@@ -432,101 +480,82 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
         else return load_row8<IO>(src + size_t(min(tok, rows - 1)) * gn + 32 * ks + 8 * q);
     };
 
+    Turn now{first / pbs, first % pbs};
+    const int portion = split - split_of(int64_t(now.hr) * pbs, turns, splits);     // of the first head
+    int side = 0;
     copy_keys();
-    fetch(first, tid0);
+    fetch_rest(now);
+    fetch_states(now);
     copies_done();
-    bool new_head = true;
-    for (int turn = first; turn < end; ++turn) {    // head h, rows pb .. pb + 31 of its state
-        const bool last_of_head = turn == end - 1 || (turn + 1) % pbs == 0;
-        const int ahead = min(turn + 1, end - 1);
+    if (w == 4) sum_gates(gd[0], lane);
+    xe += in_e * in_x;
+    put_rest(lds);
+    fetch_rest(first + 1 < end ? following(now) : now);
+    __syncthreads();
+    for (int turn = first; turn < end; ++turn, now = following(now)) {
         // a thread number the compiler does not know: addresses are formed here again rather
-        // than kept over the turns, for which there may not be the registers
-        int tid = threadIdx.x;
+        // than kept over the turns, for which there are not the registers
+        tid = threadIdx.x;
         asm volatile("" : "+v"(tid));
-        const int lane = tid & 63, c = lane & 15, q = lane >> 4, tok = tile_row(tw >> 1, tw & 1, c);    // this lane's token
-        __syncthreads();        // the tiles' last readers
-#pragma unroll
-        for (int i = 0; i < T::kLoads; ++i) {
-            const int u = i * T::kThreads + tid;
-            if (u < T::kEights) {
-                put8(lds + T::kS, u / (NB / 8), u % (NB / 8), in_s[i]);
-                put8(lds + T::kD, u / (NB / 8), u % (NB / 8), in_d[i]);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) accZ += in_s[i][e][j] * in_d[i][e][j];
-            fetch_states(i, ahead, tid);
-            if constexpr (T::kTight) __builtin_amdgcn_sched_barrier(0);
-        }
+        lane = tid & 63, c = lane & 15, q = lane >> 4;
+        const bool last_of_head = turn == end - 1 || now.pi == pbs - 1;
+        const Turn ahead = turn + 1 < end ? following(now) : now;
+        char *buf = lds + (turn - first) % 2 * T::kTurn, *other = lds + (turn - first + 1) % 2 * T::kTurn;
+        const float *gates = reinterpret_cast<const float *>(buf + T::kGates);
+        float *Tm = reinterpret_cast<float *>(buf);
+        // the states' parts; before them the next turn's rest into the other buffer, whose
+        // readers have passed the last barrier
+        f32x4 xe_next;
         {
-            const int t = (tid >> 6) & 3, row = 16 * (tid >> 8) + c, col = 32 * (t >> 1) + 8 * q + 4 * (t & 1);
-            put4(lds + T::kE, row, col, in_e);
-            put4(lds + T::kV, row, col, in_x);
-            xe += in_e * in_x;
-            constexpr int kPer = T::RP / 16;
-            if (const int y = tid / kPer; y < kC)
-                *reinterpret_cast<u32x4 *>(lds + T::kY + y * T::RP + (((tid % kPer) ^ place<T::RP>(y)) * 16)) = in_y;
-            if (tid < 3 * kC) gates[tid] = in_gate;
-        }
-        if (new_head && w == 0) {
-            double s = lane < rows ? gate(in_a) : 0.0;
+            Op<IO, kP> as[1] = {to_op<IO, kP>(f32x4{in_s[0], in_s[1], in_s[2], in_s[3]}, f32x4{in_s[4], in_s[5], in_s[6], in_s[7]})};
+            Op<IO, kP> ad[1] = {to_op<IO, kP>(f32x4{in_d[0], in_d[1], in_d[2], in_d[3]}, f32x4{in_d[4], in_d[5], in_d[6], in_d[7]})};
+            if (th == 0)
 #pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-                const double o = __shfl_up(s, off, 64);
-                if (lane >= off) s += o;
-            }
-            gd[lane] = s;
-        }
-        new_head = last_of_head;
-        fetch_rest(ahead, tid);
-        __syncthreads();
-        // the states' parts
-        const float fs = gates[tok], bt = gates[2 * kC + tok], te = gates[kC + tok] * bt, fv = fs * bt;
-        const Op<IO, 1> oy = read_row<IO, 1, T::RP>(lds + T::kY, 0, tok, 0, q);
-        const Op<IO, kP> ov = read_col<IO, kP, T::RT>(lds + T::kV, T::kTok, 0, 32 * (tw >> 1), tw & 1, c, q);
-        const Op<IO, kP> ou = read_col<IO, kP, T::RT>(lds + T::kE, T::kTok, 0, 32 * (tw >> 1), tw & 1, c, q);
-        constexpr int M = NT < 2 || T::kTight ? 1 : 2;
+                for (int j = 0; j < 8; ++j) accZ += in_s[j] * in_d[j];
+            fetch_states(ahead);
+            xe_next = in_e * in_x;
+            put_rest(other);
+            if (last_of_head && w == 4) sum_gates(gd[side ^ 1], lane);      // a wave with fewer products than others
+            fetch_rest(turn + 2 < end ? following(ahead) : ahead);
+            __builtin_amdgcn_sched_barrier(0);      // the loads first
 #pragma unroll
-        for (int i0 = 0; i0 < NT; i0 += M) {
-            Op<IO, kP> as[M], ad[M];
-            f32x4 zq[M], zv[M], zu[M];
-#pragma unroll
-            for (int i = 0; i < M; ++i) {
-                const int t = column(i0 + i);
-                as[i] = read_col<IO, kP, T::RB>(lds + T::kS, T::kState, 0, 32 * (t >> 1), t & 1, c, q);
-                ad[i] = read_col<IO, kP, T::RB>(lds + T::kD, T::kState, 0, 32 * (t >> 1), t & 1, c, q);
-                zq[i] = zv[i] = zu[i] = zero;
-            }
-            mma(zq, as, oy);
-            mma(zv, as, ov);
-            mma(zu, ad, ou);
-#pragma unroll
-            for (int i = 0; i < M; ++i) {
-                const int c4 = 8 * (column(i0 + i) >> 1) + 2 * q + (column(i0 + i) & 1);
-                const f32x4 kv = four_of(lds + T::kK, tok, c4), qv = four_of(lds + T::kQ, tok, c4);
+            for (int i = 0; i < NTT; ++i) {
+                const int tt = tile_of(i), ts = tt >> 1, te_ = tt & 1, tok = row0 + 32 * ts + 4 * te_;
+                const float fs = gates[tok], bt = gates[2 * kC + tok], te = gates[kC + tok] * bt, fv = fs * bt, fq = scale * fs;
+                const Op<IO, 1> oy = dy_operand(buf + T::kY, ts, te_);
+                const Op<IO, kP> ov = token_operand(buf + T::kV, ts, te_), ou = token_operand(buf + T::kE, ts, te_);
+                const f32x4 kv = four_of(lds + T::kK, ts, te_), qv = four_of(lds + T::kQ, ts, te_);
+                f32x4 zq[1] = {zero}, zv[1] = {zero}, zu[1] = {zero};
+                mma(zq, as, oy);
+                mma(zv, as, ov);
+                mma(zu, ad, ou);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float a = (scale * fs) * zq[i][j], b = fv * zv[i][j], d = te * zu[i][j];
-                    dq[i0 + i][j] += a;
-                    dk[i0 + i][j] += d - b;
-                    accA += a * qv[j] - b * kv[j];
-                    accB += d * kv[j];
+                    dq[i][j] += fq * zq[0][j];
+                    dk[i][j] += te * zu[0][j];
+                    dk[i][j] -= fv * zv[0][j];
+                    accQ[i] += zq[0][j] * qv[j];
+                    accV[i] += zv[0][j] * kv[j];
+                    accU[i] += zu[0][j] * kv[j];
                 }
             }
-            if constexpr (T::kTight) __builtin_amdgcn_sched_barrier(0);     // no registers to read ahead
         }
+        const int tok = tile_row(tw >> 1, tw & 1, c);       // this lane's token in what follows
         // dY E^T and X E^T (rows j, columns i: this lane's token)
-        __builtin_amdgcn_sched_barrier(0);
         if (below) {
+            const Op<IO, 1> oy = dy_operand(buf + T::kY, tw >> 1, tw & 1);
+            const Op<IO, kP> ov = token_operand(buf + T::kV, tw >> 1, tw & 1);
             Op<IO, kP> au[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) au[e] = read_col<IO, kP, T::RT>(lds + T::kE, T::kTok, 0, 32 * half, e, c, q);
+            for (int e = 0; e < 2; ++e) au[e] = token_operand(buf + T::kE, half, e);
             mma(Wh, au, oy);
             mma(Fh, au, ov);
         }
-        if (!last_of_head) continue;
-        __syncthreads();        // the tiles' last readers, T lies over them
+        __syncthreads();
+        if (!last_of_head) {
+            xe += xe_next;
+            continue;
+        }
 
         // The head's W and F, and its gates' gradients:  with T_ij = W_ij (q_i . k_j) + F_ij (k_i . k_j),
         //   A_i = scale e^{g_i} dy_i . S q_i - dv_i . e^{g_i} S k_i,  B_j = u_j . e^{g_C - g_j} dS k_j,  Z = e^{g_C} <S, dS>
@@ -546,18 +575,20 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            const double gt = gd[tok];
+            const double *gs = gd[side], gt = gs[tok];
+            const float bt = gates[2 * kC + tok];
+            const int most = tok < rows ? tok : -1;     // no j is that small
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                f32x4 wv = zero, fv = zero;
+                const int j0 = 32 * half + 8 * q + 4 * e;
+                const f32x4 bj = *reinterpret_cast<const f32x4 *>(gates + 2 * kC + j0);
+                f32x4 wv, fv;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int j = 32 * half + 8 * q + 4 * e + i;
-                    const float D = expf(j <= tok ? float(gt - gd[j]) : 0.f);
-                    const float bj = gates[2 * kC + j];
-                    if (j <= tok && tok < rows) wv[i] = (scale * D) * (bj * Wh[e][i]);
-                    if (j < tok && tok < rows) fv[i] = (-D * bt) * (bj * Fh[e][i]);
-                    Tm[tok * T::LT + j] = j < tok && tok < rows ? wv[i] * qk[e][i] + fv[i] * kk[e][i] : 0.f;
+                    const float d = decay(gt - gs[j0 + i]) * bj[i], x = scale * d * Wh[e][i], y = -bt * d * Fh[e][i];
+                    wv[i] = j0 + i <= most ? x : 0.f;
+                    fv[i] = j0 + i < most ? y : 0.f;
+                    Tm[tok * T::LT + j0 + i] = j0 + i < most ? x * qk[e][i] + y * kk[e][i] : 0.f;
                 }
                 if (below) {
                     held[128 * e] += wv;
@@ -565,18 +596,39 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
                 }
             }
         }
-        accA = group4_sum(accA);
-        accB = group4_sum(accB);
-        accZ = wave_sum(accZ);
-        if (q == 0) {
-            As[half * kC + tok] = tok < rows ? accA : 0.f;
-            Bs[half * kC + tok] = tok < rows ? accB : 0.f;
+        // sums over the 4 lane groups; of 4 token tiles, each ends up in a group of its own
+        float sa[NTT], sb[NTT];
+#pragma unroll
+        for (int i = 0; i < NTT; ++i) {
+            const int tt = tile_of(i), at = row0 + 32 * (tt >> 1) + 4 * (tt & 1);
+            const float fs = gates[at], bt = gates[2 * kC + at];
+            sa[i] = scale * fs * accQ[i] - fs * bt * accV[i];
+            sb[i] = gates[kC + at] * bt * accU[i];
         }
+        if constexpr (NTT == 4) {
+            const float a = two_sums16(two_sums32(sa[0], sa[2]), two_sums32(sa[1], sa[3])), b = two_sums16(two_sums32(sb[0], sb[2]), two_sums32(sb[1], sb[3]));
+            const int at = row0 + 32 * (q >> 1) + 4 * (q & 1);
+            As[ct * kC + at] = at < rows ? a : 0.f;
+            Bs[ct * kC + at] = at < rows ? b : 0.f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NTT; ++i) {
+                const int tt = tile_of(i), at = row0 + 32 * (tt >> 1) + 4 * (tt & 1);
+                const float a = group4_sum(sa[i]), b = group4_sum(sb[i]);
+                if (q == 0) {
+                    As[ct * kC + at] = at < rows ? a : 0.f;
+                    Bs[ct * kC + at] = at < rows ? b : 0.f;
+                }
+            }
+        }
+        accZ = wave_sum(accZ);
         if (lane == 0) zs[w] = accZ;
 #pragma unroll
         for (int j = 0; j < 4; ++j) xe[j] = row16_sum(xe[j]);
         if (c == 0) *reinterpret_cast<f32x4 *>(Xs + (tid >> 8) * kC + 32 * ((tid >> 7) & 1) + 8 * q + 4 * ((tid >> 6) & 1)) = xe;
+        const float alpha = gates[kC - 1];      // (the next turn writes this buffer)
         clear_head();
+        xe = xe_next;
         __syncthreads();
         // wave w: the sums down the columns of T, from rows 8 w .. 8 w + 7 on; lane = column j
         float v[8];
@@ -587,28 +639,30 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
         float lower = 0.f;
 #pragma unroll
         for (int i = 1; i < 8; ++i) lower += w + i < 8 ? sums[((w + i) & 7) * kC + lane] : 0.f;
-        float da = 0.f;
+        // row 8 w + i: its columns j < t; 8 sums over 64 lanes, two rows at a time ending up in
+        // half of the lanes each
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {       // row t = 8 w + i: its columns j < t
-            const float s = wave_sum(lane < 8 * w + i ? v[i] + lower : 0.f);
-            da = lane == 8 * w + i ? s : da;
-        }
-        float a = As[lane] + As[kC + lane], b = Bs[lane] + Bs[kC + lane];
+        for (int i = 0; i < 8; ++i) v[i] = lane < 8 * w + i ? v[i] + lower : 0.f;
 #pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const float oa = __shfl_down(a, off, 64), ob = __shfl_up(b, off, 64);
-            if (lane + off < 64) a += oa;
-            if (lane >= off) b += ob;
+        for (int i = 0; i < 4; ++i) v[i] = two_sums32(v[i], v[i + 4]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[i] = row16_sum(two_sums16(v[i], v[i + 2]));
+        const int t = 8 * w + 4 * (q >> 1) + 2 * (q & 1) + (c & 1);     // lane's row
+        // A from the last token down, B from the first up to the one before
+        float a = 0.f, bs = 0.f;
+#pragma unroll
+        for (int i = 0; i < T::CT; ++i) {
+            a += As[i * kC + 63 - lane];
+            bs += Bs[i * kC + lane];
         }
-        b = __shfl_up(b, 1, 64);
+        const float after = __shfl(wave_inclusive_scan(a), 63 - t, 64), before = __shfl(wave_inclusive_scan(bs), max(t - 1, 0), 64);
         const float z = ((zs[0] + zs[1]) + (zs[2] + zs[3])) + ((zs[4] + zs[5]) + (zs[6] + zs[7]));
-        da += a + (lane ? b : 0.f) + gates[kC - 1] * z;
-        if (lane >> 3 == w && lane < rows) {
-            const int hr = turn / pbs, h = g * r + hr;
-            const size_t all = size_t(gridDim.x / (kCols * splits * nc * G)) * L * H, at = (size_t(bi) * L + t0 + lane) * H + h;
-            const float db = cb == 0 ? Xs[lane] + Xs[kC + lane] : 0.f;
+        const float da = (c & 1 ? v[1] : v[0]) + after + (t ? before : 0.f) + alpha * z;
+        if (c < 2 && t < rows) {
+            const size_t all = size_t(b) * L * H, at = (size_t(bi) * L + t0 + t) * H + g * r + now.hr;
+            const float db = cb == 0 ? Xs[t] + Xs[kC + t] : 0.f;
             if (kCols > 1 || splits > 1) {
-                float *to = gate_parts + 2 * all * ((split - split_of(int64_t(hr) * pbs, turns, splits)) * kCols + cb) + at;
+                float *to = gate_parts + 2 * all * ((turn - now.pi < first ? portion : 0) * kCols + cb) + at;
                 to[0] = da;
                 to[all] = db;
             } else {
@@ -616,76 +670,50 @@ __global__ __launch_bounds__(512) void k_delta_grads(const IO *__restrict__ qg, 
                 dbg[at] = db;
             }
         }
+        side ^= 1;
     }
     __syncthreads();
-    const int lane = tid0 & 63, c = lane & 15, q = lane >> 4, tok = tile_row(tw >> 1, tw & 1, c);
-    // W [i][j] and G [i][j] = G [j][i]
-    auto put = [&](char *tile, int row, int col, float v) {
-        char *dst = tile + row * T::RT + (((col * kSz >> 4) ^ place<T::RT>(row)) << 4) + (col * kSz & 15);
-        if constexpr (kSz == 4) {
-            *reinterpret_cast<float *>(dst) = v;
-        } else {
-#pragma unroll
-            for (int p = 0; p < kP; ++p) {
-                const bf16_bits part = f32_to_bf16(v);
-                *reinterpret_cast<bf16_bits *>(dst + p * T::kMat) = part;
-                v -= bf16_to_f32(part);
-            }
-        }
-    };
+    const int tok = tile_row(tw >> 1, tw & 1, c);
+    // W [i][j] and F [i][j], 0 above the diagonal
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const f32x4 wv = below ? held[128 * e] : zero, fv = below ? held[128 * e + 64] : zero;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = 32 * half + 8 * q + 4 * e + i;
-            put(lds + T::kWm, tok, j, wv[i]);           // 0 above the diagonal
-            if (j < tok) {
-                put(lds + T::kGm, tok, j, fv[i]);
-                put(lds + T::kGm, j, tok, fv[i]);
-            } else if (j == tok) {
-                put(lds + T::kGm, j, j, 0.f);
-            }
-        }
+        const int col = 32 * half + 8 * q + 4 * e, at = tok * T::RT + (((col * kSz >> 4) ^ place<T::RT>(tok)) << 4) + (col * kSz & 15);
+        put4(lds + T::kWm + at, T::kMat, below ? held[128 * e] : zero);
+        put4(lds + T::kFm + at, T::kMat, below ? held[128 * e + 64] : zero);
     }
     __syncthreads();
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-        int l = lane;
-        if constexpr (T::kTight) asm volatile("" : "+v"(l));
-        const int c = l & 15, q = l >> 4, tok = tile_row(tw >> 1, tw & 1, c);
-        const Op<IO, kP> wr = read_row<IO, kP, T::RT>(lds + T::kWm, T::kMat, tok, ks, q);
-        const Op<IO, kP> gr = read_row<IO, kP, T::RT>(lds + T::kGm, T::kMat, tok, ks, q);
-        const Op<IO, kP> wc = read_col<IO, kP, T::RT>(lds + T::kWm, T::kMat, 32 * ks, 32 * (tw >> 1), tw & 1, c, q);
+        const Op<IO, 1> ak[1] = {read_col<IO, 1, T::RB>(lds + T::kK, 0, 32 * ks, 32 * (ct >> 1), ct & 1, c, q)};
+        const Op<IO, 1> aq[1] = {read_col<IO, 1, T::RB>(lds + T::kQ, 0, 32 * ks, 32 * (ct >> 1), ct & 1, c, q)};
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int t = column(i);
-            const Op<IO, 1> ak[1] = {read_col<IO, 1, T::RB>(lds + T::kK, 0, 32 * ks, 32 * (t >> 1), t & 1, c, q)};
-            const Op<IO, 1> aq[1] = {read_col<IO, 1, T::RB>(lds + T::kQ, 0, 32 * ks, 32 * (t >> 1), t & 1, c, q)};
-            f32x4 z[1] = {dq[i]};
-            mma(z, ak, wr);
-            dq[i] = z[0];
-            z[0] = dk[i];
-            mma(z, ak, gr);
-            mma(z, aq, wc);
-            dk[i] = z[0];
-            if constexpr (T::kTight) __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < NTT; ++i) {
+            const int tt = tile_of(i), at = tile_row(tt >> 1, tt & 1, c);
+            f32x4 zq[1] = {dq[i]}, zk[1] = {dk[i]};
+            if (ks <= (tt >> 1)) {          // rows i of the tile: j <= i
+                mma(zq, ak, read_row<IO, kP, T::RT>(lds + T::kWm, T::kMat, at, ks, q));
+                mma(zk, ak, read_row<IO, kP, T::RT>(lds + T::kFm, T::kMat, at, ks, q));
+            }
+            if (ks >= (tt >> 1)) {          // and as columns: i >= j
+                mma(zk, ak, read_col<IO, kP, T::RT>(lds + T::kFm, T::kMat, 32 * ks, 32 * (tt >> 1), tt & 1, c, q));
+                mma(zk, aq, read_col<IO, kP, T::RT>(lds + T::kWm, T::kMat, 32 * ks, 32 * (tt >> 1), tt & 1, c, q));
+            }
+            dq[i] = zq[0];
+            dk[i] = zk[0];
         }
     }
-    if (tok < rows) {
-        const size_t dst = (size_t(bi) * L + t0 + tok) * gn + size_t(g) * N + cb * NB + 8 * q;
-        const size_t all = size_t(gridDim.x / (kCols * splits * nc * G)) * L * gn;
-        float *pq = parts + 2 * split * all + dst, *pk = pq + all;
+    const size_t all = size_t(b) * L * gn;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int at = 32 * (column(i) >> 1) + 4 * (column(i) & 1);
-            if (splits > 1) {
-                *reinterpret_cast<f32x4 *>(pq + at) = dq[i];
-                *reinterpret_cast<f32x4 *>(pk + at) = dk[i];
-            } else {
-                *reinterpret_cast<Raw4<IO> *>(dqg + dst + at) = narrow<IO>(dq[i]);
-                *reinterpret_cast<Raw4<IO> *>(dkg + dst + at) = narrow<IO>(dk[i]);
-            }
+    for (int i = 0; i < NTT; ++i) {
+        const int tt = tile_of(i), at = tile_row(tt >> 1, tt & 1, c);
+        if (at >= rows) continue;
+        const size_t dst = (size_t(bi) * L + t0 + at) * gn + size_t(g) * N + cb * NB + nq + 8 * q;
+        if (splits > 1) {
+            *reinterpret_cast<f32x4 *>(parts + 2 * split * all + dst) = dq[i];
+            *reinterpret_cast<f32x4 *>(parts + (2 * split + 1) * all + dst) = dk[i];
+        } else {
+            *reinterpret_cast<Raw4<IO> *>(dqg + dst) = narrow<IO>(dq[i]);
+            *reinterpret_cast<Raw4<IO> *>(dkg + dst) = narrow<IO>(dk[i]);
         }
     }
 }
@@ -784,7 +812,7 @@ hipError_t launch_n(const DeltaBwdArgs &a, const DeltaBwdPlan &pl, hipStream_t s
     constexpr int kCols = GradTile<IO, N>::kCols;
     hipLaunchKernelGGL(grads, dim3(unsigned(int64_t(a.b) * a.G * nc * pl.splits * kCols)), dim3(GradTile<IO, N>::kThreads), lds, stream, q, k, a.a, dy, images,
                        reinterpret_cast<const f32x4 *>(saved.E), kept_x, saved.S, dS, static_cast<IO *>(a.dq), static_cast<IO *>(a.dk), a.da,
-                       a.dbeta, parts, gate_parts, pl.splits, a.L, a.H, a.P, a.G, nc, a.scale);
+                       a.dbeta, parts, gate_parts, pl.splits, a.b, a.L, a.H, a.P, a.G, nc, a.scale);
     if ((e = hipGetLastError()) != hipSuccess || pl.splits * kCols == 1) return e;
     const size_t tokens = size_t(a.b) * a.L, all = tokens * a.G * N;
     const unsigned blocks = pl.splits > 1 ? unsigned((2 * all + 2047) / 2048) : 0;

@@ -45,7 +45,7 @@ __device__ __forceinline__ float decay(double x) { return __builtin_amdgcn_exp2f
 // or consecutive ones) and at most two lanes a column to a transposing read, which only
 // ever uses one half of each column.
 template <int RB>
-__device__ __forceinline__ int place(int r) {
+__host__ __device__ constexpr __forceinline__ int place(int r) {
     if constexpr (RB >= 256) return (r & 1) ^ ((r & 2) << 1) ^ ((r & 4) >> 1) ^ ((r & 8) | ((r & 8) >> 3)) ^ ((r & 16) >> 3);
     else if constexpr (RB == 128) return ((r & 2) >> 1) ^ ((r & 4) >> 1) ^ ((r & 8) >> 1) ^ ((r & 16) >> 3);
     else return (r & 8) >> 2;
@@ -174,6 +174,14 @@ __device__ __forceinline__ Op<IO, NP> read_row(const char *tile, int stride, int
     return o;
 }
 
+// Two transposing reads of 4 values each.
+__device__ __forceinline__ bf16x8 read_tr8(const char *lo, const char *hi) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(lo));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(hi));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 // Column n0 + tile_row(0, e, c) of a tile (n0 a multiple of 32), rows k0 + 8 q .. + 7:
 // for bf16 two transposing reads of a 4 x 16 block each, in which lane c of a group of 16
 // addresses row c >> 2, columns 4 (c & 3) .. + 3, and receives column c of the 4 rows.
@@ -188,18 +196,15 @@ __device__ __forceinline__ Op<IO, NP> read_col(const char *tile, int stride, int
             o.v[j >> 2][j & 3] = *reinterpret_cast<const float *>(tile + row * RB + (((n >> 2) ^ place<RB>(row)) * 16) + (n & 3) * 4);
         }
     } else {
-        typedef short s16x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            s16x4 h[2];
+            const char *at[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int row = k0 + 8 * q + 4 * j + (c >> 2);
-                const char *at = tile + i * stride + row * RB + (((n0 / 8 + (c & 3)) ^ place<RB>(row)) * 16) + 8 * e;
-                h[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4 *)(at));
+                at[j] = tile + i * stride + row * RB + (((n0 / 8 + (c & 3)) ^ place<RB>(row)) * 16) + 8 * e;
             }
-            o.p[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+            o.p[i] = read_tr8(at[0], at[1]);
         }
     }
     return o;

@@ -144,6 +144,18 @@ __device__ __forceinline__ float xor32_sum(float v) {
     return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
+// u[l] + u[l ^ 32] in the lower 32 lanes, v[l] + v[l ^ 32] in the upper ones.
+__device__ __forceinline__ float two_sums32(float u, float v) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(u), __float_as_uint(v), false, false);
+    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+// u[l] + u[l ^ 16] in the even rows of 16 lanes, v[l] + v[l ^ 16] in the odd ones.
+__device__ __forceinline__ float two_sums16(float u, float v) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(u), __float_as_uint(v), false, false);
+    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
 // The value of lane `src` (the same for the whole wave) in every lane (v_readlane).
 __device__ __forceinline__ float lane_value(float v, int src) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), src));
