@@ -32,6 +32,10 @@ namespace ssd {
 namespace {
 
 constexpr int kBlock = 256;
+
+// Blocks of a forward pass: one dimension of a launch holds fewer than 2^32 threads, so that
+// many blocks go into two.  The last row of them may be only begun.
+__device__ __forceinline__ int64_t block_index() { return int64_t(blockIdx.y) * gridDim.x + blockIdx.x; }
 constexpr int kBwdBlocks = 1024;    // blocks of a backward pass, at the most
 
 // VEC elements of the I/O type, loaded and stored as one access.
@@ -106,7 +110,7 @@ __global__ __launch_bounds__(kBlock) void k_norm_gate_fwd(const IO *__restrict__
     __shared__ float tmp[4];
     constexpr int kTeams = kBlock / TPS;
     const int lane = threadIdx.x % TPS;
-    const int64_t seg = int64_t(blockIdx.x) * kTeams + threadIdx.x / TPS;
+    const int64_t seg = block_index() * kTeams + threadIdx.x / TPS;
     const bool live = seg < segments;           // the same for a whole team
     const int64_t at = (live ? seg : 0) * group;
     const int col = int(at % D);                // channel of the segment's first element
@@ -244,7 +248,7 @@ __global__ __launch_bounds__(kBlock) void k_norm_add_fwd(const IO *__restrict__ 
     __shared__ float tmp[4];
     constexpr int kTeams = kBlock / TPS;
     const int lane = threadIdx.x % TPS;
-    const int64_t row = int64_t(blockIdx.x) * kTeams + threadIdx.x / TPS;
+    const int64_t row = block_index() * kTeams + threadIdx.x / TPS;
     const bool live = row < rows;
     const int64_t at = (live ? row : 0) * D;
     float s[NV][VEC], xv[NV][VEC];
@@ -370,10 +374,12 @@ __global__ __launch_bounds__(kBlock) void k_norm_add_bwd(const IO *__restrict__ 
 // and once more (from the caches) for the result.
 template <typename IO>
 __global__ __launch_bounds__(kBlock) void k_norm_gate_fwd_loop(const IO *__restrict__ x, const IO *__restrict__ z,
-                                                               const float *__restrict__ w, IO *__restrict__ y, int D,
-                                                               int group, float eps, bool gate_first) {
+                                                               const float *__restrict__ w, IO *__restrict__ y,
+                                                               int64_t segments, int D, int group, float eps,
+                                                               bool gate_first) {
     __shared__ float tmp[4];
-    const int64_t at = int64_t(blockIdx.x) * group;
+    if (block_index() >= segments) return;
+    const int64_t at = block_index() * group;
     const int col = int(at % D);
     float ss = 0.f;
     for (int c = threadIdx.x; c < group; c += kBlock) {
@@ -441,9 +447,10 @@ template <typename IO, typename RES>
 __global__ __launch_bounds__(kBlock) void k_norm_add_fwd_loop(const IO *__restrict__ x, const RES *residual,
                                                               const float *__restrict__ scale,
                                                               const float *__restrict__ w, RES *sum, IO *__restrict__ y,
-                                                              int D, float eps) {
+                                                              int64_t rows, int D, float eps) {
     __shared__ float tmp[4];
-    const int64_t at = int64_t(blockIdx.x) * D;
+    if (block_index() >= rows) return;
+    const int64_t at = block_index() * D;
     float ss = 0.f;
     for (int c = threadIdx.x; c < D; c += kBlock) {
         const float xv = to_f32<IO>(x[at + c]);
@@ -566,6 +573,13 @@ hipError_t with_team(const Team &t, F &&f) {
 
 unsigned blocks_of(int64_t units, int per) { return unsigned((units + per - 1) / per); }
 
+// The same in two dimensions (block_index).
+dim3 grid_of(int64_t units, int per) {
+    constexpr int64_t kRow = 1 << 20;
+    const int64_t blocks = (units + per - 1) / per;
+    return blocks <= kRow ? dim3(unsigned(blocks)) : dim3(unsigned(kRow), unsigned((blocks + kRow - 1) / kRow));
+}
+
 template <typename IO>
 hipError_t gate_fwd(const NormGateArgs &a, hipStream_t stream) {
     const auto *x = static_cast<const IO *>(a.x), *z = static_cast<const IO *>(a.z);
@@ -573,11 +587,11 @@ hipError_t gate_fwd(const NormGateArgs &a, hipStream_t stream) {
     const int64_t segments = a.rows * (a.D / a.group);
     const Team t = pick_team(a.group, a.bf16);
     if (!t.nv) {
-        hipLaunchKernelGGL((k_norm_gate_fwd_loop<IO>), dim3(unsigned(segments)), dim3(kBlock), 0, stream, x, z, a.w, y, a.D, a.group, a.eps, a.gate_first);
+        hipLaunchKernelGGL((k_norm_gate_fwd_loop<IO>), grid_of(segments, 1), dim3(kBlock), 0, stream, x, z, a.w, y, segments, a.D, a.group, a.eps, a.gate_first);
         return hipGetLastError();
     }
     return with_team<IO>(t, [&](auto v, auto tps, auto nv) {
-        hipLaunchKernelGGL((k_norm_gate_fwd<IO, v(), tps(), nv()>), dim3(blocks_of(segments, kBlock / tps())), dim3(kBlock), 0, stream,
+        hipLaunchKernelGGL((k_norm_gate_fwd<IO, v(), tps(), nv()>), grid_of(segments, kBlock / tps()), dim3(kBlock), 0, stream,
                            x, z, a.w, y, segments, a.D, a.group, a.eps, a.gate_first);
         return hipGetLastError();
     });
@@ -615,11 +629,11 @@ hipError_t add_fwd(const NormAddArgs &a, hipStream_t stream) {
     auto *y = static_cast<IO *>(a.y);
     const Team t = pick_team(a.D, a.bf16);
     if (!t.nv) {
-        hipLaunchKernelGGL((k_norm_add_fwd_loop<IO, RES>), dim3(unsigned(a.rows)), dim3(kBlock), 0, stream, x, res, a.scale, a.w, sum, y, a.D, a.eps);
+        hipLaunchKernelGGL((k_norm_add_fwd_loop<IO, RES>), grid_of(a.rows, 1), dim3(kBlock), 0, stream, x, res, a.scale, a.w, sum, y, a.rows, a.D, a.eps);
         return hipGetLastError();
     }
     return with_team<IO>(t, [&](auto v, auto tps, auto nv) {
-        hipLaunchKernelGGL((k_norm_add_fwd<IO, RES, v(), tps(), nv()>), dim3(blocks_of(a.rows, kBlock / tps())), dim3(kBlock), 0, stream,
+        hipLaunchKernelGGL((k_norm_add_fwd<IO, RES, v(), tps(), nv()>), grid_of(a.rows, kBlock / tps()), dim3(kBlock), 0, stream,
                            x, res, a.scale, a.w, sum, y, a.rows, a.D, a.eps);
         return hipGetLastError();
     });
