@@ -529,10 +529,10 @@ ssd_status_t ssd_gated_delta_bwd(const void *q, const void *k, const void *v, co
  * The backward calls take scratch of ssd_norm_bwd_workspace_bytes bytes (group = D for
  * norm_add; params = the number of [D] gradients: 1, or 2 for norm_add with a scale;
  * (size_t)-1: invalid dimensions).  Parameter gradients are summed in a fixed order.
- * Any D >= 1, rows >= 0 (rows = 0 zeroes the parameter gradients), up to 65535 groups a row
- * and 2^31 - 1 in all.  All pointers 16-byte aligned.  Sums in fp32, every output rounded
- * once.  Outputs must not overlap inputs (but for sum), each other or the workspace.  Errors
- * as for the other entry points.
+ * D from 1 to 2^31 - 257, rows >= 0 (rows = 0 zeroes the parameter gradients), up to 65535
+ * groups a row and 2^31 - 1 in all.  All pointers 16-byte aligned.  Sums in fp32, every
+ * output rounded once.  Outputs must not overlap inputs (but for sum), each other or the
+ * workspace.  Errors as for the other entry points.
  */
 ssd_status_t ssd_norm_gate_fwd(const void *x, const void *z, const float *w, void *y, int rows,
                                int D, int group, float eps, int gate_first, ssd_dtype_t io,

@@ -19,6 +19,8 @@ size_t elem(ssd_dtype_t io) { return io == SSD_DTYPE_BF16 ? 2 : 4; }
 ssd_status_t check_dims(int rows, int D, int group) {
     if (rows < 0 || D <= 0 || group <= 0) return SSD_ERR_BAD_DIM;
     if (D % group != 0) return SSD_ERR_GROUPS;
+    // the kernels count channels in 31 bits, up to a block past the last one
+    if (D > INT_MAX - 256) return SSD_ERR_UNSUPPORTED;
     // segments counted in 31 bits (a launch's two dimensions hold as many blocks), groups of a row in 16
     if (int64_t(rows) * (D / group) > INT_MAX || D / group > 65535) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
