@@ -476,6 +476,7 @@ ssd_status_t ssd_chunk_scan_bwd(const void *x, const float *dt, const float *A, 
  *   workspace: ssd_gated_delta_bwd_workspace_bytes bytes, as above.  L = 0 copies d_final
  *   (or zeros) to d_init.
  *
+ * b and H up to 65535; L up to 2^31 - 65; P up to 2^24 - 1 blocks of 64 (N = 16) or 32 rows.
  * Outputs must not overlap inputs, each other or the workspace.  States and all sums are
  * kept in fp32; with bf16 I/O the products run on the bf16 matrix cores, 32-bit operands
  * split into bf16 planes of 8 bits, so states and the gradients da, dbeta and d_init keep

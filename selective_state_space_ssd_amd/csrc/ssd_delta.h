@@ -22,6 +22,7 @@ struct DeltaStepArgs {
 };
 
 bool delta_step_supported_n(int N);
+int delta_step_most_rows(int N);        // the largest P
 hipError_t launch_delta_step(const DeltaStepArgs &a, hipStream_t stream);
 
 // In chunks of 64 tokens on the matrix cores (ssd_delta_chunk.hip): P a multiple of 16, N

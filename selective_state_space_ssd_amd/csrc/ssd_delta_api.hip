@@ -1,4 +1,6 @@
 // ssd_delta_api.hip -- host-side checks and dispatch of the gated delta rule.
+#include <limits.h>
+
 #include "ssd_checks.h"
 #include "ssd_delta.h"
 #include "ssd_kernels.h"
@@ -17,6 +19,9 @@ ssd_status_t check_dims(int b, int L, int H, int P, int N, int G, ssd_dtype_t io
     if (b < 0 || L < 0 || H <= 0 || P <= 0 || N <= 0 || G <= 0) return SSD_ERR_BAD_DIM;
     if (H % G != 0) return SSD_ERR_GROUPS;
     if (!ssd::delta_step_supported_n(N) || H > 65535 || b > 65535) return SSD_ERR_UNSUPPORTED;
+    // the kernels count tokens in 31 bits, up to a chunk past the last one, and a launch's
+    // dimension holds fewer than 2^24 blocks of state rows
+    if (L > INT_MAX - 64 || P > ssd::delta_step_most_rows(N)) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 

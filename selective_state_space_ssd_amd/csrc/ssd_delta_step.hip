@@ -30,6 +30,7 @@ struct StepShape {
     static constexpr int J = N / (4 * LR);             // 4-column chunks per lane
     static constexpr int RW = 64 / LR;                 // rows per wave
     static constexpr int RB = 4 * RW;                  // rows per block
+    static_assert(N == 16 ? RB == 64 : RB == 32);
 };
 
 // Sum over the LR (4 or 8) consecutive lanes of a row.
@@ -156,6 +157,8 @@ hipError_t launch_io(const DeltaStepArgs &a, hipStream_t stream) {
 }  // namespace
 
 bool delta_step_supported_n(int N) { return N == 16 || N == 32 || N == 64 || N == 128 || N == 256; }
+
+int delta_step_most_rows(int N) { return ((1 << 24) - 1) * (N == 16 ? StepShape<16>::RB : StepShape<32>::RB); }
 
 hipError_t launch_delta_step(const DeltaStepArgs &a, hipStream_t stream) {
     return a.bf16 ? launch_io<bf16_bits>(a, stream) : launch_io<float>(a, stream);
