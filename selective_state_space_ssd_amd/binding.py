@@ -532,10 +532,15 @@ def ssd_gated_delta_bwd(q, k, v, a, beta, init_state, dy, d_final, dq, dk, dv, d
              _tensor(d_init, "d_init", st, f32, dev), b, L, H, P, N, G, scale, _io_code(v), ws, ws_bytes)
 
 
+def _rows(x) -> int:
+    """Rows of x [..., D]; 0 for D = 0, which the library refuses."""
+    return x.numel() // x.shape[-1] if x.shape[-1] else 0
+
+
 def ssd_norm_gate_fwd(x, z, w, y, group, eps, gate_first, stream=None) -> None:
     """Enqueue the gated norm of x [..., D] (z like x or None, w [D] float32) into y."""
     D, dev = x.shape[-1], x.device
-    rows = x.numel() // D if D else 0
+    rows = _rows(x)
     _enqueue("ssd_norm_gate_fwd", dev, stream, _tensor(x, "x", x.shape, x.dtype, dev),
              _tensor(z, "z", x.shape, x.dtype, dev), _tensor(w, "w", (D,), torch.float32, dev),
              _tensor(y, "y", x.shape, x.dtype, dev), rows, D, group, eps, 1 if gate_first else 0,
@@ -552,7 +557,7 @@ def ssd_norm_bwd_workspace_bytes(rows, D, group, params, io: int) -> int:
 def ssd_norm_gate_bwd(x, z, w, dy, dx, dz, dw, group, eps, gate_first, workspace, stream=None) -> None:
     """Enqueue the gradients of the gated norm: dx, dz like x (dz None when z is), dw [D]."""
     D, dev, f32 = x.shape[-1], x.device, torch.float32
-    rows = x.numel() // D if D else 0
+    rows = _rows(x)
     ws, ws_bytes = _workspace_arg(workspace, dev)
     _enqueue("ssd_norm_gate_bwd", dev, stream, _tensor(x, "x", x.shape, x.dtype, dev),
              _tensor(z, "z", x.shape, x.dtype, dev), _tensor(w, "w", (D,), f32, dev),
@@ -565,7 +570,7 @@ def ssd_norm_add_fwd(x, residual, scale, w, sum, y, eps, stream=None) -> None:
     """Enqueue sum = residual + scale x and y = its norm times w; x, y [..., D], residual
     and sum of x's shape (float32 or x's type), scale [D] float32 or None, w [D] float32."""
     D, dev, f32 = x.shape[-1], x.device, torch.float32
-    rows = x.numel() // D if D else 0
+    rows = _rows(x)
     _enqueue("ssd_norm_add_fwd", dev, stream, _tensor(x, "x", x.shape, x.dtype, dev),
              _tensor(residual, "residual", x.shape, residual.dtype, dev),
              _tensor(scale, "scale", (D,), f32, dev), _tensor(w, "w", (D,), f32, dev),
@@ -579,7 +584,7 @@ def ssd_norm_add_bwd(x, sum, scale, w, dy, d_sum, dx, d_residual, d_scale, dw, e
     None without scale."""
     D, dev, f32, res = dy.shape[-1], dy.device, torch.float32, sum.dtype
     shape, io = dy.shape, dy.dtype
-    rows = dy.numel() // D if D else 0
+    rows = _rows(dy)
     ws, ws_bytes = _workspace_arg(workspace, dev)
     _enqueue("ssd_norm_add_bwd", dev, stream, _tensor(x, "x", shape, io, dev),
              _tensor(sum, "sum", shape, res, dev), _tensor(scale, "scale", (D,), f32, dev),
@@ -721,7 +726,7 @@ def norm_gate_bwd(x, z, w, dy, group, eps, gate_first=False, workspace=None, str
     with _allocating_on(stream):
         dx, dz, dw = torch.empty_like(x), None if z is None else torch.empty_like(z), torch.empty_like(w)
         if workspace is None:
-            workspace = _scratch(ssd_norm_bwd_workspace_bytes(x.numel() // D, D, group, 1, _io_code(x)), x.device)
+            workspace = _scratch(ssd_norm_bwd_workspace_bytes(_rows(x), D, group, 1, _io_code(x)), x.device)
     ssd_norm_gate_bwd(x, z, w, dy, dx, dz, dw, group, eps, gate_first, workspace, stream)
     return dx, dz, dw
 
@@ -742,7 +747,7 @@ def norm_add_bwd(x, sum, w, dy, d_sum, eps, scale=None, workspace=None, stream=N
         dx, d_res, dw = torch.empty_like(dy), torch.empty_like(sum), torch.empty_like(w)
         d_scale = None if scale is None else torch.empty_like(scale)
         if workspace is None:
-            n = ssd_norm_bwd_workspace_bytes(dy.numel() // D, D, D, 1 if scale is None else 2, _io_code(dy))
+            n = ssd_norm_bwd_workspace_bytes(_rows(dy), D, D, 1 if scale is None else 2, _io_code(dy))
             workspace = _scratch(n, dy.device)
     ssd_norm_add_bwd(x, sum, scale, w, dy, d_sum, dx, d_res, d_scale, dw, eps, workspace, stream)
     return dx, d_res, dw, d_scale
