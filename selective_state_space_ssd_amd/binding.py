@@ -673,12 +673,13 @@ def selective_scan_fwd(x, dt, A, B, C, D, init_state=None, stream=None):
     return y, final_state
 
 
-def gated_delta_step(state, q, k, v, a, beta, scale, accept_len=None, stream=None):
+def gated_delta_step(state, q, k, v, a, beta, scale, accept_len=None, stream=None, err_flag=None):
     """Allocate the outputs; returns (y, state_out): y for all K tokens, the state after
-    accept_len [b] of them (None: after all)."""
+    accept_len [b] of them (None: after all).  Counts outside [0, K] are clamped and set
+    err_flag (int32, on the GPU), if there is one, to 1."""
     with _allocating_on(stream):
         y, state_out = torch.empty_like(v), torch.empty_like(state)
-    ssd_gated_delta_step(state, q, k, v, a, beta, accept_len, y, state_out, scale, stream=stream)
+    ssd_gated_delta_step(state, q, k, v, a, beta, accept_len, y, state_out, scale, err_flag, stream)
     return y, state_out
 
 
