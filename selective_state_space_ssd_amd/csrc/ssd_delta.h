@@ -78,7 +78,6 @@ struct DeltaBwdArgs {
 
 // The workspace begins with the chunk images; byte offsets of what follows.
 struct DeltaBwdPlan {
-    bool supported = false;
     size_t off_e = 0, off_x = 0, off_s = 0, off_ds = 0;
     DeltaCut cut;
     size_t off_map = 0, off_init = 0, off_dmap = 0, off_dinit = 0;      // of the segments, and of their gradients

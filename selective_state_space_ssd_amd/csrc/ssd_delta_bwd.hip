@@ -853,7 +853,6 @@ DeltaBwdPlan plan_delta_bwd(int b, int L, int H, int P, int N, int G, bool bf16)
     pl.off_parts = take(pl.splits > 1 ? size_t(pl.splits) * 2 * b * L * G * N * 4 : 0);
     pl.off_gate_parts = take(pl.splits * cols > 1 ? size_t(pl.splits > 1 ? grad_turns(P) : 1) * cols * 2 * b * L * H * 4 : 0);
     pl.total = at;
-    pl.supported = true;
     return pl;
 }
 

@@ -215,7 +215,8 @@ __device__ __forceinline__ Op<IO, NP> read_col(const char *tile, int stride, int
 // in assembly because the compiler waits for every such copy at the next LDS read,
 // whichever buffer that reads; here the copy into the other buffer stays in flight until
 // copies_done().  It has no output register; the wait states cover an M0 or an address
-// pair written just before.
+// pair written just before.  M0 is a reserved register, which a list of clobbers cannot
+// name: nothing else in the kernels that copy this way uses it.
 __device__ __forceinline__ void copy16(const void *base, uint32_t off, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
                  :: "s"(dst), "v"(off), "s"(base) : "memory");

@@ -15,9 +15,9 @@
 // registers between the sum of squares and its use.  A team of TPS lanes holds one
 // segment, NV vectors of VEC channels a lane (VEC elements = 16 bytes); teams of 16
 // lanes serve the short groups of a per-head norm, one wave or one block the whole rows
-// of a layer.  Segments that no team holds, or whose length or address does not divide
-// into vectors, take VEC = 1 teams, and beyond those the loop kernels, which read the
-// segment twice.
+// of a layer.  Segments whose length does not divide into vectors take VEC = 1 teams (all
+// arrays are 16-byte aligned), and those that no team of their kind holds the loop kernels,
+// which read the segment twice.
 //
 // Bound by the bytes: gate backward of 8192 x 4096, groups of 128, bf16 (336 MB) 70 us, 4.8
 // TB/s; residual sum and norm of 8192 x 2560, bf16 with an fp32 residual (252 MB) 51 us, 4.9
@@ -50,10 +50,8 @@ __device__ __forceinline__ void load_vec(const IO *p, float (&f)[VEC]) {
             const float4 u = *reinterpret_cast<const float4 *>(p + 4);
             f[4] = u.x; f[5] = u.y; f[6] = u.z; f[7] = u.w;
         }
-    } else if constexpr (VEC == 4) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
     } else {
+        static_assert(VEC == 8);
         const uint4 v = *reinterpret_cast<const uint4 *>(p);
         f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
         f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
@@ -67,9 +65,8 @@ __device__ __forceinline__ void store_vec(IO *p, const float (&f)[VEC]) {
     } else if constexpr (std::is_same_v<IO, float>) {
         *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
         if constexpr (VEC == 8) *reinterpret_cast<float4 *>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
-    } else if constexpr (VEC == 4) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
     } else {
+        static_assert(VEC == 8);
         *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                                    pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
     }
