@@ -480,9 +480,11 @@ ssd_status_t ssd_chunk_scan_bwd(const void *x, const float *dt, const float *A, 
  * Outputs must not overlap inputs, each other or the workspace.  States and all sums are
  * kept in fp32; with bf16 I/O the products run on the bf16 matrix cores, 32-bit operands
  * split into bf16 planes of 8 bits, so states and the gradients da, dbeta and d_init keep
- * fp32 accuracy.  Every output is rounded once.  A NaN or an infinity reaches every output
- * that depends on it; inside its chunk of 64 tokens and its head it may also reach the
- * outputs of earlier tokens.  Errors as for the other entry points.
+ * fp32 accuracy.  Every output is rounded once.  In ssd_gated_delta_step and
+ * ssd_gated_delta_fwd a NaN or an infinity reaches every output that depends on it (an infinity
+ * as a NaN, it may be) and no other: none of earlier tokens.  In ssd_gated_delta_bwd it may
+ * reach all gradients of its chunk of 64 tokens, and of what depends on those.  Errors as for
+ * the other entry points.
  */
 ssd_status_t ssd_gated_delta_step(const float *state_in, const void *q, const void *k,
                                   const void *v, const float *a, const float *beta,

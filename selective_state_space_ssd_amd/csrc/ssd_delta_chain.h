@@ -104,6 +104,35 @@ __device__ __forceinline__ void sum_of_parts(const char *first, int lane, f32x4 
     }
 }
 
+// The first token of a chunk with a value that is not finite among this lane's column (p),
+// kC if there is none; the values from there on become 0.  A matrix product multiplies the
+// zeros above a triangle too: with them, such a value would reach the tokens before it.
+__device__ __forceinline__ int stop_at(f32x4 (&v)[4], int q) {
+    int first = kC;
+#pragma unroll
+    for (int t = 3; t >= 0; --t)
+#pragma unroll
+        for (int r = 3; r >= 0; --r)
+            if (!__builtin_isfinite(v[t][r])) first = 32 * (t >> 1) + 8 * q + 4 * (t & 1) + r;
+    first = min(first, __shfl_xor(first, 16, 64));
+    first = min(first, __shfl_xor(first, 32, 64));
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (32 * (t >> 1) + 8 * q + 4 * (t & 1) + r >= first) v[t][r] = 0.f;
+    return first;
+}
+
+// `other` from token `first` on.
+__device__ __forceinline__ void from_token(f32x4 (&v)[4], int first, int q, float other) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (32 * (t >> 1) + 8 * q + 4 * (t & 1) + r >= first) v[t][r] = other;
+}
+
 // What bounds it: one wave's steps, not the matrix cores.  A chunk of a bf16 tile at N = 128
 // is 216 matrix instructions (3500 cycles) and 7500 cycles in between, of which splitting
 // values into planes and the accumulators' scaling issue for 4000; the waves of the only
@@ -275,9 +304,20 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
         if (live) {
             if constexpr (X > 1) sum_of_parts<X>(lds + T::kE + (w - x) * 4096, lane, E);
             // E = R + M (beta R), U = beta E
+            f32x4 B[4];
+            float probe = 0.f;      // NaN if any value is not finite
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                B[t] = gate_of(2, t) * E[t];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) probe = __builtin_fmaf(B[t][r], 0.f, probe);
+            }
+            const bool stop = __any(probe != probe);    // of the whole wave
+            int bad = kC;
+            if (stop) bad = stop_at(B, q);
             Op<IO, kPlanes> br[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) br[s] = to_op<IO, kPlanes>(gate_of(2, 2 * s) * E[2 * s], gate_of(2, 2 * s + 1) * E[2 * s + 1]);
+            for (int s = 0; s < 2; ++s) br[s] = to_op<IO, kPlanes>(B[2 * s], B[2 * s + 1]);
             {
                 Op<IO, kPlanes> a[4];
 #pragma unroll
@@ -293,14 +333,16 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                 E[2] = lower[0];
                 E[3] = lower[1];
             }
+            if (stop) from_token(E, bad, q, __builtin_nanf(""));
             Op<IO, kPlanes> uy[2];
             Op<IO, kPlanes> ud[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const f32x4 u0 = gate_of(2, 2 * s) * E[2 * s], u1 = gate_of(2, 2 * s + 1) * E[2 * s + 1];
-                ud[s] = to_op<IO, kPlanes>(gate_of(1, 2 * s) * u0, gate_of(1, 2 * s + 1) * u1);
-                uy[s] = to_op<IO, kPlanes>(u0, u1);
-            }
+            for (int t = 0; t < 4; ++t) B[t] = gate_of(2, t) * E[t];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) ud[s] = to_op<IO, kPlanes>(gate_of(1, 2 * s) * B[2 * s], gate_of(1, 2 * s + 1) * B[2 * s + 1]);
+            if (RUN && stop) from_token(B, bad, q, 0.f);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) uy[s] = to_op<IO, kPlanes>(B[2 * s], B[2 * s + 1]);
             ahead(std::integral_constant<int, 2>{});
             // S <- e^{g_C} S + K^T (e^{g_C - g} U)
             const float alpha = gates[kC - 1];
@@ -341,6 +383,10 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                     const Op<IO, kPlanes> a[1] = {tri_row<IO, kPlanes>(ts, t >> 1, t & 1, ks, c, q)};
                     mma(z, uy[ks], a);
                 }
+                if (stop)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)     // rows p in registers
+                        if (tile_row(t >> 1, t & 1, c) >= __shfl(bad, 4 * q + r, 64)) z[0][r] = __builtin_nanf("");
                 yo[t] = narrow<IO>(z[0]);
             }
         } else {

@@ -59,6 +59,10 @@ __device__ __forceinline__ void write_image(const float *m, char *dst, int first
     }
 }
 
+// The summed operand of a block product: what is not finite belongs to a row that the rows
+// before it have zeros for, and a product with 0 has to be 0.
+__device__ __forceinline__ float finite_or_0(float v) { return __builtin_isfinite(v) ? v : 0.f; }
+
 // Heads of a group that one block takes, sharing the products of the group's keys.
 constexpr int kPrepHeads = 4;
 
@@ -193,7 +197,7 @@ __global__ __launch_bounds__(256, 4) void k_delta_prep(const IO *__restrict__ qg
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int k = r0 + 4 * q + i;
-                z = mfma_f32(mm[(r0 + c) * kLd + k], sb[k] * y[i], z);
+                z = mfma_f32(mm[(r0 + c) * kLd + k], finite_or_0(sb[k] * y[i]), z);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) mm[(r0 + 4 * q + i) * kLd + c0 + c] = -z[i];
@@ -216,7 +220,7 @@ __global__ __launch_bounds__(256, 4) void k_delta_prep(const IO *__restrict__ qg
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
                 const int k = 4 * t + q;
-                z = mfma_f32(mm[(r0 + c) * kLd + 32 + k], sb[32 + k] * yt[k * 33 + c0 + c], z);
+                z = mfma_f32(mm[(r0 + c) * kLd + 32 + k], finite_or_0(sb[32 + k] * yt[k * 33 + c0 + c]), z);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) mm[(r0 + 4 * q + i) * kLd + c0 + c] = -z[i];
