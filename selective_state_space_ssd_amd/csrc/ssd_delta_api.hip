@@ -27,10 +27,10 @@ ssd_status_t check_dims(int b, int L, int H, int P, int N, int G, ssd_dtype_t io
 
 // Sequences up to this length go token by token, in one launch that keeps no workspace.
 // Both sides, us, token by token / in chunks, at P = 64 and one group:
-//   bf16, N = 64:   32 x 80 heads, 24 tokens 84 / 94, 32 tokens 105 / 96;  8 heads, 24 tokens 19 / 26
-//   bf16, N = 128:  32 x 80 heads, 24 tokens 110 / 119, 32 tokens 136 / 127;  8 heads, 32 tokens 23 / 25
-//   fp32, N = 64:   32 x 80 heads, 32 tokens 92 / 135, 48 tokens 130 / 138;  8 heads, 32 tokens 19 / 25, 64 tokens 31 / 26
-//   fp32, N = 128:  32 x 80 heads, 32 tokens 139 / 242;  8 heads, 32 tokens 21 / 26, 48 tokens 29 / 26
+//   bf16, N = 64:   32 x 80 heads, 16 tokens 53 / 73, 24 tokens 85 / 71;  8 heads, 24 tokens 16 / 20, 32 tokens 21 / 21
+//   bf16, N = 128:  32 x 80 heads, 16 tokens 78 / 96, 24 tokens 108 / 95;  8 heads, 24 tokens 19 / 20, 32 tokens 23 / 20
+//   fp32, N = 64:   32 x 80 heads, 32 tokens 91 / 102, 48 tokens 130 / 105;  8 heads, 32 tokens 17 / 20, 48 tokens 24 / 20
+//   fp32, N = 128:  32 x 80 heads, 32 tokens 136 / 241;  8 heads, 32 tokens 21 / 20, 48 tokens 30 / 20
 int most_by_token(ssd_dtype_t io) { return io == SSD_DTYPE_BF16 ? 24 : 32; }
 
 // The chunked path of a sequence, unless it is short or no chunk kernel runs its shape.

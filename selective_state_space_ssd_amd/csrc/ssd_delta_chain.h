@@ -434,21 +434,24 @@ constexpr int kSimds = 1024;
 // (the chain waits for its own results, so that two waves on a SIMD cost one of them little,
 // but more waves than SIMDs cost every block its exchange).  512 tokens, one group, waves per
 // tile before -> after, us of the backward pass at 128, 256, 384, 512 and 640 tiles:
-//   bf16, N = 64,  1 -> 2:  256 -> 247, 424 -> 417, 592 -> 584, 761 -> 754, 933 -> 986
-//   fp32, N = 64,  1 -> 2:  470 -> 436, 792 -> 758, 1114 -> 1082, 1441 -> 1408, 1762 -> 1817
-//   bf16, N = 128, 1 -> 2:  302 -> 287, 494 -> 482, 688 -> 672, 884 -> 872, 1077 -> 1133
-//   bf16, N = 128, 1 -> 4:  302 -> 280, 494 -> 472, 688 -> 726
-// and of the forward pass with one tile per block (4, 4) for two (8, 4):
-//   fp32, N = 128:  76 -> 58, 86 -> 69, 94 -> 112;   bf16, N = 256:  60 -> 49, 70 -> 59, 78 -> 94
+//   bf16, N = 64,  1 -> 2:  86 -> 85, 101 -> 94, 112 -> 105, 124 -> 115, 136 -> 158
+//   fp32, N = 64,  1 -> 2:  115 -> 107, 159 -> 136, 177 -> 154, 193 -> 170, 211 -> 241
+//   bf16, N = 128, 1 -> 2:  117 -> 105, 132 -> 118, 145 -> 132, 159 -> 147, 173 -> 215
+//   bf16, N = 128, 1 -> 4:  117 -> 100, 132 -> 111, 145 -> 173
+// and with one tile per block (4, 4) for two (8, 4) at 128, 256 and 384 tiles:
+//   fp32, N = 128:  177 -> 145, 217 -> 186, 258 -> 299;   bf16, N = 256:  148 -> 128, 184 -> 165, 220 -> 260
+// The forward pass goes the same way (bf16, N = 128, 512 tiles: 70 -> 63, 640: 76 -> 98).
 //
 // With more tiles than SIMDs, one chunk's buffer instead of two lets a second block onto a CU,
 // whose waves fill the waits, where the registers allow it too (the backward pass of wide
 // rows has none).  2048 tokens, two buffers -> one, us at 1024, 1280, 2048 and 4096 tiles:
-//   bf16, N = 64,  backward:  520 -> 557, 843 -> 730, 1000 -> 908, 1926 -> 1764
-//   bf16, N = 128, forward:   172 -> 184, 308 -> 271, 349 -> 329, 680 -> 627
-//   fp32, N = 64,  forward:   251 -> 272, 462 -> 392, 486 -> 430, 961 -> 840
-//   fp32, N = 64,  backward:  977 -> 1065, 1603 -> 1650, 1947 -> 2010, 3852 -> 4000 (not done)
-//   bf16, N = 32,  forward:   130 -> 132, 187 -> 190, 230 -> 234, 445 -> 454 (two blocks fit as it is)
+//   bf16, N = 32,  forward:   205 -> 226, 301 -> 281, 406 -> 395, 729 -> 743
+//   bf16, N = 64,  forward:   218 -> 240, 331 -> 320, 419 -> 405, 795 -> 760
+//   bf16, N = 64,  backward:  669 -> 691, 934 -> 902, 1309 -> 1293, 2547 -> 2571
+//   bf16, N = 128, forward:   253 -> 277, 410 -> 383, 513 -> 470, 968 -> 901
+//   bf16, N = 128, backward:  842 -> 900, 1210 -> 1189, 1643 -> 1645, 3222 -> 3223 (not done)
+//   fp32, N = 64,  forward:   312 -> 338, 522 -> 453, 576 -> 515, 1131 -> 1001
+//   fp32, N = 64,  backward:  973 -> 1042, 1425 -> 1341, 1853 -> 1774, 3685 -> 3560 (not done)
 template <typename IO, int N, bool BACK, class F>
 hipError_t with_chain_shape(int64_t tiles, F &&f) {
     using std::integral_constant;
