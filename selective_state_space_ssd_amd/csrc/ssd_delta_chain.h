@@ -86,6 +86,13 @@ __device__ __forceinline__ Raw4<IO> narrow(f32x4 v) {
     else return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
+// Element r becomes a NaN.
+template <typename IO>
+__device__ __forceinline__ void set_nan(Raw4<IO> &v, int r) {
+    if constexpr (std::is_same_v<IO, float>) v[r] = __builtin_nanf("");
+    else v[r >> 1] |= 0x7fffu << (16 * (r & 1));
+}
+
 // A range-checked view of one chunk of a [b, L, H, P] tensor, from its first token's row of
 // head h on (`base`), `rows` tokens.
 template <typename IO>
@@ -105,9 +112,9 @@ __device__ __forceinline__ void sum_of_parts(const char *first, int lane, f32x4 
 }
 
 // The first token of a chunk with a value that is not finite among this lane's column (p),
-// kC if there is none; the values from there on become 0.  A matrix product multiplies the
-// zeros above a triangle too: with them, such a value would reach the tokens before it.
-__device__ __forceinline__ int stop_at(f32x4 (&v)[4], int q) {
+// kC if there is none; v and w become 0 from there on.  A matrix product multiplies the zeros
+// above a triangle too: with them, such a value would reach the tokens before it.
+__device__ __forceinline__ int stop_at(f32x4 (&v)[4], f32x4 (&w)[4], int q) {
     int first = kC;
 #pragma unroll
     for (int t = 3; t >= 0; --t)
@@ -120,17 +127,8 @@ __device__ __forceinline__ int stop_at(f32x4 (&v)[4], int q) {
     for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            if (32 * (t >> 1) + 8 * q + 4 * (t & 1) + r >= first) v[t][r] = 0.f;
+            if (32 * (t >> 1) + 8 * q + 4 * (t & 1) + r >= first) v[t][r] = w[t][r] = 0.f;
     return first;
-}
-
-// `other` from token `first` on.
-__device__ __forceinline__ void from_token(f32x4 (&v)[4], int first, int q, float other) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (32 * (t >> 1) + 8 * q + 4 * (t & 1) + r >= first) v[t][r] = other;
 }
 
 // What bounds it: one wave's steps, not the matrix cores.  A chunk of a bf16 tile at N = 128
@@ -254,6 +252,8 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
         };
         Raw4<IO> yo[4];
         f32x4 E[4], Y[4];
+        bool stop = false;      // the same for a whole wave
+        int bad = kC;
         fetch_v(next);
         ahead(std::integral_constant<int, 0>{});
         if (live) {
@@ -305,16 +305,16 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
             if constexpr (X > 1) sum_of_parts<X>(lds + T::kE + (w - x) * 4096, lane, E);
             // E = R + M (beta R), U = beta E
             f32x4 B[4];
-            float probe = 0.f;      // NaN if any value is not finite
+            f32x4 probe = {0.f, 0.f, 0.f, 0.f};     // NaN if any bracket is not finite
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 B[t] = gate_of(2, t) * E[t];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) probe = __builtin_fmaf(B[t][r], 0.f, probe);
+                for (int r = 0; r < 4; ++r) probe[r] = __builtin_fmaf(E[t][r], 0.f, probe[r]);
             }
-            const bool stop = __any(probe != probe);    // of the whole wave
-            int bad = kC;
-            if (stop) bad = stop_at(B, q);
+            const float any = (probe[0] + probe[1]) + (probe[2] + probe[3]);
+            stop = __any(any != any);
+            if (stop) bad = stop_at(E, B, q);
             Op<IO, kPlanes> br[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) br[s] = to_op<IO, kPlanes>(B[2 * s], B[2 * s + 1]);
@@ -333,16 +333,14 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                 E[2] = lower[0];
                 E[3] = lower[1];
             }
-            if (stop) from_token(E, bad, q, __builtin_nanf(""));
             Op<IO, kPlanes> uy[2];
             Op<IO, kPlanes> ud[2];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) B[t] = gate_of(2, t) * E[t];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) ud[s] = to_op<IO, kPlanes>(gate_of(1, 2 * s) * B[2 * s], gate_of(1, 2 * s + 1) * B[2 * s + 1]);
-            if (RUN && stop) from_token(B, bad, q, 0.f);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) uy[s] = to_op<IO, kPlanes>(B[2 * s], B[2 * s + 1]);
+            for (int s = 0; s < 2; ++s) {
+                const f32x4 u0 = gate_of(2, 2 * s) * E[2 * s], u1 = gate_of(2, 2 * s + 1) * E[2 * s + 1];
+                ud[s] = to_op<IO, kPlanes>(gate_of(1, 2 * s) * u0, gate_of(1, 2 * s + 1) * u1);
+                uy[s] = to_op<IO, kPlanes>(u0, u1);
+            }
             ahead(std::integral_constant<int, 2>{});
             // S <- e^{g_C} S + K^T (e^{g_C - g} U)
             const float alpha = gates[kC - 1];
@@ -383,11 +381,21 @@ __global__ __launch_bounds__(64 * W) void k_delta_chain(const IO *__restrict__ q
                     const Op<IO, kPlanes> a[1] = {tri_row<IO, kPlanes>(ts, t >> 1, t & 1, ks, c, q)};
                     mma(z, uy[ks], a);
                 }
-                if (stop)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)     // rows p in registers
-                        if (tile_row(t >> 1, t & 1, c) >= __shfl(bad, 4 * q + r, 64)) z[0][r] = __builtin_nanf("");
                 yo[t] = narrow<IO>(z[0]);
+            }
+            if (stop) {     // NaN from that token on, and in the row's state
+                const float nan = __builtin_nanf("");
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (bad < kC) S[t] = f32x4{nan, nan, nan, nan};
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        if (32 * (t >> 1) + 8 * q + 4 * (t & 1) + r >= bad) E[t][r] = nan;
+                        if constexpr (RUN)      // y: rows p in registers, 4 q + r
+                            if (tile_row(t >> 1, t & 1, c) >= __shfl(bad, 4 * q + r, 64)) set_nan<IO>(yo[t], r);
+                    }
             }
         } else {
             ahead(std::integral_constant<int, 2>{});

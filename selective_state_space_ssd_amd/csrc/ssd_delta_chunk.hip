@@ -2,7 +2,6 @@
 // depend on the state for all chunks (ssd_delta_prep.h), then the chain over the chunks
 // (ssd_delta_chain.h).
 #include <algorithm>
-#include <cmath>
 
 #include "ssd_delta.h"
 #include "ssd_delta_chain.h"
@@ -37,27 +36,27 @@ hipError_t launch_n(const DeltaChunkArgs &a, const DeltaChunkPlan &pl, hipStream
 // enters it, but all segments run at once.  The cut is the cheapest by the measured cost of a
 // chunk, in units of one step of a chain that has its SIMD to itself (3.4 us in bf16, N =
 // 128).  One segment -> this rule -> the best of 1, 2, 3, 4, 5, 6, 8, 11, 16, 24, 32, 64, us, b = 1:
-//   bf16, P = N = 128:  3 heads, 4096 tokens 219 -> 84 -> 84, 16384: 815 -> 166 -> 165;
-//                       32 heads, 4096: 235 -> 193 -> 193, 16384: 899 -> 636 -> 636
-//   fp32, P = N = 64:   24 heads, 1600 tokens 146 -> 85 -> 84, 16384: 1252 -> 455 -> 414
-// and over 360 shapes of 1 to 64 heads and 256 to 16384 tokens 1.02 times as long as that best
-// in the mean, 1.21 times at the most.  Backward, 144 shapes: 1.01, 1.15 at the most;
-//   bf16, P = 64, N = 128:  24 heads, 2048 tokens 259 -> 200 -> 200, 6000: 715 -> 434 -> 434
-//   fp32, P = N = 64:   4 heads, 777 tokens 154 -> 115 -> 115, 6000: 837 -> 190 -> 189
-// The two have prices of their own: more tiles than SIMDs go in whole rounds backward, forward
-// two blocks a CU cover for each other (with_chain_shape).
+//   bf16, P = N = 128:  3 heads, 4096 tokens 210 -> 85 -> 83, 16384: 788 -> 161 -> 168;
+//                       32 heads, 4096: 227 -> 192 -> 191, 16384: 874 -> 664 -> 631
+//   fp32, P = N = 64:   24 heads, 1600 tokens 139 -> 85 -> 83, 16384: 1186 -> 432 -> 436
+// and over 432 shapes of 1 to 192 heads and 256 to 16384 tokens 1.01 times as long as that best
+// in the mean, 1.22 times at the most.  Backward, 216 shapes: 1.01, 1.14 at the most;
+//   bf16, P = 64, N = 128:  24 heads, 2048 tokens 256 -> 200 -> 199, 6000: 712 -> 435 -> 436
+//   fp32, P = N = 64:   4 heads, 777 tokens 152 -> 113 -> 112, 6000: 839 -> 190 -> 187
+// More tiles than SIMDs go in rounds, forward cheaper ones, where two blocks a CU cover for
+// each other (with_chain_shape).
 DeltaCut cut_sequence(int64_t bh, int nc, int P, int N, bool bf16, bool back) {
     const bool wide = N * (bf16 ? 2 : 4) > 256;     // blocks of 8 waves for 2 tiles
     auto step = [&](int64_t tiles) {
-        const double rounds = double(tiles) / (wide ? kSimds / 2 : kSimds);
-        if (wide) return tiles <= kSimds / 4 ? 1.0 : back ? 1.75 * std::ceil(rounds) : rounds <= 1.0 ? 1.3 : std::max(2.4, 1.4 * rounds);
-        return tiles <= kSimds / 4 ? back ? 0.85 : 0.8 : back ? std::ceil(rounds) : rounds <= 1.0 ? 1.0 : std::max(1.6, 0.8 * rounds);
+        if (wide) return tiles <= kSimds / 4 ? 1.0 : 1.5 * double((tiles + kSimds / 2 - 1) / (kSimds / 2));
+        if (tiles <= kSimds / 2) return tiles <= kSimds / 4 ? 0.8 : 0.85;       // shared by waves
+        return tiles <= kSimds ? 1.0 : (back ? 1.0 : 0.85) * double((tiles + kSimds - 1) / kSimds);
     };
     const double carry = N == 256 ? 1.5 : N == 128 ? 0.35 : 0.2, launches = 2.0;
     DeltaCut best{1, nc};
     // a map costs a little less than a run; backward: a chain each way, and the chain back over
     // zeros for its map
-    const double passes = back ? 2.0 : 1.0, extra = back ? 0.8 : 0.0, map = back ? 0.8 : 0.7;
+    const double passes = back ? 2.0 : 1.0, extra = back ? 0.8 : 0.0, map = 0.75;
     double least = 0.95 * nc * passes * step(bh * (P / 16));      // no cut for less than a twentieth
     for (int s = 2; s <= std::min(nc / 2, 64); ++s) {
         const int per = (nc + s - 1) / s;

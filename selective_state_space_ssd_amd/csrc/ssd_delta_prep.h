@@ -35,10 +35,14 @@ __device__ __forceinline__ Op<IO, 1> load_row8(const IO *p) {
     return o;
 }
 
+// A value that is not finite comes from a token that spoils all after it, whatever stands
+// here, and none before: where it meets the zeros of a triangle it counts as 0.
+__device__ __forceinline__ float finite_or_0(float v) { return __builtin_isfinite(v) ? v : 0.f; }
+
 // Copy an fp32 lower triangular [64][64] matrix from LDS into its image: NP planes,
 // 16-byte chunks placed as the chain's LDS tiles hold them; by `threads` threads, this one
-// the `first`.
-template <typename IO, int NP>
+// the `first`.  FINITE: see finite_or_0.
+template <typename IO, int NP, bool FINITE>
 __device__ __forceinline__ void write_image(const float *m, char *dst, int first, int threads) {
     using Img = ChunkImage<IO>;
     constexpr int kRowTop = 32 * Img::kSz, kRow = 64 * Img::kSz, E = 16 / Img::kSz;
@@ -48,20 +52,23 @@ __device__ __forceinline__ void write_image(const float *m, char *dst, int first
         const int r = at / per_row, pos = at % per_row;
         const int col = (pos ^ (top ? place<kRowTop>(r) : place<kRow>(r))) * E;
         const float *s = m + (top ? r : 32 + r) * kLd + col;
+        auto four = [&](int e) {
+            f32x4 v = *reinterpret_cast<const f32x4 *>(s + 4 * e);
+            if constexpr (FINITE)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = finite_or_0(v[j]);
+            return v;
+        };
         if constexpr (std::is_same_v<IO, float>) {
-            *reinterpret_cast<f32x4 *>(dst + i * 16) = *reinterpret_cast<const f32x4 *>(s);
+            *reinterpret_cast<f32x4 *>(dst + i * 16) = four(0);
         } else {
-            const Op<IO, NP> o = to_op<IO, NP>(*reinterpret_cast<const f32x4 *>(s), *reinterpret_cast<const f32x4 *>(s + 4));
+            const Op<IO, NP> o = to_op<IO, NP>(four(0), four(1));
 #pragma unroll
             for (int p = 0; p < NP; ++p)
                 *reinterpret_cast<uint4 *>(dst + p * Img::kPlane + i * 16) = __builtin_bit_cast(uint4, o.p[p]);
         }
     }
 }
-
-// The summed operand of a block product: what is not finite belongs to a row that the rows
-// before it have zeros for, and a product with 0 has to be 0.
-__device__ __forceinline__ float finite_or_0(float v) { return __builtin_isfinite(v) ? v : 0.f; }
 
 // Heads of a group that one block takes, sharing the products of the group's keys.
 constexpr int kPrepHeads = 4;
@@ -94,12 +101,14 @@ __global__ __launch_bounds__(256, 4) void k_delta_prep(const IO *__restrict__ qg
             if (lane >= off) s += o;
         }
         const double end = __shfl(s, 63, 64);
+        // a beta that is not finite counts as 0 and makes e^g a NaN: the token's bracket is one then
+        const bool ok = __builtin_isfinite(bt);
         gd[w][lane] = s * kPerLn2;
-        sbs[w][lane] = bt;
+        sbs[w][lane] = ok ? bt : 0.f;
         float *gates = reinterpret_cast<float *>(image(w) + Img::kGates);
-        gates[lane] = expf(float(s));
+        gates[lane] = ok ? expf(float(s)) : __builtin_nanf("");
         gates[kC + lane] = expf(float(end - s));
-        gates[2 * kC + lane] = bt;
+        gates[2 * kC + lane] = ok ? bt : 0.f;
     }
     // wave w: row tile w of k k^T and row tile 3 - w of q k^T, up to the diagonal (5 tiles)
     f32x4 kk[4], qk[4];
@@ -159,7 +168,7 @@ __global__ __launch_bounds__(256, 4) void k_delta_prep(const IO *__restrict__ qg
         }
         __syncthreads();
         if (w > 0) {    // the other waves write the scores out meanwhile
-            write_image<IO, kPlanes>(sc, img + Img::kQ, tid - 64, 192);
+            write_image<IO, kPlanes, false>(sc, img + Img::kQ, tid - 64, 192);
         } else {        // diagonal blocks of 16, lane = (block q, column c): each row found
                         // is taken out of all later ones
             float *l0 = mm + 16 * q * kLd + 16 * q;
@@ -226,7 +235,7 @@ __global__ __launch_bounds__(256, 4) void k_delta_prep(const IO *__restrict__ qg
             for (int i = 0; i < 4; ++i) mm[(r0 + 4 * q + i) * kLd + c0 + c] = -z[i];
         }
         __syncthreads();
-        write_image<IO, kPlanes>(mm, img + Img::kM, tid, 256);
+        write_image<IO, kPlanes, true>(mm, img + Img::kM, tid, 256);
     }
 }
 
