@@ -23,13 +23,14 @@
 // 2 and 3 are chains over the chunks whose waves keep 16 rows of the state each, as in the
 // forward pass: 32-bit values throughout.
 //
-// 4 x 2048 tokens, 32 heads of 128 x 128, bf16, us: prep 46, chain 150, chain back 218, grads
-// 300.  The chains are bound by a wave's steps (ssd_delta_chain.h) and write 805 MB (both
-// states, E and X, in 32 bits).  grads reads 870 MB at 2.9 TB/s, for which it is not waiting
-// (every state from the caches: 265): a wave issues vector instructions 22 % of the time (a
-// third of them splits values into planes), its SIMD's matrix unit is busy 23 %, and two
-// waves a SIMD, all that the registers allow, leave gaps at LDS reads, barriers and the ends
-// of heads (a head's gates take 30 us of the 300, a block's beginning and end 35).  With the
+// 4 x 2048 tokens, 32 heads of 128 x 128, bf16: 710 us a call; in calls back to back prep
+// 46, chain 150, chain back 218, grads 300 (under a trace 46, 161, 231, 368).  The chains
+// are bound by a wave's steps (ssd_delta_chain.h) and write 805 MB (both states, E and X,
+// in 32 bits).  grads reads 870 MB at 2.9 TB/s, for which it is not waiting (every state
+// from the caches: 265): a wave issues vector instructions 22 % of the time (a third of
+// them splits values into planes), its SIMD's matrix unit is busy 23 %, and two waves a
+// SIMD, all that the registers allow, leave gaps at LDS reads, barriers and the ends of
+// heads (a head's gates take 30 us of the 300, a block's beginning and end 35).  With the
 // states' planes in LDS, shared by all waves, it is the same time.
 #include <algorithm>
 

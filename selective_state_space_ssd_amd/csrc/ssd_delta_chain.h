@@ -132,13 +132,12 @@ __device__ __forceinline__ int stop_at(f32x4 (&v)[4], f32x4 (&w)[4], int q) {
 }
 
 // What bounds it: one wave's steps, not the matrix cores.  A chunk of a bf16 tile at N = 128
-// is 216 matrix instructions (3500 cycles) and 7500 cycles in between, of which splitting
-// values into planes and the accumulators' scaling issue for 4000; the waves of the only
+// is 216 matrix instructions (3500 cycles) and 7400 cycles in between, of which splitting
+// values into planes and the accumulators' scaling issue for 3300; the waves of the only
 // block that fits a CU find nobody to fill the rest.  4 x 2048 tokens, 32 heads of 128 x 128,
-// a wave on every SIMD: 141 us for 32 chunks in turn, 168 MB of inputs and outputs; without
-// its copies (a timing build) 115.  Tried without gain on that: 8 waves in lockstep, copies in
-// two groups with half a chunk each to arrive, products interleaved by hand, two blocks a CU
-// (spills).
+// a wave on every SIMD: 168 us for 32 chunks in turn, 168 MB of inputs and outputs.  Tried
+// without gain on an earlier, 141 us form: 8 waves in lockstep, copies in two groups with half
+// a chunk each to arrive, products interleaved by hand, two blocks a CU (spills).
 
 // What a chain is run for.
 //   run   y and the final state

@@ -8,11 +8,10 @@
 // for the blocks below the diagonal, 16 then 32 wide, on the fp32 matrix instruction.  No
 // power of Lo is formed, so keys that repeat do not make the terms grow.
 //
-// 4096 chunks of a head (4 x 2048 tokens, 32 heads in 8 groups, bf16, N = 128) take 43 us and
-// write 130 MB of images, 3.0 TB/s (a fill reaches 7): a head is seven steps between
-// barriers, and 4 blocks a CU cover for each other; the vector units are busy half of the
-// time, the waves wait for LDS and barriers the rest (one barrier less: the same 43).  With
-// registers for 3 blocks, 52; 49 with a library e^x and decays above the diagonal too.
+// 4096 chunks of a head (4 x 2048 tokens, 32 heads in 8 groups, bf16, N = 128) take 45 to
+// 48 us and write 154 MB of images, 3.3 TB/s (a fill reaches 7): a head is seven steps between
+// barriers, 4 blocks a CU cover for each other, and the waves wait for LDS and barriers 60 % of
+// their time.  With registers for 3 blocks it is the same (the forward call 193 us against 196).
 #pragma once
 
 #include <algorithm>

@@ -21,8 +21,9 @@
 //
 // Bound by the bytes: gate backward of 8192 x 4096, groups of 128, bf16 (336 MB) 70 us, 4.8
 // TB/s; residual sum and norm of 8192 x 2560, bf16 with an fp32 residual (252 MB) 51 us, 4.9
-// TB/s; its backward of 2677 x 1288 fp32 (83 MB) 16 us, 5.1 TB/s; a copy reaches 5.2.  A
-// forward call of 5 rows is its launch: 4.5 us of kernel in 9.
+// TB/s; its backward of 2677 x 1288 fp32 (83 MB) 17 us, and 5 for the sums of its
+// parameters' gradients, 3.9 TB/s together; a copy reaches 5.2.  A forward call of 5 rows is
+// its launch: 4.5 us of kernel in 9.
 #include <algorithm>
 
 #include "ssd_device.h"
