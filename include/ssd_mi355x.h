@@ -554,6 +554,45 @@ ssd_status_t ssd_norm_add_bwd(const void *x, const void *sum, const float *scale
                               ssd_dtype_t io, ssd_dtype_t res_io, void *workspace,
                               size_t workspace_bytes, void *hip_stream);
 
+/*
+ * Two more forms of the residual sum and its norm, arguments, limits and errors as for
+ * ssd_norm_add_fwd and ssd_norm_add_bwd where they have the same names.
+ *
+ * ssd_norm_add_drop_fwd: with dropout on what is added, for training:
+ *     sum = residual + scale m x / (1 - p),  y = sum r w,  m = 0 with probability p, else 1
+ *   p in [0, 1), SSD_ERR_UNSUPPORTED otherwise.  The mask is not stored: with i = row D +
+ *   channel, m is 1 where word i mod 4 of Philox4x32-10 of the counter (i / 4, offset) under
+ *   the key seed (64 bits each, low word first) is at least floor(p 2^32).  rng [2] int64
+ *   (device, 8-byte aligned) holds seed and offset and is read when the call runs: calls
+ *   recorded in a graph draw what it holds at each replay.  Calls whose masks are to differ
+ *   need seeds or offsets that do.  Where m is 0 nothing of x is read into the result, a NaN
+ *   neither.
+ * ssd_norm_add_drop_bwd: its gradients, with the same rng and p (the mask is drawn again).
+ *   Workspace of ssd_norm_bwd_workspace_bytes as for ssd_norm_add_bwd.
+ *
+ * ssd_norm_add_q8_fwd: with the norm's output in 8 bits, for a projection that reads e4m3
+ *   (1 sign, 4 exponent, 3 mantissa bits, largest value 448, no infinity), one scale for
+ *   every `group` channels of a row (group divides D; group = D: one per row):
+ *     y = sum r w (32 bits),  q_scale = max(max |y| / 448, 2^-126),  q = e4m3(y / q_scale)
+ *   q [rows, D] bytes, q_scale [rows, D / group] fp32; q q_scale is y to 2^-4 of it, or to
+ *   2^-10 q_scale where that is more.  A NaN in sum makes q and q_scale of its row NaN, an
+ *   infinity those of its group (and q 0 in the others).
+ */
+ssd_status_t ssd_norm_add_drop_fwd(const void *x, const void *residual, const float *scale,
+                                   const float *w, const int64_t *rng, void *sum, void *y, int rows,
+                                   int D, float eps, float p, ssd_dtype_t io, ssd_dtype_t res_io,
+                                   void *hip_stream);
+ssd_status_t ssd_norm_add_drop_bwd(const void *x, const void *sum, const float *scale,
+                                   const float *w, const int64_t *rng, const void *dy,
+                                   const void *d_sum, void *dx, void *d_residual, float *d_scale,
+                                   float *dw, int rows, int D, float eps, float p, ssd_dtype_t io,
+                                   ssd_dtype_t res_io, void *workspace, size_t workspace_bytes,
+                                   void *hip_stream);
+ssd_status_t ssd_norm_add_q8_fwd(const void *x, const void *residual, const float *scale,
+                                 const float *w, void *sum, void *q, float *q_scale, int rows, int D,
+                                 int group, float eps, ssd_dtype_t io, ssd_dtype_t res_io,
+                                 void *hip_stream);
+
 /* Static, human-readable name of a status code. */
 const char *ssd_status_string(ssd_status_t status);
 

@@ -51,3 +51,35 @@ def norm_add_grads_f64(x, total, w, dy, d_sum, eps, scale=None):
     if scale is None:
         return ds, ds, dw, None
     return ds * _f64(scale), ds, dw, (ds * _f64(x)).reshape(-1, s.shape[-1]).sum(0)
+
+
+def philox_words(n, seed, offset):
+    """Words 0 .. n - 1 of Philox4x32-10: word i is word i mod 4 of the counter (i / 4, offset)
+    under the key seed.  numpy, on the CPU."""
+    import numpy as np
+    u = np.uint64
+    mask, i = u(0xFFFFFFFF), np.arange((n + 3) // 4, dtype=np.uint64)
+    seed, offset = int(seed) % (1 << 64), int(offset) % (1 << 64)
+    c0, c1 = i & mask, i >> u(32)
+    c2, c3 = np.full_like(i, offset & 0xFFFFFFFF), np.full_like(i, offset >> 32)
+    k0, k1 = seed & 0xFFFFFFFF, seed >> 32
+    for _ in range(10):
+        p, q = u(0xD2511F53) * c0, u(0xCD9E8D57) * c2
+        c0, c1, c2, c3 = (q >> u(32)) ^ c1 ^ u(k0), q & mask, (p >> u(32)) ^ c3 ^ u(k1), p & mask
+        k0, k1 = (k0 + 0x9E3779B9) & 0xFFFFFFFF, (k1 + 0xBB67AE85) & 0xFFFFFFFF
+    return np.stack([c0, c1, c2, c3], 1).reshape(-1)[:n].astype(np.uint32)
+
+
+def dropout_factor(shape, p, rng):
+    """0 or 1 / (1 - p) per element (float64): what x is multiplied by.  p as 32 bits hold it."""
+    import numpy as np
+    n, p = int(np.prod(shape)), float(np.float32(p))
+    stays = philox_words(n, int(rng[0]), int(rng[1])) >= np.uint32(int(p * 4294967296.0))
+    return torch.from_numpy(stays).reshape(shape).to(torch.float64) / (1.0 - p)
+
+
+def q8_of(y, group):
+    """(y / scale, scale) per group of channels, before the rounding to e4m3."""
+    g = y.reshape(*y.shape[:-1], y.shape[-1] // group, group)
+    scale = torch.clamp_min(g.abs().amax(-1) / 448.0, 2.0 ** -126)
+    return (g / scale[..., None]).reshape(y.shape), scale

@@ -39,6 +39,7 @@ EXPORTED = ("ssd_chunk_scan_workspace_bytes", "ssd_chunk_scan_workspace_init",
             "ssd_gated_delta_fwd", "ssd_gated_delta_bwd_workspace_bytes",
             "ssd_gated_delta_bwd", "ssd_norm_gate_fwd", "ssd_norm_bwd_workspace_bytes",
             "ssd_norm_gate_bwd", "ssd_norm_add_fwd", "ssd_norm_add_bwd",
+            "ssd_norm_add_drop_fwd", "ssd_norm_add_drop_bwd", "ssd_norm_add_q8_fwd",
             "ssd_status_string", "ssd_version")
 
 _lib = None
@@ -115,6 +116,12 @@ def lib() -> ctypes.CDLL:
         L.ssd_norm_add_fwd.restype = i32
         L.ssd_norm_add_bwd.argtypes = [vp] * 10 + [i32] * 2 + [f32, i32, i32, vp, sz, vp]
         L.ssd_norm_add_bwd.restype = i32
+        L.ssd_norm_add_drop_fwd.argtypes = [vp] * 7 + [i32] * 2 + [f32, f32, i32, i32, vp]
+        L.ssd_norm_add_drop_fwd.restype = i32
+        L.ssd_norm_add_drop_bwd.argtypes = [vp] * 11 + [i32] * 2 + [f32, f32, i32, i32, vp, sz, vp]
+        L.ssd_norm_add_drop_bwd.restype = i32
+        L.ssd_norm_add_q8_fwd.argtypes = [vp] * 7 + [i32] * 3 + [f32, i32, i32, vp]
+        L.ssd_norm_add_q8_fwd.restype = i32
         L.ssd_status_string.argtypes = [i32]
         L.ssd_status_string.restype = ctypes.c_char_p
         L.ssd_version.argtypes = []
@@ -595,6 +602,49 @@ def ssd_norm_add_bwd(x, sum, scale, w, dy, d_sum, dx, d_residual, d_scale, dw, e
              eps, _io_code(dy), _io_code(sum), ws, ws_bytes)
 
 
+def ssd_norm_add_drop_fwd(x, residual, scale, w, rng, sum, y, eps, p, stream=None) -> None:
+    """Enqueue ssd_norm_add_fwd with dropout of probability p on x; rng [2] int64 on the GPU
+    holds the generator's seed and offset."""
+    D, dev, f32 = x.shape[-1], x.device, torch.float32
+    rows = _rows(x)
+    _enqueue("ssd_norm_add_drop_fwd", dev, stream, _tensor(x, "x", x.shape, x.dtype, dev),
+             _tensor(residual, "residual", x.shape, residual.dtype, dev),
+             _tensor(scale, "scale", (D,), f32, dev), _tensor(w, "w", (D,), f32, dev),
+             _tensor(rng, "rng", (2,), torch.int64, dev), _tensor(sum, "sum", x.shape, residual.dtype, dev),
+             _tensor(y, "y", x.shape, x.dtype, dev), rows, D, eps, p, _io_code(x), _io_code(residual))
+
+
+def ssd_norm_add_drop_bwd(x, sum, scale, w, rng, dy, d_sum, dx, d_residual, d_scale, dw, eps, p,
+                          workspace, stream=None) -> None:
+    """Enqueue the gradients of ssd_norm_add_drop_fwd; arguments as ssd_norm_add_bwd."""
+    D, dev, f32, res = dy.shape[-1], dy.device, torch.float32, sum.dtype
+    shape, io = dy.shape, dy.dtype
+    rows = _rows(dy)
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _enqueue("ssd_norm_add_drop_bwd", dev, stream, _tensor(x, "x", shape, io, dev),
+             _tensor(sum, "sum", shape, res, dev), _tensor(scale, "scale", (D,), f32, dev),
+             _tensor(w, "w", (D,), f32, dev), _tensor(rng, "rng", (2,), torch.int64, dev),
+             _tensor(dy, "dy", shape, io, dev), _tensor(d_sum, "d_sum", shape, res, dev),
+             _tensor(dx, "dx", shape, io, dev), _tensor(d_residual, "d_residual", shape, res, dev),
+             _tensor(d_scale, "d_scale", (D,), f32, dev), _tensor(dw, "dw", (D,), f32, dev), rows, D,
+             eps, p, _io_code(dy), _io_code(sum), ws, ws_bytes)
+
+
+def ssd_norm_add_q8_fwd(x, residual, scale, w, sum, q, q_scale, group, eps, stream=None) -> None:
+    """Enqueue ssd_norm_add_fwd with its output in 8 bits: q (float8_e4m3fn, of x's shape) and
+    q_scale [..., D / group] float32."""
+    D, dev, f32 = x.shape[-1], x.device, torch.float32
+    rows = _rows(x)
+    groups = (*x.shape[:-1], D // group if group > 0 else 0)    # a group below 1 is the library's to refuse
+    _enqueue("ssd_norm_add_q8_fwd", dev, stream, _tensor(x, "x", x.shape, x.dtype, dev),
+             _tensor(residual, "residual", x.shape, residual.dtype, dev),
+             _tensor(scale, "scale", (D,), f32, dev), _tensor(w, "w", (D,), f32, dev),
+             _tensor(sum, "sum", x.shape, residual.dtype, dev),
+             _tensor(q, "q", x.shape, torch.float8_e4m3fn, dev),
+             _tensor(q_scale, "q_scale", groups, f32, dev), rows, D, group, eps, _io_code(x),
+             _io_code(residual))
+
+
 # ------------------------------------------------------------ allocating wrappers
 def chunk_scan_workspace(x, B, Q, stream=None) -> torch.Tensor:
     """Allocate and prepare a workspace for chunk scans of x's and B's shapes."""
@@ -752,6 +802,41 @@ def norm_add_bwd(x, sum, w, dy, d_sum, eps, scale=None, workspace=None, stream=N
             workspace = _scratch(n, dy.device)
     ssd_norm_add_bwd(x, sum, scale, w, dy, d_sum, dx, d_res, d_scale, dw, eps, workspace, stream)
     return dx, d_res, dw, d_scale
+
+
+def norm_add_drop_fwd(x, residual, w, eps, p, rng, scale=None, stream=None):
+    """norm_add_fwd with dropout of probability p on x; rng [2] int64 on the GPU holds the
+    seed and the offset of the mask's generator.  Returns (y, sum)."""
+    with _allocating_on(stream):
+        y, total = torch.empty_like(x), torch.empty_like(residual)
+    ssd_norm_add_drop_fwd(x, residual, scale, w, rng, total, y, eps, p, stream)
+    return y, total
+
+
+def norm_add_drop_bwd(x, sum, w, dy, d_sum, eps, p, rng, scale=None, workspace=None, stream=None):
+    """Gradients of norm_add_drop_fwd, with the rng and p that it had; returns (dx,
+    d_residual, dw, d_scale) as norm_add_bwd does."""
+    D = dy.shape[-1]
+    with _allocating_on(stream):
+        dx, d_res, dw = torch.empty_like(dy), torch.empty_like(sum), torch.empty_like(w)
+        d_scale = None if scale is None else torch.empty_like(scale)
+        if workspace is None:
+            n = ssd_norm_bwd_workspace_bytes(_rows(dy), D, D, 1 if scale is None else 2, _io_code(dy))
+            workspace = _scratch(n, dy.device)
+    ssd_norm_add_drop_bwd(x, sum, scale, w, rng, dy, d_sum, dx, d_res, d_scale, dw, eps, p, workspace, stream)
+    return dx, d_res, dw, d_scale
+
+
+def norm_add_q8_fwd(x, residual, w, eps, group=None, scale=None, stream=None):
+    """norm_add_fwd with the norm's output in e4m3, one scale for every `group` channels
+    (None: one per row).  Returns (q, q_scale, sum); y is q times its group's scale."""
+    D = x.shape[-1]
+    group = D if group is None else group
+    with _allocating_on(stream):
+        q, total = torch.empty_like(x, dtype=torch.float8_e4m3fn), torch.empty_like(residual)
+        q_scale = torch.empty((*x.shape[:-1], D // group if group > 0 else 0), dtype=torch.float32, device=x.device)
+    ssd_norm_add_q8_fwd(x, residual, scale, w, total, q, q_scale, group, eps, stream)
+    return q, q_scale, total
 
 
 def to_device(arr, device="cuda"):

@@ -39,6 +39,19 @@ struct NormAddArgs {
     bool bf16, res_bf16;
 };
 
+// Dropout on x: seed and offset of the generator (device), the probability of a zero.
+struct NormDropArgs {
+    const uint64_t *rng;
+    float p;
+};
+
+// The norm's output in e4m3 [rows, D] and one scale [rows, D / group] per group of channels.
+struct NormQ8Args {
+    uint8_t *q;
+    float *scale;
+    int group;
+};
+
 // Backward: row slices, each of which leaves one partial sum per channel and parameter.
 struct NormBwdPlan {
     int slices = 0;
@@ -50,5 +63,11 @@ hipError_t launch_norm_gate_fwd(const NormGateArgs &a, hipStream_t stream);
 hipError_t launch_norm_gate_bwd(const NormGateArgs &a, const NormBwdPlan &plan, hipStream_t stream);
 hipError_t launch_norm_add_fwd(const NormAddArgs &a, hipStream_t stream);
 hipError_t launch_norm_add_bwd(const NormAddArgs &a, const NormBwdPlan &plan, hipStream_t stream);
+hipError_t launch_norm_add_drop_fwd(const NormAddArgs &a, const NormDropArgs &d, hipStream_t stream);
+hipError_t launch_norm_add_drop_bwd(const NormAddArgs &a, const NormDropArgs &d, const NormBwdPlan &plan, hipStream_t stream);
+hipError_t launch_norm_add_q8(const NormAddArgs &a, const NormQ8Args &o, hipStream_t stream);
+
+// out0 (and out1) [D] = the sums of a backward pass's partials over its slices.
+hipError_t launch_norm_reduce(const float *part, float *out0, float *out1, int slices, int D, hipStream_t stream);
 
 }  // namespace ssd

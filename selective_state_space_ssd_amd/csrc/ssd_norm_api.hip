@@ -28,6 +28,67 @@ ssd_status_t check_dims(int rows, int D, int group) {
 
 ssd_status_t done(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
 
+// Checks of the residual sum's forward calls.  `out` is the norm's output of `out_elem` bytes
+// an element, more_in and more_out what a call has besides.
+ssd_status_t add_fwd_args(ssd::NormAddArgs &a, const void *x, const void *residual, const float *scale, const float *w,
+                          void *sum, void *out, size_t out_elem, int rows, int D, float eps, ssd_dtype_t io,
+                          ssd_dtype_t res_io, const Range &more_in, const Range &more_out) {
+    if (!x || !residual || !w || !sum || !out) return SSD_ERR_NULL_ARG;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(scale, 16) || !aligned(w, 16) || !aligned(sum, 16) ||
+        !aligned(out, 16))
+        return SSD_ERR_ALIGN;
+    const size_t n = size_t(rows) * D;
+    const Range rres(residual, n * elem(res_io)), rsum(sum, n * elem(res_io));
+    if (rres.overlaps(rsum) && !rres.same(rsum)) return SSD_ERR_ALIAS;
+    const Range ins[] = {Range(x, n * elem(io)), Range(scale, size_t(D) * 4), Range(w, size_t(D) * 4), more_in};
+    const Range outs[] = {rsum, Range(out, n * out_elem), more_out};
+    if (any_alias(ins, outs) || outs[1].overlaps(rres) || outs[2].overlaps(rres)) return SSD_ERR_ALIAS;
+    a.x = x; a.residual = residual; a.scale = scale; a.w = w; a.sum = sum; a.y = out;
+    a.rows = rows; a.D = D; a.eps = eps;
+    a.bf16 = io == SSD_DTYPE_BF16; a.res_bf16 = res_io == SSD_DTYPE_BF16;
+    return SSD_OK;
+}
+
+ssd_status_t add_types(ssd_dtype_t io, ssd_dtype_t res_io) {
+    if (!known(io) || !known(res_io)) return SSD_ERR_UNSUPPORTED;
+    return res_io != SSD_DTYPE_F32 && res_io != io ? SSD_ERR_UNSUPPORTED : SSD_OK;
+}
+
+// The residual sum's backward calls; `drop` null: without dropout.
+ssd_status_t add_bwd(const void *x, const void *sum, const float *scale, const float *w, const void *dy,
+                     const void *d_sum, void *dx, void *d_residual, float *d_scale, float *dw, int rows, int D,
+                     float eps, const ssd::NormDropArgs *drop, ssd_dtype_t io, ssd_dtype_t res_io, void *workspace,
+                     size_t workspace_bytes, void *hip_stream) {
+    if (const ssd_status_t st = add_types(io, res_io); st != SSD_OK) return st;
+    if (const ssd_status_t st = check_dims(rows, D, D); st != SSD_OK) return st;
+    if (!dw || (scale == nullptr) != (d_scale == nullptr) || (drop && !drop->rng)) return SSD_ERR_NULL_ARG;
+    if (!aligned(dw, 16) || !aligned(d_scale, 16) || (drop && !aligned(drop->rng, 8))) return SSD_ERR_ALIGN;
+    const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    const Range rdw(dw, size_t(D) * 4), rds(d_scale, size_t(D) * 4);
+    if (rdw.overlaps(rds)) return SSD_ERR_ALIAS;
+    if (rows == 0) {
+        if (ssd::launch_copy_state(nullptr, dw, size_t(D), stream) != hipSuccess) return SSD_ERR_HIP;
+        return d_scale ? done(ssd::launch_copy_state(nullptr, d_scale, size_t(D), stream)) : SSD_OK;
+    }
+    if (!sum || !w || !dy || !dx || !d_residual || (scale && !x)) return SSD_ERR_NULL_ARG;
+    if (!aligned(x, 16) || !aligned(sum, 16) || !aligned(scale, 16) || !aligned(w, 16) || !aligned(dy, 16) ||
+        !aligned(d_sum, 16) || !aligned(dx, 16) || !aligned(d_residual, 16) || !aligned(workspace, 16))
+        return SSD_ERR_ALIGN;
+    const ssd::NormBwdPlan plan = ssd::plan_norm_bwd(rows, D, D, scale ? 2 : 1, io == SSD_DTYPE_BF16);
+    if (!workspace || workspace_bytes < plan.total) return SSD_ERR_WORKSPACE;
+    const size_t n = size_t(rows) * D * elem(io), m = size_t(rows) * D * elem(res_io);
+    const Range ins[] = {Range(scale ? x : nullptr, n), Range(sum, m), Range(scale, size_t(D) * 4),
+                         Range(w, size_t(D) * 4), Range(dy, n), Range(d_sum, m), Range(drop ? drop->rng : nullptr, 16)};
+    const Range outs[] = {Range(dx, n), Range(d_residual, m), rds, rdw, Range(workspace, plan.total)};
+    if (any_alias(ins, outs)) return SSD_ERR_ALIAS;
+    ssd::NormAddArgs a{};
+    a.x = x; a.sum = const_cast<void *>(sum); a.scale = scale; a.w = w; a.dy = dy; a.dsum = d_sum;
+    a.dx = dx; a.dres = d_residual; a.dscale = d_scale; a.dw = dw; a.workspace = workspace;
+    a.rows = rows; a.D = D; a.eps = eps;
+    a.bf16 = io == SSD_DTYPE_BF16; a.res_bf16 = res_io == SSD_DTYPE_BF16;
+    return done(drop ? ssd::launch_norm_add_drop_bwd(a, *drop, plan, stream) : ssd::launch_norm_add_bwd(a, plan, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -86,24 +147,13 @@ ssd_status_t ssd_norm_gate_bwd(const void *x, const void *z, const float *w, con
 ssd_status_t ssd_norm_add_fwd(const void *x, const void *residual, const float *scale,
                               const float *w, void *sum, void *y, int rows, int D, float eps,
                               ssd_dtype_t io, ssd_dtype_t res_io, void *hip_stream) {
-    if (!known(io) || !known(res_io)) return SSD_ERR_UNSUPPORTED;
-    if (res_io != SSD_DTYPE_F32 && res_io != io) return SSD_ERR_UNSUPPORTED;
+    if (const ssd_status_t st = add_types(io, res_io); st != SSD_OK) return st;
     if (const ssd_status_t st = check_dims(rows, D, D); st != SSD_OK) return st;
     if (rows == 0) return SSD_OK;
-    if (!x || !residual || !w || !sum || !y) return SSD_ERR_NULL_ARG;
-    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(scale, 16) || !aligned(w, 16) || !aligned(sum, 16) ||
-        !aligned(y, 16))
-        return SSD_ERR_ALIGN;
-    const size_t n = size_t(rows) * D * elem(io), m = size_t(rows) * D * elem(res_io);
-    const Range rres(residual, m), rsum(sum, m);
-    if (rres.overlaps(rsum) && !rres.same(rsum)) return SSD_ERR_ALIAS;
-    const Range ins[] = {Range(x, n), Range(scale, size_t(D) * 4), Range(w, size_t(D) * 4)};
-    const Range outs[] = {rsum, Range(y, n)};
-    if (any_alias(ins, outs) || outs[1].overlaps(rres)) return SSD_ERR_ALIAS;
     ssd::NormAddArgs a{};
-    a.x = x; a.residual = residual; a.scale = scale; a.w = w; a.sum = sum; a.y = y;
-    a.rows = rows; a.D = D; a.eps = eps;
-    a.bf16 = io == SSD_DTYPE_BF16; a.res_bf16 = res_io == SSD_DTYPE_BF16;
+    if (const ssd_status_t st = add_fwd_args(a, x, residual, scale, w, sum, y, elem(io), rows, D, eps, io, res_io, {}, {});
+        st != SSD_OK)
+        return st;
     return done(ssd::launch_norm_add_fwd(a, static_cast<hipStream_t>(hip_stream)));
 }
 
@@ -112,35 +162,56 @@ ssd_status_t ssd_norm_add_bwd(const void *x, const void *sum, const float *scale
                               float *d_scale, float *dw, int rows, int D, float eps,
                               ssd_dtype_t io, ssd_dtype_t res_io, void *workspace,
                               size_t workspace_bytes, void *hip_stream) {
-    if (!known(io) || !known(res_io)) return SSD_ERR_UNSUPPORTED;
-    if (res_io != SSD_DTYPE_F32 && res_io != io) return SSD_ERR_UNSUPPORTED;
+    return add_bwd(x, sum, scale, w, dy, d_sum, dx, d_residual, d_scale, dw, rows, D, eps, nullptr, io, res_io, workspace,
+                   workspace_bytes, hip_stream);
+}
+
+ssd_status_t ssd_norm_add_drop_fwd(const void *x, const void *residual, const float *scale,
+                                   const float *w, const int64_t *rng, void *sum, void *y, int rows,
+                                   int D, float eps, float p, ssd_dtype_t io, ssd_dtype_t res_io,
+                                   void *hip_stream) {
+    if (const ssd_status_t st = add_types(io, res_io); st != SSD_OK) return st;
     if (const ssd_status_t st = check_dims(rows, D, D); st != SSD_OK) return st;
-    if (!dw || (scale == nullptr) != (d_scale == nullptr)) return SSD_ERR_NULL_ARG;
-    if (!aligned(dw, 16) || !aligned(d_scale, 16)) return SSD_ERR_ALIGN;
-    const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-    const Range rdw(dw, size_t(D) * 4), rds(d_scale, size_t(D) * 4);
-    if (rdw.overlaps(rds)) return SSD_ERR_ALIAS;
-    if (rows == 0) {
-        if (ssd::launch_copy_state(nullptr, dw, size_t(D), stream) != hipSuccess) return SSD_ERR_HIP;
-        return d_scale ? done(ssd::launch_copy_state(nullptr, d_scale, size_t(D), stream)) : SSD_OK;
-    }
-    if (!sum || !w || !dy || !dx || !d_residual || (scale && !x)) return SSD_ERR_NULL_ARG;
-    if (!aligned(x, 16) || !aligned(sum, 16) || !aligned(scale, 16) || !aligned(w, 16) || !aligned(dy, 16) ||
-        !aligned(d_sum, 16) || !aligned(dx, 16) || !aligned(d_residual, 16) || !aligned(workspace, 16))
-        return SSD_ERR_ALIGN;
-    const ssd::NormBwdPlan plan = ssd::plan_norm_bwd(rows, D, D, scale ? 2 : 1, io == SSD_DTYPE_BF16);
-    if (!workspace || workspace_bytes < plan.total) return SSD_ERR_WORKSPACE;
-    const size_t n = size_t(rows) * D * elem(io), m = size_t(rows) * D * elem(res_io);
-    const Range ins[] = {Range(scale ? x : nullptr, n), Range(sum, m), Range(scale, size_t(D) * 4),
-                         Range(w, size_t(D) * 4), Range(dy, n), Range(d_sum, m)};
-    const Range outs[] = {Range(dx, n), Range(d_residual, m), rds, rdw, Range(workspace, plan.total)};
-    if (any_alias(ins, outs)) return SSD_ERR_ALIAS;
+    if (!(p >= 0.f && p < 1.f)) return SSD_ERR_UNSUPPORTED;
+    if (rows == 0) return SSD_OK;
+    if (!rng) return SSD_ERR_NULL_ARG;
+    if (!aligned(rng, 8)) return SSD_ERR_ALIGN;
     ssd::NormAddArgs a{};
-    a.x = x; a.sum = const_cast<void *>(sum); a.scale = scale; a.w = w; a.dy = dy; a.dsum = d_sum;
-    a.dx = dx; a.dres = d_residual; a.dscale = d_scale; a.dw = dw; a.workspace = workspace;
-    a.rows = rows; a.D = D; a.eps = eps;
-    a.bf16 = io == SSD_DTYPE_BF16; a.res_bf16 = res_io == SSD_DTYPE_BF16;
-    return done(ssd::launch_norm_add_bwd(a, plan, stream));
+    if (const ssd_status_t st = add_fwd_args(a, x, residual, scale, w, sum, y, elem(io), rows, D, eps, io, res_io, Range(rng, 16), {});
+        st != SSD_OK)
+        return st;
+    const ssd::NormDropArgs d{reinterpret_cast<const uint64_t *>(rng), p};
+    return done(ssd::launch_norm_add_drop_fwd(a, d, static_cast<hipStream_t>(hip_stream)));
+}
+
+ssd_status_t ssd_norm_add_drop_bwd(const void *x, const void *sum, const float *scale,
+                                   const float *w, const int64_t *rng, const void *dy,
+                                   const void *d_sum, void *dx, void *d_residual, float *d_scale,
+                                   float *dw, int rows, int D, float eps, float p, ssd_dtype_t io,
+                                   ssd_dtype_t res_io, void *workspace, size_t workspace_bytes,
+                                   void *hip_stream) {
+    if (!(p >= 0.f && p < 1.f)) return SSD_ERR_UNSUPPORTED;
+    const ssd::NormDropArgs d{reinterpret_cast<const uint64_t *>(rng), p};
+    return add_bwd(x, sum, scale, w, dy, d_sum, dx, d_residual, d_scale, dw, rows, D, eps, &d, io, res_io, workspace,
+                   workspace_bytes, hip_stream);
+}
+
+ssd_status_t ssd_norm_add_q8_fwd(const void *x, const void *residual, const float *scale,
+                                 const float *w, void *sum, void *q, float *q_scale, int rows, int D,
+                                 int group, float eps, ssd_dtype_t io, ssd_dtype_t res_io,
+                                 void *hip_stream) {
+    if (const ssd_status_t st = add_types(io, res_io); st != SSD_OK) return st;
+    if (const ssd_status_t st = check_dims(rows, D, group); st != SSD_OK) return st;
+    if (rows == 0) return SSD_OK;
+    if (!q_scale) return SSD_ERR_NULL_ARG;
+    if (!aligned(q_scale, 16)) return SSD_ERR_ALIGN;
+    ssd::NormAddArgs a{};
+    if (const ssd_status_t st = add_fwd_args(a, x, residual, scale, w, sum, q, 1, rows, D, eps, io, res_io, {},
+                                             Range(q_scale, size_t(rows) * (D / group) * 4));
+        st != SSD_OK)
+        return st;
+    const ssd::NormQ8Args o{static_cast<uint8_t *>(q), q_scale, group};
+    return done(ssd::launch_norm_add_q8(a, o, static_cast<hipStream_t>(hip_stream)));
 }
 
 }  // extern "C"
