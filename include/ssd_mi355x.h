@@ -508,6 +508,62 @@ ssd_status_t ssd_gated_delta_bwd(const void *q, const void *k, const void *v, co
                                  size_t workspace_bytes, void *hip_stream);
 
 /*
+ * The gated scan: a recurrence of one number per channel, with a gate per token and channel.
+ * Per batch row and channel, with h the state:
+ *
+ *   h_t = alpha_t h_{t-1} + u_t,   y_t = h_t
+ *     sigmoid == 0:  alpha = exp(a),            u = x               (a is a log decay)
+ *     sigmoid != 0:  alpha = 1 / (1 + exp(-a)), u = (1 - alpha) x   (a is the gate's projection)
+ *
+ *   x, y  [b, L, D]  io;   a  [b, L, D]  a_io (fp32, or io);   states  [b, D]  fp32
+ * a <= 0 is the domain of a log decay.  a = -infinity forgets a finite state; a token with
+ * a = 0 and x = 0 (sigmoid: a = +infinity, any finite x) leaves it as it is, so sequences of
+ * unequal length are padded with such tokens.
+ *
+ * ssd_gated_scan_step: K tokens on an existing state, K in [1, 16]; accept_len, state_out
+ *   and err_flag as for ssd_gated_delta_step.
+ *
+ * ssd_gated_scan_fwd: a whole sequence from init_state (NULL = zeros); final_state (NULL =
+ *   skip) is the state after the last token.  states [b, ceil(L / SSD_GATED_SCAN_KEEP), D]
+ *   fp32 (NULL = skip) takes the state before every SSD_GATED_SCAN_KEEP-th token, for the
+ *   backward pass.  workspace: ssd_gated_scan_fwd_workspace_bytes bytes ((size_t)-1: invalid
+ *   dimensions), 16-byte aligned, scratch without preparation; calls that overlap in time
+ *   need one each.  L = 0 copies init_state (or zeros) to final_state.
+ *
+ * ssd_gated_scan_bwd: from dy (of y) and d_final (of final_state; NULL = zero) the gradients
+ *   of sum(dy y) + sum(d_final final_state): dx (like x), da (like a), d_init (like
+ *   init_state; NULL = skip).  states as the forward call left them (init_state is not read
+ *   then), or NULL: they are computed again from init_state.  workspace:
+ *   ssd_gated_scan_bwd_workspace_bytes bytes (with_states != 0: states are given), as above.
+ *   L = 0 copies d_final (or zeros) to d_init.
+ *
+ * b up to 65535, L up to 2^31 - 65, D up to 2^31 - 257.  accept_len and err_flag are 4-byte, all other pointers 16-byte aligned.
+ * Outputs must not overlap inputs (but for state_out and state_in, which may be the same),
+ * each other or the workspace.  States, gradients' sums and gates are kept in fp32 (a gate
+ * near 1 as its distance from 1), every output is rounded once, in an order of operations
+ * that does not change from run to run.  A NaN or an infinity reaches the outputs that
+ * depend on it (an infinity as a NaN, it may be) and no other.  Errors as for the other
+ * entry points.
+ */
+#define SSD_GATED_SCAN_KEEP 32
+ssd_status_t ssd_gated_scan_step(const float *state_in, const void *x, const void *a,
+                                 const int32_t *accept_len, void *y, float *state_out,
+                                 int32_t *err_flag, int b, int K, int D, int sigmoid, ssd_dtype_t io,
+                                 ssd_dtype_t a_io, void *hip_stream);
+size_t ssd_gated_scan_fwd_workspace_bytes(int b, int L, int D, ssd_dtype_t io, ssd_dtype_t a_io);
+ssd_status_t ssd_gated_scan_fwd(const void *x, const void *a, const float *init_state, void *y,
+                                float *states, float *final_state, int b, int L, int D, int sigmoid,
+                                ssd_dtype_t io, ssd_dtype_t a_io, void *workspace,
+                                size_t workspace_bytes, void *hip_stream);
+size_t ssd_gated_scan_bwd_workspace_bytes(int b, int L, int D, int with_states, ssd_dtype_t io,
+                                          ssd_dtype_t a_io);
+ssd_status_t ssd_gated_scan_bwd(const void *x, const void *a, const float *init_state,
+                                const float *states, const void *dy, const float *d_final, void *dx,
+                                void *da, float *d_init, int b, int L, int D, int sigmoid,
+                                ssd_dtype_t io, ssd_dtype_t a_io, void *workspace,
+                                size_t workspace_bytes, void *hip_stream);
+
+/*
  * The norms around a mixer block, each fused with what stands next to it; act(z) =
  * z / (1 + e^-z), w fp32.
  *

@@ -37,7 +37,9 @@ EXPORTED = ("ssd_chunk_scan_workspace_bytes", "ssd_chunk_scan_workspace_init",
             "ssd_seq_total_decay", "ssd_seq_combine", "ssd_seq_apply_state",
             "ssd_gated_delta_step", "ssd_gated_delta_fwd_workspace_bytes",
             "ssd_gated_delta_fwd", "ssd_gated_delta_bwd_workspace_bytes",
-            "ssd_gated_delta_bwd", "ssd_norm_gate_fwd", "ssd_norm_bwd_workspace_bytes",
+            "ssd_gated_delta_bwd", "ssd_gated_scan_step", "ssd_gated_scan_fwd_workspace_bytes",
+            "ssd_gated_scan_fwd", "ssd_gated_scan_bwd_workspace_bytes", "ssd_gated_scan_bwd",
+            "ssd_norm_gate_fwd", "ssd_norm_bwd_workspace_bytes",
             "ssd_norm_gate_bwd", "ssd_norm_add_fwd", "ssd_norm_add_bwd",
             "ssd_norm_add_drop_fwd", "ssd_norm_add_drop_bwd", "ssd_norm_add_q8_fwd",
             "ssd_status_string", "ssd_version")
@@ -106,6 +108,16 @@ def lib() -> ctypes.CDLL:
         L.ssd_gated_delta_bwd_workspace_bytes.restype = sz
         L.ssd_gated_delta_bwd.argtypes = [vp] * 14 + [i32] * 6 + [f32, i32, vp, sz, vp]
         L.ssd_gated_delta_bwd.restype = i32
+        L.ssd_gated_scan_step.argtypes = [vp] * 7 + [i32] * 6 + [vp]
+        L.ssd_gated_scan_step.restype = i32
+        L.ssd_gated_scan_fwd_workspace_bytes.argtypes = [i32] * 5
+        L.ssd_gated_scan_fwd_workspace_bytes.restype = sz
+        L.ssd_gated_scan_fwd.argtypes = [vp] * 6 + [i32] * 6 + [vp, sz, vp]
+        L.ssd_gated_scan_fwd.restype = i32
+        L.ssd_gated_scan_bwd_workspace_bytes.argtypes = [i32] * 6
+        L.ssd_gated_scan_bwd_workspace_bytes.restype = sz
+        L.ssd_gated_scan_bwd.argtypes = [vp] * 9 + [i32] * 6 + [vp, sz, vp]
+        L.ssd_gated_scan_bwd.restype = i32
         L.ssd_norm_gate_fwd.argtypes = [vp] * 4 + [i32] * 3 + [f32, i32, i32, vp]
         L.ssd_norm_gate_fwd.restype = i32
         L.ssd_norm_bwd_workspace_bytes.argtypes = [i32] * 5
@@ -539,6 +551,80 @@ def ssd_gated_delta_bwd(q, k, v, a, beta, init_state, dy, d_final, dq, dk, dv, d
              _tensor(d_init, "d_init", st, f32, dev), b, L, H, P, N, G, scale, _io_code(v), ws, ws_bytes)
 
 
+# tokens from one kept state of the gated scan's forward pass to the next
+GATED_SCAN_KEEP = 32
+
+
+def _scan_dims(x):
+    try:
+        b, L, D = x.shape
+    except ValueError:
+        raise ValueError("x and a are [b, L, D]") from None
+    return b, L, D
+
+
+def _kept_shape(b, L, D):
+    return (b, (L + GATED_SCAN_KEEP - 1) // GATED_SCAN_KEEP, D)
+
+
+def ssd_gated_scan_step(state_in, x, a, accept_len, y, state_out, sigmoid=False, err_flag=None,
+                        stream=None) -> None:
+    """Enqueue K tokens of the gated scan on a kept state [b,D] (see include/ssd_mi355x.h)."""
+    b, K, D = _scan_dims(x)
+    dev, io, f32, xy, st = x.device, x.dtype, torch.float32, (b, K, D), (b, D)
+    _enqueue("ssd_gated_scan_step", dev, stream, _tensor(state_in, "state_in", st, f32, dev),
+             _tensor(x, "x", xy, io, dev), _tensor(a, "a", xy, a.dtype, dev),
+             _tensor(accept_len, "accept_len", (b,), torch.int32, dev), _tensor(y, "y", xy, io, dev),
+             _tensor(state_out, "state_out", st, f32, dev),
+             None if err_flag is None else _tensor(err_flag, "err_flag", err_flag.shape, torch.int32, dev),
+             b, K, D, 1 if sigmoid else 0, _io_code(x), _io_code(a))
+
+
+def ssd_gated_scan_fwd_workspace_bytes(b, L, D, io: int, a_io: int) -> int:
+    n = lib().ssd_gated_scan_fwd_workspace_bytes(b, L, D, io, a_io)
+    if n == ctypes.c_size_t(-1).value:
+        raise SSDError(4, "ssd_gated_scan_fwd_workspace_bytes")
+    return n
+
+
+def ssd_gated_scan_fwd(x, a, init_state, y, states, final_state, sigmoid, workspace,
+                       stream=None) -> None:
+    """Enqueue the gated scan over whole sequences: x, y [b,L,D] of one type, a [b,L,D] of that
+    type or float32, init_state and final_state [b,D], states [b,ceil(L/32),D] float32 (each
+    of the three may be None)."""
+    b, L, D = _scan_dims(x)
+    dev, io, f32, xy, st = x.device, x.dtype, torch.float32, (b, L, D), (b, D)
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _enqueue("ssd_gated_scan_fwd", dev, stream, _tensor(x, "x", xy, io, dev),
+             _tensor(a, "a", xy, a.dtype, dev), _tensor(init_state, "init_state", st, f32, dev),
+             _tensor(y, "y", xy, io, dev), _tensor(states, "states", _kept_shape(b, L, D), f32, dev),
+             _tensor(final_state, "final_state", st, f32, dev), b, L, D, 1 if sigmoid else 0,
+             _io_code(x), _io_code(a), ws, ws_bytes)
+
+
+def ssd_gated_scan_bwd_workspace_bytes(b, L, D, with_states, io: int, a_io: int) -> int:
+    n = lib().ssd_gated_scan_bwd_workspace_bytes(b, L, D, 1 if with_states else 0, io, a_io)
+    if n == ctypes.c_size_t(-1).value:
+        raise SSDError(4, "ssd_gated_scan_bwd_workspace_bytes")
+    return n
+
+
+def ssd_gated_scan_bwd(x, a, init_state, states, dy, d_final, dx, da, d_init, sigmoid, workspace,
+                       stream=None) -> None:
+    """Enqueue the gradients of ssd_gated_scan_fwd: its inputs and states (None: computed again
+    from init_state), dy (like x) and d_final [b,D] (may be None); dx like x, da like a,
+    d_init [b,D] float32 (may be None)."""
+    b, L, D = _scan_dims(x)
+    dev, io, f32, xy, st = x.device, x.dtype, torch.float32, (b, L, D), (b, D)
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _enqueue("ssd_gated_scan_bwd", dev, stream, _tensor(x, "x", xy, io, dev),
+             _tensor(a, "a", xy, a.dtype, dev), _tensor(init_state, "init_state", st, f32, dev),
+             _tensor(states, "states", _kept_shape(b, L, D), f32, dev), _tensor(dy, "dy", xy, io, dev),
+             _tensor(d_final, "d_final", st, f32, dev), _tensor(dx, "dx", xy, io, dev),
+             _tensor(da, "da", xy, a.dtype, dev), _tensor(d_init, "d_init", st, f32, dev), b, L, D,
+             1 if sigmoid else 0, _io_code(x), _io_code(a), ws, ws_bytes)
+
+
 def _rows(x) -> int:
     """Rows of x [..., D]; 0 for D = 0, which the library refuses."""
     return x.numel() // x.shape[-1] if x.shape[-1] else 0
@@ -760,6 +846,46 @@ def gated_delta_bwd(q, k, v, a, beta, scale, dy, init_state=None, d_final=None, 
     ssd_gated_delta_bwd(q, k, v, a, beta, init_state, dy, d_final, dq, dk, dv, da, dbeta, d_init, scale,
                         workspace, stream)
     return dq, dk, dv, da, dbeta, d_init
+
+
+def gated_scan_step(state, x, a, sigmoid=False, accept_len=None, stream=None, err_flag=None):
+    """Allocate the outputs; returns (y, state_out): y for all K tokens, the state after
+    accept_len [b] of them (None: after all).  Counts outside [0, K] are clamped and set
+    err_flag (int32, on the GPU), if there is one, to 1."""
+    with _allocating_on(stream):
+        y, state_out = torch.empty_like(x), torch.empty_like(state)
+    ssd_gated_scan_step(state, x, a, accept_len, y, state_out, sigmoid, err_flag, stream)
+    return y, state_out
+
+
+def gated_scan_fwd(x, a, sigmoid=False, init_state=None, keep_states=False, workspace=None, stream=None):
+    """Allocate the outputs (and the workspace if not given); returns (y, final_state), and
+    with keep_states the states that gated_scan_bwd takes as a third."""
+    b, L, D = _scan_dims(x)
+    dev, f32 = x.device, torch.float32
+    with _allocating_on(stream):
+        y, final_state = torch.empty_like(x), torch.empty((b, D), dtype=f32, device=dev)
+        states = torch.empty(_kept_shape(b, L, D), dtype=f32, device=dev) if keep_states else None
+        if workspace is None:
+            workspace = _scratch(ssd_gated_scan_fwd_workspace_bytes(b, L, D, _io_code(x), _io_code(a)), dev)
+    ssd_gated_scan_fwd(x, a, init_state, y, states, final_state, sigmoid, workspace, stream)
+    return (y, final_state, states) if keep_states else (y, final_state)
+
+
+def gated_scan_bwd(x, a, dy, sigmoid=False, init_state=None, d_final=None, states=None, workspace=None,
+                   stream=None):
+    """Allocate the gradients (and the workspace if not given); returns (dx, da, d_init).
+    states from gated_scan_fwd spare their computation from init_state."""
+    b, L, D = _scan_dims(x)
+    dev = x.device
+    with _allocating_on(stream):
+        dx, da = torch.empty_like(x), torch.empty_like(a)
+        d_init = torch.empty((b, D), dtype=torch.float32, device=dev)
+        if workspace is None:
+            n = ssd_gated_scan_bwd_workspace_bytes(b, L, D, states is not None, _io_code(x), _io_code(a))
+            workspace = _scratch(n, dev)
+    ssd_gated_scan_bwd(x, a, init_state, states, dy, d_final, dx, da, d_init, sigmoid, workspace, stream)
+    return dx, da, d_init
 
 
 def norm_gate_fwd(x, z, w, group, eps, gate_first=False, stream=None):

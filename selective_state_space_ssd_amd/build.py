@@ -30,7 +30,8 @@ SOURCES = ["ssd_api.hip", "ssd_verify.hip", "ssd_chunk_scan.hip", "ssd_chunk_fus
            "ssd_chunk_bwd_bf16.hip", "ssd_seqpar.hip", "ssd_slice_state.hip",
            "ssd_delta_api.hip", "ssd_delta_step.hip",
            "ssd_delta_chunk.hip", "ssd_delta_bwd.hip", "ssd_norm_api.hip", "ssd_norm.hip",
-           "ssd_norm_drop.hip", "ssd_norm_q8.hip"]
+           "ssd_norm_drop.hip", "ssd_norm_q8.hip",
+           "ssd_gated_scan_api.hip", "ssd_gated_scan.hip", "ssd_gated_scan_step.hip"]
 ARCH = "gfx950"
 
 COMMON_FLAGS = [
