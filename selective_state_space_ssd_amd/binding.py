@@ -421,7 +421,7 @@ def _tensor(t, name, shape, dtype, device) -> Optional[int]:
     """The device pointer of ``t`` after checking what the C call cannot see; None stays None."""
     if t is None:
         return None
-    if t.device == device and t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous() and t.is_cuda:
         return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
@@ -437,17 +437,18 @@ def _tensor(t, name, shape, dtype, device) -> Optional[int]:
 def _enqueue(name, device, stream, *args) -> None:
     """Call the C entry point ``name`` with ``args`` and a stream of ``device`` (default:
     its current one)."""
+    entry = getattr(_lib or lib(), name)
     if stream is None:      # the handle alone: 0.2 us where a Stream object takes 1.9
         handle = torch._C._cuda_getCurrentRawStream(device.index)
     elif stream.device != device:
         raise ValueError(f"{name}: the stream is on {stream.device}, the tensors are on {device}")
     else:
         handle = stream.cuda_stream
-    if device.index == torch.cuda.current_device():
-        st = getattr(lib(), name)(*args, handle)
+    if device.index == torch._C._cuda_getDevice():
+        st = entry(*args, handle)
     else:
         with torch.cuda.device(device):
-            st = getattr(lib(), name)(*args, handle)
+            st = entry(*args, handle)
     if st != 0:
         raise SSDError(st, name)
 
@@ -864,7 +865,8 @@ def gated_scan_fwd(x, a, sigmoid=False, init_state=None, keep_states=False, work
     b, L, D = _scan_dims(x)
     dev, f32 = x.device, torch.float32
     with _allocating_on(stream):
-        y, final_state = torch.empty_like(x), torch.empty((b, D), dtype=f32, device=dev)
+        y = torch.empty_like(x)
+        final_state = torch.empty((b, D), dtype=f32, device=dev) if init_state is None else torch.empty_like(init_state)
         states = torch.empty(_kept_shape(b, L, D), dtype=f32, device=dev) if keep_states else None
         if workspace is None:
             workspace = _scratch(ssd_gated_scan_fwd_workspace_bytes(b, L, D, _io_code(x), _io_code(a)), dev)
@@ -880,7 +882,7 @@ def gated_scan_bwd(x, a, dy, sigmoid=False, init_state=None, d_final=None, state
     dev = x.device
     with _allocating_on(stream):
         dx, da = torch.empty_like(x), torch.empty_like(a)
-        d_init = torch.empty((b, D), dtype=torch.float32, device=dev)
+        d_init = torch.empty((b, D), dtype=torch.float32, device=dev) if d_final is None else torch.empty_like(d_final)
         if workspace is None:
             n = ssd_gated_scan_bwd_workspace_bytes(b, L, D, states is not None, _io_code(x), _io_code(a))
             workspace = _scratch(n, dev)

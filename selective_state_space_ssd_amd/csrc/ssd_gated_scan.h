@@ -40,7 +40,7 @@ struct GatedStepArgs {
 
 // Whether the launches of this shape stay inside a grid's limits.
 bool gated_scan_supported(int b, int L, int D);
-size_t gated_scan_workspace(int b, int L, int D, bool bf16);    // of either pass, without kept states
+size_t gated_scan_workspace(int b, int L, int D, bool bf16, bool backward);    // without kept states
 
 hipError_t launch_gated_scan_fwd(const GatedScanArgs &a, hipStream_t stream);
 hipError_t launch_gated_scan_bwd(const GatedScanArgs &a, hipStream_t stream);   // kept is an input

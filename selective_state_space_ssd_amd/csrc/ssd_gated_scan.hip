@@ -32,8 +32,10 @@
 namespace ssd {
 namespace {
 
-constexpr int kT = kGatedScanKeep;  // tokens of a wave
-constexpr int kW = 8;               // waves of a block
+#ifndef KT
+#define KT 32
+#endif
+constexpr int kT = KT;  // tokens of a wave
 constexpr int kSpins = 1 << 20;     // looks at a word before a wait gives up (about a second)
 
 // ------------------------------------------------------------- V channels of a lane
@@ -59,13 +61,55 @@ __device__ __forceinline__ Raw<T, V> raw_same(float f) {
     return raw_of<T, V>(reinterpret_cast<const float (&)[V]>(v));
 }
 
-// Rows [0, kT) of a stretch of n tokens; those past it repeat the last.  `p` is at the lane's
-// channels of the first row.
+// As here(float): what is made of r (unpacked values, products, signs) is made again where it is
+// used again.  Kept from one use to the other they would take more registers than there are.
 template <typename T, int V>
-__device__ __forceinline__ void load_rows(const T *p, size_t D, int n, Raw<T, V> (&out)[kT]) {
+__device__ __forceinline__ Raw<T, V> again(Raw<T, V> r) {
+    if constexpr (sizeof(r) == 2) {
+        uint32_t v = r.r;
+        asm("" : "+v"(v));
+        r.r = uint16_t(v);
+    } else if constexpr (sizeof(r) == 8) {
+        asm("" : "+v"(r.r.x), "+v"(r.r.y));
+    } else {
+        asm("" : "+v"(r.r));
+    }
+    return r;
+}
+
+// Rows of a stretch of n tokens, through a buffer view of them: a row's place is a scalar
+// register's, the channels' place in it the lane's.  What is read is read once: it does not stay
+// in the caches (the layer of 4 x 2048 tokens, 5120 channels 100 -> 92 us backward, 16384 tokens 85
+// -> 80; stores marked so gained nothing).
+struct Rows {
+    __amdgpu_buffer_rsrc_t view;
+    uint32_t lane, row;     // bytes
+
+    template <typename T, int V>
+    __device__ __forceinline__ Raw<T, V> load(int t) const {
+        if constexpr (sizeof(Raw<T, V>) == 2) return __builtin_bit_cast(Raw<T, V>, __builtin_amdgcn_raw_buffer_load_b16(view, lane, t * row, kBufNonTemporal));
+        else if constexpr (sizeof(Raw<T, V>) == 4) return __builtin_bit_cast(Raw<T, V>, __builtin_amdgcn_raw_buffer_load_b32(view, lane, t * row, kBufNonTemporal));
+        else return __builtin_bit_cast(Raw<T, V>, __builtin_amdgcn_raw_buffer_load_b64(view, lane, t * row, kBufNonTemporal));
+    }
+    // Rows [0, TOK); those past the n-th repeat it.
+    template <typename T, int V, int TOK>
+    __device__ __forceinline__ void load_all(int n, Raw<T, V> (&out)[TOK]) const {
 #pragma unroll
-    for (int t = 0; t < kT; ++t)
-        out[t] = *reinterpret_cast<const Raw<T, V> *>(p + size_t(n == kT ? t : min(t, n - 1)) * D);
+        for (int t = 0; t < TOK; ++t) out[t] = load<T, V>(n == TOK ? t : min(t, n - 1));
+    }
+    template <typename T, int V>
+    __device__ __forceinline__ void store(int t, Raw<T, V> r) const {
+        if constexpr (sizeof(r) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, r), view, lane, t * row, 0);
+        else if constexpr (sizeof(r) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, r), view, lane, t * row, 0);
+        else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, r), view, lane, t * row, 0);
+    }
+};
+
+// n > 0 rows of D <= 2^24 channels from `first` on.
+template <typename T>
+__device__ __forceinline__ Rows rows_at(const T *first, int n, int D, int channel) {
+    const uint32_t row = uint32_t(D) * uint32_t(sizeof(T));
+    return {buffer_rsrc(first, uint32_t(n) * row), uint32_t(channel) * uint32_t(sizeof(T)), row};
 }
 
 // ----------------------------------------------------------------- pairs and their words
@@ -73,7 +117,7 @@ __device__ __forceinline__ void load_rows(const T *p, size_t D, int n, Raw<T, V>
 __device__ __forceinline__ float both_decays(float m1, float m2) {
     const float a = alpha_of(m1) * alpha_of(m2), b1 = beta_of(m1), b2 = beta_of(m2);
     const float b = fmaf(b1, 1.f - b2, b2);
-    return a > 0.5f && b > 0.f ? -b : a;
+    return a > 0.5f && b >= 0.f ? -b : a;
 }
 
 // The decay of the tokens of a stretch, taken one by one.  Near 1 from the sum of what each
@@ -83,13 +127,15 @@ template <bool SIGMOID>
 struct Decay {
     float alpha = 1.f, lost = 0.f;      // lost: 1 - alpha (sigmoid), the sum of a (log decay)
     __device__ __forceinline__ void token(float m, float a) {
-        alpha *= alpha_of(m);
-        if constexpr (SIGMOID) lost = fmaf(beta_of(m), 1.f - lost, lost);
+        alpha = decayed(m, alpha);
+        if constexpr (SIGMOID) lost = step_state<true>(m, lost, 1.f);
         else lost += a;
     }
     __device__ __forceinline__ float m() const {
-        if constexpr (SIGMOID) return alpha > 0.5f && lost > 0.f ? -lost : alpha;
-        else return lost > -1.f ? gate_of<false>(lost) : alpha;
+        // here(): the product is not put off into a branch on the sum
+        const float product = here(alpha), near = here(SIGMOID ? -lost : gate_of<false>(lost));
+        if constexpr (SIGMOID) return alpha > 0.5f && lost >= 0.f ? near : product;
+        else return lost > -1.f ? near : product;
     }
 };
 
@@ -135,18 +181,21 @@ __device__ __forceinline__ bool look_all(const word_t *p, word_t (&w)[V]) {
     return all_there<V>(w);
 }
 
-template <int V>
+template <int V, int W>
 struct ChainLds {
-    float2 pair[kW][64 * V];        // of the block's waves
-    float2 before[kW][64 * V];      // of the blocks before: pair, or (., outgoing state)
-    int state[kW];                  // whether it is a state
+    // blocks before that are looked at: one for each of the last kNear waves, and kFar more
+    // for each where none of those has a state yet
+    static constexpr int kNear = W < 8 ? W : 8, kFar = 3;
+    float2 pair[W][64 * V];         // of the block's waves
+    float2 before[kNear * (1 + kFar)][64 * V];      // of the blocks before: pair, or (., outgoing state)
+    int state[kNear * (1 + kFar)];  // whether it is a state
     unsigned place;
 };
 
 // The state that enters a wave's tokens.  `wave` counts in the order of the scan; m and s are
 // the pair of the wave's tokens, `start` the state before the first block.
-template <int V>
-__device__ __forceinline__ void enter(const Tiles &tiles, ChainLds<V> &lds, int bi, int seg, int strip, int wave, int lane,
+template <int V, int W>
+__device__ __forceinline__ void enter(const Tiles &tiles, ChainLds<V, W> &lds, int bi, int seg, int strip, int wave, int lane,
                                       const float (&m)[V], const float (&s)[V], const float (&start)[V], float (&h)[V]) {
 #pragma unroll
     for (int j = 0; j < V; ++j) lds.pair[wave][lane * V + j] = make_float2(m[j], s[j]);
@@ -154,80 +203,106 @@ __device__ __forceinline__ void enter(const Tiles &tiles, ChainLds<V> &lds, int 
     float pm[V], ps[V];             // of the waves before
 #pragma unroll
     for (int j = 0; j < V; ++j) { pm[j] = 1.f; ps[j] = 0.f; }
+#pragma unroll 2
     for (int k = 0; k < wave; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const float2 p = lds.pair[k][lane * V + j];
             pm[j] = both_decays(pm[j], p.x);
-            ps[j] = step_state(p.x, ps[j], p.y);
+            ps[j] = apply_pair(p.x, ps[j], p.y);
         }
     if (tiles.segs == 1) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) h[j] = step_state(pm[j], start[j], ps[j]);
+        for (int j = 0; j < V; ++j) h[j] = apply_pair(pm[j], start[j], ps[j]);
         return;
     }
     word_t *own = words_of<V>(tiles, bi, seg, strip) + lane * V;
     float bm[V], bs[V];             // of the block
-    if (wave == kW - 1) {
+    if (wave == W - 1) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             bm[j] = both_decays(pm[j], m[j]);
-            bs[j] = step_state(m[j], ps[j], s[j]);
+            bs[j] = apply_pair(m[j], ps[j], s[j]);
             publish(own + j, word_of(bm[j], bs[j]));
         }
     }
-    const int n = min(kW, seg);     // blocks before that are looked at
-    const int back = kW - wave;     // this wave's: 1 is the nearest
-    bool lost = false;
-    if (back <= n) {
-        const word_t *p = words_of<V>(tiles, bi, seg - back, strip) + lane * V;
+    constexpr int kNear = ChainLds<V, W>::kNear, kFar = ChainLds<V, W>::kFar;
+    const int back = W - wave;      // this wave's of the blocks before: 1 is the nearest
+    const float nan = __uint_as_float(0x7fc00000u);
+    // the words of the block `at` before, into its place
+    auto gather = [&](int at) {
+        const word_t *p = words_of<V>(tiles, bi, seg - at, strip) + lane * V;
         word_t w[V], o[V];
-        int spins = 0;
-        while (!look_all<V>(p, w) && ++spins < kSpins) __builtin_amdgcn_s_sleep(1);
-        const bool state = look_all<V>(p + 64 * V, o);
-        lost = spins >= kSpins;
+        bool state = false, there = false;
+#pragma unroll 1
+        for (int spins = 0; spins < kSpins; ++spins) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) { w[j] = look(p + j); o[j] = look(p + 64 * V + j); }
+            state = all_there<V>(o);
+            there = state || all_there<V>(w);
+            if (there) break;
+            __builtin_amdgcn_s_sleep(1);
+        }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const word_t v = state ? o[j] : w[j];
-            lds.before[back - 1][lane * V + j] = make_float2(first_of(v), lost ? __uint_as_float(0x7fc00000u) : second_of(v));
+            const word_t pair = w[j], out = o[j], v = state ? out : pair;
+            lds.before[at - 1][lane * V + j] = make_float2(first_of(v), there ? second_of(v) : nan);
         }
-        if (lane == 0) lds.state[back - 1] = state;
-    }
+        if (lane == 0) lds.state[at - 1] = state;
+    };
+    // the nearest state among the first n places; n: none
+    auto nearest = [&](int n) {
+        const unsigned long long have = __ballot(lane < n && lds.state[lane < n ? lane : 0]);
+        return have ? int(__builtin_ctzll(have)) : n;
+    };
+    int n = min(kNear, seg), k = 0;
+    if (back <= n) gather(back);
     __syncthreads();
     float in[V];
-    int k = 0;                      // the nearest state
-    while (k < n && !lds.state[k]) ++k;
     if (seg == 0) {
 #pragma unroll
         for (int j = 0; j < V; ++j) in[j] = start[j];
-    } else if (k < n) {
+    } else {
+        k = nearest(n);
+        if (k == n && seg > n) {    // the block runs far ahead of the states
+            n = min(kNear * (1 + kFar), seg);
+            if (back <= kNear)
+#pragma unroll 1
+                for (int at = back + kNear; at <= n; at += kNear) gather(at);
+            __syncthreads();
+            k = nearest(n);
+        }
+        if (k < n) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) in[j] = lds.before[k][lane * V + j].y;
-    } else {                        // none yet: the furthest one's
-        const word_t *p = words_of<V>(tiles, bi, seg - n, strip) + 64 * V + lane * V;
-        word_t o[V];
-        int spins = 0;
-        while (!look_all<V>(p, o) && ++spins < kSpins) __builtin_amdgcn_s_sleep(1);
-        k = n - 1;
+            for (int j = 0; j < V; ++j) in[j] = lds.before[k][lane * V + j].y;
+        } else {                    // none yet: the furthest one's
+            const word_t *p = words_of<V>(tiles, bi, seg - n, strip) + 64 * V + lane * V;
+            word_t o[V];
+            int spins = 0;
+#pragma unroll 1
+            while (!look_all<V>(p, o) && ++spins < kSpins) __builtin_amdgcn_s_sleep(1);
+            k = n - 1;
 #pragma unroll
-        for (int j = 0; j < V; ++j) in[j] = spins < kSpins ? second_of(o[j]) : __uint_as_float(0x7fc00000u);
+            for (int j = 0; j < V; ++j) in[j] = spins < kSpins ? second_of(o[j]) : nan;
+        }
     }
+#pragma unroll 2
     for (int i = k - 1; i >= 0; --i)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const float2 p = lds.before[i][lane * V + j];
-            in[j] = step_state(p.x, in[j], p.y);
+            in[j] = apply_pair(p.x, in[j], p.y);
         }
-    if (wave == kW - 1)
+    if (wave == W - 1)
 #pragma unroll
-        for (int j = 0; j < V; ++j) publish(own + 64 * V + j, word_of(0.f, step_state(bm[j], in[j], bs[j])));
+        for (int j = 0; j < V; ++j) publish(own + 64 * V + j, word_of(0.f, apply_pair(bm[j], in[j], bs[j])));
 #pragma unroll
-    for (int j = 0; j < V; ++j) h[j] = step_state(pm[j], in[j], ps[j]);
+    for (int j = 0; j < V; ++j) h[j] = apply_pair(pm[j], in[j], ps[j]);
 }
 
 // A block's place: strip fastest, then the batch row, then the stretch of the sequence.
-template <int V>
-__device__ __forceinline__ void place_of(const Tiles &tiles, ChainLds<V> &lds, int &bi, int &seg, int &strip) {
+template <int V, int W>
+__device__ __forceinline__ void place_of(const Tiles &tiles, ChainLds<V, W> &lds, int &bi, int &seg, int &strip) {
     unsigned p = blockIdx.x;
     if (tiles.segs > 1) {
         if (threadIdx.x == 0) lds.place = atomicAdd(tiles.counter, 1u);
@@ -241,49 +316,53 @@ __device__ __forceinline__ void place_of(const Tiles &tiles, ChainLds<V> &lds, i
 }
 
 // --------------------------------------------------------------------------- forward
-template <typename IO, typename AIO, bool SIGMOID, int V>
-__global__ __launch_bounds__(64 * kW) void k_gated_scan_fwd(const IO *__restrict__ x, const AIO *__restrict__ a,
+template <typename IO, typename AIO, bool SIGMOID, int V, int T, int W>
+__global__ __launch_bounds__(64 * W, 4) void k_gated_scan_fwd(const IO *__restrict__ x, const AIO *__restrict__ a,
                                                             const float *__restrict__ init_state, IO *__restrict__ y,
                                                             float *__restrict__ kept, float *__restrict__ final_state,
                                                             int L, int D, Tiles tiles) {
-    __shared__ ChainLds<V> lds;
+    __shared__ ChainLds<V, W> lds;
     int bi, seg, strip;
-    place_of<V>(tiles, lds, bi, seg, strip);
+    place_of<V, W>(tiles, lds, bi, seg, strip);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = strip * 64 * V + lane * V;
     const bool on = c < D;                  // V divides D
     const int cl = on ? c : 0;
-    const int t0 = (seg * kW + wave) * kT, n = min(kT, L - t0);     // n <= 0: past the end
+    const int t0 = (seg * W + wave) * T, n = min(T, L - t0);     // n <= 0: past the end
     const size_t row = size_t(bi) * L + t0;
 
-    Raw<IO, V> xr[kT];
-    float m[kT][V], pm[V], ps[V];
+    Raw<IO, V> xr[T];
+    float m[T][V], pm[V], ps[V];
     if (n > 0) {
-        Raw<AIO, V> ar[kT];
-        load_rows<AIO, V>(a + row * D + cl, D, n, ar);
-        load_rows<IO, V>(x + row * D + cl, D, n, xr);
-        if (n < kT) {                       // tokens that leave the state as it is
+        Raw<AIO, V> ar[T];
+        rows_at(a + row * D, n, D, cl).template load_all<AIO, V, T>(n, ar);
+        rows_at(x + row * D, n, D, cl).template load_all<IO, V, T>(n, xr);
+        if (n < T) {                       // tokens that leave the state as it is
 #pragma unroll
-            for (int t = 0; t < kT; ++t)
+            for (int t = 0; t < T; ++t)
                 if (t >= n) {
                     ar[t] = raw_same<AIO, V>(SIGMOID ? __builtin_inff() : 0.f);
                     xr[t] = raw_same<IO, V>(0.f);
                 }
         }
+        // token by token: a gate takes the place of the values that it comes from
+        Decay<SIGMOID> d[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            Decay<SIGMOID> d;
-            float s = 0.f;
+        for (int j = 0; j < V; ++j) ps[j] = 0.f;
 #pragma unroll
-            for (int t = 0; t < kT; ++t) {
+        for (int t = 0; t < T; ++t) {
+            ar[t] = again<AIO, V>(ar[t]);
+            xr[t] = again<IO, V>(xr[t]);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
                 const float av = ar[t].get(j);
                 m[t][j] = gate_of<SIGMOID>(av);
-                d.token(m[t][j], av);
-                s = step_state(m[t][j], s, entering<SIGMOID>(m[t][j], xr[t].get(j)));
+                d[j].token(m[t][j], av);
+                ps[j] = step_state<SIGMOID>(m[t][j], ps[j], xr[t].get(j));
             }
-            pm[j] = d.m();
-            ps[j] = s;
         }
+#pragma unroll
+        for (int j = 0; j < V; ++j) pm[j] = d[j].m();
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) { pm[j] = 1.f; ps[j] = 0.f; }
@@ -291,18 +370,21 @@ __global__ __launch_bounds__(64 * kW) void k_gated_scan_fwd(const IO *__restrict
     float start[V], h[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) start[j] = init_state ? init_state[size_t(bi) * D + cl + j] : 0.f;
-    enter<V>(tiles, lds, bi, seg, strip, wave, lane, pm, ps, start, h);
+    enter<V, W>(tiles, lds, bi, seg, strip, wave, lane, pm, ps, start, h);
     if (n <= 0 || !on) return;
-    if (kept) {
-        float *k = kept + (size_t(bi) * ((unsigned(L) + kT - 1) / kT) + t0 / kT) * D + c;
+    if (kept && t0 % kGatedScanKeep == 0) {
+        float *k = kept + (size_t(bi) * ((unsigned(L) + kGatedScanKeep - 1) / kGatedScanKeep) + t0 / kGatedScanKeep) * D + c;
 #pragma unroll
         for (int j = 0; j < V; ++j) k[j] = h[j];
     }
+    // without y the rows' view is empty, and what is stored into it is dropped
+    const Rows out = rows_at(y ? y + row * D : y, y ? n : 0, D, c);
 #pragma unroll
-    for (int t = 0; t < kT; ++t) {
+    for (int t = 0; t < T; ++t) {
+        xr[t] = again<IO, V>(xr[t]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) h[j] = step_state(m[t][j], h[j], entering<SIGMOID>(m[t][j], xr[t].get(j)));
-        if (y && t < n) *reinterpret_cast<Raw<IO, V> *>(y + (row + t) * D + c) = raw_of<IO, V>(h);
+        for (int j = 0; j < V; ++j) h[j] = step_state<SIGMOID>(here(m[t][j]), h[j], xr[t].get(j));
+        if (t < n) out.template store<IO, V>(t, raw_of<IO, V>(h));
     }
     if (final_state && t0 + n == L)
 #pragma unroll
@@ -311,56 +393,81 @@ __global__ __launch_bounds__(64 * kW) void k_gated_scan_fwd(const IO *__restrict
 
 // -------------------------------------------------------------------------- backward
 // The order of the scan is that of the tokens backwards: segment and wave 0 are the last.
-template <typename IO, typename AIO, bool SIGMOID, int V>
-__global__ __launch_bounds__(64 * kW) void k_gated_scan_bwd(const IO *__restrict__ x, const AIO *__restrict__ a,
+template <typename IO, typename AIO, bool SIGMOID, int V, int T, int W>
+__global__ __launch_bounds__(64 * W, T == kGatedScanKeep ? 2 : 4) void k_gated_scan_bwd(const IO *__restrict__ x, const AIO *__restrict__ a,
                                                             const float *__restrict__ kept, const IO *__restrict__ dy,
                                                             const float *__restrict__ d_final, IO *__restrict__ dx,
                                                             AIO *__restrict__ da, float *__restrict__ d_init, int L,
                                                             int D, Tiles tiles) {
-    __shared__ ChainLds<V> lds;
+    // waves of a kept state's stretch, and what each does to the state (forward)
+    constexpr int kParts = kGatedScanKeep / T;
+    static_assert(W % kParts == 0);
+    __shared__ float2 ahead[kParts > 1 ? W : 1][64 * V];
+    __shared__ ChainLds<V, W> lds;
     int bi, seg, strip;
-    place_of<V>(tiles, lds, bi, seg, strip);
+    place_of<V, W>(tiles, lds, bi, seg, strip);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = strip * 64 * V + lane * V;
     const bool on = c < D;
     const int cl = on ? c : 0;
-    const int t0 = ((tiles.segs - 1 - seg) * kW + kW - 1 - wave) * kT, n = min(kT, L - t0);
+    const int t0 = ((tiles.segs - 1 - seg) * W + W - 1 - wave) * T, n = min(T, L - t0);
     const size_t row = size_t(bi) * L + t0;
 
-    Raw<IO, V> xr[kT], gr[kT];
-    float m[kT][V], before[kT][V], pm[V], ps[V];
-    if (n > 0) {
-        Raw<AIO, V> ar[kT];
-        load_rows<AIO, V>(a + row * D + cl, D, n, ar);
-        load_rows<IO, V>(dy + row * D + cl, D, n, gr);
-        load_rows<IO, V>(x + row * D + cl, D, n, xr);
-        if (n < kT) {
+    Raw<IO, V> xr[T], gr[T];
+    float m[T][V], slope[T][V], pm[V], ps[V], h[V];
+    // what da_t is g_{t-1} times: h_{t-1}, or beta_t (h_{t-1} - x_t); x is done with then
+    auto slopes = [&]() {
 #pragma unroll
-            for (int t = 0; t < kT; ++t)
+        for (int t = 0; t < T; ++t) {
+            xr[t] = again<IO, V>(xr[t]);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float xv = xr[t].get(j), hb = h[j], mt = here(m[t][j]);
+                h[j] = step_state<SIGMOID>(mt, hb, xv);
+                slope[t][j] = SIGMOID ? beta_of(mt) * (hb - xv) : hb;
+            }
+        }
+    };
+    if (n > 0) {
+        Raw<AIO, V> ar[T];
+        rows_at(a + row * D, n, D, cl).template load_all<AIO, V, T>(n, ar);
+        rows_at(dy + row * D, n, D, cl).template load_all<IO, V, T>(n, gr);
+        rows_at(x + row * D, n, D, cl).template load_all<IO, V, T>(n, xr);
+        if (n < T) {
+#pragma unroll
+            for (int t = 0; t < T; ++t)
                 if (t >= n) {
                     ar[t] = raw_same<AIO, V>(SIGMOID ? __builtin_inff() : 0.f);
                     gr[t] = xr[t] = raw_same<IO, V>(0.f);
                 }
         }
-        const float *k = kept + (size_t(bi) * ((unsigned(L) + kT - 1) / kT) + t0 / kT) * D + cl;
+        const float *k = kept + (size_t(bi) * ((unsigned(L) + kGatedScanKeep - 1) / kGatedScanKeep) + t0 / kGatedScanKeep) * D + cl;
+        Decay<SIGMOID> d[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            Decay<SIGMOID> d;
-            float g = 0.f;
+        for (int j = 0; j < V; ++j) { ps[j] = 0.f; h[j] = k[j]; }
 #pragma unroll
-            for (int t = kT - 1; t >= 0; --t) {
+        for (int t = T - 1; t >= 0; --t) {
+            ar[t] = again<AIO, V>(ar[t]);
+            gr[t] = again<IO, V>(gr[t]);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
                 const float av = ar[t].get(j);
                 m[t][j] = gate_of<SIGMOID>(av);
-                d.token(m[t][j], av);
-                g = step_state(m[t][j], gr[t].get(j) + g, 0.f);
+                d[j].token(m[t][j], av);
+                ps[j] = decayed(m[t][j], gr[t].get(j) + ps[j]);
             }
-            pm[j] = d.m();
-            ps[j] = g;
-            float h = k[j];
+        }
 #pragma unroll
-            for (int t = 0; t < kT; ++t) {
-                before[t][j] = h;
-                h = step_state(m[t][j], h, entering<SIGMOID>(m[t][j], xr[t].get(j)));
+        for (int j = 0; j < V; ++j) pm[j] = d[j].m();
+        if constexpr (kParts == 1) {
+            slopes();
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float sf = 0.f;
+#pragma unroll
+                for (int t = 0; t < T; ++t) sf = step_state<SIGMOID>(m[t][j], sf, xr[t].get(j));
+                ahead[wave][lane * V + j] = make_float2(pm[j], sf);
             }
         }
     } else {
@@ -370,21 +477,35 @@ __global__ __launch_bounds__(64 * kW) void k_gated_scan_bwd(const IO *__restrict
     float start[V], g[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) start[j] = d_final ? d_final[size_t(bi) * D + cl + j] : 0.f;
-    enter<V>(tiles, lds, bi, seg, strip, wave, lane, pm, ps, start, g);
+    enter<V, W>(tiles, lds, bi, seg, strip, wave, lane, pm, ps, start, g);
     if (n <= 0 || !on) return;
+    if constexpr (kParts > 1) {
+        // from the kept state over the waves between it and this one's tokens
+        const int part = t0 / T % kParts;
+#pragma unroll 1
+        for (int k = part; k > 0; --k)
 #pragma unroll
-    for (int t = kT - 1; t >= 0; --t) {
+            for (int j = 0; j < V; ++j) {
+                const float2 p = ahead[wave + k][lane * V + j];
+                h[j] = apply_pair(p.x, h[j], p.y);
+            }
+        slopes();
+    }
+    const Rows outx = rows_at(dx + row * D, n, D, c), outa = rows_at(da + row * D, n, D, c);
+#pragma unroll
+    for (int t = T - 1; t >= 0; --t) {
         if (t >= n) continue;
         float ox[V], oa[V];
+        gr[t] = again<IO, V>(gr[t]);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float lam = gr[t].get(j) + g[j];
-            g[j] = step_state(m[t][j], lam, 0.f);
-            ox[j] = SIGMOID ? beta_of(m[t][j]) * lam : lam;
-            oa[j] = SIGMOID ? g[j] * beta_of(m[t][j]) * (before[t][j] - xr[t].get(j)) : g[j] * before[t][j];
+            const float lam = gr[t].get(j) + g[j], mt = here(m[t][j]);
+            g[j] = decayed(mt, lam);
+            ox[j] = SIGMOID ? beta_of(mt) * lam : lam;
+            oa[j] = g[j] * slope[t][j];
         }
-        *reinterpret_cast<Raw<IO, V> *>(dx + (row + t) * D + c) = raw_of<IO, V>(ox);
-        *reinterpret_cast<Raw<AIO, V> *>(da + (row + t) * D + c) = raw_of<AIO, V>(oa);
+        outx.template store<IO, V>(t, raw_of<IO, V>(ox));
+        outa.template store<AIO, V>(t, raw_of<AIO, V>(oa));
     }
     if (d_init && t0 == 0)
 #pragma unroll
@@ -392,22 +513,46 @@ __global__ __launch_bounds__(64 * kW) void k_gated_scan_bwd(const IO *__restrict
 }
 
 // ---------------------------------------------------------------------------- launches
+__global__ __launch_bounds__(256) void k_gated_scan_clear(uint4 *p, size_t n) {
+    const size_t i = size_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i < n) p[i] = make_uint4(0, 0, 0, 0);
+}
+
 // Channels of a lane: two bf16 in one 4-byte access where the rows allow it.
 int lane_channels(int D, bool bf16) { return bf16 && D % 2 == 0 ? 2 : 1; }
 
+// Tokens of a block: W waves of T tokens.  Much work takes long stretches (fewer pairs to hand
+// on for as many bytes): forward 8 x 32 tokens, backward 4 x 32 with two channels a lane (186
+// registers, of which a SIMD holds two waves) and 16 x 16 with one (66 registers).  Less than a
+// block of 128 tokens for every CU takes 8 x 16, unless the sequence is so long that the
+// chain from block to block counts for more; and so do sequences that end within one.
 struct Shape {
-    int V;
+    int V, T, W;
     int64_t strips, segs, blocks;
 };
 
-Shape shape_of(int b, int L, int D, bool bf16) {
+constexpr int kFwdT = 32, kFwdW = 8;
+template <int V> constexpr int kBwdT = V == 2 ? 32 : 16;
+template <int V> constexpr int kBwdW = V == 2 ? 4 : 16;
+constexpr int kShortT = 16, kShortW = 8, kShort = kShortT * kShortW, kCus = 256, kLongChain = 32;
+
+Shape shape_of(int b, int L, int D, bool bf16, bool backward) {
     Shape s;
     s.V = lane_channels(D, bf16);
     s.strips = (int64_t(D) + 64 * s.V - 1) / (64 * s.V);
-    s.segs = (int64_t(L) + kT * kW - 1) / (kT * kW);
+    s.segs = (int64_t(L) + kShort - 1) / kShort;
+    s.T = kShortT;
+    s.W = kShortW;
+    if (s.segs > 1 && (s.strips * s.segs * b > kCus || s.segs > kLongChain)) {
+        s.T = !backward ? kFwdT : s.V == 2 ? kBwdT<2> : kBwdT<1>;
+        s.W = !backward ? kFwdW : s.V == 2 ? kBwdW<2> : kBwdW<1>;
+        s.segs = (int64_t(L) + s.T * s.W - 1) / (s.T * s.W);
+    }
     s.blocks = s.strips * s.segs * b;
     return s;
 }
+
+size_t words_bytes(const Shape &s) { return s.segs <= 1 ? 0 : 16 + size_t(s.blocks) * 64 * s.V * 2 * sizeof(word_t); }
 
 hipError_t tiles_of(const GatedScanArgs &a, const Shape &s, Tiles &t, hipStream_t stream) {
     t.strips = int(s.strips);
@@ -418,59 +563,75 @@ hipError_t tiles_of(const GatedScanArgs &a, const Shape &s, Tiles &t, hipStream_
     if (s.segs <= 1) return hipSuccess;
     t.counter = static_cast<unsigned *>(a.workspace);
     t.words = reinterpret_cast<word_t *>(static_cast<char *>(a.workspace) + 16);
-    return launch_copy_state(nullptr, static_cast<float *>(a.workspace), gated_scan_workspace(a.b, a.L, a.D, a.bf16) / 4, stream);
+    const size_t n = words_bytes(s) / 16;
+    hipLaunchKernelGGL(k_gated_scan_clear, dim3(unsigned((n + 255) / 256)), dim3(256), 0, stream, static_cast<uint4 *>(a.workspace), n);
+    return hipGetLastError();
 }
 
-template <typename IO, typename AIO, int V>
+template <typename IO, typename AIO, int V, int T, int W>
 hipError_t fwd(const GatedScanArgs &s, const Shape &shape, const Tiles &tiles, hipStream_t stream) {
     auto run = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(unsigned(shape.blocks)), dim3(64 * kW), 0, stream, static_cast<const IO *>(s.x),
+        hipLaunchKernelGGL(kernel, dim3(unsigned(shape.blocks)), dim3(64 * W), 0, stream, static_cast<const IO *>(s.x),
                            static_cast<const AIO *>(s.a), s.init_state, static_cast<IO *>(s.y), s.kept, s.final_state, s.L, s.D, tiles);
         return hipGetLastError();
     };
-    return s.sigmoid ? run(k_gated_scan_fwd<IO, AIO, true, V>) : run(k_gated_scan_fwd<IO, AIO, false, V>);
+    return s.sigmoid ? run(k_gated_scan_fwd<IO, AIO, true, V, T, W>) : run(k_gated_scan_fwd<IO, AIO, false, V, T, W>);
 }
 
-template <typename IO, typename AIO, int V>
+template <typename IO, typename AIO, int V, int T, int W>
 hipError_t bwd(const GatedScanArgs &s, const Shape &shape, const Tiles &tiles, hipStream_t stream) {
     auto run = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(unsigned(shape.blocks)), dim3(64 * kW), 0, stream, static_cast<const IO *>(s.x),
+        hipLaunchKernelGGL(kernel, dim3(unsigned(shape.blocks)), dim3(64 * W), 0, stream, static_cast<const IO *>(s.x),
                            static_cast<const AIO *>(s.a), s.kept, static_cast<const IO *>(s.dy), s.d_final,
                            static_cast<IO *>(s.dx), static_cast<AIO *>(s.da), s.d_init, s.L, s.D, tiles);
         return hipGetLastError();
     };
-    return s.sigmoid ? run(k_gated_scan_bwd<IO, AIO, true, V>) : run(k_gated_scan_bwd<IO, AIO, false, V>);
+    return s.sigmoid ? run(k_gated_scan_bwd<IO, AIO, true, V, T, W>) : run(k_gated_scan_bwd<IO, AIO, false, V, T, W>);
+}
+
+// f(IO{}, AIO{}, V) for the call's types and channels of a lane.
+template <class F>
+hipError_t by_types(const GatedScanArgs &a, int V, F &&f) {
+    using std::integral_constant;
+    if (!a.bf16) return f(float{}, float{}, integral_constant<int, 1>{});
+    if (V == 2) return a.a_bf16 ? f(bf16_bits{}, bf16_bits{}, integral_constant<int, 2>{}) : f(bf16_bits{}, float{}, integral_constant<int, 2>{});
+    return a.a_bf16 ? f(bf16_bits{}, bf16_bits{}, integral_constant<int, 1>{}) : f(bf16_bits{}, float{}, integral_constant<int, 1>{});
 }
 
 }  // namespace
 
-// the kernels count tokens and channels in 31 bits, up to a block past the last one, and
-// blocks in 31
+// the kernels count tokens in 31 bits, up to a block past the last one, and the bytes of a
+// wave's rows in 32; the blocks have to stay inside a launch (2^32 threads)
 bool gated_scan_supported(int b, int L, int D) {
-    return b <= 65535 && L <= INT_MAX - kT * kW && D <= INT_MAX - 256 && shape_of(b, L, D, false).blocks <= (1 << 22);
+    return b <= 65535 && L <= INT_MAX - 256 && D <= (1 << 24) &&
+           b * ((int64_t(L) + 127) / 128) * ((int64_t(D) + 63) / 64) <= (1 << 21);
 }
 
-size_t gated_scan_workspace(int b, int L, int D, bool bf16) {
-    const Shape s = shape_of(b, L, D, bf16);
-    return s.segs <= 1 ? 0 : 16 + size_t(s.blocks) * 64 * s.V * 2 * sizeof(word_t);
-}
+size_t gated_scan_workspace(int b, int L, int D, bool bf16, bool backward) { return words_bytes(shape_of(b, L, D, bf16, backward)); }
 
 hipError_t launch_gated_scan_fwd(const GatedScanArgs &a, hipStream_t stream) {
-    const Shape s = shape_of(a.b, a.L, a.D, a.bf16);
+    const Shape s = shape_of(a.b, a.L, a.D, a.bf16, false);
     Tiles t;
     if (const hipError_t e = tiles_of(a, s, t, stream); e != hipSuccess) return e;
-    if (!a.bf16) return fwd<float, float, 1>(a, s, t, stream);
-    if (s.V == 2) return a.a_bf16 ? fwd<bf16_bits, bf16_bits, 2>(a, s, t, stream) : fwd<bf16_bits, float, 2>(a, s, t, stream);
-    return a.a_bf16 ? fwd<bf16_bits, bf16_bits, 1>(a, s, t, stream) : fwd<bf16_bits, float, 1>(a, s, t, stream);
+    return by_types(a, s.V, [&](auto io, auto aio, auto v) {
+        using IO = decltype(io);
+        using AIO = decltype(aio);
+        if (s.T == kFwdT) return fwd<IO, AIO, v(), kFwdT, kFwdW>(a, s, t, stream);
+        return fwd<IO, AIO, v(), kShortT, kShortW>(a, s, t, stream);
+    });
 }
 
 hipError_t launch_gated_scan_bwd(const GatedScanArgs &a, hipStream_t stream) {
-    const Shape s = shape_of(a.b, a.L, a.D, a.bf16);
+    const Shape s = shape_of(a.b, a.L, a.D, a.bf16, true);
     Tiles t;
     if (const hipError_t e = tiles_of(a, s, t, stream); e != hipSuccess) return e;
-    if (!a.bf16) return bwd<float, float, 1>(a, s, t, stream);
-    if (s.V == 2) return a.a_bf16 ? bwd<bf16_bits, bf16_bits, 2>(a, s, t, stream) : bwd<bf16_bits, float, 2>(a, s, t, stream);
-    return a.a_bf16 ? bwd<bf16_bits, bf16_bits, 1>(a, s, t, stream) : bwd<bf16_bits, float, 1>(a, s, t, stream);
+    return by_types(a, s.V, [&](auto io, auto aio, auto v) {
+        using IO = decltype(io);
+        using AIO = decltype(aio);
+        constexpr int V = v(), T = kBwdT<V>, W = kBwdW<V>;
+        if (s.T == T && s.W == W) return bwd<IO, AIO, V, T, W>(a, s, t, stream);
+        return bwd<IO, AIO, V, kShortT, kShortW>(a, s, t, stream);
+    });
 }
 
 }  // namespace ssd

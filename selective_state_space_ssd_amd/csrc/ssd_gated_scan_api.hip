@@ -1,6 +1,8 @@
 // ssd_gated_scan_api.hip -- host-side checks and dispatch of the gated scan.
 #include <limits.h>
 
+#include <algorithm>
+
 #include "ssd_checks.h"
 #include "ssd_gated_scan.h"
 #include "ssd_kernels.h"
@@ -26,7 +28,12 @@ size_t kept_bytes(int b, int L, int D) {
     return size_t(b) * ((size_t(L) + SSD_GATED_SCAN_KEEP - 1) / SSD_GATED_SCAN_KEEP) * D * 4;
 }
 
-size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+// Of the backward call without its kept states: the two passes that it may run use the same place.
+size_t words_bytes(int b, int L, int D, ssd_dtype_t io) {
+    const bool bf16 = io == SSD_DTYPE_BF16;
+    const size_t n = std::max(ssd::gated_scan_workspace(b, L, D, bf16, false), ssd::gated_scan_workspace(b, L, D, bf16, true));
+    return (n + 15) / 16 * 16;
+}
 
 ssd_status_t done(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
 
@@ -60,7 +67,7 @@ ssd_status_t ssd_gated_scan_step(const float *state_in, const void *x, const voi
 
 size_t ssd_gated_scan_fwd_workspace_bytes(int b, int L, int D, ssd_dtype_t io, ssd_dtype_t a_io) {
     if (check_dims(b, L, D, io, a_io) != SSD_OK) return size_t(-1);
-    return ssd::gated_scan_workspace(b, L, D, io == SSD_DTYPE_BF16);
+    return ssd::gated_scan_workspace(b, L, D, io == SSD_DTYPE_BF16, false);
 }
 
 ssd_status_t ssd_gated_scan_fwd(const void *x, const void *a, const float *init_state, void *y,
@@ -78,7 +85,7 @@ ssd_status_t ssd_gated_scan_fwd(const void *x, const void *a, const float *init_
     if (!x || !a || !y) return SSD_ERR_NULL_ARG;
     if (!aligned(x, 16) || !aligned(a, 16) || !aligned(y, 16) || !aligned(states, 16) || !aligned(workspace, 16))
         return SSD_ERR_ALIGN;
-    const size_t need = ssd::gated_scan_workspace(b, L, D, io == SSD_DTYPE_BF16);
+    const size_t need = ssd::gated_scan_workspace(b, L, D, io == SSD_DTYPE_BF16, false);
     if (need && (!workspace || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
     const Range ins[] = {Range(x, n * elem(io)), Range(a, n * elem(a_io)), rinit};
     const Range outs[] = {Range(y, n * elem(io)), Range(states, kept_bytes(b, L, D)), rfinal, Range(workspace, need)};
@@ -92,7 +99,7 @@ ssd_status_t ssd_gated_scan_fwd(const void *x, const void *a, const float *init_
 size_t ssd_gated_scan_bwd_workspace_bytes(int b, int L, int D, int with_states, ssd_dtype_t io,
                                           ssd_dtype_t a_io) {
     if (check_dims(b, L, D, io, a_io) != SSD_OK) return size_t(-1);
-    return up16(ssd::gated_scan_workspace(b, L, D, io == SSD_DTYPE_BF16)) + (with_states ? 0 : kept_bytes(b, L, D));
+    return words_bytes(b, L, D, io) + (with_states ? 0 : kept_bytes(b, L, D));
 }
 
 ssd_status_t ssd_gated_scan_bwd(const void *x, const void *a, const float *init_state,
@@ -112,8 +119,7 @@ ssd_status_t ssd_gated_scan_bwd(const void *x, const void *a, const float *init_
     if (!aligned(x, 16) || !aligned(a, 16) || !aligned(init_state, 16) || !aligned(states, 16) || !aligned(dy, 16) ||
         !aligned(dx, 16) || !aligned(da, 16) || !aligned(workspace, 16))
         return SSD_ERR_ALIGN;
-    const size_t own = ssd::gated_scan_workspace(b, L, D, io == SSD_DTYPE_BF16);
-    const size_t need = states ? up16(own) : up16(own) + kept_bytes(b, L, D);
+    const size_t own = words_bytes(b, L, D, io), need = own + (states ? 0 : kept_bytes(b, L, D));
     if (need && (!workspace || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
     const Range ins[] = {Range(x, n * elem(io)), Range(a, n * elem(a_io)), Range(states ? nullptr : init_state, st),
                          Range(states, kept_bytes(b, L, D)), Range(dy, n * elem(io)), rfinal};
@@ -126,7 +132,7 @@ ssd_status_t ssd_gated_scan_bwd(const void *x, const void *a, const float *init_
         s.kept = const_cast<float *>(states);       // read only
     } else {
         // the states of the forward pass once more, without its outputs
-        s.kept = reinterpret_cast<float *>(static_cast<char *>(workspace) + up16(own));
+        s.kept = reinterpret_cast<float *>(static_cast<char *>(workspace) + own);
         if (const hipError_t e = ssd::launch_gated_scan_fwd(s, stream); e != hipSuccess) return SSD_ERR_HIP;
     }
     s.dy = dy; s.d_final = d_final; s.dx = dx; s.da = da; s.d_init = d_init;

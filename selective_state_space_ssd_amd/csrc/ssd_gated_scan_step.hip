@@ -28,7 +28,7 @@ __global__ __launch_bounds__(kBlock) void k_gated_scan_step(const float *state_i
     for (int t = 0; t < K; ++t) {
         const size_t at = (size_t(bi) * K + t) * D + c;
         const float m = gate_of<SIGMOID>(to_f32<AIO>(a[at]));
-        h = step_state(m, h, entering<SIGMOID>(m, to_f32<IO>(x[at])));
+        h = step_state<SIGMOID>(m, h, to_f32<IO>(x[at]));
         y[at] = from_f32<IO>(h);
         if (t + 1 == acc) kept = h;
     }
