@@ -19,7 +19,7 @@
 //     block's outgoing state is there too,
 //   - all fold the pairs behind the nearest such state, one by one, into the entering state
 //     (the same operations in the same order whichever block that was, so results repeat),
-//   - the last wave publishes the outgoing state.
+//   - the last wave publishes the outgoing state in the pair's place.
 // Blocks take their places from a counter, earlier stretches first, so whatever a block
 // waits for belongs to a block that is running already.  A pair or a state is one 8-byte
 // word, written at once and never zero; zero means not there yet.
@@ -141,19 +141,19 @@ struct Decay {
 
 typedef unsigned long long word_t;
 
-// Never zero: the complement of two floats of which the first is not all ones.
-__device__ __forceinline__ word_t word_of(float first, float second) {
-    const uint32_t f = first == first ? __float_as_uint(first) : 0x7fc00000u;
-    return ~(word_t(f) << 32 | __float_as_uint(second));
-}
-__device__ __forceinline__ float first_of(word_t w) { return __uint_as_float(uint32_t(~w >> 32)); }
+// A pair (m, S), or a state behind a mark that no m is.  Never zero: the complement of two floats
+// of which the first is not all ones.
+constexpr uint32_t kNan = 0x7fc00000u, kState = 0x7fc00001u;
+__device__ __forceinline__ word_t word_of(uint32_t first, float second) { return ~(word_t(first) << 32 | __float_as_uint(second)); }
+__device__ __forceinline__ word_t pair_word(float m, float s) { return word_of(m == m ? __float_as_uint(m) : kNan, s); }
+__device__ __forceinline__ word_t state_word(float h) { return word_of(kState, h); }
+__device__ __forceinline__ uint32_t first_of(word_t w) { return uint32_t(~w >> 32); }
 __device__ __forceinline__ float second_of(word_t w) { return __uint_as_float(uint32_t(~w)); }
 
 __device__ __forceinline__ word_t look(const word_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ void publish(word_t *p, word_t w) { __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
-// Workspace: the counter (16 bytes), then per block 64 V words of its pair and 64 V of its
-// outgoing state.
+// Workspace: the counter (16 bytes), then per block 64 V words.
 struct Tiles {
     word_t *words;          // null: one block a strip, nothing to wait for
     unsigned *counter;
@@ -162,23 +162,26 @@ struct Tiles {
 
 template <int V>
 __device__ __forceinline__ word_t *words_of(const Tiles &s, int bi, int seg, int strip) {
-    return s.words + ((size_t(seg) * s.b + bi) * s.strips + strip) * (2 * 64 * V);
+    return s.words + ((size_t(seg) * s.b + bi) * s.strips + strip) * (64 * V);
 }
 
-// Whether all V words of every lane are there.
-template <int V>
-__device__ __forceinline__ bool all_there(const word_t (&w)[V]) {
-    bool there = true;
-#pragma unroll
-    for (int j = 0; j < V; ++j) there = there && w[j] != 0;
-    return __all(there);
-}
+enum Seen { kNothing, kPairs, kStates };
 
+// What all V words of every lane are; kNothing while they differ.
 template <int V>
-__device__ __forceinline__ bool look_all(const word_t *p, word_t (&w)[V]) {
+__device__ __forceinline__ Seen look_all(const word_t *p, word_t (&w)[V]) {
+    bool there = true, state = true, pair = true;
 #pragma unroll
     for (int j = 0; j < V; ++j) w[j] = look(p + j);
-    return all_there<V>(w);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const bool is_state = first_of(w[j]) == kState;
+        there = there && w[j] != 0;
+        state = state && is_state;
+        pair = pair && !is_state;
+    }
+    if (!__all(there)) return kNothing;
+    return __all(state) ? kStates : __all(pair) ? kPairs : kNothing;
 }
 
 template <int V, int W>
@@ -223,32 +226,27 @@ __device__ __forceinline__ void enter(const Tiles &tiles, ChainLds<V, W> &lds, i
         for (int j = 0; j < V; ++j) {
             bm[j] = both_decays(pm[j], m[j]);
             bs[j] = apply_pair(m[j], ps[j], s[j]);
-            publish(own + j, word_of(bm[j], bs[j]));
+            publish(own + j, pair_word(bm[j], bs[j]));
         }
     }
     constexpr int kNear = ChainLds<V, W>::kNear, kFar = ChainLds<V, W>::kFar;
     const int back = W - wave;      // this wave's of the blocks before: 1 is the nearest
-    const float nan = __uint_as_float(0x7fc00000u);
+    const float nan = __uint_as_float(kNan);
     // the words of the block `at` before, into its place
     auto gather = [&](int at) {
         const word_t *p = words_of<V>(tiles, bi, seg - at, strip) + lane * V;
-        word_t w[V], o[V];
-        bool state = false, there = false;
+        word_t w[V];
+        Seen seen = kNothing;
 #pragma unroll 1
         for (int spins = 0; spins < kSpins; ++spins) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) { w[j] = look(p + j); o[j] = look(p + 64 * V + j); }
-            state = all_there<V>(o);
-            there = state || all_there<V>(w);
-            if (there) break;
+            seen = look_all<V>(p, w);
+            if (seen != kNothing) break;
             __builtin_amdgcn_s_sleep(1);
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const word_t pair = w[j], out = o[j], v = state ? out : pair;
-            lds.before[at - 1][lane * V + j] = make_float2(first_of(v), there ? second_of(v) : nan);
-        }
-        if (lane == 0) lds.state[at - 1] = state;
+        for (int j = 0; j < V; ++j)
+            lds.before[at - 1][lane * V + j] = make_float2(__uint_as_float(first_of(w[j])), seen != kNothing ? second_of(w[j]) : nan);
+        if (lane == 0) lds.state[at - 1] = seen == kStates;
     };
     // the nearest state among the first n places; n: none
     auto nearest = [&](int n) {
@@ -276,14 +274,14 @@ __device__ __forceinline__ void enter(const Tiles &tiles, ChainLds<V, W> &lds, i
 #pragma unroll
             for (int j = 0; j < V; ++j) in[j] = lds.before[k][lane * V + j].y;
         } else {                    // none yet: the furthest one's
-            const word_t *p = words_of<V>(tiles, bi, seg - n, strip) + 64 * V + lane * V;
-            word_t o[V];
+            const word_t *p = words_of<V>(tiles, bi, seg - n, strip) + lane * V;
+            word_t w[V];
             int spins = 0;
 #pragma unroll 1
-            while (!look_all<V>(p, o) && ++spins < kSpins) __builtin_amdgcn_s_sleep(1);
+            while (look_all<V>(p, w) != kStates && ++spins < kSpins) __builtin_amdgcn_s_sleep(1);
             k = n - 1;
 #pragma unroll
-            for (int j = 0; j < V; ++j) in[j] = spins < kSpins ? second_of(o[j]) : nan;
+            for (int j = 0; j < V; ++j) in[j] = spins < kSpins ? second_of(w[j]) : nan;
         }
     }
 #pragma unroll 2
@@ -295,7 +293,7 @@ __device__ __forceinline__ void enter(const Tiles &tiles, ChainLds<V, W> &lds, i
         }
     if (wave == W - 1)
 #pragma unroll
-        for (int j = 0; j < V; ++j) publish(own + 64 * V + j, word_of(0.f, apply_pair(bm[j], in[j], bs[j])));
+        for (int j = 0; j < V; ++j) publish(own + j, state_word(apply_pair(bm[j], in[j], bs[j])));
 #pragma unroll
     for (int j = 0; j < V; ++j) h[j] = apply_pair(pm[j], in[j], ps[j]);
 }
@@ -552,7 +550,7 @@ Shape shape_of(int b, int L, int D, bool bf16, bool backward) {
     return s;
 }
 
-size_t words_bytes(const Shape &s) { return s.segs <= 1 ? 0 : 16 + size_t(s.blocks) * 64 * s.V * 2 * sizeof(word_t); }
+size_t words_bytes(const Shape &s) { return s.segs <= 1 ? 0 : 16 + size_t(s.blocks) * 64 * s.V * sizeof(word_t); }
 
 hipError_t tiles_of(const GatedScanArgs &a, const Shape &s, Tiles &t, hipStream_t stream) {
     t.strips = int(s.strips);
