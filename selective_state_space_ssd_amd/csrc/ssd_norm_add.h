@@ -81,23 +81,23 @@ __global__ __launch_bounds__(kBlock) void k_norm_add_fwd(const IO *__restrict__ 
     }
 }
 
+// TPS = 0: the team is the block, of as many waves as the row fills with one vector a lane.
 template <typename IO, typename RES, class DROP, int VEC, int TPS, int NV>
-__global__ __launch_bounds__(kBlock) void k_norm_add_bwd(const IO *__restrict__ x, const RES *__restrict__ sum,
+__global__ __launch_bounds__(TPS ? kBlock : kWideBlock, TPS ? 1 : 4) void k_norm_add_bwd(const IO *__restrict__ x, const RES *__restrict__ sum,
                                                          const float *__restrict__ scale, const float *__restrict__ w,
                                                          const IO *__restrict__ dy, const RES *__restrict__ dsum,
                                                          IO *__restrict__ dx, RES *__restrict__ dres,
                                                          float *__restrict__ dwp, float *__restrict__ dsp, int64_t rows,
                                                          int D, int slices, float eps, DROP drop) {
-    __shared__ float tmp[4];
-    constexpr int kTeams = kBlock / TPS;
-    const int lane = threadIdx.x % TPS;
-    const int64_t team = int64_t(blockIdx.x) * kTeams + threadIdx.x / TPS;
+    __shared__ float tmp[TPS ? 4 : kWideBlock / 64];
+    const int tps = TPS ? TPS : int(blockDim.x), lane = threadIdx.x % tps;
+    const int64_t team = TPS ? int64_t(blockIdx.x) * (kBlock / (TPS ? TPS : 1)) + threadIdx.x / tps : blockIdx.x;
     const bool live = team < slices;
     const int slice = live ? int(team) : 0;
     float wv[NV][VEC], dw[NV][VEC], ds[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPS + lane) * VEC;
+        const int c = (i * tps + lane) * VEC;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) dw[i][j] = ds[i][j] = wv[i][j] = 0.f;
         if (c < D) load_vec<float, VEC>(w + c, wv[i]);
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(kBlock) void k_norm_add_bwd(const IO *__restrict__ 
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPS + lane) * VEC;
+            const int c = (i * tps + lane) * VEC;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) s[i][j] = d[i][j] = e[i][j] = xv[i][j] = 0.f;
             if (on && c < D) {
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kBlock) void k_norm_add_bwd(const IO *__restrict__ 
         const float mean = team_sum<TPS>(dot, tmp) / float(D);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPS + lane) * VEC;
+            const int c = (i * tps + lane) * VEC;
             if (!(on && c < D)) continue;
             float sc[VEC], ox[VEC];
             if (scale) load_vec<float, VEC>(scale + c, sc);
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(kBlock) void k_norm_add_bwd(const IO *__restrict__ 
     if (!live) return;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPS + lane) * VEC;
+        const int c = (i * tps + lane) * VEC;
         if (c >= D) continue;
         store_vec<float, VEC>(dwp + int64_t(slice) * D + c, dw[i]);
         if (dsp) store_vec<float, VEC>(dsp + int64_t(slice) * D + c, ds[i]);
@@ -262,6 +262,17 @@ hipError_t add_bwd(const NormAddArgs &a, const NormBwdPlan &plan, const DROP &dr
     auto *part = static_cast<float *>(a.workspace);
     float *dsp = a.scale ? part + size_t(plan.slices) * a.D : nullptr;
     const Team t = pick_team(a.D, a.bf16);
+    if constexpr (DROP::kOn && std::is_same_v<IO, bf16_bits>) {
+        // Rows of 257 to 512 vectors leave most of a 256-lane team idle at its second vectors, and
+        // the others wait: 8192 rows of 2560 channels 92 us, one vector a lane 83, 3584 111 and 104.
+        // Longer rows make blocks of which a CU holds one: 4096 rows of 5120 86 and 93 us.
+        // (fp32 I/O, with half the channels a vector: 22 and 23 us of 2677 rows of 1288.)
+        if (t.vec == 8 && a.D / 8 > kBlock && a.D / 8 <= kWideBlock) {
+            hipLaunchKernelGGL((k_norm_add_bwd<IO, RES, DROP, 8, 0, 1>), dim3(plan.slices), dim3((a.D / 8 + 63) / 64 * 64), 0, stream,
+                               x, sum, a.scale, a.w, dy, dsum, dx, dres, part, dsp, a.rows, a.D, plan.slices, a.eps, drop);
+            return hipGetLastError();
+        }
+    }
     if (!t.nv) {
         hipLaunchKernelGGL((k_norm_add_bwd_loop<IO, RES, DROP>), dim3(plan.slices), dim3(kBlock), 0, stream, x, sum, a.scale, a.w, dy, dsum, dx, dres,
                            part, dsp, a.rows, a.D, plan.slices, a.eps, drop);
@@ -283,11 +294,18 @@ hipError_t add_fwd_by_type(const NormAddArgs &a, const DROP &drop, hipStream_t s
 
 template <class DROP>
 hipError_t add_bwd_by_type(const NormAddArgs &a, const NormBwdPlan &plan, const DROP &drop, hipStream_t stream) {
+    NormBwdPlan p = plan;
+    if constexpr (DROP::kOn) {
+        // two blocks for every CU, which holds two: half the partial sums of 1024 blocks, and no
+        // second round (8192 rows of 2560 channels 97 -> 92 us, of 1024 52 -> 39)
+        const Team t = pick_team(a.D, a.bf16);
+        p.slices = std::min(p.slices, 512 * (t.nv ? kBlock / t.tps : 1));
+    }
     hipError_t e;
-    if (!a.bf16) e = add_bwd<float, float>(a, plan, drop, stream);
-    else e = a.res_bf16 ? add_bwd<bf16_bits, bf16_bits>(a, plan, drop, stream) : add_bwd<bf16_bits, float>(a, plan, drop, stream);
+    if (!a.bf16) e = add_bwd<float, float>(a, p, drop, stream);
+    else e = a.res_bf16 ? add_bwd<bf16_bits, bf16_bits>(a, p, drop, stream) : add_bwd<bf16_bits, float>(a, p, drop, stream);
     if (e != hipSuccess) return e;
-    return launch_norm_reduce(static_cast<const float *>(a.workspace), a.dw, a.dscale, plan.slices, a.D, stream);
+    return launch_norm_reduce(static_cast<const float *>(a.workspace), a.dw, a.dscale, p.slices, a.D, stream);
 }
 
 }  // namespace

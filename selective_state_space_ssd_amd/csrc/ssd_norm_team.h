@@ -10,6 +10,7 @@ namespace ssd {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int kWideBlock = 512;     // at the most, of a team that is a block of its own size
 
 // Blocks of a forward pass: one dimension of a launch holds fewer than 2^32 threads, so that
 // many blocks go into two.  The last row of them may be only begun.
@@ -49,8 +50,8 @@ __device__ __forceinline__ void store_vec(IO *p, const float (&f)[VEC]) {
     }
 }
 
-// Sum over a team of TPS lanes (16, 64 or the whole 256-thread block); every lane of the
-// team ends with the total.  TPS = 256 holds two block barriers.
+// Sum over a team of TPS lanes (16, 64, the whole 256-thread block, or 0: a block of any number
+// of waves); every lane of the team ends with the total.  A block's holds two barriers.
 template <int TPS>
 __device__ __forceinline__ float team_sum(float v, float *tmp) {
     v = row16_sum(v);
@@ -59,7 +60,12 @@ __device__ __forceinline__ float team_sum(float v, float *tmp) {
     if constexpr (TPS == 64) return v;
     if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
+    if constexpr (TPS == 0) {
+        v = 0.f;
+        for (unsigned i = 0; i < blockDim.x / 64; ++i) v += tmp[i];
+    } else {
+        v = (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
+    }
     __syncthreads();
     return v;
 }
