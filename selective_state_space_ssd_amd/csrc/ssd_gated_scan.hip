@@ -128,7 +128,8 @@ struct Decay {
     float alpha = 1.f, lost = 0.f;      // lost: 1 - alpha (sigmoid), the sum of a (log decay)
     __device__ __forceinline__ void token(float m, float a) {
         alpha = decayed(m, alpha);
-        if constexpr (SIGMOID) lost = step_state<true>(m, lost, 1.f);
+        // (a token far from 1 makes the product what counts: lost may be anything then)
+        if constexpr (SIGMOID) lost = fmaf(-m, 1.f - lost, lost);
         else lost += a;
     }
     __device__ __forceinline__ float m() const {
