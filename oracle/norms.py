@@ -53,12 +53,12 @@ def norm_add_grads_f64(x, total, w, dy, d_sum, eps, scale=None):
     return ds * _f64(scale), ds, dw, (ds * _f64(x)).reshape(-1, s.shape[-1]).sum(0)
 
 
-def philox_words(n, seed, offset):
-    """Words 0 .. n - 1 of Philox4x32-10: word i is word i mod 4 of the counter (i / 4, offset)
-    under the key seed.  numpy, on the CPU."""
+def philox_words(n, seed, offset, first=0):
+    """Words first .. first + n - 1 (first a multiple of 4) of Philox4x32-10: word i is word
+    i mod 4 of the counter (i / 4, offset) under the key seed.  numpy, on the CPU."""
     import numpy as np
     u = np.uint64
-    mask, i = u(0xFFFFFFFF), np.arange((n + 3) // 4, dtype=np.uint64)
+    mask, i = u(0xFFFFFFFF), np.arange((n + 3) // 4, dtype=np.uint64) + u(first // 4)
     seed, offset = int(seed) % (1 << 64), int(offset) % (1 << 64)
     c0, c1 = i & mask, i >> u(32)
     c2, c3 = np.full_like(i, offset & 0xFFFFFFFF), np.full_like(i, offset >> 32)

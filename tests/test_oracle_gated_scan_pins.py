@@ -73,12 +73,10 @@ def test_generator_against_published_words():
     digits of pi."""
     def words(counter, key):
         at = counter[0] | counter[1] << 32
-        if at >= 1 << 20:
-            return None
-        return [int(w) for w in norms.philox_words(4 * at + 4, key[0] | key[1] << 32, counter[2] | counter[3] << 32)[4 * at:]]
+        return [int(w) for w in norms.philox_words(4, key[0] | key[1] << 32, counter[2] | counter[3] << 32, first=4 * at)]
 
     assert words((0, 0, 0, 0), (0, 0)) == [0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8]
-    # the other two by the same rounds on one counter far along: in plain integers
+    # the other two by the same rounds in plain integers (their counters lie past any array)
     def plain(c, k):
         for _ in range(10):
             p, q = 0xD2511F53 * c[0], 0xCD9E8D57 * c[2]
@@ -90,8 +88,8 @@ def test_generator_against_published_words():
     assert plain((ones,) * 4, (ones, ones)) == [0x408F276D, 0x41C83B0E, 0xA20BC7C6, 0x6D5451FD]
     assert plain((0x243F6A88, 0x85A308D3, 0x13198A2E, 0x03707344), (0xA4093822, 0x299F31D0)) == [0xD16CFE09, 0x94FDCCEB, 0x5001E420, 0x24126EA1]
     seed, offset = 0x1234567890ABCDEF, 0xFEDCBA0987654321
-    for at in (0, 1, 77):
-        assert words((at, 0, offset & ones, offset >> 32), (seed & ones, seed >> 32)) == plain((at, 0, offset & ones, offset >> 32), (seed & ones, seed >> 32))
+    for at, up in ((0, 0), (1, 0), (77, 0), (5, 9)):
+        assert words((at, up, offset & ones, offset >> 32), (seed & ones, seed >> 32)) == plain((at, up, offset & ones, offset >> 32), (seed & ones, seed >> 32))
 
 
 def test_dropout_keeps_its_share():
