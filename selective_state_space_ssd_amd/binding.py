@@ -151,10 +151,10 @@ def ssd_status_string(status: int) -> str:
 
 
 def _io_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return SSD_DTYPE_F32
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return SSD_DTYPE_BF16
+    if t.dtype is torch.float32:
+        return SSD_DTYPE_F32
     raise TypeError(f"x/B/C/y must be float32 or bfloat16, got {t.dtype}")
 
 
@@ -421,8 +421,8 @@ def _tensor(t, name, shape, dtype, device) -> Optional[int]:
     """The device pointer of ``t`` after checking what the C call cannot see; None stays None."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous() and t.is_cuda:
-        return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()         # on a GPU: _enqueue looks at the device, once a call
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.device != device:
@@ -437,6 +437,8 @@ def _tensor(t, name, shape, dtype, device) -> Optional[int]:
 def _enqueue(name, device, stream, *args) -> None:
     """Call the C entry point ``name`` with ``args`` and a stream of ``device`` (default:
     its current one)."""
+    if device.type != "cuda":
+        raise ValueError(f"{name}: the tensors must be on a GPU, not on {device}")
     entry = getattr(_lib or lib(), name)
     if stream is None:      # the handle alone: 0.2 us where a Stream object takes 1.9
         handle = torch._C._cuda_getCurrentRawStream(device.index)
@@ -722,7 +724,7 @@ def ssd_norm_add_q8_fwd(x, residual, scale, w, sum, q, q_scale, group, eps, stre
     q_scale [..., D / group] float32."""
     D, dev, f32 = x.shape[-1], x.device, torch.float32
     rows = _rows(x)
-    groups = (*x.shape[:-1], D // group if group > 0 else 0)    # a group below 1 is the library's to refuse
+    groups = x.shape[:-1] + (D // group if group > 0 else 0,)   # a group below 1 is the library's to refuse
     _enqueue("ssd_norm_add_q8_fwd", dev, stream, _tensor(x, "x", x.shape, x.dtype, dev),
              _tensor(residual, "residual", x.shape, residual.dtype, dev),
              _tensor(scale, "scale", (D,), f32, dev), _tensor(w, "w", (D,), f32, dev),
@@ -962,7 +964,7 @@ def norm_add_q8_fwd(x, residual, w, eps, group=None, scale=None, stream=None):
     group = D if group is None else group
     with _allocating_on(stream):
         q, total = torch.empty_like(x, dtype=torch.float8_e4m3fn), torch.empty_like(residual)
-        q_scale = torch.empty((*x.shape[:-1], D // group if group > 0 else 0), dtype=torch.float32, device=x.device)
+        q_scale = w.new_empty(x.shape[:-1] + (D // group if group > 0 else 0,))
     ssd_norm_add_q8_fwd(x, residual, scale, w, total, q, q_scale, group, eps, stream)
     return q, q_scale, total
 
