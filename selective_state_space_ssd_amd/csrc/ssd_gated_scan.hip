@@ -15,27 +15,37 @@
 // of the waves before it, and steps its tokens a second time from the state that enters.
 // From block to block:
 //   - the last wave publishes the block's pair as soon as it has it,
-//   - every wave waits for the pair of one of the W blocks before, and looks whether that
-//     block's outgoing state is there too,
+//   - eight of the waves (four of a block of four) wait for one block before each, until its
+//     pair or already its outgoing state is there; where there is no state among them, as in
+//     long sequences of few channels, they look at three blocks more each,
 //   - all fold the pairs behind the nearest such state, one by one, into the entering state
 //     (the same operations in the same order whichever block that was, so results repeat),
 //   - the last wave publishes the outgoing state in the pair's place.
 // Blocks take their places from a counter, earlier stretches first, so whatever a block
 // waits for belongs to a block that is running already.  A pair or a state is one 8-byte
 // word, written at once and never zero; zero means not there yet.
+//
+// Tiles of 256 tokens (8 waves of 32) by 128 bf16 channels put 131 KB of loads under way per
+// block, two blocks a CU; a token's gate takes the place of its value in registers, so that the
+// second walk starts from what the first left (122 registers forward, 193 backward).
+//
+// bf16, kernel times (call times are 2 to 4 us more, the words cleared before): 4 x 2048 tokens of
+// 5120 channels behind gates, forward 252 MB in 56 us, 4.5 TB/s; 16384 tokens of 2560 with fp32
+// decays, 335 MB in 76, 4.4 TB/s; backward of the former 425 MB in 85 to 90, 4.8 TB/s.  A product of
+// two such arrays into a third reaches 5.6, a copy 5.15.  25 vector instructions an element
+// forward (37 backward) keep the vector ALU busy for 60 % of that time, which loads do not wholly
+// cover.  Not better: tiles of half and of twice the tokens, four channels a lane (fewer
+// waves a CU: 74 us), loads in the order of their use, all looks further back at once (spills).
+// fp32, 2 x 1337 tokens of 1288: 41 MB in 14.5 us, one block a CU, whose latencies add up;
+// backward of 2 x 777 tokens of 645: 11 us.
 #include <limits.h>
 
 #include "ssd_gated_scan.h"
 #include "ssd_gated_scan_gate.h"
-#include "ssd_kernels.h"
 
 namespace ssd {
 namespace {
 
-#ifndef KT
-#define KT 32
-#endif
-constexpr int kT = KT;  // tokens of a wave
 constexpr int kSpins = 1 << 20;     // looks at a word before a wait gives up (about a second)
 
 // ------------------------------------------------------------- V channels of a lane
@@ -376,14 +386,14 @@ __global__ __launch_bounds__(64 * W, 4) void k_gated_scan_fwd(const IO *__restri
 #pragma unroll
         for (int j = 0; j < V; ++j) k[j] = h[j];
     }
-    // without y the rows' view is empty, and what is stored into it is dropped
-    const Rows out = rows_at(y ? y + row * D : y, y ? n : 0, D, c);
+    const int ny = y ? n : 0;
+    const Rows out = rows_at(y ? y + row * D : y, n, D, c);
 #pragma unroll
     for (int t = 0; t < T; ++t) {
         xr[t] = again<IO, V>(xr[t]);
 #pragma unroll
         for (int j = 0; j < V; ++j) h[j] = step_state<SIGMOID>(here(m[t][j]), h[j], xr[t].get(j));
-        if (t < n) out.template store<IO, V>(t, raw_of<IO, V>(h));
+        if (t < ny) out.template store<IO, V>(t, raw_of<IO, V>(h));
     }
     if (final_state && t0 + n == L)
 #pragma unroll
@@ -517,14 +527,21 @@ __global__ __launch_bounds__(256) void k_gated_scan_clear(uint4 *p, size_t n) {
     if (i < n) p[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Channels of a lane: two bf16 in one 4-byte access where the rows allow it.
+// Channels of a lane: two bf16 in one 4-byte access where the rows allow it.  (Four, in 8 bytes,
+// leave a CU half the waves: 4 x 2048 tokens of 5120 channels 74 instead of 58 us.)
 int lane_channels(int D, bool bf16) { return bf16 && D % 2 == 0 ? 2 : 1; }
 
-// Tokens of a block: W waves of T tokens.  Much work takes long stretches (fewer pairs to hand
-// on for as many bytes): forward 8 x 32 tokens, backward 4 x 32 with two channels a lane (186
-// registers, of which a SIMD holds two waves) and 16 x 16 with one (66 registers).  Less than a
-// block of 128 tokens for every CU takes 8 x 16, unless the sequence is so long that the
-// chain from block to block counts for more; and so do sequences that end within one.
+// Tokens of a block: W waves of T tokens.  Much work takes long stretches, fewer pairs to hand on
+// for as many bytes: forward 8 x 32 tokens, backward 4 x 32 with two channels a lane (193
+// registers, of which a SIMD holds two waves) and 16 x 16 with one (66 registers).  Where 128
+// tokens a block make no more blocks than there are CUs, and for sequences that end within
+// one, 8 x 16, the long way / the short way in us:
+//   forward, bf16    4 x 2048 tokens of 2560 36.1 / 37.7; 1 x 1000 of 512 12.9 / 10.4; 32 x 100 of 2560 15.8 / 13.9
+//   forward, fp32    4 x 2048 of 2560 53.8 / 60.5; 2 x 777 of 645 11.4 / 10.1; 32 x 100 of 2560 19.8 / 17.1
+//   backward, bf16   4 x 2048 of 2560 55.0 / 57.0; 2 x 777 of 645 12.9 / 11.7; 32 x 100 of 2560 23.1 / 20.7
+//   backward, fp32   4 x 2048 of 2560 91.4 / 94.2 (4 x 32: 97.2); 2 x 777 of 645 13.8 / 11.9; 32 x 100 of 2560 33.0 / 28.5
+// A chain of more than 32 of the short blocks costs more than their latency spares: one sequence
+// of 16384 tokens of 128 channels, forward, bf16 19.3 / 21.6, fp32 15.7 / 17.4.
 struct Shape {
     int V, T, W;
     int64_t strips, segs, blocks;

@@ -9,6 +9,11 @@
 // 2011) of the counter (i / 4, offset) under the key `seed`, 64 bits each, and stays where
 // that word is at least p 2^32.  Seed and offset are read on the device: a captured step
 // that counts the offset on draws another mask in each replay.
+//
+// The generator hides behind the loads: 8192 rows of 2560 bf16 channels with an fp32 residual
+// (252 MB) take 43 us forward, 5.9 TB/s, as without dropout, and 79 + 4 backward (377 MB and
+// 21 of partial sums), 4.8 TB/s.  (20 wide products and about as many other instructions a
+// counter, four elements: 5.3 us of the vector ALU's time forward.)
 #include "ssd_norm_add.h"
 
 namespace ssd {

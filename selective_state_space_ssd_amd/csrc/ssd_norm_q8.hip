@@ -11,7 +11,11 @@
 //
 // The team of ssd_norm_team.h holds the row; a group's maximum is taken as the largest bit
 // pattern of |y|, an order in which NaN is above infinity, so nothing of it depends on who
-// comes first.
+// comes first.  Groups that fill 2^k lanes of a wave (128 bf16 channels: 16) meet in the lanes'
+// registers, others in LDS.
+//
+// Bound by the bytes: 8192 rows of 2560 bf16 channels, fp32 residual, a scale per 128 (232 MB)
+// 44 us, 5.3 TB/s; a copy reaches 5.15.  5 rows of 5120 are the call: 4.6 us of kernel in 13.5.
 #include "ssd_norm.h"
 #include "ssd_norm_team.h"
 
