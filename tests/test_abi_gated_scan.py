@@ -52,6 +52,12 @@ def test_scan_dimensions(lib, call, over, code):
     assert call(lib, **over) == code
 
 
+def test_scan_sizes_past_a_launch(lib):
+    for call in (FWD, BWD):
+        assert call(lib, b=65535, L=128 * 40, D=64) == UNSUP and call(lib, D=(1 << 24) + 1) == UNSUP
+    assert STEP(lib, b=65535, D=64 * 40) == UNSUP
+
+
 def test_scan_lengths(lib):
     for call in (FWD, BWD):
         assert call(lib, L=(1 << 31) - 64) == UNSUP

@@ -62,3 +62,16 @@ def test_offsets_past_31_bits():
     t = (16 + 2 * D ** 0.5) * U
     assert bool(((qs[-n:].double() - es).abs() <= t * es).all())
     assert bool(((q[-n:].double() - eq).abs() <= torch.clamp_min(eq.abs() * 2.0 ** -4, 2.0 ** -10) + 3 * t * eq.abs()).all())
+
+
+@pytest.mark.parametrize("rows,D,group", [(5, 40, 1), (3, 2056, 1), (4, 520, 2), (4, 520, 4), (2, 4104, 3), (2, 4104, 1), (1, 12296, 2), (70, 128, 16), (9, 4096, 256), (9, 4096, 2048),
+                                          (1030, 2560, 128)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_q8_groups_of_few_and_many_channels(rows, D, group, dtype):
+    x, residual, w = draw((rows, D), dtype, 1), draw((rows, D), F32, 2, 2.0), draw((D,), F32, 4, 0.2, 1.0)
+    q, qs, total = bd.norm_add_q8_fwd(x, residual, w, EPS, group=group)
+    eq, es = norms.q8_of(norms.norm_add_f64(total.double() * 0, total, w, EPS)[0], group)
+    t = (16 + 2 * D ** 0.5) * U
+    assert bool(((qs.double() - es).abs() <= t * es).all())
+    assert bool(((q.double() - eq).abs() <= torch.clamp_min(eq.abs() * 2.0 ** -4, 2.0 ** -10) + 3 * t * eq.abs()).all())
+    assert bool((q.double().view(rows, -1, group).abs().amax(-1) == 448).all())
