@@ -434,6 +434,11 @@ def _tensor(t, name, shape, dtype, device) -> Optional[int]:
     raise ValueError(f"{name} must be contiguous")
 
 
+def _fresh(t, *_) -> Optional[int]:
+    """As _tensor, of what an allocating wrapper has just made: there is nothing to check."""
+    return None if t is None else t.data_ptr()
+
+
 def _enqueue(name, device, stream, *args) -> None:
     """Call the C entry point ``name`` with ``args`` and a stream of ``device`` (default:
     its current one)."""
@@ -571,14 +576,14 @@ def _kept_shape(b, L, D):
 
 
 def ssd_gated_scan_step(state_in, x, a, accept_len, y, state_out, sigmoid=False, err_flag=None,
-                        stream=None) -> None:
+                        stream=None, _out=_tensor) -> None:
     """Enqueue K tokens of the gated scan on a kept state [b,D] (see include/ssd_mi355x.h)."""
     b, K, D = _scan_dims(x)
     dev, io, f32, xy, st = x.device, x.dtype, torch.float32, (b, K, D), (b, D)
     _enqueue("ssd_gated_scan_step", dev, stream, _tensor(state_in, "state_in", st, f32, dev),
              _tensor(x, "x", xy, io, dev), _tensor(a, "a", xy, a.dtype, dev),
-             _tensor(accept_len, "accept_len", (b,), torch.int32, dev), _tensor(y, "y", xy, io, dev),
-             _tensor(state_out, "state_out", st, f32, dev),
+             _tensor(accept_len, "accept_len", (b,), torch.int32, dev), _out(y, "y", xy, io, dev),
+             _out(state_out, "state_out", st, f32, dev),
              None if err_flag is None else _tensor(err_flag, "err_flag", err_flag.shape, torch.int32, dev),
              b, K, D, 1 if sigmoid else 0, _io_code(x), _io_code(a))
 
@@ -591,7 +596,7 @@ def ssd_gated_scan_fwd_workspace_bytes(b, L, D, io: int, a_io: int) -> int:
 
 
 def ssd_gated_scan_fwd(x, a, init_state, y, states, final_state, sigmoid, workspace,
-                       stream=None) -> None:
+                       stream=None, _out=_tensor) -> None:
     """Enqueue the gated scan over whole sequences: x, y [b,L,D] of one type, a [b,L,D] of that
     type or float32, init_state and final_state [b,D], states [b,ceil(L/32),D] float32 (each
     of the three may be None)."""
@@ -600,8 +605,8 @@ def ssd_gated_scan_fwd(x, a, init_state, y, states, final_state, sigmoid, worksp
     ws, ws_bytes = _workspace_arg(workspace, dev)
     _enqueue("ssd_gated_scan_fwd", dev, stream, _tensor(x, "x", xy, io, dev),
              _tensor(a, "a", xy, a.dtype, dev), _tensor(init_state, "init_state", st, f32, dev),
-             _tensor(y, "y", xy, io, dev), _tensor(states, "states", _kept_shape(b, L, D), f32, dev),
-             _tensor(final_state, "final_state", st, f32, dev), b, L, D, 1 if sigmoid else 0,
+             _out(y, "y", xy, io, dev), _out(states, "states", _kept_shape(b, L, D), f32, dev),
+             _out(final_state, "final_state", st, f32, dev), b, L, D, 1 if sigmoid else 0,
              _io_code(x), _io_code(a), ws, ws_bytes)
 
 
@@ -613,7 +618,7 @@ def ssd_gated_scan_bwd_workspace_bytes(b, L, D, with_states, io: int, a_io: int)
 
 
 def ssd_gated_scan_bwd(x, a, init_state, states, dy, d_final, dx, da, d_init, sigmoid, workspace,
-                       stream=None) -> None:
+                       stream=None, _out=_tensor) -> None:
     """Enqueue the gradients of ssd_gated_scan_fwd: its inputs and states (None: computed again
     from init_state), dy (like x) and d_final [b,D] (may be None); dx like x, da like a,
     d_init [b,D] float32 (may be None)."""
@@ -623,8 +628,8 @@ def ssd_gated_scan_bwd(x, a, init_state, states, dy, d_final, dx, da, d_init, si
     _enqueue("ssd_gated_scan_bwd", dev, stream, _tensor(x, "x", xy, io, dev),
              _tensor(a, "a", xy, a.dtype, dev), _tensor(init_state, "init_state", st, f32, dev),
              _tensor(states, "states", _kept_shape(b, L, D), f32, dev), _tensor(dy, "dy", xy, io, dev),
-             _tensor(d_final, "d_final", st, f32, dev), _tensor(dx, "dx", xy, io, dev),
-             _tensor(da, "da", xy, a.dtype, dev), _tensor(d_init, "d_init", st, f32, dev), b, L, D,
+             _tensor(d_final, "d_final", st, f32, dev), _out(dx, "dx", xy, io, dev),
+             _out(da, "da", xy, a.dtype, dev), _out(d_init, "d_init", st, f32, dev), b, L, D,
              1 if sigmoid else 0, _io_code(x), _io_code(a), ws, ws_bytes)
 
 
@@ -691,7 +696,7 @@ def ssd_norm_add_bwd(x, sum, scale, w, dy, d_sum, dx, d_residual, d_scale, dw, e
              eps, _io_code(dy), _io_code(sum), ws, ws_bytes)
 
 
-def ssd_norm_add_drop_fwd(x, residual, scale, w, rng, sum, y, eps, p, stream=None) -> None:
+def ssd_norm_add_drop_fwd(x, residual, scale, w, rng, sum, y, eps, p, stream=None, _out=_tensor) -> None:
     """Enqueue ssd_norm_add_fwd with dropout of probability p on x; rng [2] int64 on the GPU
     holds the generator's seed and offset."""
     D, dev, f32 = x.shape[-1], x.device, torch.float32
@@ -699,12 +704,12 @@ def ssd_norm_add_drop_fwd(x, residual, scale, w, rng, sum, y, eps, p, stream=Non
     _enqueue("ssd_norm_add_drop_fwd", dev, stream, _tensor(x, "x", x.shape, x.dtype, dev),
              _tensor(residual, "residual", x.shape, residual.dtype, dev),
              _tensor(scale, "scale", (D,), f32, dev), _tensor(w, "w", (D,), f32, dev),
-             _tensor(rng, "rng", (2,), torch.int64, dev), _tensor(sum, "sum", x.shape, residual.dtype, dev),
-             _tensor(y, "y", x.shape, x.dtype, dev), rows, D, eps, p, _io_code(x), _io_code(residual))
+             _tensor(rng, "rng", (2,), torch.int64, dev), _out(sum, "sum", x.shape, residual.dtype, dev),
+             _out(y, "y", x.shape, x.dtype, dev), rows, D, eps, p, _io_code(x), _io_code(residual))
 
 
 def ssd_norm_add_drop_bwd(x, sum, scale, w, rng, dy, d_sum, dx, d_residual, d_scale, dw, eps, p,
-                          workspace, stream=None) -> None:
+                          workspace, stream=None, _out=_tensor) -> None:
     """Enqueue the gradients of ssd_norm_add_drop_fwd; arguments as ssd_norm_add_bwd."""
     D, dev, f32, res = dy.shape[-1], dy.device, torch.float32, sum.dtype
     shape, io = dy.shape, dy.dtype
@@ -714,12 +719,12 @@ def ssd_norm_add_drop_bwd(x, sum, scale, w, rng, dy, d_sum, dx, d_residual, d_sc
              _tensor(sum, "sum", shape, res, dev), _tensor(scale, "scale", (D,), f32, dev),
              _tensor(w, "w", (D,), f32, dev), _tensor(rng, "rng", (2,), torch.int64, dev),
              _tensor(dy, "dy", shape, io, dev), _tensor(d_sum, "d_sum", shape, res, dev),
-             _tensor(dx, "dx", shape, io, dev), _tensor(d_residual, "d_residual", shape, res, dev),
-             _tensor(d_scale, "d_scale", (D,), f32, dev), _tensor(dw, "dw", (D,), f32, dev), rows, D,
+             _out(dx, "dx", shape, io, dev), _out(d_residual, "d_residual", shape, res, dev),
+             _out(d_scale, "d_scale", (D,), f32, dev), _out(dw, "dw", (D,), f32, dev), rows, D,
              eps, p, _io_code(dy), _io_code(sum), ws, ws_bytes)
 
 
-def ssd_norm_add_q8_fwd(x, residual, scale, w, sum, q, q_scale, group, eps, stream=None) -> None:
+def ssd_norm_add_q8_fwd(x, residual, scale, w, sum, q, q_scale, group, eps, stream=None, _out=_tensor) -> None:
     """Enqueue ssd_norm_add_fwd with its output in 8 bits: q (float8_e4m3fn, of x's shape) and
     q_scale [..., D / group] float32."""
     D, dev, f32 = x.shape[-1], x.device, torch.float32
@@ -728,9 +733,9 @@ def ssd_norm_add_q8_fwd(x, residual, scale, w, sum, q, q_scale, group, eps, stre
     _enqueue("ssd_norm_add_q8_fwd", dev, stream, _tensor(x, "x", x.shape, x.dtype, dev),
              _tensor(residual, "residual", x.shape, residual.dtype, dev),
              _tensor(scale, "scale", (D,), f32, dev), _tensor(w, "w", (D,), f32, dev),
-             _tensor(sum, "sum", x.shape, residual.dtype, dev),
-             _tensor(q, "q", x.shape, torch.float8_e4m3fn, dev),
-             _tensor(q_scale, "q_scale", groups, f32, dev), rows, D, group, eps, _io_code(x),
+             _out(sum, "sum", x.shape, residual.dtype, dev),
+             _out(q, "q", x.shape, torch.float8_e4m3fn, dev),
+             _out(q_scale, "q_scale", groups, f32, dev), rows, D, group, eps, _io_code(x),
              _io_code(residual))
 
 
@@ -857,7 +862,7 @@ def gated_scan_step(state, x, a, sigmoid=False, accept_len=None, stream=None, er
     err_flag (int32, on the GPU), if there is one, to 1."""
     with _allocating_on(stream):
         y, state_out = torch.empty_like(x), torch.empty_like(state)
-    ssd_gated_scan_step(state, x, a, accept_len, y, state_out, sigmoid, err_flag, stream)
+    ssd_gated_scan_step(state, x, a, accept_len, y, state_out, sigmoid, err_flag, stream, _fresh)
     return y, state_out
 
 
@@ -872,7 +877,7 @@ def gated_scan_fwd(x, a, sigmoid=False, init_state=None, keep_states=False, work
         states = torch.empty(_kept_shape(b, L, D), dtype=f32, device=dev) if keep_states else None
         if workspace is None:
             workspace = _scratch(ssd_gated_scan_fwd_workspace_bytes(b, L, D, _io_code(x), _io_code(a)), dev)
-    ssd_gated_scan_fwd(x, a, init_state, y, states, final_state, sigmoid, workspace, stream)
+    ssd_gated_scan_fwd(x, a, init_state, y, states, final_state, sigmoid, workspace, stream, _fresh)
     return (y, final_state, states) if keep_states else (y, final_state)
 
 
@@ -888,7 +893,7 @@ def gated_scan_bwd(x, a, dy, sigmoid=False, init_state=None, d_final=None, state
         if workspace is None:
             n = ssd_gated_scan_bwd_workspace_bytes(b, L, D, states is not None, _io_code(x), _io_code(a))
             workspace = _scratch(n, dev)
-    ssd_gated_scan_bwd(x, a, init_state, states, dy, d_final, dx, da, d_init, sigmoid, workspace, stream)
+    ssd_gated_scan_bwd(x, a, init_state, states, dy, d_final, dx, da, d_init, sigmoid, workspace, stream, _fresh)
     return dx, da, d_init
 
 
@@ -939,7 +944,7 @@ def norm_add_drop_fwd(x, residual, w, eps, p, rng, scale=None, stream=None):
     seed and the offset of the mask's generator.  Returns (y, sum)."""
     with _allocating_on(stream):
         y, total = torch.empty_like(x), torch.empty_like(residual)
-    ssd_norm_add_drop_fwd(x, residual, scale, w, rng, total, y, eps, p, stream)
+    ssd_norm_add_drop_fwd(x, residual, scale, w, rng, total, y, eps, p, stream, _fresh)
     return y, total
 
 
@@ -953,7 +958,7 @@ def norm_add_drop_bwd(x, sum, w, dy, d_sum, eps, p, rng, scale=None, workspace=N
         if workspace is None:
             n = ssd_norm_bwd_workspace_bytes(_rows(dy), D, D, 1 if scale is None else 2, _io_code(dy))
             workspace = _scratch(n, dy.device)
-    ssd_norm_add_drop_bwd(x, sum, scale, w, rng, dy, d_sum, dx, d_res, d_scale, dw, eps, p, workspace, stream)
+    ssd_norm_add_drop_bwd(x, sum, scale, w, rng, dy, d_sum, dx, d_res, d_scale, dw, eps, p, workspace, stream, _fresh)
     return dx, d_res, dw, d_scale
 
 
@@ -965,7 +970,7 @@ def norm_add_q8_fwd(x, residual, w, eps, group=None, scale=None, stream=None):
     with _allocating_on(stream):
         q, total = torch.empty_like(x, dtype=torch.float8_e4m3fn), torch.empty_like(residual)
         q_scale = w.new_empty(x.shape[:-1] + (D // group if group > 0 else 0,))
-    ssd_norm_add_q8_fwd(x, residual, scale, w, total, q, q_scale, group, eps, stream)
+    ssd_norm_add_q8_fwd(x, residual, scale, w, total, q, q_scale, group, eps, stream, _fresh)
     return q, q_scale, total
 
 
