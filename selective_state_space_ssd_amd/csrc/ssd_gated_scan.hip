@@ -542,6 +542,13 @@ int lane_channels(int D, bool bf16) { return bf16 && D % 2 == 0 ? 2 : 1; }
 //   backward, fp32   4 x 2048 of 2560 91.4 / 94.2 (4 x 32: 97.2); 2 x 777 of 645 13.8 / 11.9; 32 x 100 of 2560 33.0 / 28.5
 // A chain of more than 32 of the short blocks costs more than their latency spares: one sequence
 // of 16384 tokens of 128 channels, forward, bf16 19.3 / 21.6, fp32 15.7 / 17.4.
+//
+// Sequences of 129 to 256 tokens take one block of 16 x 16: no words to clear, one launch instead
+// of two.  Two blocks of 8 x 16 / this, kernel times and, of the first, call times: forward, bf16
+// 4 x 200 of 640 9.7 / 8.6 (15.0 / 10.6), fp32 8.9 / 6.4; backward, bf16 12.0 / 12.1 (17.8 / 13.1),
+// fp32 10.4 / 7.7.  Where that makes many blocks, 4 x 32 / this, backward, bf16: 32 x 256 of 2560
+// 52.0 / 48.4, 64 x 256 of 1024 44.9 / 37.8; but 8 x 32 / this, forward, bf16: 27.6 / 33.7, 20.3 /
+// 27.4 (fp32 the same).
 struct Shape {
     int V, T, W;
     int64_t strips, segs, blocks;
@@ -550,7 +557,7 @@ struct Shape {
 constexpr int kFwdT = 32, kFwdW = 8;
 template <int V> constexpr int kBwdT = V == 2 ? 32 : 16;
 template <int V> constexpr int kBwdW = V == 2 ? 4 : 16;
-constexpr int kShortT = 16, kShortW = 8, kShort = kShortT * kShortW, kCus = 256, kLongChain = 32;
+constexpr int kShortT = 16, kShortW = 8, kShort = kShortT * kShortW, kPairW = 16, kCus = 256, kLongChain = 32;
 
 Shape shape_of(int b, int L, int D, bool bf16, bool backward) {
     Shape s;
@@ -559,7 +566,11 @@ Shape shape_of(int b, int L, int D, bool bf16, bool backward) {
     s.segs = (int64_t(L) + kShort - 1) / kShort;
     s.T = kShortT;
     s.W = kShortW;
-    if (s.segs > 1 && (s.strips * s.segs * b > kCus || s.segs > kLongChain)) {
+    const bool much = s.strips * s.segs * b > kCus || s.segs > kLongChain;
+    if (s.segs == 2 && (backward || !much)) {
+        s.W = kPairW;
+        s.segs = 1;
+    } else if (s.segs > 1 && much) {
         s.T = !backward ? kFwdT : s.V == 2 ? kBwdT<2> : kBwdT<1>;
         s.W = !backward ? kFwdW : s.V == 2 ? kBwdW<2> : kBwdW<1>;
         s.segs = (int64_t(L) + s.T * s.W - 1) / (s.T * s.W);
@@ -633,6 +644,7 @@ hipError_t launch_gated_scan_fwd(const GatedScanArgs &a, hipStream_t stream) {
         using IO = decltype(io);
         using AIO = decltype(aio);
         if (s.T == kFwdT) return fwd<IO, AIO, v(), kFwdT, kFwdW>(a, s, t, stream);
+        if (s.W == kPairW) return fwd<IO, AIO, v(), kShortT, kPairW>(a, s, t, stream);
         return fwd<IO, AIO, v(), kShortT, kShortW>(a, s, t, stream);
     });
 }
@@ -646,6 +658,7 @@ hipError_t launch_gated_scan_bwd(const GatedScanArgs &a, hipStream_t stream) {
         using AIO = decltype(aio);
         constexpr int V = v(), T = kBwdT<V>, W = kBwdW<V>;
         if (s.T == T && s.W == W) return bwd<IO, AIO, V, T, W>(a, s, t, stream);
+        if (s.W == kPairW) return bwd<IO, AIO, V, kShortT, kPairW>(a, s, t, stream);
         return bwd<IO, AIO, V, kShortT, kShortW>(a, s, t, stream);
     });
 }

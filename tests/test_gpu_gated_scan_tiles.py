@@ -15,8 +15,8 @@ pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 
 # b, L, D: more blocks than CUs with two channels a lane and with one (odd D), ragged in tokens
-# and channels; the last length of a short tile and the first of two; long chains of few blocks
-TILES = [(4, 700, 2050), (3, 600, 2047), (64, 128, 640), (64, 129, 640), (1, 4096, 258), (1, 4097, 258), (1, 9000, 6), (2, 9217, 1)]
+# and channels; the last length of a short tile and lengths of a double one; long chains of few blocks
+TILES = [(4, 700, 2050), (3, 600, 2047), (64, 128, 640), (64, 129, 640), (2, 129, 67), (4, 200, 640), (16, 256, 2050), (1, 4096, 258), (1, 4097, 258), (1, 9000, 6), (2, 9217, 1)]
 
 
 @pytest.mark.parametrize("b,L,D", TILES)
