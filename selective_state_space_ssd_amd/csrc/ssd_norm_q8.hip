@@ -15,7 +15,7 @@
 // registers, others in LDS.
 //
 // Bound by the bytes: 8192 rows of 2560 bf16 channels, fp32 residual, a scale per 128 (232 MB)
-// 44 us, 5.3 TB/s; a copy reaches 5.15.  5 rows of 5120 are the call: 4.6 us of kernel in 13.5.
+// 44 us, 5.3 TB/s; a copy reaches 5.15.  5 rows of 5120 are the call: 4.6 us of kernel in 13.
 #include "ssd_norm.h"
 #include "ssd_norm_team.h"
 
