@@ -544,6 +544,25 @@ ssd_status_t ssd_gated_delta_bwd(const void *q, const void *k, const void *v, co
  * that does not change from run to run.  A NaN or an infinity reaches the outputs that
  * depend on it (an infinity as a NaN, it may be) and no other.  Errors as for the other
  * entry points.
+ *
+ * Long sequences are cut into blocks that hand their states on through the workspace.  A
+ * block that waits for another one (which is running by then: blocks start in order) looks
+ * at its word up to a limit of times, 2^20 unless ssd_gated_scan_wait_limit says otherwise,
+ * which take about a second; a block may wait five times, one after another.  A wait that
+ * gives up ends with NaN in what depends on it (outputs, final_state, states, gradients) and
+ * sets the workspace's error word; the call has returned SSD_OK by then.  A healthy device
+ * never gets there.
+ *
+ * ssd_gated_scan_workspace_error: err_out (device int32) = the error word that the last
+ *   ssd_gated_scan_fwd or ssd_gated_scan_bwd call on the workspace left, 1 if one of its waits
+ *   gave up, else 0.  b and L as for that call: sequences of one block wait for nothing, use
+ *   no word and give 0.  Enqueued on hip_stream, so behind that call and before the next.
+ *   SSD_ERR_BAD_DIM, SSD_ERR_NULL_ARG (err_out), SSD_ERR_ALIGN, SSD_ERR_WORKSPACE (a
+ *   workspace of less than 16 bytes where there is a word), SSD_ERR_ALIAS, SSD_ERR_HIP.
+ * ssd_gated_scan_wait_limit: sets how often the calls from now on look at a word before they
+ *   give up (process-wide; captured calls keep the limit of their capture), and returns what
+ *   the limit was; a negative value changes nothing.  0 gives up at once: a test of what a
+ *   caller does then.
  */
 #define SSD_GATED_SCAN_KEEP 32
 ssd_status_t ssd_gated_scan_step(const float *state_in, const void *x, const void *a,
@@ -562,6 +581,9 @@ ssd_status_t ssd_gated_scan_bwd(const void *x, const void *a, const float *init_
                                 void *da, float *d_init, int b, int L, int D, int sigmoid,
                                 ssd_dtype_t io, ssd_dtype_t a_io, void *workspace,
                                 size_t workspace_bytes, void *hip_stream);
+ssd_status_t ssd_gated_scan_workspace_error(const void *workspace, size_t workspace_bytes, int b, int L,
+                                            int32_t *err_out, void *hip_stream);
+int ssd_gated_scan_wait_limit(int looks);
 
 /*
  * The norms around a mixer block, each fused with what stands next to it; act(z) =

@@ -39,6 +39,7 @@ EXPORTED = ("ssd_chunk_scan_workspace_bytes", "ssd_chunk_scan_workspace_init",
             "ssd_gated_delta_fwd", "ssd_gated_delta_bwd_workspace_bytes",
             "ssd_gated_delta_bwd", "ssd_gated_scan_step", "ssd_gated_scan_fwd_workspace_bytes",
             "ssd_gated_scan_fwd", "ssd_gated_scan_bwd_workspace_bytes", "ssd_gated_scan_bwd",
+            "ssd_gated_scan_workspace_error", "ssd_gated_scan_wait_limit",
             "ssd_norm_gate_fwd", "ssd_norm_bwd_workspace_bytes",
             "ssd_norm_gate_bwd", "ssd_norm_add_fwd", "ssd_norm_add_bwd",
             "ssd_norm_add_drop_fwd", "ssd_norm_add_drop_bwd", "ssd_norm_add_q8_fwd",
@@ -118,6 +119,10 @@ def lib() -> ctypes.CDLL:
         L.ssd_gated_scan_bwd_workspace_bytes.restype = sz
         L.ssd_gated_scan_bwd.argtypes = [vp] * 9 + [i32] * 6 + [vp, sz, vp]
         L.ssd_gated_scan_bwd.restype = i32
+        L.ssd_gated_scan_workspace_error.argtypes = [vp, sz, i32, i32, vp, vp]
+        L.ssd_gated_scan_workspace_error.restype = i32
+        L.ssd_gated_scan_wait_limit.argtypes = [i32]
+        L.ssd_gated_scan_wait_limit.restype = i32
         L.ssd_norm_gate_fwd.argtypes = [vp] * 4 + [i32] * 3 + [f32, i32, i32, vp]
         L.ssd_norm_gate_fwd.restype = i32
         L.ssd_norm_bwd_workspace_bytes.argtypes = [i32] * 5
@@ -631,6 +636,22 @@ def ssd_gated_scan_bwd(x, a, init_state, states, dy, d_final, dx, da, d_init, si
              _tensor(d_final, "d_final", st, f32, dev), _out(dx, "dx", xy, io, dev),
              _out(da, "da", xy, a.dtype, dev), _out(d_init, "d_init", st, f32, dev), b, L, D,
              1 if sigmoid else 0, _io_code(x), _io_code(a), ws, ws_bytes)
+
+
+def ssd_gated_scan_workspace_error(workspace, b, L, err_out, stream=None) -> None:
+    """Enqueue a copy of the error word that the last gated scan of b sequences of L tokens left
+    in ``workspace`` into ``err_out`` (an int32 GPU tensor of one element): 1 if one of its
+    waits gave up, and NaN is in what depends on it."""
+    dev = err_out.device
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _enqueue("ssd_gated_scan_workspace_error", dev, stream, ws, ws_bytes, b, L,
+             _tensor(err_out, "err_out", (1,), torch.int32, dev))
+
+
+def ssd_gated_scan_wait_limit(looks: int = -1) -> int:
+    """Set how often gated scans look at another block's word before they give up (negative:
+    leave it); returns what the limit was."""
+    return lib().ssd_gated_scan_wait_limit(looks)
 
 
 def _rows(x) -> int:

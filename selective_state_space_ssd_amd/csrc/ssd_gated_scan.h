@@ -24,7 +24,9 @@ struct GatedScanArgs {
     float *d_init;              // null: not wanted
     void *workspace;
     int b, L, D;
+    int looks;                  // at another block's word, before a wait gives up
     bool sigmoid, bf16, a_bf16;
+    bool keep_error;            // the workspace's error word stays, of the pass before
 };
 
 struct GatedStepArgs {
@@ -41,9 +43,14 @@ struct GatedStepArgs {
 // Whether the launches of this shape stay inside a grid's limits.
 bool gated_scan_supported(int b, int L, int D);
 size_t gated_scan_workspace(int b, int L, int D, bool bf16, bool backward);    // without kept states
+// Whether sequences of L > 0 tokens are cut into blocks that wait for each other, whatever their type
+// and pass; the others use no workspace.
+bool gated_scan_waits(int L);
 
 hipError_t launch_gated_scan_fwd(const GatedScanArgs &a, hipStream_t stream);
 hipError_t launch_gated_scan_bwd(const GatedScanArgs &a, hipStream_t stream);   // kept is an input
+// err_out = the error word of the last pass in the workspace; null: 0.
+hipError_t launch_gated_scan_error(const void *workspace, int32_t *err_out, hipStream_t stream);
 hipError_t launch_gated_scan_step(const GatedStepArgs &a, hipStream_t stream);
 
 }  // namespace ssd

@@ -23,7 +23,8 @@
 //   - the last wave publishes the outgoing state in the pair's place.
 // Blocks take their places from a counter, earlier stretches first, so whatever a block
 // waits for belongs to a block that is running already.  A pair or a state is one 8-byte
-// word, written at once and never zero; zero means not there yet.
+// word, written at once and never zero; zero means not there yet.  A wait that gives up all
+// the same sets the workspace's error word and goes on with NaN.
 //
 // Tiles of 256 tokens (8 waves of 32) by 128 bf16 channels put 131 KB of loads under way per
 // block, two blocks a CU; a token's gate takes the place of its value in registers, so that the
@@ -45,8 +46,6 @@
 
 namespace ssd {
 namespace {
-
-constexpr int kSpins = 1 << 20;     // looks at a word before a wait gives up (about a second)
 
 // ------------------------------------------------------------- V channels of a lane
 template <typename T, int V>
@@ -164,11 +163,12 @@ __device__ __forceinline__ float second_of(word_t w) { return __uint_as_float(ui
 __device__ __forceinline__ word_t look(const word_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ void publish(word_t *p, word_t w) { __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
-// Workspace: the counter (16 bytes), then per block 64 V words.
+// Workspace: 16 bytes with the counter of places and the error word, then per block 64 V words.
 struct Tiles {
     word_t *words;          // null: one block a strip, nothing to wait for
-    unsigned *counter;
+    unsigned *counter;      // the error word behind it
     int strips, segs, b;
+    int looks;              // at a word, before a wait gives up
 };
 
 template <int V>
@@ -193,6 +193,22 @@ __device__ __forceinline__ Seen look_all(const word_t *p, word_t (&w)[V]) {
     }
     if (!__all(there)) return kNothing;
     return __all(state) ? kStates : __all(pair) ? kPairs : kNothing;
+}
+
+// Looks at a block's words until they are there, or until all are states if `states` says so.
+// A wait that gives up leaves kNothing, and the error word set.
+template <int V>
+__device__ __forceinline__ Seen wait_for(const Tiles &tiles, const word_t *p, bool states, int lane, word_t (&w)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) w[j] = 0;
+#pragma unroll 1
+    for (int n = 0; n < tiles.looks; ++n) {
+        const Seen seen = look_all<V>(p, w);
+        if (seen == kStates || (seen == kPairs && !states)) return seen;
+        __builtin_amdgcn_s_sleep(1);
+    }
+    if (lane == 0) __hip_atomic_store(tiles.counter + 1, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return kNothing;
 }
 
 template <int V, int W>
@@ -247,13 +263,7 @@ __device__ __forceinline__ void enter(const Tiles &tiles, ChainLds<V, W> &lds, i
     auto gather = [&](int at) {
         const word_t *p = words_of<V>(tiles, bi, seg - at, strip) + lane * V;
         word_t w[V];
-        Seen seen = kNothing;
-#pragma unroll 1
-        for (int spins = 0; spins < kSpins; ++spins) {
-            seen = look_all<V>(p, w);
-            if (seen != kNothing) break;
-            __builtin_amdgcn_s_sleep(1);
-        }
+        const Seen seen = wait_for<V>(tiles, p, false, lane, w);
 #pragma unroll
         for (int j = 0; j < V; ++j)
             lds.before[at - 1][lane * V + j] = make_float2(__uint_as_float(first_of(w[j])), seen != kNothing ? second_of(w[j]) : nan);
@@ -287,12 +297,10 @@ __device__ __forceinline__ void enter(const Tiles &tiles, ChainLds<V, W> &lds, i
         } else {                    // none yet: the furthest one's
             const word_t *p = words_of<V>(tiles, bi, seg - n, strip) + lane * V;
             word_t w[V];
-            int spins = 0;
-#pragma unroll 1
-            while (look_all<V>(p, w) != kStates && ++spins < kSpins) __builtin_amdgcn_s_sleep(1);
+            const bool there = wait_for<V>(tiles, p, true, lane, w) == kStates;
             k = n - 1;
 #pragma unroll
-            for (int j = 0; j < V; ++j) in[j] = spins < kSpins ? second_of(w[j]) : nan;
+            for (int j = 0; j < V; ++j) in[j] = there ? second_of(w[j]) : nan;
         }
     }
 #pragma unroll 2
@@ -522,9 +530,14 @@ __global__ __launch_bounds__(64 * W, T == kGatedScanKeep ? 2 : 4) void k_gated_s
 }
 
 // ---------------------------------------------------------------------------- launches
-__global__ __launch_bounds__(256) void k_gated_scan_clear(uint4 *p, size_t n) {
+// keep: the error word stays, of a pass before this one in the same call.
+__global__ __launch_bounds__(256) void k_gated_scan_clear(uint4 *p, size_t n, bool keep) {
     const size_t i = size_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i < n) p[i] = make_uint4(0, 0, 0, 0);
+    if (i < n) p[i] = make_uint4(0, i == 0 && keep ? p[0].y : 0, 0, 0);
+}
+
+__global__ void k_gated_scan_error(const unsigned *header, int32_t *err_out) {
+    *err_out = header ? int32_t(__hip_atomic_load(header + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) : 0;
 }
 
 // Channels of a lane: two bf16 in one 4-byte access where the rows allow it.  (Four, in 8 bytes,
@@ -585,13 +598,14 @@ hipError_t tiles_of(const GatedScanArgs &a, const Shape &s, Tiles &t, hipStream_
     t.strips = int(s.strips);
     t.segs = int(s.segs);
     t.b = a.b;
+    t.looks = a.looks;
     t.words = nullptr;
     t.counter = nullptr;
     if (s.segs <= 1) return hipSuccess;
     t.counter = static_cast<unsigned *>(a.workspace);
     t.words = reinterpret_cast<word_t *>(static_cast<char *>(a.workspace) + 16);
     const size_t n = words_bytes(s) / 16;
-    hipLaunchKernelGGL(k_gated_scan_clear, dim3(unsigned((n + 255) / 256)), dim3(256), 0, stream, static_cast<uint4 *>(a.workspace), n);
+    hipLaunchKernelGGL(k_gated_scan_clear, dim3(unsigned((n + 255) / 256)), dim3(256), 0, stream, static_cast<uint4 *>(a.workspace), n, a.keep_error);
     return hipGetLastError();
 }
 
@@ -632,6 +646,14 @@ hipError_t by_types(const GatedScanArgs &a, int V, F &&f) {
 bool gated_scan_supported(int b, int L, int D) {
     return b <= 65535 && L <= INT_MAX - 256 && D <= (1 << 24) &&
            b * ((int64_t(L) + 127) / 128) * ((int64_t(D) + 63) / 64) <= (1 << 21);
+}
+
+// shape_of: up to kPairW short waves of tokens are one block's, and any more are several blocks'
+bool gated_scan_waits(int L) { return L > kPairW * kShortT; }
+
+hipError_t launch_gated_scan_error(const void *workspace, int32_t *err_out, hipStream_t stream) {
+    hipLaunchKernelGGL(k_gated_scan_error, dim3(1), dim3(1), 0, stream, static_cast<const unsigned *>(workspace), err_out);
+    return hipGetLastError();
 }
 
 size_t gated_scan_workspace(int b, int L, int D, bool bf16, bool backward) { return words_bytes(shape_of(b, L, D, bf16, backward)); }

@@ -2,6 +2,7 @@
 #include <limits.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "ssd_checks.h"
 #include "ssd_gated_scan.h"
@@ -34,6 +35,9 @@ size_t words_bytes(int b, int L, int D, ssd_dtype_t io) {
     const size_t n = std::max(ssd::gated_scan_workspace(b, L, D, bf16, false), ssd::gated_scan_workspace(b, L, D, bf16, true));
     return (n + 15) / 16 * 16;
 }
+
+// looks at another block's word before a wait gives up; 2^20 take about a second
+std::atomic<int> wait_limit{1 << 20};
 
 ssd_status_t done(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
 
@@ -91,6 +95,7 @@ ssd_status_t ssd_gated_scan_fwd(const void *x, const void *a, const float *init_
     const Range outs[] = {Range(y, n * elem(io)), Range(states, kept_bytes(b, L, D)), rfinal, Range(workspace, need)};
     if (any_alias(ins, outs)) return SSD_ERR_ALIAS;
     ssd::GatedScanArgs s{};
+    s.looks = wait_limit.load(std::memory_order_relaxed);
     s.x = x; s.a = a; s.init_state = init_state; s.y = y; s.kept = states; s.final_state = final_state; s.workspace = workspace;
     s.b = b; s.L = L; s.D = D; s.sigmoid = sigmoid != 0; s.bf16 = io == SSD_DTYPE_BF16; s.a_bf16 = a_io == SSD_DTYPE_BF16;
     return done(ssd::launch_gated_scan_fwd(s, stream));
@@ -126,6 +131,7 @@ ssd_status_t ssd_gated_scan_bwd(const void *x, const void *a, const float *init_
     const Range outs[] = {Range(dx, n * elem(io)), Range(da, n * elem(a_io)), rinit, Range(workspace, need)};
     if (any_alias(ins, outs)) return SSD_ERR_ALIAS;
     ssd::GatedScanArgs s{};
+    s.looks = wait_limit.load(std::memory_order_relaxed);
     s.x = x; s.a = a; s.init_state = init_state; s.workspace = workspace;
     s.b = b; s.L = L; s.D = D; s.sigmoid = sigmoid != 0; s.bf16 = io == SSD_DTYPE_BF16; s.a_bf16 = a_io == SSD_DTYPE_BF16;
     if (states) {
@@ -134,9 +140,25 @@ ssd_status_t ssd_gated_scan_bwd(const void *x, const void *a, const float *init_
         // the states of the forward pass once more, without its outputs
         s.kept = reinterpret_cast<float *>(static_cast<char *>(workspace) + own);
         if (const hipError_t e = ssd::launch_gated_scan_fwd(s, stream); e != hipSuccess) return SSD_ERR_HIP;
+        s.keep_error = ssd::gated_scan_waits(L);
     }
     s.dy = dy; s.d_final = d_final; s.dx = dx; s.da = da; s.d_init = d_init;
     return done(ssd::launch_gated_scan_bwd(s, stream));
+}
+
+ssd_status_t ssd_gated_scan_workspace_error(const void *workspace, size_t workspace_bytes, int b, int L,
+                                            int32_t *err_out, void *hip_stream) {
+    if (b < 0 || L < 0) return SSD_ERR_BAD_DIM;
+    if (!err_out) return SSD_ERR_NULL_ARG;
+    if (!aligned(workspace, 16) || !aligned(err_out, 4)) return SSD_ERR_ALIGN;
+    const bool waits = b > 0 && ssd::gated_scan_waits(L);
+    if (waits && (!workspace || workspace_bytes < 16)) return SSD_ERR_WORKSPACE;
+    if (Range(workspace, workspace_bytes).overlaps(Range(err_out, 4))) return SSD_ERR_ALIAS;
+    return done(ssd::launch_gated_scan_error(waits ? workspace : nullptr, err_out, static_cast<hipStream_t>(hip_stream)));
+}
+
+int ssd_gated_scan_wait_limit(int looks) {
+    return looks < 0 ? wait_limit.load(std::memory_order_relaxed) : wait_limit.exchange(looks, std::memory_order_relaxed);
 }
 
 }  // extern "C"
