@@ -394,14 +394,14 @@ __global__ __launch_bounds__(64 * W, 4) void k_gated_scan_fwd(const IO *__restri
 #pragma unroll
         for (int j = 0; j < V; ++j) k[j] = h[j];
     }
-    const int ny = y ? n : 0;
     const Rows out = rows_at(y ? y + row * D : y, n, D, c);
 #pragma unroll
     for (int t = 0; t < T; ++t) {
+        if (t >= n) continue;       // the last token's state as it is, also where it is infinite
         xr[t] = again<IO, V>(xr[t]);
 #pragma unroll
         for (int j = 0; j < V; ++j) h[j] = step_state<SIGMOID>(here(m[t][j]), h[j], xr[t].get(j));
-        if (t < ny) out.template store<IO, V>(t, raw_of<IO, V>(h));
+        if (y) out.template store<IO, V>(t, raw_of<IO, V>(h));
     }
     if (final_state && t0 + n == L)
 #pragma unroll
