@@ -537,7 +537,9 @@ ssd_status_t ssd_gated_delta_bwd(const void *q, const void *k, const void *v, co
  *   ssd_gated_scan_bwd_workspace_bytes bytes (with_states != 0: states are given), as above.
  *   L = 0 copies d_final (or zeros) to d_init.
  *
- * b up to 65535, L up to 2^31 - 257, D up to 2^24, b ceil(L / 128) ceil(D / 64) up to 2^21.  accept_len and err_flag are 4-byte, all other pointers 16-byte aligned.
+ * b up to 65535, D up to 2^24, b ceil(L / 128) ceil(D / 64) up to 2^21 (one sequence of up to
+ * 64 channels: 2^28 tokens), the steps too, with L = K.  SSD_ERR_UNSUPPORTED beyond.
+ * accept_len and err_flag are 4-byte, all other pointers 16-byte aligned.
  * Outputs must not overlap inputs (but for state_out and state_in, which may be the same),
  * each other or the workspace.  States, gradients' sums and gates are kept in fp32 (a gate
  * near 1 as its distance from 1), every output is rounded once, in an order of operations

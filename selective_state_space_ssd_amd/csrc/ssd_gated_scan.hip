@@ -39,8 +39,6 @@
 // waves a CU: 74 us), loads in the order of their use, all looks further back at once (spills).
 // fp32, 2 x 1337 tokens of 1288: 41 MB in 14.5 us, one block a CU, whose latencies add up;
 // backward of 2 x 777 tokens of 645: 11 us.
-#include <limits.h>
-
 #include "ssd_gated_scan.h"
 #include "ssd_gated_scan_gate.h"
 
@@ -641,11 +639,12 @@ hipError_t by_types(const GatedScanArgs &a, int V, F &&f) {
 
 }  // namespace
 
-// the kernels count tokens in 31 bits, up to a block past the last one, and the bytes of a
-// wave's rows in 32; the blocks have to stay inside a launch (2^32 threads)
+// The bytes of a wave's rows are counted in 32 bits.  One bound on the blocks for every type, pass
+// and tile, counted with the smallest tile at one channel a lane: as many take 2^30 of a launch's
+// 2^32 threads, and two channels a lane or longer tiles a quarter of that or less, so it is not
+// the launch's own.  It keeps L below 2^28 + 1 and with it the kernels' token counters.
 bool gated_scan_supported(int b, int L, int D) {
-    return b <= 65535 && L <= INT_MAX - 256 && D <= (1 << 24) &&
-           b * ((int64_t(L) + 127) / 128) * ((int64_t(D) + 63) / 64) <= (1 << 21);
+    return b <= 65535 && D <= (1 << 24) && b * ((int64_t(L) + 127) / 128) * ((int64_t(D) + 63) / 64) <= (1 << 21);
 }
 
 // shape_of: up to kPairW short waves of tokens are one block's, and any more are several blocks'

@@ -1,6 +1,4 @@
 // ssd_gated_scan_api.hip -- host-side checks and dispatch of the gated scan.
-#include <limits.h>
-
 #include <algorithm>
 #include <atomic>
 
