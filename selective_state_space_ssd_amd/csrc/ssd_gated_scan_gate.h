@@ -4,7 +4,8 @@
 //   sigmoid:    alpha = 1 / (1 + e^-a),  u = (1 - alpha) x
 //
 // A decay near 1 is kept as beta = 1 - alpha, a smaller one as alpha, each to a few 2^-24 of
-// itself.  Near 1, where long memories lie, alpha in 32 bits is off by up to 2^-25 however
+// itself (a log decay's series for beta to 1.1), and where exp2 makes it |a| 2^-24 more, the
+// rounding of a log2 e: 9 2^-24 of a state that a gate of 1e-4 leaves.  Near 1, where long memories lie, alpha in 32 bits is off by up to 2^-25 however
 // small beta is, and the same way at every token of a constant gate: at a = -1e-6 the
 // memory's length would be off by 3 %, and a state decayed with it by 2^-25 a token.  Far
 // from 1 it is beta that says too little of alpha, as after a gate that erases a large state.
