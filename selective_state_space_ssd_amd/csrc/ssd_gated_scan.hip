@@ -30,14 +30,18 @@
 // block, two blocks a CU; a token's gate takes the place of its value in registers, so that the
 // second walk starts from what the first left (122 registers forward, 193 backward).
 //
-// bf16, kernel times (call times are 2 to 4 us more, the words cleared before): 4 x 2048 tokens of
-// 5120 channels behind gates, forward 252 MB in 56 us, 4.5 TB/s; 16384 tokens of 2560 with fp32
-// decays, 335 MB in 76, 4.4 TB/s; backward of the former 425 MB in 85 to 90, 4.8 TB/s.  A product of
-// two such arrays into a third reaches 5.6, a copy 5.15.  25 vector instructions an element
-// forward (37 backward) keep the vector ALU busy for 60 % of that time, which loads do not wholly
-// cover.  Not better: tiles of half and of twice the tokens, four channels a lane (fewer
-// waves a CU: 74 us), loads in the order of their use, all looks further back at once (spills).
-// fp32, 2 x 1337 tokens of 1288: 41 MB in 14.5 us, one block a CU, whose latencies add up;
+// bf16, medians of kernel times: 4 x 2048 tokens of 5120 channels behind gates, forward 252 MB in
+// 58 us, 4.3 TB/s; 16384 tokens of 2560 with fp32 decays, 335 MB in 78, 4.3 TB/s; backward of the
+// former 425 MB in 88, 4.8 TB/s (with an fp32 gate 593 MB in 106, 5.6), without kept states 47 more
+// for a forward pass that stores nothing else, its second walk included.  One array into
+// another reaches 6.1 TB/s on this card.  24 vector instructions an element forward (36 backward)
+// keep the vector ALU busy for 60 % of that time, which loads do not wholly cover.  Blocks come
+// in rounds of two a CU, 1280 forward and 2560 backward for 5120 channels, 2.5 and 5 rounds.  The
+// fewer the rounds, the more a part-filled last one counts: 2560 channels, 1.25 and 2.5 rounds,
+// take 35 us, 3.6 TB/s, and 51, 4.2.  Not better: tiles of half and of twice the tokens, four
+// channels a lane (fewer waves a CU: 74 us), loads in the order of their use, all looks further
+// back at once (spills).
+// fp32, 2 x 1337 tokens of 1288: 41 MB in 15 us, one block a CU, whose latencies add up;
 // backward of 2 x 777 tokens of 645: 11 us.
 #include "ssd_gated_scan.h"
 #include "ssd_gated_scan_gate.h"
@@ -544,15 +548,24 @@ int lane_channels(int D, bool bf16) { return bf16 && D % 2 == 0 ? 2 : 1; }
 
 // Tokens of a block: W waves of T tokens.  Much work takes long stretches, fewer pairs to hand on
 // for as many bytes: forward 8 x 32 tokens, backward 4 x 32 with two channels a lane (193
-// registers, of which a SIMD holds two waves) and 16 x 16 with one (66 registers).  Where 128
+// registers, of which a SIMD holds two waves) and 16 x 16 with one (68 registers).  Where 128
 // tokens a block make no more blocks than there are CUs, and for sequences that end within
-// one, 8 x 16, the long way / the short way in us:
-//   forward, bf16    4 x 2048 tokens of 2560 36.1 / 37.7; 1 x 1000 of 512 12.9 / 10.4; 32 x 100 of 2560 15.8 / 13.9
-//   forward, fp32    4 x 2048 of 2560 53.8 / 60.5; 2 x 777 of 645 11.4 / 10.1; 32 x 100 of 2560 19.8 / 17.1
-//   backward, bf16   4 x 2048 of 2560 55.0 / 57.0; 2 x 777 of 645 12.9 / 11.7; 32 x 100 of 2560 23.1 / 20.7
-//   backward, fp32   4 x 2048 of 2560 91.4 / 94.2 (4 x 32: 97.2); 2 x 777 of 645 13.8 / 11.9; 32 x 100 of 2560 33.0 / 28.5
-// A chain of more than 32 of the short blocks costs more than their latency spares: one sequence
-// of 16384 tokens of 128 channels, forward, bf16 19.3 / 21.6, fp32 15.7 / 17.4.
+// one, 8 x 16.  The long way / the short way in us, both launches:
+//   blocks of 8 x 16   154 (2 x 777 tokens)  304 (2 x 1024)  464          704          1008         1504         2560 (4 x 2048)
+//   forward, fp32      13.1 / 11.4           14.1 / 14.9     16.1 / 18.1  21.5 / 24.6  26.1 / 33.3  37.6 / 43.8  51.8 / 59.9
+//   forward, bf16                            16.6 / 17.5     19.0 / 20.7  25.1 / 27.8  29.1 / 39.2  41.6 / 45.2  59.6 / 63.3
+//   backward, fp32     17.2 / 13.4           17.3 / 17.8     19.7 / 21.6  31.1 / 34.3  39.8 / 44.6  55.3 / 56.5  84.2 / 82.3
+//   backward, bf16                           21.7 / 21.4     25.2 / 25.1  36.9 / 35.5  46.3 / 46.5  58.9 / 58.1  90.6 / 87.3
+// (The gradients in bf16 hardly depend on it.  16 x 16 would take 20.8, 22.8, 36.3, 42.1, 60.7 and
+// 101.4 there; forward, in bf16, 16.8, 18.9, 28.8, 31.5, 43.6 and 67.6.)  Sequences that end within
+// a block, 32 x 100 tokens of 2560 channels: forward bf16 15.8 / 13.9, fp32 19.8 / 17.1, backward
+// 23.1 / 20.7 and 33.0 / 28.5.
+// A chain of more than 32 of the short blocks costs more than their latency spares.  One sequence,
+// forward: 16384 tokens, bf16, 64, 128 and 256 channels 19.5 / 22.0, 19.9 / 22.7, 21.6 / 24.8, fp32, half
+// as many channels, 14.6 / 16.3, 15.1 / 16.5, 16.6 / 18.5; 8192 tokens of 256 or 128 channels 17.7 / 18.1
+// and 14.1 / 13.8, 5000 of 512 or 256 17.5 / 17.4 and 14.0 / 14.0; 60000 of 64 or 32 34.0 / 55.6 and
+// 23.8 / 36.4.  (Backward, at 5000, 8192, 16384 and 60000 tokens, bf16 19.8 / 19.7, 20.5 / 19.9,
+// 26.2 / 24.6, 60.8 / 58.4, fp32 17.4 / 15.7, 17.2 / 15.1, 18.1 / 17.8, 28.4 / 37.8.)
 //
 // Sequences of 129 to 256 tokens take one block of 16 x 16: no words to clear, one launch instead
 // of two.  Two blocks of 8 x 16 / this, kernel times and, of the first, call times: forward, bf16

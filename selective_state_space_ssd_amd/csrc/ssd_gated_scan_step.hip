@@ -2,7 +2,7 @@
 //
 // A stream over the state and the tokens: a lane holds a channel of one batch row, steps it
 // through the K tokens and writes the state after the accepted ones.  One token of 64 sequences
-// of 5120 channels (4.6 MB) is 2.9 us of kernel, five tokens of 3 sequences 3.2: a call is its
+// of 5120 channels (4.6 MB) is 3.2 us of kernel, five tokens of 3 sequences 3.4: a call is its
 // launch, 10 us from Python.
 #include "ssd_gated_scan.h"
 #include "ssd_gated_scan_gate.h"

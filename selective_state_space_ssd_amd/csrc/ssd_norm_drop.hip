@@ -11,9 +11,10 @@
 // that counts the offset on draws another mask in each replay.
 //
 // The generator hides behind the loads: 8192 rows of 2560 bf16 channels with an fp32 residual
-// (252 MB) take 43 us forward, 5.9 TB/s, as without dropout, and 79 + 4 backward (377 MB and
-// 21 of partial sums), 4.8 TB/s.  (20 wide products and about as many other instructions a
-// counter, four elements: 5.3 us of the vector ALU's time forward.)
+// (252 MB) take 42 us forward, 5.9 TB/s, as without dropout, and 77 backward (377 MB and 11 of
+// partial sums), 5.0 TB/s, and 5 more for adding those up; medians of a trace.  (20 wide products
+// and about as many other instructions a counter, four elements: 5.3 us of the vector ALU's time
+// forward.)
 #include "ssd_norm_add.h"
 
 namespace ssd {
